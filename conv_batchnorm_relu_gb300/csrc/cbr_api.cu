@@ -11,6 +11,7 @@
 
 #include "../../include/cbr.h"
 #include "cbr_internal.h"
+#include "token_ops.h"
 
 namespace cbr {
 
@@ -298,6 +299,15 @@ int check_forward_train(const void* desc, const void* x, const void* w, const fl
 int check_device() {
   DeviceInfo* dev = nullptr;
   return current_device(&dev);
+}
+
+int device_for_call(int* num_sms, uint32_t** err) {
+  DeviceInfo* dev = nullptr;
+  const int st = current_device(&dev);
+  if (st) return st;
+  *num_sms = dev->num_sms;
+  *err = dev->err;
+  return CBR_OK;
 }
 
 bool ensure_smem_attr(const void* func, int bytes) {

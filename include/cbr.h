@@ -65,7 +65,8 @@ typedef enum {
   CBR_ERR_TIMEOUT = 7      /* (cbr_stream_status) a kernel gave up on a bounded wait */
 } cbr_status_t;
 
-typedef enum { CBR_F16 = 0, CBR_BF16 = 1 } cbr_dtype_t;
+/* CBR_F32 is taken by the token operators only. */
+typedef enum { CBR_F16 = 0, CBR_BF16 = 1, CBR_F32 = 2 } cbr_dtype_t;
 
 /* Source of the ReLU mask for cbr_backward. */
 typedef enum {
@@ -326,6 +327,163 @@ cbr_status_t cbr_selftest_bounded_wait(int32_t limit_us, cbr_stream_t stream);
  */
 cbr_status_t cbr_profile_next_call(void* const* events, int32_t count);
 int32_t cbr_profile_last_count(void);
+
+/* ======================================================================= token operators
+ *
+ * What a trunk of blocks and a training objective need on top of a CBR stem, whose NHWC feature
+ * map is a grid of tokens: norms around a gated residual block, rotary positions over several
+ * axes, and a distillation loss from a teacher's top logits.  The conventions above hold (caller
+ * owns every buffer, asynchronous on `stream`, host-side validation before anything is enqueued),
+ * with these differences: strides are in elements and counted in 64 bits; a tensor need only be
+ * aligned to its element; a call whose output is empty (no rows, no tokens) does nothing and
+ * returns CBR_OK; and device data is never trusted (an entry id outside the vocabulary is an
+ * absent entry, an axis outside the position's axes is the last one).
+ * Rows of one output may not overlap, and no output may overlap an input except where it says so.
+ */
+
+/*
+ * Distillation from a teacher's top logits.  For each row r of student logits s (temperature T):
+ *   x = s / T,  log q_v = x_v - log sum_u exp x_u
+ *   the row's entries k are (top_ids[r][k], top_logits[r][k]); an id outside [0, vocab) marks an
+ *   absent entry, whose logit is not used
+ *   teacher_lse NULL: p = softmax of t / T over the present entries, no tail (p_rest = 0)
+ *   teacher_lse set:  p_k = exp(t_k / T - teacher_lse[r]) (the log-sum-exp of t / T over the
+ *                     teacher's whole vocabulary), p_rest = max(0, 1 - sum p_k), and q_rest is the
+ *                     student's mass outside the listed ids; p_rest = 0 where q_rest is 0
+ *   loss_r  = w_r T^2 (sum_k p_k (log p_k - log q_k) + p_rest (log p_rest - log q_rest))
+ *   dlogits = dloss_r w_r T (q_v (sum p + p_rest) - sum over the entries of v of p_k
+ *                            - [v is not listed] q_v p_rest / q_rest)
+ * An id listed twice counts twice in the sums.  0 log 0 is 0.  w = row_weight, or 1 where NULL.
+ * A row has loss 0, gradient 0 and statistics 0, whatever its other values (NaN included), if
+ * w_r = 0; or no entry is present (teacher_lse NULL: none above -infinity); or no student logit
+ * is above -infinity.  Other NaN and infinities go through the formulas, in their row alone.
+ */
+typedef struct {
+  int64_t rows, vocab;      /* rows >= 0; 1 <= vocab <= 393216 */
+  int64_t topk;             /* entries a row, 0 <= topk <= 1024 */
+  int64_t logits_stride;    /* elements between rows, >= vocab */
+  int64_t dlogits_stride;
+  int64_t ids_stride;       /* elements between rows of top_ids, >= topk */
+  int64_t top_stride;       /* elements between rows of top_logits, >= topk */
+  int32_t dtype;            /* of logits and dlogits */
+  int32_t top_dtype;        /* of top_logits */
+  int32_t id_bytes;         /* 4 (int32) or 8 (int64) */
+  float temperature;        /* > 0 */
+} cbr_distill_desc_t;
+
+/*
+ * Loss.  logits [rows][vocab], top_ids and top_logits [rows][topk], teacher_lse [rows] fp32 or
+ * NULL, row_weight [rows] fp32 or NULL -> loss [rows] fp32, stats [rows][3] fp32 (the largest
+ * logit, the sum of exp((s - largest) / T) over the row and over its unlisted ids) for the
+ * backward.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, DEVICE, CUDA.
+ */
+cbr_status_t cbr_distill_forward(const cbr_distill_desc_t* desc, const void* logits, const void* top_ids,
+                                 const void* top_logits, const float* teacher_lse, const float* row_weight,
+                                 float* loss, float* stats, cbr_stream_t stream);
+
+/*
+ * Gradient, from the forward's stats and dloss [rows] fp32 (NULL: ones) -> dlogits [rows][vocab].
+ * dlogits may be logits itself (same address and stride).
+ */
+cbr_status_t cbr_distill_backward(const cbr_distill_desc_t* desc, const float* dloss, const void* logits,
+                                  const void* top_ids, const void* top_logits, const float* teacher_lse,
+                                  const float* row_weight, const float* stats, void* dlogits, cbr_stream_t stream);
+
+/*
+ * Loss and gradient (of the loss itself: dloss = 1) in one call that reads the logits once.  loss
+ * and dlogits are those of the two calls above; stats may be NULL.  dlogits may be logits itself.
+ */
+cbr_status_t cbr_distill_forward_backward(const cbr_distill_desc_t* desc, const void* logits, const void* top_ids,
+                                          const void* top_logits, const float* teacher_lse,
+                                          const float* row_weight, float* loss, float* stats, void* dlogits,
+                                          cbr_stream_t stream);
+
+/*
+ * The norms around a block f, its gate and its residual scale, in one pass over the rows:
+ *   n     = (f - m1) r1 post_weight                    the norm after the block
+ *   x_out = residual_scale x + branch_scale gate n     the join
+ *   h     = (x_out - m2) r2 pre_weight                 the norm before the next block
+ * with r = 1 / sqrt(mean((a - m)^2) + eps) over a row, m its mean (CBR_NORM_LAYER) or 0
+ * (CBR_NORM_RMS).  h is computed from x_out before it is rounded.  Either half may stand alone:
+ * post_weight and branch NULL: h = norm of x (there is no x_out); pre_weight NULL: x_out only.
+ * gate [rows / gate_rows][dim]: one row for each gate_rows consecutive rows (gate_rows = rows: one
+ * gate vector; 1: a gate for every row); NULL: no gate.  Weights, gate and their gradients are
+ * fp32, the rest has the storage dtype.
+ */
+typedef enum { CBR_NORM_RMS = 0, CBR_NORM_LAYER = 1 } cbr_norm_kind_t;
+typedef struct {
+  int64_t rows;             /* >= 0 */
+  int64_t dim;              /* 1 .. 16384 */
+  int64_t gate_rows;        /* rows is a multiple of it; not used without a gate */
+  int64_t x_stride, branch_stride, x_out_stride, h_stride;           /* elements between rows, >= dim */
+  int64_t dx_out_stride, dh_stride, dx_stride, dbranch_stride;       /* backward */
+  int32_t dtype, kind;
+  float eps;                /* > 0 (forward) */
+  float residual_scale, branch_scale;
+} cbr_block_norm_desc_t;
+
+/*
+ * Forward -> x_out [rows][dim], h [rows][dim], stats [rows][4] fp32 (m1, r1, m2, r2; 0 for a norm
+ * that is not there), which may be NULL.  x_out may be x or branch itself, and h branch itself or
+ * (without a branch) x itself: same address and stride.
+ */
+cbr_status_t cbr_block_norm_forward(const cbr_block_norm_desc_t* desc, const void* x, const void* branch,
+                                    const float* post_weight, const float* gate, const float* pre_weight,
+                                    void* x_out, void* h, float* stats, cbr_stream_t stream);
+
+/* Workspace bytes of the backward for this desc (dim, dtype): per-block sums of the parameter gradients. */
+cbr_status_t cbr_block_norm_workspace_size(const cbr_block_norm_desc_t* desc, size_t* bytes);
+
+/*
+ * Backward.  dx_out [rows][dim] is the gradient that reaches x_out from later in the residual
+ * stream (NULL where there is none: only h is used), dh that at h (unused without pre_weight).
+ * x_out is the forward's (without a branch: x itself).  With u = dh pre_weight, c = (x_out - m2) r2:
+ *   D = dx_out + r2 (u - [LAYER] mean(u) - c mean(u c));     dpre_weight = sum over rows of dh c
+ *   dx = residual_scale D  (without a branch: D)
+ *   with e = (f - m1) r1:  dgate = sum over a gate's rows of branch_scale D e post_weight
+ *   dpost_weight = sum over rows of branch_scale D gate e;  v = branch_scale D gate post_weight
+ *   dbranch = r1 (v - [LAYER] mean(v) - e mean(v e))
+ * Sums over rows are kept in fp32 and added in a fixed order, so results repeat bit for bit.
+ * dx may be dx_out itself, dbranch may be branch or dh itself.
+ */
+cbr_status_t cbr_block_norm_backward(const cbr_block_norm_desc_t* desc, const void* dx_out, const void* dh,
+                                     const void* x_out, const void* branch, const float* post_weight,
+                                     const float* gate, const float* pre_weight, const float* stats, void* dx,
+                                     void* dbranch, float* dpost_weight, float* dgate, float* dpre_weight,
+                                     void* ws, size_t ws_bytes, cbr_stream_t stream);
+
+/*
+ * Rotary positions over several axes (time, height, width, ...), on queries and keys in one call.
+ * The first rot_dim elements of a head are rot_dim / 2 pairs: (i, i + rot_dim / 2) in
+ * CBR_ROTARY_HALVES, (2 i, 2 i + 1) in CBR_ROTARY_NEIGHBOURS; the others are copied.  Pair i
+ * follows the position's axis axis[i], at freq[i] turns a step:
+ *   angle = 2 pi positions[b][t][axis[i]] freq[i] / 2^64
+ *   (y1, y2) = (x1 cos(angle) - x2 sin(angle), x2 cos(angle) + x1 sin(angle))
+ * freq is the frequency f_i (radians a step) as a fixed-point fraction of a turn,
+ * round(f_i / (2 pi) 2^64): the product with a position is taken modulo 2^64, that is modulo whole
+ * turns, without rounding, so far positions lose nothing.  Positions may be negative.
+ */
+typedef enum { CBR_ROTARY_HALVES = 0, CBR_ROTARY_NEIGHBOURS = 1 } cbr_rotary_layout_t;
+typedef struct {
+  int64_t batch, tokens;                 /* >= 0 */
+  int64_t q_stride[3], k_stride[3];      /* elements between batches, tokens, heads; the head's own are adjacent */
+  int64_t q_out_stride[3], k_out_stride[3];
+  int64_t pos_stride[3];                 /* elements between batches, tokens, axes; 0 repeats */
+  int32_t heads_q, heads_k;              /* 0 without q or k */
+  int32_t head_dim, rot_dim;             /* head_dim <= 1024; rot_dim even, 2 .. head_dim */
+  int32_t axes;                          /* 1 .. 8 */
+  int32_t layout, dtype;
+} cbr_rotary_desc_t;
+
+/* q_out may be q itself and k_out k itself (same address and strides). */
+cbr_status_t cbr_rotary_forward(const cbr_rotary_desc_t* desc, const void* q, const void* k,
+                                const int32_t* positions, const int64_t* freq, const uint8_t* axis, void* q_out,
+                                void* k_out, cbr_stream_t stream);
+
+/* The gradients at q and k from those at q_out and k_out: the rotation by the opposite angle. */
+cbr_status_t cbr_rotary_backward(const cbr_rotary_desc_t* desc, const void* dq_out, const void* dk_out,
+                                 const int32_t* positions, const int64_t* freq, const uint8_t* axis, void* dq,
+                                 void* dk, cbr_stream_t stream);
 
 #ifdef __cplusplus
 }
