@@ -1,18 +1,22 @@
 // Distillation from a teacher's top logits, forward and backward (formulas: include/cbr.h).
 //
-// A row is cut into slices, one for each block of a cluster (one block where the row is short), and
-// stays in shared memory between its sweeps, so the logits cross HBM once.  A block works through
-// rows with three kinds of warps:
-//   producer   one thread: bulk copies of coming rows into a ring of buffers, bulk copies of
-//              finished gradients out of them;
-//   teacher    one warp, a row ahead: the entries' ids, p and log p into shared memory;
-//   consumers  take the listed logits out of the slice (each one's place holds -infinity from then
-//              on, so the sweep sums unlisted words alone, with no test in it), sweep for the
-//              largest logit and the sum of exponentials, exchange (largest, unlisted, listed) with
-//              the cluster's other blocks, sweep again turning logits into gradients in place, and
-//              put the listed words' gradients in.
-// The exponent is formed from the difference to the largest logit, not from scaled logits: exact
-// near the largest, and finite for rows masked with the type's lowest value.
+// A block takes a row (or, where rows are few, one of a cluster's slices of it) through a ring of
+// shared-memory buffers: a first pass for the largest logit and the sums of exponentials, a second
+// one that turns logits into gradients in place.  The ring keeps the chunks that came last, the
+// second pass begins with them, and only what did not fit is fetched again, from L2; so the logits
+// cross HBM once.  Warps have their own jobs and meet at barriers in shared memory, chunk by chunk:
+//   loader     one thread: bulk copies of chunks into the ring;
+//   consumers  both passes, each warp on its own part of every chunk.  A warp takes the listed logits
+//              of its part out first (-infinity stands there from then on, so that the sweep sums
+//              unlisted words alone, with no test in it) and puts the listed words' gradients in last.
+//              Between the passes they merge their sums, and exchange them with the cluster;
+//   storer     one thread: bulk copies of finished chunks out of the ring;
+//   teachers   two warps, for every other row: some rows ahead the ids and log p of the row's entries,
+//              behind the others its loss.
+// Exponentials are 2^(s c - b), c = log2(e) / T, with b the largest logit's s c, rounded: one fused
+// multiply-add whose product and difference are exact, and b itself, being the same everywhere, drops
+// out of every quotient.  Where the largest is so low that b is not finite (a row masked with the
+// type's lowest value), the difference is taken first: 2^((s - largest) c).
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -30,27 +34,36 @@ using namespace tok;
 
 enum Mode { kLoss, kBoth, kGradient };
 
-constexpr int kMaxWarps = 8;        // consumers
-constexpr int kMaxBuffers = 4;
+constexpr int kMaxWarps = 16;       // consumers
+constexpr int kMaxBuffers = 16;
 constexpr int kMaxCluster = 8;
-constexpr int kRepeated = 1 << 30;  // in an entry's id: the same id was listed before
+constexpr int kFewRows = 4;         // rows of a call whose rows are each shared by a cluster
+constexpr int kRows = 4;            // whose entries are held at once; a multiple of kTeachers
+constexpr int kBatch = 4;           // 16-byte vectors that a consumer has in hand at once
+constexpr int kTeachers = 2;        // warps, for a row each in turn
+constexpr int kOthers = 2 + kTeachers;  // warps that are not consumers
+constexpr int kAbsent = -(1 << 30); // the id of an absent entry
 
 struct Plan {
   int slices;       // of a row: the cluster's blocks (kGradient: independent work items)
   int width;        // elements of a slice, a multiple of 128
-  int buffers;
-  int buffer_bytes;
-  int warps;
+  int part;         // log2 of the 16-byte vectors of a chunk that one consumer warp works on
+  int warps;        // consumers; a power of two
+  int buffers;      // of the ring
   int kp;           // room for entries
   int smem;
 };
 
 struct Header {
-  uint64_t full[kMaxBuffers], empty[kMaxBuffers], t_full[2], t_free[2], x_full[2];
-  float red[kMaxWarps][4];
-  float xch[2][kMaxCluster][4];   // (largest, unlisted, listed) of each block of the cluster
-  float teacher[2][8];            // mass, rest, weight, state
-  int repeated;
+  // chunk by chunk: copied in; worked through; copied out
+  uint64_t full[kMaxBuffers], done[kMaxBuffers], free[kMaxBuffers];
+  // row by row: teacher's entries; its probabilities; no longer needed; row's sums; the consumers'
+  // own sums; the cluster's sums
+  uint64_t t_full[kRows], m_full[kRows], t_free[kRows], r_full[kRows], c_full[2], x_full;
+  float red[2][kMaxWarps][4];       // (largest, unlisted, listed) of each consumer
+  float xch[kMaxCluster][4];        // and of each block of the cluster
+  float teacher[kRows][4];          // mass, rest, weight, state
+  float result[kRows][4];           // of the row: largest, total, unlisted; live
 };
 enum { kMass, kRest, kWeight, kState };
 enum { kDead, kEmpty, kLive };    // weight 0 (not even loaded), nothing to learn from, the rest
@@ -86,8 +99,27 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void bulk_store_1d(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+// Bulk copies that tell L2 what to keep: the chunks that will be read again, and nothing else.
+__device__ __forceinline__ uint64_t l2_keep() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t l2_pass() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes, uint64_t policy) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;" ::"l"(dst), "r"(src),
+               "r"(bytes), "l"(policy)
+               : "memory");
 }
 
 // 2^x.  With 16-bit logits results below 2^-126 are taken as 0 (below what f16 and the sums can
@@ -100,172 +132,315 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// The logits of 16 bytes.
+// Two floats in one register pair, and arithmetic on both at once.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The logits of 16 bytes, in pairs.
 template <typename T>
 struct Chunk {
-  static constexpr int n = 16 / sizeof(T);
-  float v[n];
+  static constexpr int kPairs = 8 / sizeof(T);
+  uint64_t v[kPairs];
   __device__ __forceinline__ Chunk(uint4 w) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    if constexpr (sizeof(T) == 4) {
+      v[0] = pair(__uint_as_float(u[0]), __uint_as_float(u[1]));
+      v[1] = pair(__uint_as_float(u[2]), __uint_as_float(u[3]));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 4) {
-        v[i] = __uint_as_float(u[i]);
-      } else {
+      for (int i = 0; i < 4; ++i) {
         const float2 f = unpack2<std::is_same_v<T, __nv_bfloat16>>(u[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+        v[i] = pair(f.x, f.y);
       }
     }
   }
   __device__ __forceinline__ uint4 packed() const {
     uint32_t u[4];
+    if constexpr (sizeof(T) == 4) {
+      const float2 a = unpair(v[0]), b = unpair(v[1]);
+      return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (sizeof(T) == 4) u[i] = __float_as_uint(v[i]);
-      else u[i] = pack2<std::is_same_v<T, __nv_bfloat16>>(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpair(v[i]);
+        u[i] = pack2<std::is_same_v<T, __nv_bfloat16>>(f.x, f.y);
+      }
+      return make_uint4(u[0], u[1], u[2], u[3]);
     }
-    return make_uint4(u[0], u[1], u[2], u[3]);
   }
-  __device__ __forceinline__ float largest() const {
-    float m = v[0];
+  // The exponential of every element: from minus b (kFar: minus the largest logit).
+  template <bool kFar>
+  __device__ __forceinline__ void exponentials(uint64_t minus, uint64_t c) {
 #pragma unroll
-    for (int i = 1; i < n; ++i) m = Max::of(m, v[i]);
-    return m;
+    for (int i = 0; i < kPairs; ++i) {
+      const float2 f = unpair(kFar ? mul2(add2(v[i], minus), c) : fma2(v[i], c, minus));
+      v[i] = pair(ex2<T>(f.x), ex2<T>(f.y));
+    }
   }
 };
 
-// A running (largest, sum of 2^((s - largest) c)) pair, the sum in two parts.
+// The exponent's b (not to be fused with what it meets: it has to be the same everywhere), and whether
+// it is out of range.
+__device__ __forceinline__ float base_of(float top, float c) { return __fmul_rn(top, c); }
+__device__ __forceinline__ bool is_far(float top, float c) { return !(fabsf(base_of(top, c)) < 1e38f); }
+__device__ __forceinline__ float minus_base(float top, float c) { return is_far(top, c) ? -top : -base_of(top, c); }
+template <typename T>
+__device__ __forceinline__ float exponential(float s, float top, float c) {
+  return ex2<T>(is_far(top, c) ? (s - top) * c : __fmaf_rn(s, c, -base_of(top, c)));
+}
+// What a sum relative to `from` is multiplied by to be relative to `to`, the larger.
+template <typename T>
+__device__ __forceinline__ float rebase(float from, float to, float c) {
+  if (from == -INFINITY) return 0.f;
+  return ex2<T>(is_far(to, c) ? (from - to) * c : __fsub_rn(base_of(from, c), base_of(to, c)));
+}
+// 2^(top c - b), b's rounding: what a sum relative to the largest logit is multiplied by to be relative to b.
+__device__ __forceinline__ float rounding_of_base(float top, float c) {
+  return is_far(top, c) ? 1.f : exp2f(__fmaf_rn(top, c, -base_of(top, c)));
+}
+
+// The largest of `n` vectors of logits, NaN if one is.
+template <typename T, int n>
+__device__ __forceinline__ float largest(const uint4 (&w)[n]) {
+  if constexpr (sizeof(T) == 4) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      m = Max::of(m, Max::of(Max::of(__uint_as_float(w[i].x), __uint_as_float(w[i].y)),
+                             Max::of(__uint_as_float(w[i].z), __uint_as_float(w[i].w))));
+    return m;
+  } else {
+    using T2 = std::conditional_t<std::is_same_v<T, __half>, __half2, __nv_bfloat162>;
+    T2 m;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      T2 a[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[k] = *reinterpret_cast<const T2*>(&u[k]);
+      const T2 x = __hmax2_nan(__hmax2_nan(a[0], a[1]), __hmax2_nan(a[2], a[3]));
+      m = i ? __hmax2_nan(m, x) : x;
+    }
+    const float2 f = unpack2<std::is_same_v<T, __nv_bfloat16>>(*reinterpret_cast<uint32_t*>(&m));
+    return Max::of(f.x, f.y);
+  }
+}
+
+// A running (largest, sum of exponentials relative to it) pair, the sum in three parts: two of unlisted
+// words, one of listed.
 struct Running {
-  float top = -INFINITY, unlisted = 0.f, listed = 0.f;
+  float top = -INFINITY, listed = 0.f;
+  uint64_t sum = 0;
 };
 template <typename T>
 __device__ __forceinline__ void raise(Running& r, float m, float c) {
   if (!(m <= r.top)) {   // NaN gets in, too, and stays
     m = Max::of(m, r.top);
-    const float f = r.top == -INFINITY ? 0.f : ex2<T>((r.top - m) * c);
-    r.unlisted *= f;
+    const float f = rebase<T>(r.top, m, c);
     r.listed *= f;
+    r.sum = m == m ? mul2(r.sum, pair(f, f)) : pair(m, m);
     r.top = m;
-    if (m != m) r.unlisted = m;
   }
 }
+// The same, merged over threads.
+struct Sums {
+  float top = -INFINITY, unlisted = 0.f, listed = 0.f;
+};
+// The lanes' pairs as one.
 template <typename T>
-__device__ __forceinline__ Running merge_warp(Running r, float c) {
-  const float m = warp_reduce<Max>(r.top);
-  const float f = r.top == -INFINITY ? 0.f : ex2<T>((r.top - m) * c);
-  return Running{m, warp_reduce<Sum>(r.unlisted * f), warp_reduce<Sum>(r.listed * f)};
+__device__ __forceinline__ Sums merge_warp(Sums r, float c) {
+  const float m = warp_max(r.top);
+  const float f = rebase<T>(r.top, m, c);
+  uint64_t s = pair(r.unlisted * f, r.listed * f);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float2 v = unpair(s);
+    s = add2(s, pair(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+  }
+  const float2 v = unpair(s);
+  return Sums{m, v.x, v.y};
 }
 
-// Where a slice's elements lie in a buffer: element j at lead + j, so that global and shared
-// addresses agree modulo 16; chunks [c0, c1) are whole, the others hold `edge` elements.
+// Where a slice's elements lie in its chunks: element j at place lead + j, so that global and shared
+// addresses agree modulo 16.  16-byte vectors [v0, v1) are whole and are copied in bulk; the first and
+// the last may not be, and their elements go one by one.
 template <typename T>
 struct Slice {
   static constexpr int kN = 16 / sizeof(T);
-  int n, lead, c0, c1, chunks;
+  int n, lead, v0, v1, vectors;
   __device__ __forceinline__ Slice(const T* p, int n_) : n(n_) {
     lead = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
-    c0 = lead ? 1 : 0;
-    c1 = max(c0, (lead + n) / kN);
-    chunks = n ? (lead + n + kN - 1) / kN : 0;
+    v0 = lead ? 1 : 0;
+    v1 = max(v0, (lead + n) / kN);
+    vectors = n ? (lead + n + kN - 1) / kN : 0;
   }
-  __device__ __forceinline__ uint32_t whole_bytes() const { return (uint32_t)(c1 - c0) * 16u; }
-  __device__ __forceinline__ bool ragged() const { return n && (c0 != 0 || c1 != chunks); }
-  // Thread i of the first 2 * kN holds a place of the first or of the last chunk; -1: none.
+  // Lane i holds a place of the first vector (0 .. kN - 1) or of the last (kN .. 2 kN - 1), or -1.
   __device__ __forceinline__ int edge_place(int i) const {
     if (i >= 2 * kN || !n) return -1;
-    if (i < kN) return c0 ? i : -1;
-    if (c1 >= chunks || (chunks == 1 && c0)) return -1;
-    return (chunks - 1) * kN + i - kN;
+    if (i < kN) return v0 ? i : -1;
+    if (v1 >= vectors || (vectors == 1 && v0)) return -1;
+    return (vectors - 1) * kN + i - kN;
   }
+  __device__ __forceinline__ bool inside(int place) const { return place >= lead && place < lead + n; }
 };
 
-__device__ __forceinline__ int entry_id(const DistillArgs& a, long long row, int k) {
+// What the teacher warp reads of a row, a row ahead of its use: the entries of the first kAhead rounds
+// of 32 as they are in memory.
+constexpr int kAhead = 4;
+struct Fetched {
+  float weight, lse;
+  long long id[kAhead];
+  uint32_t logit[kAhead];
+};
+__device__ __forceinline__ long long raw_id(const DistillArgs& a, long long row, int k) {
   const long long i = row * a.d.ids_stride + k;
-  const long long id = a.d.id_bytes == 8 ? static_cast<const long long*>(a.top_ids)[i]
-                                         : (long long)static_cast<const int*>(a.top_ids)[i];
-  return id >= 0 && id < a.d.vocab ? (int)id : -1;
+  return a.d.id_bytes == 8 ? static_cast<const long long*>(a.top_ids)[i]
+                           : (long long)static_cast<const int*>(a.top_ids)[i];
+}
+__device__ __forceinline__ uint32_t raw_logit(const DistillArgs& a, long long row, int k) {
+  const long long i = row * a.d.top_stride + k;
+  return a.d.top_dtype == CBR_F32 ? static_cast<const uint32_t*>(a.top_logits)[i]
+                                  : (uint32_t)static_cast<const uint16_t*>(a.top_logits)[i];
+}
+__device__ __forceinline__ float logit_of(const DistillArgs& a, uint32_t raw) {
+  if (a.d.top_dtype == CBR_F32) return __uint_as_float(raw);
+  if (a.d.top_dtype == CBR_BF16) return __uint_as_float(raw << 16);
+  return unpack2<false>(raw).x;
+}
+__device__ __forceinline__ void fetch(const DistillArgs& a, long long row, Fetched& f) {
+  const int lane = threadIdx.x & 31;
+  f.weight = a.row_weight ? a.row_weight[row] : 1.f;
+  f.lse = a.teacher_lse ? a.teacher_lse[row] : 0.f;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int k = lane + i * 32;
+    if (k < (int)a.d.topk) {
+      f.id[i] = raw_id(a, row, k);
+      f.logit[i] = raw_logit(a, row, k);
+    }
+  }
 }
 
-// The teacher's distribution of a row, by one warp.
-__device__ void teach(const DistillArgs& a, long long row, float inv_t, int* ids, float* p, float* lp, float* out) {
+// The teacher's distribution of a row, by one warp: `begun` is called once the ids and the row's state
+// are there, which is all that the first pass needs.
+template <typename F>
+__device__ void teach(const DistillArgs& a, long long row, const Fetched& f, float inv_t, int* ids, float* lp, float* out,
+                      F begun) {
   const int lane = threadIdx.x & 31, k_n = (int)a.d.topk;
-  const float w = a.row_weight ? a.row_weight[row] : 1.f;
-  if (w == 0.f) {
-    if (lane == 0) out[kWeight] = 0.f, out[kState] = (float)kDead;
-    return;
-  }
   float top = -INFINITY;
   bool any = false;
-  for (int k = lane; k < k_n; k += 32) {
-    const int id = entry_id(a, row, k);
-    const float x = id < 0 ? -INFINITY : load_as_float(a.top_logits, a.d.top_dtype, row * a.d.top_stride + k) * inv_t;
+  auto put = [&](int k, long long raw, uint32_t logit) {
+    const int id = raw >= 0 && raw < a.d.vocab ? (int)raw : kAbsent;
+    const float x = id < 0 ? -INFINITY : logit_of(a, logit) * inv_t;
     ids[k] = id;
     lp[k] = x;
     top = Max::of(top, x);
     any |= id >= 0;
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (lane + i * 32 < k_n) put(lane + i * 32, f.id[i], f.logit[i]);
+  for (int k = lane + kAhead * 32; k < k_n; k += 32) put(k, raw_id(a, row, k), raw_logit(a, row, k));
   any = __any_sync(0xffffffffu, any);
-  top = warp_reduce<Max>(top);
-  float norm, mass = 0.f;
-  if (a.teacher_lse) {
-    norm = a.teacher_lse[row];
-  } else {
-    any = any && top != -INFINITY;
+  top = warp_max(top);
+  if (!a.teacher_lse) any = any && top != -INFINITY;
+  if (lane == 0) {
+    out[kWeight] = f.weight;
+    out[kState] = (float)(f.weight == 0.f ? kDead : any ? kLive : kEmpty);
+  }
+  __syncwarp();
+  begun();
+  float norm = f.lse, mass = 0.f;
+  if (!a.teacher_lse) {
     float s = 0.f;
-    for (int k = lane; k < k_n; k += 32)
-      if (ids[k] >= 0) s += expf(lp[k] - top);
+    for (int k = lane; k < k_n; k += 32) s += expf(lp[k] - top);   // 0 for an absent entry
     norm = top + logf(warp_reduce<Sum>(s));
   }
   for (int k = lane; k < k_n; k += 32) {
-    const float l = lp[k] - norm, q = ids[k] >= 0 ? expf(l) : 0.f;
+    const float l = lp[k] - norm;
     lp[k] = l;
-    p[k] = q;
-    mass += q;
+    if (a.teacher_lse) mass += expf(l);
   }
-  mass = warp_reduce<Sum>(mass);
+  if (a.teacher_lse) mass = warp_reduce<Sum>(mass);
   if (lane == 0) {
     out[kMass] = a.teacher_lse ? mass : 1.f;
     out[kRest] = a.teacher_lse ? fmaxf(0.f, 1.f - mass) : 0.f;
-    out[kWeight] = w;
-    out[kState] = (float)(any ? kLive : kEmpty);
   }
 }
 
+// A place in the ring: chunks take buffers in the order of their loads.
+struct Turn {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int buffers) {
+    if (++slot == buffers) slot = 0, parity ^= 1;
+  }
+};
+
+// 80 registers: two blocks of 12 warps, or one of 20, on an SM.
 template <typename T, int kMode>
-__global__ void __launch_bounds__((kMaxWarps + 2) * 32, 2)
+__global__ void __maxnreg__(80)
     distill_kernel(const __grid_constant__ DistillArgs a, const __grid_constant__ Plan plan) {
   extern __shared__ __align__(128) uint8_t smem[];
   Header& h = *reinterpret_cast<Header*>(smem);
   int* const ids0 = reinterpret_cast<int*>(smem + (sizeof(Header) + 15) / 16 * 16);
-  float* const p0 = reinterpret_cast<float*>(ids0 + 2 * plan.kp);
-  float* const lp0 = p0 + 2 * plan.kp;
-  float* const sk0 = lp0 + 2 * plan.kp;
-  uint8_t* const ring = smem + plan.smem - plan.buffers * plan.buffer_bytes;
+  float* const lp0 = reinterpret_cast<float*>(ids0 + kRows * plan.kp);
+  float* const sk0 = lp0 + kRows * plan.kp;                                  // the listed logits
+  uint16_t* const mine0 = reinterpret_cast<uint16_t*>(sk0 + kRows * plan.kp);  // each consumer's entries
+  const int buffers = plan.buffers, chunk_bits = plan.part + 31 - __clz(plan.warps);
+  const int per_chunk = 1 << chunk_bits, buffer_bytes = per_chunk * 16;
+  uint8_t* const ring = smem + plan.smem - buffers * buffer_bytes;
   const uint32_t bars = smem_u32(&h);
   auto bar = [&](const uint64_t* b) { return bars + (uint32_t)(reinterpret_cast<const uint8_t*>(b) - smem); };
 
   constexpr bool kAcross = kMode != kGradient;   // whether a row's blocks exchange their sums
+  constexpr int kN = Slice<T>::kN;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int across = kAcross ? plan.slices : 1;
   const int rank = across > 1 ? (int)(blockIdx.x % across) : 0;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kMaxBuffers; ++i) {
+    for (int i = 0; i < buffers; ++i) {
       mbar_init(bar(&h.full[i]), 1);
-      mbar_init(bar(&h.empty[i]), plan.warps);
+      mbar_init(bar(&h.done[i]), plan.warps);
+      mbar_init(bar(&h.free[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kRows; ++i) {
       mbar_init(bar(&h.t_full[i]), 1);
+      mbar_init(bar(&h.m_full[i]), 1);
       mbar_init(bar(&h.t_free[i]), plan.warps);
-      mbar_init(bar(&h.x_full[i]), across);
+      mbar_init(bar(&h.r_full[i]), 1);
     }
-    h.repeated = -1;
+    for (int i = 0; i < 2; ++i) mbar_init(bar(&h.c_full[i]), plan.warps);
+    mbar_init(bar(&h.x_full), across);
     fence_mbarrier_init();
   }
   if (across > 1) cluster_sync();
   else __syncthreads();
 
-  // Work item i of this block: a row and a slice of it.
+  // Work item i of this block: a row and a slice of it.  A cluster of several blocks has one row.
   const long long first = kAcross ? blockIdx.x / across : blockIdx.x;
   const long long step = kAcross ? gridDim.x / across : gridDim.x;
   const long long items = kAcross ? a.d.rows : a.d.rows * plan.slices;
@@ -276,122 +451,226 @@ __global__ void __launch_bounds__((kMaxWarps + 2) * 32, 2)
     return static_cast<const T*>(a.logits) + row * a.d.logits_stride + begin;
   };
   auto grad_at = [&](long long row, int begin) { return static_cast<T*>(a.dlogits) + row * a.d.dlogits_stride + begin; };
-  // A wait that runs out is reported, and its warps leave their loop; the others' waits then run out,
+  auto chunks_of = [&](const Slice<T>& s) { return (s.vectors + per_chunk - 1) >> chunk_bits; };
+  // Chunks of a row that do not stay for the second pass and are loaded again after the others.
+  auto again_of = [&](int chunks) { return kMode == kBoth ? max(0, chunks - buffers) : 0; };
+  auto dead_row = [&](long long row) { return a.row_weight && a.row_weight[row] == 0.f; };
+  // A wait that runs out is reported, and its warp leaves its loop; the others' waits then run out,
   // too, so that every block comes to its end.
+  bool ok = true;
 
-  if (warp == plan.warps) {   // ------------------------------------------------ producer
+  if (warp == plan.warps) {   // ------------------------------------------------ loader
     if (lane == 0) {
-      auto load = [&](long long i, int b) {
+      const uint64_t keep = l2_keep(), pass = l2_pass();
+      Turn t;
+      long long loads = 0;
+      bool next_dead = first < items && dead_row(row_of(first));
+      for (long long i = first; ok && i < items; i += step) {
         const long long row = row_of(i);
-        const uint32_t full = bar(&h.full[b]);
-        if (a.row_weight && a.row_weight[row] == 0.f) {
-          mbar_arrive(full);
-          return;
-        }
+        const bool dead = next_dead;
+        next_dead = i + step < items && dead_row(row_of(i + step));
+        if (dead && kMode == kLoss) continue;
         const int begin = begin_of(i);
         const T* src = logits_at(row, begin);
         const Slice<T> s(src, slice_n(begin));
-        const uint32_t bytes = s.whole_bytes();
-        if (!bytes) {
-          mbar_arrive(full);
-          return;
-        }
-        mbar_arrive_expect_tx(full, bytes);
-        bulk_load_1d(smem_u32(ring + b * plan.buffer_bytes + s.c0 * 16), src - s.lead + s.c0 * Slice<T>::kN, bytes, full);
-      };
-      long long ahead = first;
-      int loads = 0;
-      for (; loads < plan.buffers && ahead < items; ++loads, ahead += step) load(ahead, loads);
-      int b = 0;
-      uint32_t phase = 0;
-      for (long long i = first; i < items; i += step) {
-        if (!mbar_wait_backoff(bar(&h.empty[b]), phase, 64)) {
-          report_error(a.err, kErrWaitOperand);
-          break;
-        }
-        if (kMode != kLoss) {
-          const int begin = begin_of(i);
-          const Slice<T> s(logits_at(row_of(i), begin), slice_n(begin));
-          T* dst = grad_at(row_of(i), begin) - s.lead + s.c0 * Slice<T>::kN;
-          if (s.whole_bytes() && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
-            bulk_store_1d(dst, smem_u32(ring + b * plan.buffer_bytes + s.c0 * 16), s.whole_bytes());
-            bulk_commit_group();
-            bulk_wait_group_read<0>();
+        const int chunks = chunks_of(s), again = dead ? 0 : again_of(chunks);
+        for (int q = 0; q < chunks + again; ++q) {
+          // the buffer's last chunk was copied out before this one comes in
+          if (loads >= buffers && !(ok = mbar_wait(bar(&h.free[t.slot]), t.parity ^ 1))) break;
+          const int c = q < chunks ? q : q - chunks, from = max(s.v0, c << chunk_bits), to = min(s.v1, (c + 1) << chunk_bits);
+          const uint32_t full = bar(&h.full[t.slot]);
+          if (dead || from >= to) {
+            mbar_arrive(full);
+          } else {
+            const uint32_t bytes = (uint32_t)(to - from) * 16u;
+            mbar_arrive_expect_tx(full, bytes);
+            bulk_load(smem_u32(ring + t.slot * buffer_bytes + (from - (c << chunk_bits)) * 16),
+                      src - s.lead + (long long)from * kN, bytes, full, q < again ? keep : pass);
           }
-        }
-        if (ahead < items) {
-          load(ahead, b);
-          ahead += step;
           ++loads;
+          t.next(buffers);
         }
-        if (++b == plan.buffers) b = 0, phase ^= 1;
       }
-      bulk_wait_group<0>();
       // no copy is in flight when the block ends, also where a wait ran out (else: all are complete)
-      for (int l = max(0, loads - plan.buffers); l < loads; ++l)
-        if (!mbar_wait(bar(&h.full[l % plan.buffers]), (l / plan.buffers) & 1)) report_error(a.err, kErrWaitOperand);
+      for (long long l = max(0ll, loads - buffers); l < loads; ++l)
+        ok &= mbar_wait(bar(&h.full[l % buffers]), (uint32_t)(l / buffers) & 1);
     }
-  } else if (warp == plan.warps + 1) {   // ------------------------------------ teacher
-    const float inv_t = 1.f / a.d.temperature;
-    int n = 0;
-    for (long long i = first; i < items; i += step, ++n) {
-      const int slot = n & 1;
-      if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait_backoff(bar(&h.t_free[slot]), ((n >> 1) & 1) ^ 1, 64))) {
-        if (lane == 0) report_error(a.err, kErrWaitOperand);
-        break;
+  } else if (warp == plan.warps + 1) {   // ------------------------------------ storer
+    if (lane == 0) {
+      const uint64_t pass = l2_pass();
+      Turn t;
+      int leaving = -1;   // the buffer whose copy out was started last
+      auto all_left = [&] {
+        bulk_wait_group_read<0>();
+        if (leaving >= 0) mbar_arrive(bar(&h.free[leaving]));
+        leaving = -1;
+      };
+      bool next_dead = first < items && dead_row(row_of(first));
+      for (long long i = first; ok && i < items; i += step) {
+        const long long row = row_of(i);
+        const bool dead = next_dead;
+        next_dead = i + step < items && dead_row(row_of(i + step));
+        if (dead && kMode == kLoss) continue;
+        const int begin = begin_of(i);
+        const Slice<T> s(logits_at(row, begin), slice_n(begin));
+        const int chunks = chunks_of(s), again = dead ? 0 : again_of(chunks);
+        const int passing = kMode == kLoss ? chunks : again, total = kMode == kLoss ? chunks : chunks + again;
+        T* const dst = kMode == kLoss ? nullptr : grad_at(row, begin) - s.lead;
+        const bool apart = (reinterpret_cast<uintptr_t>(dst) & 15) != 0;
+        for (int j = 0; j < total; ++j) {
+          // the buffers go back as soon as they can, unless the next chunk is there already
+          if (leaving >= 0 && !mbar_test(bar(&h.done[t.slot]), t.parity)) all_left();
+          if (!(ok = mbar_wait(bar(&h.done[t.slot]), t.parity))) break;
+          // chunks that do not stay for the second pass, those that did, those that came again
+          const int q = j < chunks ? j : j - chunks;
+          const int from = max(s.v0, q << chunk_bits), to = min(s.v1, (q + 1) << chunk_bits);
+          if (j >= passing && !apart && from < to) {
+            bulk_store(dst + (long long)from * kN, smem_u32(ring + t.slot * buffer_bytes + (from - (q << chunk_bits)) * 16),
+                       (uint32_t)(to - from) * 16u, pass);
+            bulk_commit_group();
+            bulk_wait_group_read<1>();
+            if (leaving >= 0) mbar_arrive(bar(&h.free[leaving]));
+            leaving = t.slot;
+          } else {
+            mbar_arrive(bar(&h.free[t.slot]));
+          }
+          t.next(buffers);
+        }
       }
-      teach(a, row_of(i), inv_t, ids0 + slot * plan.kp, p0 + slot * plan.kp, lp0 + slot * plan.kp, h.teacher[slot]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(&h.t_full[slot]));
+      all_left();
+      bulk_wait_group<0>();
     }
-  } else {   // ---------------------------------------------------------------- consumers
-    const int tid = threadIdx.x, threads = plan.warps * 32, k_n = (int)a.d.topk;
+  } else if (warp >= plan.warps + 2) {   // ------------------------------------ teachers
     const float inv_t = 1.f / a.d.temperature, c = inv_t * 1.4426950408889634f;
-    int n = 0, b = 0, exchanges = 0;
-    uint32_t phase = 0;
-    bool ok = true;
+    // The loss of the block's n-th row, once its sums are there.
+    auto settle = [&](long long row, int n) {
+      const int slot = n % kRows;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(&h.r_full[slot]), n / kRows & 1))) return ok = false;
+      if (!kAcross || rank) return true;
+      const int* const ids = ids0 + slot * plan.kp;
+      const float* const lp = lp0 + slot * plan.kp;
+      const float* const sk = sk0 + slot * plan.kp;
+      const float top = h.result[slot][0], total = h.result[slot][1], unlisted = h.result[slot][2];
+      const bool live = h.result[slot][3] != 0.f;
+      const float to_top = 1.f / rounding_of_base(top, c);
+      float l = 0.f;
+      if (live) {
+        const float log_total = logf(total * to_top), q_rest = unlisted / total;
+        const float rest = q_rest == 0.f ? 0.f : h.teacher[slot][kRest];
+        for (int k = lane; k < (int)a.d.topk; k += 32) {
+          const float p = ids[k] >= 0 ? expf(lp[k]) : 0.f;
+          if (!(p == 0.f)) l += p * (lp[k] - ((sk[k] - top) * inv_t - log_total));
+        }
+        l = warp_reduce<Sum>(l);
+        if (rest != 0.f) l += rest * (logf(rest) - logf(q_rest));
+      }
+      if (lane == 0) {
+        a.loss[row] = live ? l * h.teacher[slot][kWeight] * a.d.temperature * a.d.temperature : 0.f;
+        if (a.stats) {
+          a.stats[row * 3] = live ? top : 0.f;
+          a.stats[row * 3 + 1] = live ? total * to_top : 0.f;
+          a.stats[row * 3 + 2] = live ? unlisted * to_top : 0.f;
+        }
+      }
+      return true;
+    };
+    const int start = warp - plan.warps - 2;
+    int n = start;   // of the block's rows
+    Fetched next;
+    if (first + n * step < items) fetch(a, row_of(first + n * step), next);
+    for (long long i = first + n * step; ok && i < items; i += kTeachers * step, n += kTeachers) {
+      const int slot = n % kRows;
+      const Fetched now = next;
+      if (i + kTeachers * step < items) fetch(a, row_of(i + kTeachers * step), next);
+      if (n >= kRows) {
+        if (!settle(row_of(i - kRows * step), n - kRows)) break;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(&h.t_free[slot]), (n / kRows & 1) ^ 1));
+        if (!ok) break;
+      }
+      teach(a, row_of(i), now, inv_t, ids0 + slot * plan.kp, lp0 + slot * plan.kp, h.teacher[slot], [&] {
+        if (lane == 0) mbar_arrive(bar(&h.t_full[slot]));
+      });
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(&h.m_full[slot]));
+    }
+    for (int m = max(start, n - kRows); ok && m < n; m += kTeachers) settle(row_of(first + m * step), m);
+  } else {   // ---------------------------------------------------------------- consumers
+    const int part = 1 << plan.part, k_n = (int)a.d.topk;
+    const float inv_t = 1.f / a.d.temperature, c = inv_t * 1.4426950408889634f;
+    const uint64_t cc = pair(c, c);
+    uint16_t* const mine = mine0 + warp * plan.kp;
+    Turn t;
+    int n = 0, merges = 0;
+    auto wait = [](uint32_t b, uint32_t parity) { return (bool)__all_sync(0xffffffffu, mbar_wait(b, parity)); };
+    // Part of a chunk's places that are this warp's, and whose ragged elements (the row's first and last,
+    // which a bulk copy cannot move) it puts in; they are read a row ahead of their use.
+    constexpr int kLog = sizeof(T) == 4 ? 2 : 3;
+    auto is_mine = [&](int place) { return (place >> (plan.part + kLog) & (plan.warps - 1)) == warp; };
+    auto edge_of = [&](long long i) {
+      const int begin = begin_of(i);
+      const T* src = logits_at(row_of(i), begin);
+      const Slice<T> s(src, slice_n(begin));
+      const int place = s.edge_place(lane);
+      return place >= 0 && is_mine(place) && s.inside(place) ? src[place - s.lead] : from_f<T>(-INFINITY);
+    };
+    T next_edge = from_f<T>(0.f);
+    if (first < items) next_edge = edge_of(first);
     for (long long i = first; i < items; i += step, ++n) {
       const long long row = row_of(i);
-      const int begin = begin_of(i), slot = n & 1;
-      const T* src = logits_at(row, begin);
-      const Slice<T> s(src, slice_n(begin));
-      T* const buf = reinterpret_cast<T*>(ring + b * plan.buffer_bytes);
-      const uint32_t buf_at = smem_u32(buf);
-      int* const ids = ids0 + slot * plan.kp;
-      const float* const p = p0 + slot * plan.kp;
-      const float* const lp = lp0 + slot * plan.kp;
-      if (!mbar_wait(bar(&h.t_full[slot]), (n >> 1) & 1)) {
-        ok = false;
-        if (lane == 0) report_error(a.err, kErrWaitWeights);
-      }
+      const int begin = begin_of(i), slot = n % kRows;
+      const Slice<T> s(logits_at(row, begin), slice_n(begin));
+      const int chunks = chunks_of(s);
+      int edge_at = s.edge_place(lane);
+      if (edge_at >= 0 && !is_mine(edge_at)) edge_at = -1;
+      const T edge = next_edge;
+      if (i + step < items) next_edge = edge_of(i + step);
+      if (!(ok = wait(bar(&h.t_full[slot]), n / kRows & 1))) break;
       const int state = (int)h.teacher[slot][kState];
-      const float weight = h.teacher[slot][kWeight];
-      const int place = s.edge_place(tid);
-      T edge = from_f<T>(-INFINITY);
-      if (state != kDead && place >= s.lead && place < s.lead + s.n) edge = src[place - s.lead];
-      if (ok && !mbar_wait(bar(&h.full[b]), phase)) {
-        ok = false;
-        if (lane == 0) report_error(a.err, kErrWaitHalo);
-      }
-      if (state != kDead && place >= 0) buf[place] = edge;
-      // every thread or none goes on: those of a block stay together at the barriers below
-      if (!(ok = named_bar_and(1, threads, ok))) break;
-      bool live = state == kLive, repeated = false;
-      float top = 0.f, total = 0.f, unlisted = 0.f;
-      if (kMode == kGradient) {
-        top = a.stats[row * 3], total = a.stats[row * 3 + 1], unlisted = a.stats[row * 3 + 2];
-        live = live && !(total == 0.f);
-      }
-      float* const sk = sk0 + (kAcross ? (exchanges & 1) : slot) * plan.kp;
+      const int* const ids = ids0 + slot * plan.kp;
+      const float* const lp = lp0 + slot * plan.kp;
+      float* const sk = sk0 + slot * plan.kp;
+      const int shift = s.lead - begin;   // a listed id's place: id + shift
+      bool live = state == kLive;
+      // This warp's entries.
+      int count = 0;
       if (live) {
-        // Take the listed logits out: the first thread to fill a place with ones has its logit (an
-        // id listed again, or a NaN of all ones, finds ones), and once all have, puts -infinity there.
-        Running r;
-        for (int k = tid; k < k_n; k += threads) {
-          const int at = ids[k] - begin;
-          if (ids[k] < 0 || at < 0 || at >= s.n) continue;
-          const int e = s.lead + at;
+        for (int k = lane; k < plan.kp; k += 32) {
+          const int place = k < k_n ? ids[k] + shift : -1;
+          const bool hit = s.inside(place) && is_mine(place);
+          const uint32_t mask = __ballot_sync(0xffffffffu, hit);
+          if (hit) mine[count + __popc(mask & ((1u << lane) - 1))] = (uint16_t)k;
+          count += __popc(mask);
+        }
+        __syncwarp();
+      }
+      const int k0 = lane < count ? mine[lane] : -1;   // the first 32 stay in registers
+      const int place0 = k0 >= 0 ? ids[k0] + shift : -1;
+      // Calls f(entry, place, round) for this warp's entries in chunk q.
+      auto entries = [&](int q, auto f) {
+        if (place0 >= 0 && place0 >> (chunk_bits + kLog) == q) f(k0, place0, 0);
+        for (int i = lane + 32, round = 1; i < count; i += 32, ++round) {
+          const int k = mine[i], place = ids[k] + shift;
+          if (place >> (chunk_bits + kLog) == q) f(k, place, round);
+        }
+      };
+      bool repeated = false;   // whether an id is among them twice, and the rounds of such entries
+      uint32_t twice = 0;
+      Running run;
+      // Puts the ragged elements of a loaded chunk in.
+      auto mend = [&](int q, T* buf) {
+        if (edge_at >= 0 && edge_at >> (chunk_bits + kLog) == q) buf[edge_at - (q << (chunk_bits + kLog))] = edge;
+        __syncwarp();
+      };
+      // Takes the listed logits out.  The first lane to fill a place with ones has its logit (an id
+      // listed again, or a NaN of all ones, finds ones), and once all have, -infinity goes there.
+      auto extract = [&](int q, T* buf) {
+        const int origin = q << (chunk_bits + kLog);
+        bool hit = false;
+        uint32_t found = 0;
+        entries(q, [&](int k, int place, int round) {
+          const int e = place - origin;
           float v;
+          hit = true;
           bool had;
           if constexpr (sizeof(T) == 4) {
             const uint32_t old = atomicExch(reinterpret_cast<uint32_t*>(buf) + e, 0xffffffffu);
@@ -401,151 +680,245 @@ __global__ void __launch_bounds__((kMaxWarps + 2) * 32, 2)
             const int sh = (e & 1) * 16;
             const uint16_t old = (uint16_t)(atomicOr(reinterpret_cast<uint32_t*>(buf) + (e >> 1), 0xffffu << sh) >> sh);
             had = old == 0xffffu;
-            T t;
-            *reinterpret_cast<uint16_t*>(&t) = old;
-            v = to_f(t);
+            T x;
+            *reinterpret_cast<uint16_t*>(&x) = old;
+            v = to_f(x);
           }
           if (had) {
-            ids[k] |= kRepeated;
-            h.repeated = n;
+            found |= 1u << round;   // at most kMaxTopk / 32 rounds
           } else {
             sk[k] = v;
             if (rank) st_cluster(map_to_rank(smem_u32(sk + k), 0), v);
-            if (kAcross) {
-              raise<T>(r, v, c);
-              r.listed += r.top == -INFINITY ? 0.f : ex2<T>((v - r.top) * c);
-            }
           }
-        }
-        named_bar_sync(1, threads);
-        repeated = h.repeated == n;   // the next row's marks come after another barrier
-        for (int k = tid; k < k_n; k += threads) {
-          const int at = ids[k] - begin;
-          if (ids[k] >= 0 && at >= 0 && at < s.n) buf[s.lead + at] = from_f<T>(-INFINITY);
-        }
-        if (repeated) {   // a repeated id has the logit of its first entry (or a NaN that was there)
-          for (int k = tid; k < k_n; k += threads) {
-            if (ids[k] < 0 || !(ids[k] & kRepeated)) continue;
+        });
+        if (!__any_sync(0xffffffffu, hit)) return;
+        __syncwarp();
+        entries(q, [&](int k, int place, int round) {
+            if (!(found >> round & 1)) buf[place - origin] = from_f<T>(-INFINITY);
+          });
+        if (__any_sync(0xffffffffu, found != 0)) {   // the logit of the id's first entry, or that NaN
+          repeated = true;
+          twice |= found;
+          entries(q, [&](int k, int place, int round) {
+            if (found >> round & 1) sk[k] = __int_as_float(0x7fffffff);
+          });
+          __syncwarp();
+          // sk of a later entry is that NaN so far, and its first entry's is not, or both are
+          entries(q, [&](int k, int place, int round) {
+            if (!(found >> round & 1)) return;
             float v = __int_as_float(0x7fffffff);
-            for (int j = 0; j < k_n; ++j)
-              if (ids[j] == (ids[k] & ~kRepeated)) v = sk[j];
+            for (int m = 0; m < count; ++m)
+              if (ids[mine[m]] == ids[k] && __float_as_int(sk[mine[m]]) != 0x7fffffff) v = sk[mine[m]];
             sk[k] = v;
             if (rank) st_cluster(map_to_rank(smem_u32(sk + k), 0), v);
-          }
+          });
         }
-        named_bar_sync(1, threads);
-        if constexpr (kAcross) {
-          float base = r.top == -INFINITY ? 0.f : r.top;
-          for (int q = tid; q < s.chunks; q += threads) {
-            const Chunk<T> x(ld_shared_v4(buf_at + q * 16));
-            const float m = x.largest();
-            if (!(m <= r.top)) {
-              raise<T>(r, m, c);
-              base = r.top == -INFINITY ? 0.f : r.top;
-            }
-            float e = 0.f;
+        __syncwarp();
+      };
+
+      const bool two = kAcross && state != kDead;   // passes; else the second alone
+      const int again = two ? again_of(chunks) : 0;
+      Turn u = t;   // where the second pass begins: the first chunk that stays
+      float up = 1.f;
+      Sums r;
+      if (two) {
+        float based = -INFINITY, minus = 0.f;   // no base yet: every logit so far is -infinity
+        bool far = false;
+        for (int q = 0; q < chunks; ++q) {
+          if (!(ok = wait(bar(&h.full[t.slot]), t.parity))) break;
+          if (live) {
+            T* const buf = reinterpret_cast<T*>(ring + t.slot * buffer_bytes);
+            mend(q, buf);
+            extract(q, buf);
+            const uint32_t at = smem_u32(buf);
+            const int from = warp << plan.part, to = min(from + part, s.vectors - (q << chunk_bits));
+            // kBatch vectors at a time: their loads and exponentials overlap, and one look at the largest
+            auto add = [&](const auto& w) {
+              constexpr int kCount = sizeof(w) / sizeof(uint4);
+              const float m = largest<T>(w);
+              raise<T>(run, m, c);
+              if (run.top != based) {
+                based = run.top;
+                minus = minus_base(run.top, c);
+                far = is_far(run.top, c);
+              }
+              const uint64_t mm = pair(minus, minus);
+              uint64_t e[kCount];
 #pragma unroll
-            for (int j = 0; j < Chunk<T>::n; ++j) e += ex2<T>((x.v[j] - base) * c);
-            r.unlisted += e;
-          }
-          r = merge_warp<T>(r, c);
-          if (lane == 0) h.red[warp][0] = r.top, h.red[warp][1] = r.unlisted, h.red[warp][2] = r.listed;
-          named_bar_sync(1, threads);
-          r = Running{};
-          if (lane < plan.warps) r = Running{h.red[lane][0], h.red[lane][1], h.red[lane][2]};
-          r = merge_warp<T>(r, c);
-          if (across > 1) {
-            const int x = exchanges & 1;
-            if (warp == 0 && lane < across) {
-              const uint32_t to = map_to_rank(smem_u32(h.xch[x][rank]), lane);
-              st_cluster(to, r.top);
-              st_cluster(to + 4, r.unlisted);
-              st_cluster(to + 8, r.listed);
-              arrive_cluster(map_to_rank(bar(&h.x_full[x]), lane));
+              for (int k = 0; k < kCount; ++k) {
+                Chunk<T> x(w[k]);
+                if (far) x.template exponentials<true>(mm, cc);
+                else x.template exponentials<false>(mm, cc);
+                e[k] = x.v[0];
+#pragma unroll
+                for (int j = 1; j < Chunk<T>::kPairs; ++j) e[k] = add2(e[k], x.v[j]);
+              }
+#pragma unroll
+              for (int k = 0; k < kCount; ++k) run.sum = add2(run.sum, e[k]);
+            };
+            int v = from + lane;
+            for (; v + (kBatch - 1) * 32 < to; v += kBatch * 32) {
+              uint4 w[kBatch];
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) w[k] = ld_shared_v4(at + (v + k * 32) * 16);
+              add(w);
             }
-            if (!wait_cluster(bar(&h.x_full[x]), (exchanges >> 1) & 1)) {
-              ok = false;
-              if (lane == 0) report_error(a.err, kErrWaitAccum);
+            for (; v < to; v += 32) {
+              const uint4 w[1] = {ld_shared_v4(at + v * 16)};
+              add(w);
             }
-            if (!(ok = named_bar_and(1, threads, ok))) break;
-            r = Running{};
-            if (lane < across) r = Running{h.xch[x][lane][0], h.xch[x][lane][1], h.xch[x][lane][2]};
-            r = merge_warp<T>(r, c);
           }
-          ++exchanges;
-          top = r.top;
-          unlisted = r.unlisted;
-          total = r.unlisted + r.listed;
-          live = top != -INFINITY;
+          if (kMode == kLoss || q < again) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(&h.done[t.slot]));
+          }
+          t.next(buffers);
+          if (q + 1 == again) u = t;
         }
-      }
-      const float mass = h.teacher[slot][kMass], inv = 1.f / total, q_rest = unlisted * inv;
-      float rest = h.teacher[slot][kRest];
-      if (q_rest == 0.f) rest = 0.f;
-      if (kAcross && rank == 0 && warp == plan.warps - 1) {   // the row's loss, by one warp
-        float l = 0.f;
-        if (live) {
-          const float log_total = logf(total);
-          for (int k = lane; k < k_n; k += 32)
-            if (ids[k] >= 0 && !(p[k] == 0.f)) l += p[k] * (lp[k] - ((sk[k] - top) * inv_t - log_total));
-          l = warp_reduce<Sum>(l);
-          if (rest != 0.f) l += rest * (logf(rest) - logf(q_rest));
+        if (!ok) break;
+        for (int i = lane, round = 0; i < count; i += 32, ++round) {   // the listed words, each id once
+          const float v = sk[mine[i]];
+          if (!live || (twice >> round & 1) || v == -INFINITY) continue;
+          raise<T>(run, v, c);
+          run.listed += exponential<T>(v, run.top, c);
         }
+        const float2 f = unpair(run.sum);
+        r = merge_warp<T>(Sums{run.top, f.x + f.y, run.listed}, c);
+        float(*const red)[4] = h.red[merges & 1];   // the last row's may still be read
         if (lane == 0) {
-          a.loss[row] = live ? l * weight * a.d.temperature * a.d.temperature : 0.f;
-          if (a.stats) {
-            a.stats[row * 3] = live ? top : 0.f;
-            a.stats[row * 3 + 1] = live ? total : 0.f;
-            a.stats[row * 3 + 2] = live ? unlisted : 0.f;
-          }
+          red[warp][0] = r.top;
+          red[warp][1] = r.unlisted;
+          red[warp][2] = r.listed;
+          mbar_arrive(bar(&h.c_full[merges & 1]));
         }
+        if (!(ok = wait(bar(&h.c_full[merges & 1]), merges >> 1 & 1))) break;
+        ++merges;
+        r = Sums{};
+        if (lane < plan.warps) r = Sums{red[lane][0], red[lane][1], red[lane][2]};
+        r = merge_warp<T>(r, c);
+        if (across > 1 && live) {
+          if (warp == 0 && lane < across) {
+            const uint32_t to = map_to_rank(smem_u32(h.xch[rank]), lane);
+            st_cluster(to, r.top);
+            st_cluster(to + 4, r.unlisted);
+            st_cluster(to + 8, r.listed);
+            arrive_cluster(map_to_rank(bar(&h.x_full), lane));
+          }
+          if (!(ok = __all_sync(0xffffffffu, wait_cluster(bar(&h.x_full), 0)))) break;
+          r = Sums{};
+          if (lane < across) r = Sums{h.xch[lane][0], h.xch[lane][1], h.xch[lane][2]};
+          r = merge_warp<T>(r, c);
+        }
+        live = live && r.top != -INFINITY;
+      }
+      float total = r.unlisted + r.listed;
+      if (kMode == kGradient) {
+        const float* st = a.stats + row * 3;
+        const float from_top = rounding_of_base(st[0], c);
+        r = Sums{st[0], st[2] * from_top, 0.f};
+        total = st[1] * from_top;
+        live = live && !(total == 0.f);
+        if (a.dloss) up = a.dloss[row];
+      }
+      if (threadIdx.x == 0) {
+        h.result[slot][0] = r.top;
+        h.result[slot][1] = total;
+        h.result[slot][2] = r.unlisted;
+        h.result[slot][3] = live ? 1.f : 0.f;
+        mbar_arrive(bar(&h.r_full[slot]));
       }
       if constexpr (kMode != kLoss) {
-        const float scale = weight * a.d.temperature * (kMode == kGradient && a.dloss ? a.dloss[row] : 1.f);
-        const float all = mass + rest;
-        if (live) {
-          const float coef = scale * (rest != 0.f ? all - rest / q_rest : all) * inv;
-          for (int q = tid; q < s.chunks; q += threads) {
-            Chunk<T> x(ld_shared_v4(buf_at + q * 16));
+        if (!(ok = wait(bar(&h.m_full[slot]), n / kRows & 1))) break;
+        const float inv = 1.f / total, q_rest = r.unlisted * inv, mass = h.teacher[slot][kMass];
+        const float rest = q_rest == 0.f ? 0.f : h.teacher[slot][kRest];
+        const float scale = h.teacher[slot][kWeight] * a.d.temperature * up, all = mass + rest;
+        const float coef = scale * (rest != 0.f ? all - rest / q_rest : all) * inv;
+        T* const dst = grad_at(row, begin) - s.lead;
+        const bool apart = (reinterpret_cast<uintptr_t>(dst) & 15) != 0, far = is_far(r.top, c);
+        const float minus = minus_base(r.top, c);
+        const uint64_t mm = pair(minus, minus), kk = pair(coef, coef);
+        // The teacher's part of an entry's gradient; an id listed twice has the sum at each of its entries.
+        auto entry_p = [&](int k) {
+          if (kMode == kBoth && !repeated) return expf(lp[k]);
+          float pk = 0.f;
+          for (int m = 0; m < count; ++m)
+            if (ids[mine[m]] == ids[k]) pk += expf(lp[mine[m]]);
+          return pk;
+        };
+        auto entry_gradient = [&](float s, float pk) {
+          return from_f<T>(scale * (exponential<T>(s, r.top, c) * inv * all - pk));
+        };
+        const float p0 = live && k0 >= 0 ? entry_p(k0) : 0.f;
+        const T g0 = kMode == kBoth && live && k0 >= 0 ? entry_gradient(sk[k0], p0) : from_f<T>(0.f);
+        for (int j = 0; j < chunks; ++j) {
+          const int q = j < chunks - again ? j + again : j - (chunks - again);   // those that stayed come first
+          const bool came = !two || j >= chunks - again;
+          if (came && !(ok = wait(bar(&h.full[u.slot]), u.parity))) break;
+          T* const buf = reinterpret_cast<T*>(ring + u.slot * buffer_bytes);
+          const uint32_t at = smem_u32(buf);
+          const int from = warp << plan.part, to = min(from + part, s.vectors - (q << chunk_bits));
+          const int origin = q << (chunk_bits + kLog);
+          if (came && state != kDead) mend(q, buf);
+          if (kMode == kGradient && live) {
+            entries(q, [&](int k, int place, int round) { sk[k] = to_f(buf[place - origin]); });
+            __syncwarp();
+          }
+          auto turn = [&](uint4 w) {
+            if (!live) return make_uint4(0, 0, 0, 0);
+            Chunk<T> x(w);
+            if (far) x.template exponentials<true>(mm, cc);
+            else x.template exponentials<false>(mm, cc);
 #pragma unroll
-            for (int j = 0; j < Chunk<T>::n; ++j) x.v[j] = ex2<T>((x.v[j] - top) * c) * coef;
-            st_shared_v4(buf_at + q * 16, x.packed());
-          }
-          named_bar_sync(1, threads);
-          for (int k = tid; k < k_n; k += threads) {
-            const int id = ids[k] & ~kRepeated, at = id - begin;
-            if (ids[k] < 0 || at < 0 || at >= s.n) continue;
-            float pk = p[k];
-            if (repeated) {
-              pk = 0.f;
-              for (int j = 0; j < k_n; ++j)
-                if (ids[j] >= 0 && (ids[j] & ~kRepeated) == id) pk += p[j];
+            for (int k = 0; k < Chunk<T>::kPairs; ++k) x.v[k] = mul2(x.v[k], kk);
+            return x.packed();
+          };
+          int v = from + lane;
+          if (!apart)
+            for (; v + (kBatch - 1) * 32 < to; v += kBatch * 32) {
+              uint4 w[kBatch];
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) w[k] = ld_shared_v4(at + (v + k * 32) * 16);
+#pragma unroll
+              for (int k = 0; k < kBatch; ++k) st_shared_v4(at + (v + k * 32) * 16, turn(w[k]));
             }
-            buf[s.lead + at] = from_f<T>(scale * (ex2<T>((sk[k] - top) * c) * inv * all - pk));
+          for (; v < to; v += 32) {
+            const uint4 w = turn(ld_shared_v4(at + v * 16));
+            if (!apart) {
+              st_shared_v4(at + v * 16, w);
+            } else {   // the gradient's rows start at other phases than the logits'
+              const T* g = reinterpret_cast<const T*>(&w);
+#pragma unroll
+              for (int k = 0; k < kN; ++k) {
+                const int place = ((q << chunk_bits) + v) * kN + k;
+                if (s.inside(place)) dst[place] = g[k];
+              }
+            }
           }
-        } else {
-          for (int q = tid; q < s.chunks; q += threads) st_shared_v4(buf_at + q * 16, make_uint4(0, 0, 0, 0));
-        }
-        T* dst = grad_at(row, begin);
-        const bool apart = (reinterpret_cast<uintptr_t>(dst - s.lead) & 15) != 0;
-        if (s.ragged() || apart) {
-          named_bar_sync(1, threads);
-          if (apart) {   // the gradient's rows start at other phases than the logits'
-            for (int j = tid; j < s.n; j += threads) dst[j] = buf[s.lead + j];
-          } else if (place >= s.lead && place < s.lead + s.n) {
-            dst[place - s.lead] = buf[place];
+          __syncwarp();
+          if (live) {
+            entries(q, [&](int k, int place, int round) {
+              const T g = kMode == kBoth && round == 0 ? g0 : entry_gradient(sk[k], round == 0 ? p0 : entry_p(k));
+              if (apart) dst[place] = g;
+              else buf[place - origin] = g;
+            });
+            __syncwarp();
           }
+          if (!apart && edge_at >= 0 && edge_at >> (chunk_bits + kLog) == q && s.inside(edge_at))
+            dst[edge_at] = buf[edge_at - origin];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(&h.done[u.slot]));
+          u.next(buffers);
         }
+        t = u;
       }
-      fence_proxy_async_smem();
+      if (!ok) break;
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar(&h.empty[b]));
-        mbar_arrive(bar(&h.t_free[slot]));
-      }
-      if (++b == plan.buffers) b = 0, phase ^= 1;
+      if (lane == 0) mbar_arrive(bar(&h.t_free[slot]));
     }
   }
+  if (!ok) report_error(a.err, kErrWaitHalo);
   // no block leaves while another may still write to its shared memory
   if (across > 1) {
     __syncwarp();
@@ -553,24 +926,29 @@ __global__ void __launch_bounds__((kMaxWarps + 2) * 32, 2)
   }
 }
 
-Plan make_plan(const DistillArgs& a, int elt, int num_sms) {
+Plan make_plan(const DistillArgs& a, int elt) {
   Plan p{};
   const long long v = a.d.vocab;
-  // Slices of at most 32 KB, so that two blocks with three buffers each share an SM; more slices
-  // while there are rows for fewer than that many blocks and a slice keeps 2 KB.
+  // A block for each row.  In calls of a few rows a cluster shares each, while a slice keeps 2 KB; its
+  // sums are added in another order, so the rule goes by the rows alone and its bound is low: other calls
+  // give a row the same result whatever rows are beside it.
   p.slices = 1;
-  while (p.slices < kMaxCluster && (v + p.slices - 1) / p.slices * elt > 32 * 1024) p.slices *= 2;
-  while (p.slices < kMaxCluster && a.d.rows * p.slices * 2 <= 2 * num_sms && v * elt / (2 * p.slices) >= 2048) p.slices *= 2;
+  if (a.d.rows <= kFewRows)
+    while (p.slices < kMaxCluster && v * elt / (2 * p.slices) >= 2048) p.slices *= 2;
   p.width = (int)(((v + p.slices - 1) / p.slices + 127) / 128 * 128);
-  p.buffer_bytes = (p.width * elt + 32 + 127) / 128 * 128;
+  const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.d.logits_stride * elt % 16 == 0;
+  const int vectors = (int)(std::min<long long>(p.width, v) * elt + 15) / 16 + !aligned;
+  // Chunks of 32 KB for eight warps, two batches of vectors for each lane; smaller where the row is.
+  p.part = 8;
+  p.warps = 8;
+  while (p.warps > 1 && (p.warps << p.part) / 2 >= vectors) p.warps /= 2;
+  while (p.part > 5 && (p.warps << p.part) / 2 >= vectors) --p.part;
+  const int chunk = p.warps << p.part << 4;
   p.kp = (int)((a.d.topk + 31) / 32 * 32);
-  const int fixed = (int)((sizeof(Header) + 15) / 16 * 16 + (size_t)p.kp * 32 + 127) / 128 * 128;
-  const int half = 113 * 1024 - fixed, whole = 226 * 1024 - fixed;
-  p.buffers = half / p.buffer_bytes >= 2 ? half / p.buffer_bytes : whole / p.buffer_bytes;
-  p.buffers = std::max(1, std::min(p.buffers, kMaxBuffers));
-  p.smem = fixed + p.buffers * p.buffer_bytes;
-  const int chunks = p.width * elt / 16;
-  p.warps = std::max(1, std::min(kMaxWarps, (chunks + 63) / 64));
+  const int fixed = (int)((sizeof(Header) + 15) / 16 * 16 + (size_t)p.kp * (kRows * 12 + p.warps * 2) + 127) / 128 * 128;
+  // Two blocks an SM: while one waits for loads or for its sums, the other computes.
+  p.buffers = std::max(2, std::min((113 * 1024 - fixed) / chunk, kMaxBuffers));
+  p.smem = fixed + p.buffers * chunk;
   return p;
 }
 
@@ -578,11 +956,11 @@ template <typename T, int kMode>
 int launch(const DistillArgs& a, int num_sms, cudaStream_t st) {
   auto kernel = distill_kernel<T, kMode>;
   constexpr bool kAcross = kMode != kGradient;
-  Plan p = make_plan(a, sizeof(T), num_sms);
+  Plan p = make_plan(a, sizeof(T));
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kernel), 227 * 1024)) return CBR_ERR_CUDA;
   const int across = kAcross ? p.slices : 1;
   const long long items = kAcross ? a.d.rows : a.d.rows * p.slices;
-  const int threads = (p.warps + 2) * 32;
+  const int threads = (p.warps + kOthers) * 32;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -609,7 +987,7 @@ int launch(const DistillArgs& a, int num_sms, cudaStream_t st) {
     clusters = n;
   }
   if (clusters < 1) return CBR_ERR_CUDA;
-  cfg.gridDim = dim3((unsigned)(std::min<long long>(items, clusters) * across));
+  cfg.gridDim = dim3((unsigned)((across > 1 ? items : std::min<long long>(items, clusters)) * across));
   if (cudaLaunchKernelEx(&cfg, kernel, a, p) != cudaSuccess) {
     cudaGetLastError();
     return CBR_ERR_CUDA;

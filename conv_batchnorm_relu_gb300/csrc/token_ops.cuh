@@ -56,6 +56,13 @@ __device__ __forceinline__ float warp_reduce(float v) {
   return v;
 }
 
+// The largest of a warp's values (NaN if one is), in one instruction.
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // Every thread of the block gets the result; `red` holds one float a warp (at most 32).
 template <typename Op>
 __device__ __forceinline__ float block_reduce(float v, float* red) {

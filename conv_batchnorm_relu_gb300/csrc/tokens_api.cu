@@ -7,7 +7,7 @@
 namespace cbr {
 namespace {
 
-constexpr int64_t kMaxVocab = 327680, kMaxTopk = 1024, kMaxDim = 16384;
+constexpr int64_t kMaxVocab = 393216, kMaxTopk = 1024, kMaxDim = 16384;
 constexpr int kMaxHeadDim = 1024, kMaxAxes = 8;
 // Row counts and strides up to 2^40, so that no product of checked sizes leaves 64 bits.
 constexpr int64_t kMaxExtent = int64_t(1) << 40;

@@ -359,7 +359,7 @@ int32_t cbr_profile_last_count(void);
  * is above -infinity.  Other NaN and infinities go through the formulas, in their row alone.
  */
 typedef struct {
-  int64_t rows, vocab;      /* rows >= 0; 1 <= vocab <= 327680 */
+  int64_t rows, vocab;      /* rows >= 0; 1 <= vocab <= 393216 */
   int64_t topk;             /* entries a row, 0 <= topk <= 1024 */
   int64_t logits_stride;    /* elements between rows, >= vocab */
   int64_t dlogits_stride;
