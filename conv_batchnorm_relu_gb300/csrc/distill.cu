@@ -391,15 +391,6 @@ __device__ void teach(const DistillArgs& a, long long row, const Fetched& f, flo
   }
 }
 
-// A place in the ring: chunks take buffers in the order of their loads.
-struct Turn {
-  int slot = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ void next(int buffers) {
-    if (++slot == buffers) slot = 0, parity ^= 1;
-  }
-};
-
 // 80 registers: two blocks of 12 warps, or one of 20, on an SM.
 template <typename T, int kMode>
 __global__ void __maxnreg__(80)

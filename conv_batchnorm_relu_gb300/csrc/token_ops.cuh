@@ -75,5 +75,14 @@ __device__ __forceinline__ float block_reduce(float v, float* red) {
   return warp_reduce<Op>(v);
 }
 
+// A place in a ring of buffers that are used in turn, and the parity of that use.
+struct Turn {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int buffers) {
+    if (++slot == buffers) slot = 0, parity ^= 1;
+  }
+};
+
 }  // namespace tok
 }  // namespace cbr

@@ -47,6 +47,7 @@ struct BlockNormArgs {
   float* dgate;
   float* dpre_weight;
   float* part;               // backward: per-block sums
+  uint32_t* err;
 };
 int launch_block_norm(const BlockNormArgs& a, int num_sms, cudaStream_t st);
 int launch_block_norm_backward(const BlockNormArgs& a, int num_sms, cudaStream_t st);

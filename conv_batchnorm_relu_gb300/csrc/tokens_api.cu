@@ -256,6 +256,7 @@ cbr_status_t cbr_block_norm_backward(const cbr_block_norm_desc_t* desc, const vo
   a.dgate = dgate;
   a.dpre_weight = dpre_weight;
   a.part = static_cast<float*>(ws);
+  a.err = err;
   return (cbr_status_t)launch_block_norm_backward(a, sms, st);
 }
 
