@@ -21,7 +21,7 @@ import struct
 import torch
 
 from . import cbr
-from .cbr import CBRError, _check, _ptr, _stream
+from .cbr import CBRError, _check, _stream
 
 _INVALID, _UNSUPPORTED = 1, 3
 _DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
@@ -68,49 +68,61 @@ def _dtype(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def _matrix(t: torch.Tensor, rows: int, width: int, dtype, like: torch.Tensor, what: str) -> int:
+def _matrix(t: torch.Tensor, shape, dtype, dev, what: str) -> int:
     """Checks a [rows][width] tensor whose rows lie anywhere but are contiguous; its row stride."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != width or t.dtype != dtype or t.device != like.device:
-        _bad(f"{what} has to be [{rows}][{width}] {dtype} on {like.device}: {list(t.shape)} {t.dtype} on {t.device}")
+    if t.shape != shape or t.dtype != dtype or t.device != dev:
+        _bad(f"{what} has to be {list(shape)} {dtype} on {dev}: {list(t.shape)} {t.dtype} on {t.device}")
     s, e = t.stride()
-    if e != 1 and width > 1:
+    if e != 1 and shape[1] > 1:
         _bad(f"{what}: a row has to be contiguous")
-    return s if rows > 1 else width
+    return s if shape[0] > 1 else shape[1]
 
 
-def _vector(t: torch.Tensor | None, n: int, like: torch.Tensor, what: str):
-    """Checks an optional contiguous fp32 tensor of n elements."""
-    if t is not None and (t.numel() != n or t.dtype != torch.float32 or t.device != like.device or
-                          not t.is_contiguous()):
-        _bad(f"{what} has to be {n} contiguous fp32 values on {like.device}")
+def _vector(t: torch.Tensor | None, n: int, dev, what: str):
+    """Checks an optional contiguous fp32 tensor of n elements; its address."""
+    if t is None:
+        return None
+    if t.numel() != n or t.dtype != torch.float32 or t.device != dev or not t.is_contiguous():
+        _bad(f"{what} has to be {n} contiguous fp32 values on {dev}")
+    return t.data_ptr()
 
 
-def _given(out: dict | None, name: str, shape, dtype, like: torch.Tensor) -> torch.Tensor:
+def _given(out: dict | None, name: str, shape, dtype, dev) -> torch.Tensor:
     """The caller's output of that name, or a new one."""
     if out and name in out:
         return out[name]
-    return torch.empty(shape, dtype=dtype, device=like.device)
+    return torch.empty(shape, dtype=dtype, device=dev)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(dev) -> int:
+    """The device's current stream (without building the stream's object, where torch has that)."""
+    return _raw_stream(dev.index) if _raw_stream is not None else _stream()
 
 
 # ------------------------------------------------------------------------------- distillation
 
 def _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_weight, dlogits):
+    """The packed descriptor and the addresses of the calls' common arguments."""
     if logits.dim() != 2 or not logits.is_cuda:
         _bad("logits have to be a [rows][vocab] CUDA tensor")
-    rows, vocab = logits.shape
+    shape, dev = logits.shape, logits.device
+    rows, vocab = shape
     dtype = _dtype(logits, "logits")
     top_dtype = _dtype(top_logits, "top_logits")
     if top_ids.dtype not in (torch.int32, torch.int64):
         _bad(f"top_ids: {top_ids.dtype}", _UNSUPPORTED)
     k = top_ids.shape[-1] if top_ids.dim() else 0
-    s = _matrix(logits, rows, vocab, logits.dtype, logits, "logits")
-    s_id = _matrix(top_ids, rows, k, top_ids.dtype, logits, "top_ids")
-    s_top = _matrix(top_logits, rows, k, top_logits.dtype, logits, "top_logits")
-    _vector(teacher_lse, rows, logits, "teacher_lse")
-    _vector(row_weight, rows, logits, "row_weight")
-    s_out = vocab if dlogits is None else _matrix(dlogits, rows, vocab, logits.dtype, logits, "dlogits")
-    return _DISTILL.pack(rows, vocab, k, s, s_out, s_id, s_top, dtype, top_dtype, top_ids.element_size(),
+    s = _matrix(logits, shape, logits.dtype, dev, "logits")
+    s_id = _matrix(top_ids, (rows, k), top_ids.dtype, dev, "top_ids")
+    s_top = _matrix(top_logits, (rows, k), top_logits.dtype, dev, "top_logits")
+    s_out = vocab if dlogits is None else _matrix(dlogits, shape, logits.dtype, dev, "dlogits")
+    desc = _DISTILL.pack(rows, vocab, k, s, s_out, s_id, s_top, dtype, top_dtype, top_ids.element_size(),
                          float(temperature))
+    return desc, (logits.data_ptr(), top_ids.data_ptr(), top_logits.data_ptr(),
+                  _vector(teacher_lse, rows, dev, "teacher_lse"), _vector(row_weight, rows, dev, "row_weight"))
 
 
 def distill_forward(logits, top_ids, top_logits, *, temperature=1.0, teacher_lse=None, row_weight=None,
@@ -122,14 +134,12 @@ def distill_forward(logits, top_ids, top_logits, *, temperature=1.0, teacher_lse
     over its entries; with it (the log-sum-exp of the teacher's logits / temperature over its whole
     vocabulary, [rows]) the mass it leaves out is one more class.  ``row_weight`` [rows] scales a row;
     0 masks it."""
-    desc = _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_weight, None)
-    rows = logits.shape[0]
-    loss = _given(out, "loss", rows, torch.float32, logits)
-    stats = _given(out, "stats", (rows, 3), torch.float32, logits)
-    _vector(loss, rows, logits, "loss")
-    _vector(stats, 3 * rows, logits, "stats")
-    _check(_load().cbr_distill_forward(desc, _ptr(logits), _ptr(top_ids), _ptr(top_logits), _ptr(teacher_lse),
-                                       _ptr(row_weight), _ptr(loss), _ptr(stats), _stream()), "cbr_distill_forward")
+    desc, args = _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_weight, None)
+    rows, dev = logits.shape[0], logits.device
+    loss = _given(out, "loss", rows, torch.float32, dev)
+    stats = _given(out, "stats", (rows, 3), torch.float32, dev)
+    _check(_load().cbr_distill_forward(desc, *args, _vector(loss, rows, dev, "loss"),
+                                       _vector(stats, 3 * rows, dev, "stats"), _stream_of(dev)), "cbr_distill_forward")
     return {"loss": loss, "stats": stats}
 
 
@@ -139,12 +149,10 @@ def distill_backward(dloss, logits, top_ids, top_logits, stats, *, temperature=1
 
     dloss [rows] fp32 or None (ones); stats from :func:`distill_forward`; the rest as there."""
     dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format) if out is None else out
-    desc = _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_weight, dlogits)
-    rows = logits.shape[0]
-    _vector(dloss, rows, logits, "dloss")
-    _vector(stats, 3 * rows, logits, "stats")
-    _check(_load().cbr_distill_backward(desc, _ptr(dloss), _ptr(logits), _ptr(top_ids), _ptr(top_logits),
-                                        _ptr(teacher_lse), _ptr(row_weight), _ptr(stats), _ptr(dlogits), _stream()),
+    desc, args = _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_weight, dlogits)
+    rows, dev = logits.shape[0], logits.device
+    _check(_load().cbr_distill_backward(desc, _vector(dloss, rows, dev, "dloss"), *args,
+                                        _vector(stats, 3 * rows, dev, "stats"), dlogits.data_ptr(), _stream_of(dev)),
            "cbr_distill_backward")
     return dlogits
 
@@ -156,15 +164,13 @@ def distill_forward_backward(logits, top_ids, top_logits, *, temperature=1.0, te
     logits themselves, to save their memory), "loss" and "stats"."""
     dlogits = out["dlogits"] if out and "dlogits" in out else torch.empty_like(
         logits, memory_format=torch.contiguous_format)
-    desc = _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_weight, dlogits)
-    rows = logits.shape[0]
-    loss = _given(out, "loss", rows, torch.float32, logits)
+    desc, args = _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_weight, dlogits)
+    rows, dev = logits.shape[0], logits.device
+    loss = _given(out, "loss", rows, torch.float32, dev)
     stats = out.get("stats") if out else None
-    _vector(loss, rows, logits, "loss")
-    _vector(stats, 3 * rows, logits, "stats")
     _check(_load().cbr_distill_forward_backward(
-        desc, _ptr(logits), _ptr(top_ids), _ptr(top_logits), _ptr(teacher_lse), _ptr(row_weight), _ptr(loss),
-        _ptr(stats), _ptr(dlogits), _stream()), "cbr_distill_forward_backward")
+        desc, *args, _vector(loss, rows, dev, "loss"), _vector(stats, 3 * rows, dev, "stats"), dlogits.data_ptr(),
+        _stream_of(dev)), "cbr_distill_forward_backward")
     return {"loss": loss, "dlogits": dlogits} if stats is None else {"loss": loss, "dlogits": dlogits, "stats": stats}
 
 
@@ -176,28 +182,26 @@ def _kind(kind: str) -> int:
     return _KIND[kind]
 
 
-def _gate_rows(gate, rows: int, dim: int, like) -> int:
-    """Rows of one gate, from the gate's [dim] or [groups][dim]."""
+def _gate(gate, rows: int, dim: int, dev):
+    """(rows of one gate, address, number of elements) of a gate [dim] or [groups][dim]."""
     if gate is None:
-        return 0
-    if gate.dtype != torch.float32 or gate.device != like.device or gate.dim() not in (1, 2) or \
-            gate.shape[-1] != dim or not gate.is_contiguous():
-        _bad(f"gate has to be contiguous fp32 [{dim}] or [groups][{dim}] on {like.device}")
+        return 0, None
+    if gate.dtype != torch.float32 or gate.device != dev or gate.dim() not in (1, 2) or gate.shape[-1] != dim or \
+            not gate.is_contiguous():
+        _bad(f"gate has to be contiguous fp32 [{dim}] or [groups][{dim}] on {dev}")
     groups = gate.shape[0] if gate.dim() == 2 else 1
     if groups < 1 or rows % groups:
         _bad(f"{rows} rows do not split over {groups} gates")
-    return max(1, rows // groups)
+    return max(1, rows // groups), gate.data_ptr()
 
 
-def _norm_weights(x, branch, post_weight, gate, pre_weight, dim):
+def _forms(branch, post_weight, gate, pre_weight):
     if (branch is None) != (post_weight is None):
         _bad("branch and post_weight go together")
     if branch is None and gate is not None:
         _bad("a gate needs a branch")
     if branch is None and pre_weight is None:
         _bad("neither a branch nor a pre_weight")
-    _vector(post_weight, dim, x, "post_weight")
-    _vector(pre_weight, dim, x, "pre_weight")
 
 
 def block_norm_forward(x, branch=None, post_weight=None, gate=None, pre_weight=None, *, kind="rms", eps=1e-6,
@@ -213,36 +217,46 @@ def block_norm_forward(x, branch=None, post_weight=None, gate=None, pre_weight=N
     serve the backward (None without want_stats)."""
     if x.dim() != 2 or not x.is_cuda:
         _bad("x has to be a [rows][dim] CUDA tensor")
-    rows, dim = x.shape
+    shape, dt, dev = x.shape, x.dtype, x.device
+    rows, dim = shape
     dtype = _dtype(x, "x")
-    s_x = _matrix(x, rows, dim, x.dtype, x, "x")
-    _norm_weights(x, branch, post_weight, gate, pre_weight, dim)
+    s_x = _matrix(x, shape, dt, dev, "x")
+    _forms(branch, post_weight, gate, pre_weight)
     s_f = s_xo = s_h = dim
-    x_out = h = stats = None
+    x_out = h = stats = f_at = xo_at = h_at = None
     if branch is not None:
-        s_f = _matrix(branch, rows, dim, x.dtype, x, "branch")
-        x_out = _given(out, "x_out", (rows, dim), x.dtype, x)
-        s_xo = _matrix(x_out, rows, dim, x.dtype, x, "x_out")
+        s_f = _matrix(branch, shape, dt, dev, "branch")
+        x_out = _given(out, "x_out", shape, dt, dev)
+        s_xo = _matrix(x_out, shape, dt, dev, "x_out")
+        f_at, xo_at = branch.data_ptr(), x_out.data_ptr()
     if pre_weight is not None:
-        h = _given(out, "h", (rows, dim), x.dtype, x)
-        s_h = _matrix(h, rows, dim, x.dtype, x, "h")
+        h = _given(out, "h", shape, dt, dev)
+        s_h = _matrix(h, shape, dt, dev, "h")
+        h_at = h.data_ptr()
     if want_stats:
-        stats = _given(out, "stats", (rows, 4), torch.float32, x)
-        _vector(stats, 4 * rows, x, "stats")
-    desc = _NORM.pack(rows, dim, _gate_rows(gate, rows, dim, x), s_x, s_f, s_xo, s_h, 0, 0, 0, 0, dtype,
-                      _kind(kind), eps, residual_scale, branch_scale)
-    _check(_load().cbr_block_norm_forward(desc, _ptr(x), _ptr(branch), _ptr(post_weight), _ptr(gate),
-                                          _ptr(pre_weight), _ptr(x_out), _ptr(h), _ptr(stats), _stream()),
-           "cbr_block_norm_forward")
+        stats = _given(out, "stats", (rows, 4), torch.float32, dev)
+    gate_rows, gate_at = _gate(gate, rows, dim, dev)
+    desc = _NORM.pack(rows, dim, gate_rows, s_x, s_f, s_xo, s_h, 0, 0, 0, 0, dtype, _kind(kind), eps, residual_scale,
+                      branch_scale)
+    _check(_load().cbr_block_norm_forward(
+        desc, x.data_ptr(), f_at, _vector(post_weight, dim, dev, "post_weight"), gate_at,
+        _vector(pre_weight, dim, dev, "pre_weight"), xo_at, h_at, _vector(stats, 4 * rows, dev, "stats"),
+        _stream_of(dev)), "cbr_block_norm_forward")
     return {"x_out": x_out, "h": h, "stats": stats}
 
 
+_sizes: dict = {}   # block_norm_workspace_size's answers
+
+
 def block_norm_workspace_size(rows: int, dim: int, dtype=torch.float16) -> int:
-    """Workspace bytes of :func:`block_norm_backward`."""
-    n = ctypes.c_size_t()
-    desc = _NORM.pack(rows, dim, 0, dim, dim, dim, dim, dim, dim, dim, dim, _DTYPE[dtype], 0, 1.0, 1.0, 1.0)
-    _check(_load().cbr_block_norm_workspace_size(desc, ctypes.byref(n)), "cbr_block_norm_workspace_size")
-    return n.value
+    """Workspace bytes of :func:`block_norm_backward` (they go by dim alone)."""
+    size = _sizes.get(dim)
+    if size is None:
+        n = ctypes.c_size_t()
+        desc = _NORM.pack(rows, dim, 0, dim, dim, dim, dim, dim, dim, dim, dim, _DTYPE[dtype], 0, 1.0, 1.0, 1.0)
+        _check(_load().cbr_block_norm_workspace_size(desc, ctypes.byref(n)), "cbr_block_norm_workspace_size")
+        size = _sizes[dim] = n.value
+    return size
 
 
 def block_norm_backward(dx_out, dh, x_out, branch=None, post_weight=None, gate=None, pre_weight=None, stats=None, *,
@@ -256,48 +270,47 @@ def block_norm_backward(dx_out, dh, x_out, branch=None, post_weight=None, gate=N
     given = dx_out if dx_out is not None else dh
     if given is None or given.dim() != 2 or not given.is_cuda:
         _bad("dx_out or dh has to be a [rows][dim] CUDA tensor")
-    rows, dim = given.shape
-    dt, dtype = given.dtype, _dtype(given, "the gradient")
-    _norm_weights(given, branch, post_weight, gate, pre_weight, dim)
+    shape, dt, dev = given.shape, given.dtype, given.device
+    rows, dim = shape
+    dtype = _dtype(given, "the gradient")
+    _forms(branch, post_weight, gate, pre_weight)
     if (pre_weight is None) != (dh is None):
         _bad("dh and pre_weight go together")
     if stats is None:
         _bad("the backward needs the forward's stats")
-    _vector(stats, 4 * rows, given, "stats")
     s_f = s_xo = s_dxo = s_dh = s_df = dim
+    dpre = dpost = dgate = dbranch = dxo_at = xo_at = dh_at = f_at = df_at = None
     if dx_out is not None:
-        s_dxo = _matrix(dx_out, rows, dim, dt, given, "dx_out")
-    dpre = dpost = dgate = dbranch = None
+        s_dxo = _matrix(dx_out, shape, dt, dev, "dx_out")
+        dxo_at = dx_out.data_ptr()
     if pre_weight is not None:
-        s_xo = _matrix(x_out, rows, dim, dt, given, "x_out")
-        s_dh = _matrix(dh, rows, dim, dt, given, "dh")
-        dpre = _given(out, "dpre_weight", dim, torch.float32, given)
-        _vector(dpre, dim, given, "dpre_weight")
-    gate_rows = _gate_rows(gate, rows, dim, given)
+        s_xo = _matrix(x_out, shape, dt, dev, "x_out")
+        s_dh = _matrix(dh, shape, dt, dev, "dh")
+        xo_at, dh_at = x_out.data_ptr(), dh.data_ptr()
+        dpre = _given(out, "dpre_weight", dim, torch.float32, dev)
+    gate_rows, gate_at = _gate(gate, rows, dim, dev)
     if branch is not None:
-        s_f = _matrix(branch, rows, dim, dt, given, "branch")
-        dbranch = _given(out, "dbranch", (rows, dim), dt, given)
-        s_df = _matrix(dbranch, rows, dim, dt, given, "dbranch")
-        dpost = _given(out, "dpost_weight", dim, torch.float32, given)
-        _vector(dpost, dim, given, "dpost_weight")
+        s_f = _matrix(branch, shape, dt, dev, "branch")
+        dbranch = _given(out, "dbranch", shape, dt, dev)
+        s_df = _matrix(dbranch, shape, dt, dev, "dbranch")
+        f_at, df_at = branch.data_ptr(), dbranch.data_ptr()
+        dpost = _given(out, "dpost_weight", dim, torch.float32, dev)
         if gate is not None:
-            dgate = _given(out, "dgate", gate.shape, torch.float32, given)
-            _vector(dgate, gate.numel(), given, "dgate")
+            dgate = _given(out, "dgate", gate.shape, torch.float32, dev)
             if rows == 0:
                 dgate.zero_()
-    dx = _given(out, "dx", (rows, dim), dt, given)
-    s_dx = _matrix(dx, rows, dim, dt, given, "dx")
+    dx = _given(out, "dx", shape, dt, dev)
+    s_dx = _matrix(dx, shape, dt, dev, "dx")
     desc = _NORM.pack(rows, dim, gate_rows, dim, s_f, s_xo, dim, s_dxo, s_dh, s_dx, s_df, dtype, _kind(kind), 1.0,
                       residual_scale, branch_scale)
-    lib = _load()
     if ws is None:
-        n = ctypes.c_size_t()
-        _check(lib.cbr_block_norm_workspace_size(desc, ctypes.byref(n)), "cbr_block_norm_workspace_size")
-        ws = torch.empty(n.value, dtype=torch.uint8, device=given.device)
-    _check(lib.cbr_block_norm_backward(
-        desc, _ptr(dx_out), _ptr(dh), _ptr(x_out) if pre_weight is not None else None, _ptr(branch),
-        _ptr(post_weight), _ptr(gate), _ptr(pre_weight), _ptr(stats), _ptr(dx), _ptr(dbranch), _ptr(dpost),
-        _ptr(dgate), _ptr(dpre), _ptr(ws), ws.numel() * ws.element_size(), _stream()), "cbr_block_norm_backward")
+        ws = torch.empty(block_norm_workspace_size(rows, dim, dt), dtype=torch.uint8, device=dev)
+    _check(_load().cbr_block_norm_backward(
+        desc, dxo_at, dh_at, xo_at, f_at, _vector(post_weight, dim, dev, "post_weight"), gate_at,
+        _vector(pre_weight, dim, dev, "pre_weight"), _vector(stats, 4 * rows, dev, "stats"), dx.data_ptr(), df_at,
+        _vector(dpost, dim, dev, "dpost_weight"), _vector(dgate, dgate.numel() if dgate is not None else 0, dev, "dgate"),
+        _vector(dpre, dim, dev, "dpre_weight"), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev)),
+        "cbr_block_norm_backward")
     return {"dx": dx, "dbranch": dbranch, "dpost_weight": dpost, "dgate": dgate, "dpre_weight": dpre}
 
 
@@ -342,14 +355,15 @@ def grid_positions(*extents: int, device="cuda") -> torch.Tensor:
     return torch.stack(torch.meshgrid(*axes, indexing="ij"), -1).reshape(-1, len(extents))
 
 
-def _heads(t, batch, tokens, head_dim, like, what):
-    if t.dim() != 4 or t.shape[0] != batch or t.shape[1] != tokens or t.shape[3] != head_dim or \
-            t.dtype != like.dtype or t.device != like.device:
-        _bad(f"{what} has to be [{batch}][{tokens}][heads][{head_dim}] {like.dtype} on {like.device}")
+def _heads(t, batch, tokens, head_dim, dtype, dev, what):
+    """Checks a [batch][tokens][heads][head_dim] tensor; its strides, its heads and its address."""
+    n = t.shape
+    if len(n) != 4 or n[0] != batch or n[1] != tokens or n[3] != head_dim or t.dtype != dtype or t.device != dev:
+        _bad(f"{what} has to be [{batch}][{tokens}][heads][{head_dim}] {dtype} on {dev}")
     sb, st, sh, se = t.stride()
     if se != 1:
         _bad(f"{what}: a head's elements have to be adjacent")
-    return sb, st, sh, t.shape[2]
+    return (sb, st, sh), n[2], t.data_ptr()
 
 
 def _rotary(f, q, k, positions, freq, axis, layout, out):
@@ -357,43 +371,43 @@ def _rotary(f, q, k, positions, freq, axis, layout, out):
     if first is None or first.dim() != 4 or not first.is_cuda:
         _bad("q or k has to be a [batch][tokens][heads][head_dim] CUDA tensor")
     batch, tokens, _, head_dim = first.shape
+    dt, dev = first.dtype, first.device
     dtype = _dtype(first, "q and k")
-    if layout not in _LAYOUT:
+    code = _LAYOUT.get(layout)
+    if code is None:
         _bad(f"layout {layout!r}: one of {sorted(_LAYOUT)}")
-    if positions.dtype != torch.int32 or positions.dim() not in (2, 3) or positions.device != first.device:
-        _bad(f"positions have to be int32 [tokens][axes] or [batch][tokens][axes] on {first.device}")
-    if positions.shape[-2] != tokens or (positions.dim() == 3 and positions.shape[0] not in (1, batch)):
-        _bad(f"positions {list(positions.shape)} do not go with {batch} x {tokens} tokens")
+    p = positions.shape
+    if positions.dtype != torch.int32 or len(p) not in (2, 3) or positions.device != dev:
+        _bad(f"positions have to be int32 [tokens][axes] or [batch][tokens][axes] on {dev}")
+    if p[-2] != tokens or (len(p) == 3 and p[0] not in (1, batch)):
+        _bad(f"positions {list(p)} do not go with {batch} x {tokens} tokens")
     sp = positions.stride()
-    if positions.dim() == 2 or positions.shape[0] == 1:
+    if len(p) == 2 or p[0] == 1:
         sp = (0,) + sp[-2:]
     pairs = freq.numel()
-    if freq.dtype != torch.int64 or axis.dtype != torch.uint8 or axis.numel() != pairs or \
-            not freq.is_contiguous() or not axis.is_contiguous() or freq.device != first.device or \
-            axis.device != first.device:
+    if freq.dtype != torch.int64 or axis.dtype != torch.uint8 or axis.numel() != pairs or freq.device != dev or \
+            axis.device != dev or not freq.is_contiguous() or not axis.is_contiguous():
         _bad("freq (int64) and axis (uint8) have to be contiguous, one each for every pair")
-    strides, heads, res = [], [], []
-    for i, t in enumerate((q, k)):
-        if t is None:
-            strides.append((0, 0, 0, 0, 0, 0))
-            heads.append(0)
-            res.append(None)
-            continue
-        sb, st, sh, n = _heads(t, batch, tokens, head_dim, first, "qk"[i])
-        o = out[i] if out is not None else torch.empty_like(t, memory_format=torch.contiguous_format)
-        ob, ot, oh, m = _heads(o, batch, tokens, head_dim, first, "out")
-        if m != n:
-            _bad("out has another number of heads")
-        strides.append((sb, st, sh, ob, ot, oh))
-        heads.append(n)
-        res.append(o)
-    (a, b) = strides
-    desc = _ROTARY.pack(batch, tokens, *a[:3], *b[:3], *a[3:], *b[3:], *sp, heads[0], heads[1], head_dim, 2 * pairs,
-                        positions.shape[-1], _LAYOUT[layout], dtype)
-    lib = _load()
-    _check(getattr(lib, f)(desc, _ptr(q), _ptr(k), _ptr(positions), _ptr(freq), _ptr(axis), _ptr(res[0]),
-                           _ptr(res[1]), _stream()), f)
-    return tuple(res)
+    none = (0, 0, 0)
+    sq = sqo = sk = sko = none
+    hq = hk = 0
+    q_at = k_at = qo_at = ko_at = q_out = k_out = None
+    if q is not None:
+        sq, hq, q_at = _heads(q, batch, tokens, head_dim, dt, dev, "q")
+        q_out = out[0] if out is not None else torch.empty_like(q, memory_format=torch.contiguous_format)
+        sqo, n, qo_at = _heads(q_out, batch, tokens, head_dim, dt, dev, "out[0]")
+        if n != hq:
+            _bad("out[0] has another number of heads")
+    if k is not None:
+        sk, hk, k_at = _heads(k, batch, tokens, head_dim, dt, dev, "k")
+        k_out = out[1] if out is not None else torch.empty_like(k, memory_format=torch.contiguous_format)
+        sko, n, ko_at = _heads(k_out, batch, tokens, head_dim, dt, dev, "out[1]")
+        if n != hk:
+            _bad("out[1] has another number of heads")
+    desc = _ROTARY.pack(batch, tokens, *sq, *sk, *sqo, *sko, *sp, hq, hk, head_dim, 2 * pairs, p[-1], code, dtype)
+    _check(getattr(_load(), f)(desc, q_at, k_at, positions.data_ptr(), freq.data_ptr(), axis.data_ptr(), qo_at, ko_at,
+                               _stream_of(dev)), f)
+    return q_out, k_out
 
 
 def rotary_forward(q, k, positions, freq, axis, *, layout="halves", out=None) -> tuple:
