@@ -5,6 +5,9 @@
 // over its run of rows.  Variances are sums of squared differences from the mean, over the registers.
 // Bound by HBM: x and the branch in, x_out and h out.
 #include <algorithm>
+#include <map>
+#include <mutex>
+#include <tuple>
 #include <type_traits>
 
 #include "cbr_internal.h"
@@ -118,11 +121,8 @@ __global__ void __launch_bounds__(kThreads, kFit) norm_forward_kernel(const __gr
 template <typename T, int kVec, int kEpt, bool kBlock, int kThreads, int kFit>
 int launch(const BlockNormArgs& a, const Shape& s, int num_sms, cudaStream_t st) {
   auto kernel = norm_forward_kernel<T, kVec, kEpt, kBlock, kThreads, kFit>;
-  int blocks = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, s.threads, 0) != cudaSuccess || blocks < 1) {
-    cudaGetLastError();
-    return CBR_ERR_CUDA;
-  }
+  const int blocks = blocks_that_fit(reinterpret_cast<const void*>(kernel), s.threads, 0);
+  if (blocks < 1) return CBR_ERR_CUDA;
   const int teams = kBlock ? 1 : s.threads / s.team;
   const long long want = (a.d.rows + teams - 1) / teams;
   kernel<<<(unsigned)std::min<long long>(want, (long long)blocks * num_sms), s.threads, 0, st>>>(a, s.team);
@@ -158,6 +158,23 @@ int by_alignment(const BlockNormArgs& a, int num_sms, cudaStream_t st) {
 }
 
 }  // namespace
+
+int blocks_that_fit(const void* kernel, int threads, int smem) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int, int>, int> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  const auto key = std::make_tuple(kernel, threads, smem, dev);
+  const auto it = known.find(key);
+  if (it != known.end()) return it->second;
+  int blocks = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return known[key] = blocks;
+}
 
 int launch_block_norm(const BlockNormArgs& a, int num_sms, cudaStream_t st) {
   if (a.d.dtype == CBR_F32) return by_alignment<float>(a, num_sms, st);

@@ -397,11 +397,8 @@ int launch_kind(const BlockNormArgs& a, int team, int threads, int num_sms, cuda
     p.stages = std::max(2, std::min(kMaxStages, 200 * 1024 / share / (4 * p.row_bytes)));
     smem = p.stages * 4 * p.row_bytes;
   }
-  int fit = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, smem) != cudaSuccess || fit < 1) {
-    cudaGetLastError();
-    return CBR_ERR_CUDA;
-  }
+  const int fit = blocks_that_fit(reinterpret_cast<const void*>(kernel), threads, smem);
+  if (fit < 1) return CBR_ERR_CUDA;
   const long long most = (long long)std::min(fit, blocks_per_sm(a.d.dim)) * num_sms;
   const int teams = kBlock ? 1 : threads / team;
   p.team = team;

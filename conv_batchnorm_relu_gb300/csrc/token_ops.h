@@ -12,6 +12,10 @@ namespace cbr {
 // The current device if this library runs on it (cbr_api.cu): its SM count and its error word.
 int device_for_call(int* num_sms, uint32_t** err);
 
+// Blocks of `threads` threads and `smem` bytes of dynamic shared memory that fit on an SM at once; 0 if the
+// runtime refuses.  Asked once for each kernel, shape and device (block_norm.cu).
+int blocks_that_fit(const void* kernel, int threads, int smem);
+
 struct DistillArgs {
   cbr_distill_desc_t d;
   const float* dloss;        // null: ones

@@ -87,18 +87,39 @@ def _vector(t: torch.Tensor | None, n: int, dev, what: str):
     return t.data_ptr()
 
 
+# A small call's time is host time: torch's short ways to a new tensor, the current stream and the current
+# device, where it has them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _new(shape, dtype, dev) -> torch.Tensor:
+    """A new contiguous tensor on the current device."""
+    if _empty_cuda is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    strides = [1]
+    for n in shape[:0:-1]:
+        strides.append(strides[-1] * (n or 1))
+    return _empty_cuda(tuple(shape), tuple(strides[::-1]), dtype)
+
+
 def _given(out: dict | None, name: str, shape, dtype, dev) -> torch.Tensor:
     """The caller's output of that name, or a new one."""
     if out and name in out:
         return out[name]
-    return torch.empty(shape, dtype=dtype, device=dev)
+    return _new(shape, dtype, dev)
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+def _device_of(t: torch.Tensor):
+    """The tensor's device, which has to be the current one: the library launches there."""
+    dev = t.device
+    if dev.index != _get_device():
+        _bad(f"tensors on {dev}, which is not the current device", 5)
+    return dev
 
 
 def _stream_of(dev) -> int:
-    """The device's current stream (without building the stream's object, where torch has that)."""
     return _raw_stream(dev.index) if _raw_stream is not None else _stream()
 
 
@@ -108,7 +129,7 @@ def _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_wei
     """The packed descriptor and the addresses of the calls' common arguments."""
     if logits.dim() != 2 or not logits.is_cuda:
         _bad("logits have to be a [rows][vocab] CUDA tensor")
-    shape, dev = logits.shape, logits.device
+    shape, dev = logits.shape, _device_of(logits)
     rows, vocab = shape
     dtype = _dtype(logits, "logits")
     top_dtype = _dtype(top_logits, "top_logits")
@@ -136,7 +157,7 @@ def distill_forward(logits, top_ids, top_logits, *, temperature=1.0, teacher_lse
     0 masks it."""
     desc, args = _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_weight, None)
     rows, dev = logits.shape[0], logits.device
-    loss = _given(out, "loss", rows, torch.float32, dev)
+    loss = _given(out, "loss", (rows,), torch.float32, dev)
     stats = _given(out, "stats", (rows, 3), torch.float32, dev)
     _check(_load().cbr_distill_forward(desc, *args, _vector(loss, rows, dev, "loss"),
                                        _vector(stats, 3 * rows, dev, "stats"), _stream_of(dev)), "cbr_distill_forward")
@@ -148,7 +169,7 @@ def distill_backward(dloss, logits, top_ids, top_logits, stats, *, temperature=1
     """cbr_distill_backward -> dlogits [rows][vocab] (``out`` may be the logits themselves).
 
     dloss [rows] fp32 or None (ones); stats from :func:`distill_forward`; the rest as there."""
-    dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format) if out is None else out
+    dlogits = _new(logits.shape, logits.dtype, logits.device) if out is None and logits.is_cuda else out
     desc, args = _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_weight, dlogits)
     rows, dev = logits.shape[0], logits.device
     _check(_load().cbr_distill_backward(desc, _vector(dloss, rows, dev, "dloss"), *args,
@@ -162,11 +183,12 @@ def distill_forward_backward(logits, top_ids, top_logits, *, temperature=1.0, te
     """cbr_distill_forward_backward -> dict(loss [rows], dlogits [rows][vocab]): the loss and its gradient
     (a mean is a row_weight of 1 / rows) with one read of the logits.  ``out`` may hold "dlogits" (the
     logits themselves, to save their memory), "loss" and "stats"."""
-    dlogits = out["dlogits"] if out and "dlogits" in out else torch.empty_like(
-        logits, memory_format=torch.contiguous_format)
+    dlogits = out["dlogits"] if out and "dlogits" in out else None
+    if dlogits is None and logits.is_cuda:
+        dlogits = _new(logits.shape, logits.dtype, logits.device)
     desc, args = _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_weight, dlogits)
     rows, dev = logits.shape[0], logits.device
-    loss = _given(out, "loss", rows, torch.float32, dev)
+    loss = _given(out, "loss", (rows,), torch.float32, dev)
     stats = out.get("stats") if out else None
     _check(_load().cbr_distill_forward_backward(
         desc, *args, _vector(loss, rows, dev, "loss"), _vector(stats, 3 * rows, dev, "stats"), dlogits.data_ptr(),
@@ -217,7 +239,7 @@ def block_norm_forward(x, branch=None, post_weight=None, gate=None, pre_weight=N
     serve the backward (None without want_stats)."""
     if x.dim() != 2 or not x.is_cuda:
         _bad("x has to be a [rows][dim] CUDA tensor")
-    shape, dt, dev = x.shape, x.dtype, x.device
+    shape, dt, dev = x.shape, x.dtype, _device_of(x)
     rows, dim = shape
     dtype = _dtype(x, "x")
     s_x = _matrix(x, shape, dt, dev, "x")
@@ -270,7 +292,7 @@ def block_norm_backward(dx_out, dh, x_out, branch=None, post_weight=None, gate=N
     given = dx_out if dx_out is not None else dh
     if given is None or given.dim() != 2 or not given.is_cuda:
         _bad("dx_out or dh has to be a [rows][dim] CUDA tensor")
-    shape, dt, dev = given.shape, given.dtype, given.device
+    shape, dt, dev = given.shape, given.dtype, _device_of(given)
     rows, dim = shape
     dtype = _dtype(given, "the gradient")
     _forms(branch, post_weight, gate, pre_weight)
@@ -287,14 +309,14 @@ def block_norm_backward(dx_out, dh, x_out, branch=None, post_weight=None, gate=N
         s_xo = _matrix(x_out, shape, dt, dev, "x_out")
         s_dh = _matrix(dh, shape, dt, dev, "dh")
         xo_at, dh_at = x_out.data_ptr(), dh.data_ptr()
-        dpre = _given(out, "dpre_weight", dim, torch.float32, dev)
+        dpre = _given(out, "dpre_weight", (dim,), torch.float32, dev)
     gate_rows, gate_at = _gate(gate, rows, dim, dev)
     if branch is not None:
         s_f = _matrix(branch, shape, dt, dev, "branch")
         dbranch = _given(out, "dbranch", shape, dt, dev)
         s_df = _matrix(dbranch, shape, dt, dev, "dbranch")
         f_at, df_at = branch.data_ptr(), dbranch.data_ptr()
-        dpost = _given(out, "dpost_weight", dim, torch.float32, dev)
+        dpost = _given(out, "dpost_weight", (dim,), torch.float32, dev)
         if gate is not None:
             dgate = _given(out, "dgate", gate.shape, torch.float32, dev)
             if rows == 0:
@@ -304,7 +326,7 @@ def block_norm_backward(dx_out, dh, x_out, branch=None, post_weight=None, gate=N
     desc = _NORM.pack(rows, dim, gate_rows, dim, s_f, s_xo, dim, s_dxo, s_dh, s_dx, s_df, dtype, _kind(kind), 1.0,
                       residual_scale, branch_scale)
     if ws is None:
-        ws = torch.empty(block_norm_workspace_size(rows, dim, dt), dtype=torch.uint8, device=dev)
+        ws = _new((block_norm_workspace_size(rows, dim, dt),), torch.uint8, dev)
     _check(_load().cbr_block_norm_backward(
         desc, dxo_at, dh_at, xo_at, f_at, _vector(post_weight, dim, dev, "post_weight"), gate_at,
         _vector(pre_weight, dim, dev, "pre_weight"), _vector(stats, 4 * rows, dev, "stats"), dx.data_ptr(), df_at,
@@ -371,7 +393,7 @@ def _rotary(f, q, k, positions, freq, axis, layout, out):
     if first is None or first.dim() != 4 or not first.is_cuda:
         _bad("q or k has to be a [batch][tokens][heads][head_dim] CUDA tensor")
     batch, tokens, _, head_dim = first.shape
-    dt, dev = first.dtype, first.device
+    dt, dev = first.dtype, _device_of(first)
     dtype = _dtype(first, "q and k")
     code = _LAYOUT.get(layout)
     if code is None:
@@ -394,13 +416,13 @@ def _rotary(f, q, k, positions, freq, axis, layout, out):
     q_at = k_at = qo_at = ko_at = q_out = k_out = None
     if q is not None:
         sq, hq, q_at = _heads(q, batch, tokens, head_dim, dt, dev, "q")
-        q_out = out[0] if out is not None else torch.empty_like(q, memory_format=torch.contiguous_format)
+        q_out = out[0] if out is not None else _new(q.shape, dt, dev)
         sqo, n, qo_at = _heads(q_out, batch, tokens, head_dim, dt, dev, "out[0]")
         if n != hq:
             _bad("out[0] has another number of heads")
     if k is not None:
         sk, hk, k_at = _heads(k, batch, tokens, head_dim, dt, dev, "k")
-        k_out = out[1] if out is not None else torch.empty_like(k, memory_format=torch.contiguous_format)
+        k_out = out[1] if out is not None else _new(k.shape, dt, dev)
         sko, n, ko_at = _heads(k_out, batch, tokens, head_dim, dt, dev, "out[1]")
         if n != hk:
             _bad("out[1] has another number of heads")
