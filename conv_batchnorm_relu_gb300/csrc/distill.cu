@@ -52,6 +52,7 @@ struct Plan {
   int buffers;      // of the ring
   int kp;           // room for entries
   int smem;
+  bool ragged;      // a row may start or end inside a 16-byte vector
 };
 
 struct Header {
@@ -605,16 +606,19 @@ __global__ void __maxnreg__(80)
       return place >= 0 && is_mine(place) && s.inside(place) ? src[place - s.lead] : from_f<T>(-INFINITY);
     };
     T next_edge = from_f<T>(0.f);
-    if (first < items) next_edge = edge_of(first);
+    if (plan.ragged && first < items) next_edge = edge_of(first);
     for (long long i = first; i < items; i += step, ++n) {
       const long long row = row_of(i);
       const int begin = begin_of(i), slot = n % kRows;
       const Slice<T> s(logits_at(row, begin), slice_n(begin));
       const int chunks = chunks_of(s);
-      int edge_at = s.edge_place(lane);
-      if (edge_at >= 0 && !is_mine(edge_at)) edge_at = -1;
+      int edge_at = -1;
       const T edge = next_edge;
-      if (i + step < items) next_edge = edge_of(i + step);
+      if (plan.ragged) {
+        edge_at = s.edge_place(lane);
+        if (edge_at >= 0 && !is_mine(edge_at)) edge_at = -1;
+        if (i + step < items) next_edge = edge_of(i + step);
+      }
       if (!(ok = wait(bar(&h.t_full[slot]), n / kRows & 1))) break;
       const int state = (int)h.teacher[slot][kState];
       const int* const ids = ids0 + slot * plan.kp;
@@ -649,6 +653,7 @@ __global__ void __maxnreg__(80)
       Running run;
       // Puts the ragged elements of a loaded chunk in.
       auto mend = [&](int q, T* buf) {
+        if (!plan.ragged) return;
         if (edge_at >= 0 && edge_at >> (chunk_bits + kLog) == q) buf[edge_at - (q << (chunk_bits + kLog))] = edge;
         __syncwarp();
       };
@@ -928,6 +933,7 @@ Plan make_plan(const DistillArgs& a, int elt) {
     while (p.slices < kMaxCluster && v * elt / (2 * p.slices) >= 2048) p.slices *= 2;
   p.width = (int)(((v + p.slices - 1) / p.slices + 127) / 128 * 128);
   const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.d.logits_stride * elt % 16 == 0;
+  p.ragged = !aligned || v * elt % 16 != 0;
   const int vectors = (int)(std::min<long long>(p.width, v) * elt + 15) / 16 + !aligned;
   // Chunks of 32 KB for eight warps, two batches of vectors for each lane; smaller where the row is.
   p.part = 8;
