@@ -18,7 +18,7 @@ namespace {
 
 using namespace norm;
 
-template <typename T, int kVec, int kEpt, bool kBlock, int kThreads, int kFit>
+template <typename T, int kVec, int kEpt, bool kBlock, bool kCenter, int kThreads, int kFit>
 __global__ void __launch_bounds__(kThreads, kFit) norm_forward_kernel(const __grid_constant__ BlockNormArgs a, int team_) {
   using R = Row<T, kVec, kEpt>;
   __shared__ float red[2][1][kMaxTeamWarps];
@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(kThreads, kFit) norm_forward_kernel(const __gr
   TeamSum<kBlock, 1> sum{red};
   const int dim = (int)a.d.dim, col = at * kVec, left = dim - col;
   const float inv_d = 1.f / (float)dim;
-  const bool center = a.d.kind == CBR_NORM_LAYER, join = a.branch != nullptr, next = a.pre_weight != nullptr;
+  const bool join = a.branch != nullptr, next = a.pre_weight != nullptr;
   const int teams_a_block = kBlock ? 1 : blockDim.x / team;
   const long long teams = (long long)gridDim.x * teams_a_block;
   const long long mine = (long long)blockIdx.x * teams_a_block + (kBlock ? 0 : threadIdx.x / team);
@@ -38,23 +38,22 @@ __global__ void __launch_bounds__(kThreads, kFit) norm_forward_kernel(const __gr
 
   // mean and 1 / sqrt(variance + eps) of the row in v
   auto moments = [&](const float(&v)[kEpt], float& m, float& r) __attribute__((always_inline)) {
-    float s[1];
+    float s[1] = {0.f};
     m = 0.f;
-    if (center) {
-      s[0] = 0.f;
+    if constexpr (kCenter) {
 #pragma unroll
       for (int i = 0; i < kEpt; ++i) s[0] += v[i];
       sum(s, team);
       m = s[0] * inv_d;
+      s[0] = 0.f;
     }
-    s[0] = 0.f;
 #pragma unroll
     for (int i = 0; i < kEpt; ++i) {
-      const float d = R::inside(i, team, left) ? v[i] - m : 0.f;
+      const float d = !kCenter ? v[i] : R::inside(i, team, left) ? v[i] - m : 0.f;   // v: 0 past the row
       s[0] += d * d;
     }
     sum(s, team);
-    r = 1.f / sqrtf(s[0] * inv_d + a.d.eps);
+    r = inverse_root(s[0] * inv_d + a.d.eps);
   };
 
   R x, f;
@@ -100,14 +99,14 @@ __global__ void __launch_bounds__(kThreads, kFit) norm_forward_kernel(const __gr
     if (join) {
       moments(n, m1, r1);
 #pragma unroll
-      for (int k = 0; k < kEpt; ++k) v[k] = a.d.residual_scale * v[k] + (n[k] - m1) * r1 * w1[k];
+      for (int k = 0; k < kEpt; ++k) v[k] = a.d.residual_scale * v[k] + (kCenter ? n[k] - m1 : n[k]) * (r1 * w1[k]);
       if (here) R::store(op, v, team, left);
       op += a.d.x_out_stride;
     }
     if (next) {
       moments(v, m2, r2);
 #pragma unroll
-      for (int k = 0; k < kEpt; ++k) v[k] = (v[k] - m2) * r2 * w2[k];
+      for (int k = 0; k < kEpt; ++k) v[k] = (kCenter ? v[k] - m2 : v[k]) * (r2 * w2[k]);
       if (here) R::store(hp, v, team, left);
       hp += a.d.h_stride;
     }
@@ -120,7 +119,8 @@ __global__ void __launch_bounds__(kThreads, kFit) norm_forward_kernel(const __gr
 
 template <typename T, int kVec, int kEpt, bool kBlock, int kThreads, int kFit>
 int launch(const BlockNormArgs& a, const Shape& s, int num_sms, cudaStream_t st) {
-  auto kernel = norm_forward_kernel<T, kVec, kEpt, kBlock, kThreads, kFit>;
+  auto kernel = a.d.kind == CBR_NORM_LAYER ? norm_forward_kernel<T, kVec, kEpt, kBlock, true, kThreads, kFit>
+                                           : norm_forward_kernel<T, kVec, kEpt, kBlock, false, kThreads, kFit>;
   const int blocks = blocks_that_fit(reinterpret_cast<const void*>(kernel), s.threads, 0);
   if (blocks < 1) return CBR_ERR_CUDA;
   const int teams = kBlock ? 1 : s.threads / s.team;

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, kFit)
       if (next) {
 #pragma unroll
         for (int k = 0; k < kEpt; ++k) {
-          n[k] = (n[k] - m2) * r2;
+          n[k] = (kCenter ? n[k] - m2 : n[k]) * r2;
           const float t = u[k] * n[k];
           if (here) dw2[k] += t;
           u[k] *= w2[k];
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, kFit)
       }
       if (join) {
 #pragma unroll
-        for (int k = 0; k < kEpt; ++k) e[k] = (e[k] - m1) * r1;
+        for (int k = 0; k < kEpt; ++k) e[k] = (kCenter ? e[k] - m1 : e[k]) * r1;
       }
       if constexpr (kCenter) {
         if (next) {
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, kFit)
 #pragma unroll
         for (int k = 0; k < kEpt; ++k) {
           if (here) de[k] += d[k] * e[k];
-          e[k] = r1 * (p[k] * d[k] - mv - e[k] * me);
+          e[k] = kCenter ? r1 * (p[k] * d[k] - mv - e[k] * me) : r1 * (p[k] * d[k] - e[k] * me);
           d[k] *= a.d.residual_scale;
         }
         if (here) R::store(df_at, e, team, left);

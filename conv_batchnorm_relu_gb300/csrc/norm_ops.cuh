@@ -184,6 +184,13 @@ struct Shape {
   int team;      // threads
   int threads;   // of a block
 };
+// 1 / sqrt(x), x > 0: the hardware's estimate and a Newton step, which leaves about a rounding (a square
+// root and a division would be a fifth of a row's instructions).
+__device__ __forceinline__ float inverse_root(float x) {
+  const float y = rsqrtf(x);
+  return y * fmaf(-0.5f * x * y, y, 1.5f);
+}
+
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 }  // namespace norm
