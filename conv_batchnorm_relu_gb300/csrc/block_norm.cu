@@ -118,32 +118,30 @@ __global__ void __launch_bounds__(kThreads, kFit) norm_forward_kernel(const __gr
 }
 
 template <typename T, int kVec, int kEpt, bool kBlock, int kThreads, int kFit>
-int launch(const BlockNormArgs& a, const Shape& s, int num_sms, cudaStream_t st) {
+int launch(const BlockNormArgs& a, int team, int threads, int num_sms, cudaStream_t st) {
   auto kernel = a.d.kind == CBR_NORM_LAYER ? norm_forward_kernel<T, kVec, kEpt, kBlock, true, kThreads, kFit>
                                            : norm_forward_kernel<T, kVec, kEpt, kBlock, false, kThreads, kFit>;
-  const int blocks = blocks_that_fit(reinterpret_cast<const void*>(kernel), s.threads, 0);
+  const int blocks = blocks_that_fit(reinterpret_cast<const void*>(kernel), threads, 0);
   if (blocks < 1) return CBR_ERR_CUDA;
-  const int teams = kBlock ? 1 : s.threads / s.team;
+  const int teams = kBlock ? 1 : threads / team;
   const long long want = (a.d.rows + teams - 1) / teams;
-  kernel<<<(unsigned)std::min<long long>(want, (long long)blocks * num_sms), s.threads, 0, st>>>(a, s.team);
+  kernel<<<(unsigned)std::min<long long>(want, (long long)blocks * num_sms), threads, 0, st>>>(a, team);
   return cudaGetLastError() == cudaSuccess ? CBR_OK : CBR_ERR_CUDA;
 }
 
 template <typename T, int kVec>
 int pick(const BlockNormArgs& a, int num_sms, cudaStream_t st) {
   const int dim = (int)a.d.dim;
-  Shape s{};
   if (dim <= 256) {   // eight elements a thread, a warp or less
-    s.team = 1;
-    while (s.team * 8 < dim) s.team *= 2;
-    s.threads = 256;
-    return launch<T, kVec, 8, false, 256, 3>(a, s, num_sms, st);
+    int team = 1;
+    while (team * 8 < dim) team *= 2;
+    return launch<T, kVec, 8, false, 256, 3>(a, team, 256, num_sms, st);
   }
   const int ept = dim <= 4096 ? 8 : dim <= 8192 ? 16 : 32;
-  s.threads = ((dim + ept - 1) / ept + 31) / 32 * 32;
-  if (ept == 8) return launch<T, kVec, 8, true, 512, 2>(a, s, num_sms, st);
-  if (ept == 16) return launch<T, kVec, 16, true, 512, 1>(a, s, num_sms, st);
-  return launch<T, kVec, 32, true, 512, 1>(a, s, num_sms, st);
+  const int threads = ((dim + ept - 1) / ept + 31) / 32 * 32;
+  if (ept == 8) return launch<T, kVec, 8, true, 512, 2>(a, threads, threads, num_sms, st);
+  if (ept == 16) return launch<T, kVec, 16, true, 512, 1>(a, threads, threads, num_sms, st);
+  return launch<T, kVec, 32, true, 512, 1>(a, threads, threads, num_sms, st);
 }
 
 template <typename T>

@@ -238,7 +238,6 @@ __global__ void __launch_bounds__(kThreads, kFit)
       auto sum_first = [&] __attribute__((always_inline)) {
         sum(s, team);
         if constexpr (kRing) {
-          if (blockDim.x == 32) __syncwarp();
           if (threadIdx.x == 0 && row + plan.stages < last) fill(row + plan.stages, turn.slot);
           turn.next(plan.stages);
         }

@@ -143,7 +143,6 @@ struct TeamSum {
     } else if constexpr (kValues == 1) {
 #pragma unroll
       for (int o = 16; o; o >>= 1) v[0] += from_lane(v[0], o);
-      if (blockDim.x == 32) return;
       float* r = red[turn][0];
       turn ^= 1;
       if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v[0];
@@ -161,34 +160,25 @@ struct TeamSum {
       float x = (b ? k1 : k0) + from_lane(b ? k0 : k1, 8);
 #pragma unroll
       for (int o = 4; o; o >>= 1) x += from_lane(x, o);
-      if (blockDim.x > 32) {
-        float(*r)[kMaxTeamWarps] = red[turn];
-        turn ^= 1;
-        if ((lane & 7) == 0) r[lane >> 3][threadIdx.x >> 5] = x;
-        __syncthreads();
-        x = r[lane >> 3][lane & 7] + r[lane >> 3][(lane & 7) + 8];
+      float(*r)[kMaxTeamWarps] = red[turn];
+      turn ^= 1;
+      if ((lane & 7) == 0) r[lane >> 3][threadIdx.x >> 5] = x;
+      __syncthreads();
+      x = r[lane >> 3][lane & 7] + r[lane >> 3][(lane & 7) + 8];
 #pragma unroll
-        for (int o = 4; o; o >>= 1) x += from_lane(x, o);
-      }
+      for (int o = 4; o; o >>= 1) x += from_lane(x, o);
 #pragma unroll
       for (int i = 0; i < kValues; ++i) v[i] = __shfl_sync(0xffffffffu, x, 8 * i);
     }
   }
 };
 
-// How rows of a width are laid over teams.
-struct Shape {
-  bool vec;      // 16-byte vectors, else single elements
-  bool block;    // a team is a block
-  int ept;       // elements a thread
-  int team;      // threads
-  int threads;   // of a block
-};
 // 1 / sqrt(x), x > 0: the hardware's estimate and a Newton step, which leaves about a rounding (a square
-// root and a division would be a fifth of a row's instructions).
+// root and a division would be a fifth of a row's instructions).  0 for infinity, whose step would be
+// infinity times 0.
 __device__ __forceinline__ float inverse_root(float x) {
   const float y = rsqrtf(x);
-  return y * fmaf(-0.5f * x * y, y, 1.5f);
+  return x == INFINITY ? 0.f : y * fmaf(-0.5f * x * y, y, 1.5f);
 }
 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }

@@ -175,6 +175,22 @@ def test_a_bad_row_stays_alone():
     assert bool(torch.isnan(got["h"][3]).all()) and bool(torch.isnan(got["h"][7]).all())
 
 
+@pytest.mark.parametrize("form", ["pre", "both"])
+@pytest.mark.parametrize("dim", [130, 1001, 2048])
+def test_an_infinite_rms_scales_a_row_to_nothing(dim, form):
+    """1 / sqrt(infinity) is 0: the other elements of such a row become exact zeros (in x_out: the rest of
+    the sum), the infinity itself times 0 is NaN; so does a row whose squares pass the range of 32 bits."""
+    s, _ = make(6, dim, "f32", 12, form)
+    f = s["x"] if form == "pre" else s["branch"]
+    f[2, 7] = float("inf")
+    f[4] = 1e25
+    got = forward(s, "rms")
+    out, rest = (got["h"], 0 * s["x"]) if form == "pre" else (got["x_out"], RHO * s["x"])
+    others = [c for c in range(dim) if c != 7]
+    assert torch.equal(out[2][others], rest[2][others]) and bool(torch.isnan(out[2, 7]))
+    assert torch.equal(out[4], rest[4])
+
+
 @pytest.mark.parametrize("kind", ["rms", "layer"])
 def test_gradients_against_differences(kind):
     """A loss of fixed random weights on x_out and h, in the kernel's 32 bits: the central difference
