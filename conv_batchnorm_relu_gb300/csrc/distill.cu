@@ -13,10 +13,12 @@
 //   storer     one thread: bulk copies of finished chunks out of the ring;
 //   teachers   two warps, for every other row: some rows ahead the ids and log p of the row's entries,
 //              behind the others its loss.
-// Exponentials are 2^(s c - b), c = log2(e) / T, with b the largest logit's s c, rounded: one fused
-// multiply-add whose product and difference are exact, and b itself, being the same everywhere, drops
-// out of every quotient.  Where the largest is so low that b is not finite (a row masked with the
-// type's lowest value), the difference is taken first: 2^((s - largest) c).
+// Exponentials, c = log2(e) / T.  16-bit logits: 2^((s - largest) c), the difference in 32 bits by an add
+// that takes the 16-bit operand as it is, which needs no instruction to convert it (conversions by shifts
+// and masks kept the integer pipe busiest: 2048 rows of 32000 bf16 took 64.1 us with them, 58.4 without).
+// 32-bit ones: 2^(s c - b), with b the largest logit's s c, rounded: one fused multiply-add whose product
+// and difference are exact, and b itself, being the same everywhere, drops out of every quotient; where
+// the largest is so low that b is not finite (a row masked with the type's lowest value), the difference.
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -160,22 +162,39 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// The logits of 16 bytes, in pairs.
+// A 16-bit logit (the lower or upper half of w) plus m.
+template <typename T, bool kUpper>
+__device__ __forceinline__ float plus(uint32_t w, float m) {
+  float r;
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    if constexpr (kUpper) asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.bf16 %0, h, %2;}" : "=f"(r) : "r"(w), "f"(m));
+    else asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.bf16 %0, l, %2;}" : "=f"(r) : "r"(w), "f"(m));
+  } else {
+    if constexpr (kUpper) asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.f16 %0, h, %2;}" : "=f"(r) : "r"(w), "f"(m));
+    else asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tadd.rn.f32.f16 %0, l, %2;}" : "=f"(r) : "r"(w), "f"(m));
+  }
+  return r;
+}
+
+// The exponentials of the logits of 16 bytes, in pairs.
 template <typename T>
 struct Chunk {
   static constexpr int kPairs = 8 / sizeof(T);
   uint64_t v[kPairs];
-  __device__ __forceinline__ Chunk(uint4 w) {
+  // minus: -b, or (far) minus the largest logit
+  __device__ __forceinline__ Chunk(uint4 w, float minus, float c, bool far) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    if constexpr (sizeof(T) == 4) {
-      v[0] = pair(__uint_as_float(u[0]), __uint_as_float(u[1]));
-      v[1] = pair(__uint_as_float(u[2]), __uint_as_float(u[3]));
-    } else {
+    const uint64_t mm = pair(minus, minus), cc = pair(c, c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<std::is_same_v<T, __nv_bfloat16>>(u[i]);
-        v[i] = pair(f.x, f.y);
+    for (int i = 0; i < kPairs; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        const uint64_t x = pair(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+        v[i] = far ? mul2(add2(x, mm), cc) : fma2(x, cc, mm);
+      } else {
+        v[i] = mul2(pair(plus<T, false>(u[i], minus), plus<T, true>(u[i], minus)), cc);
       }
+      const float2 f = unpair(v[i]);
+      v[i] = pair(ex2<T>(f.x), ex2<T>(f.y));
     }
   }
   __device__ __forceinline__ uint4 packed() const {
@@ -192,35 +211,33 @@ struct Chunk {
       return make_uint4(u[0], u[1], u[2], u[3]);
     }
   }
-  // The exponential of every element: from minus b (kFar: minus the largest logit).
-  template <bool kFar>
-  __device__ __forceinline__ void exponentials(uint64_t minus, uint64_t c) {
-#pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      const float2 f = unpair(kFar ? mul2(add2(v[i], minus), c) : fma2(v[i], c, minus));
-      v[i] = pair(ex2<T>(f.x), ex2<T>(f.y));
-    }
-  }
 };
 
 // The exponent's b (not to be fused with what it meets: it has to be the same everywhere), and whether
-// it is out of range.
+// it is out of range.  16-bit logits have no b: the difference comes with their conversion to 32 bits.
 __device__ __forceinline__ float base_of(float top, float c) { return __fmul_rn(top, c); }
-__device__ __forceinline__ bool is_far(float top, float c) { return !(fabsf(base_of(top, c)) < 1e38f); }
-__device__ __forceinline__ float minus_base(float top, float c) { return is_far(top, c) ? -top : -base_of(top, c); }
+template <typename T>
+__device__ __forceinline__ bool is_far(float top, float c) {
+  return sizeof(T) == 2 || !(fabsf(base_of(top, c)) < 1e38f);
+}
+template <typename T>
+__device__ __forceinline__ float minus_base(float top, float c) {
+  return is_far<T>(top, c) ? -top : -base_of(top, c);
+}
 template <typename T>
 __device__ __forceinline__ float exponential(float s, float top, float c) {
-  return ex2<T>(is_far(top, c) ? (s - top) * c : __fmaf_rn(s, c, -base_of(top, c)));
+  return ex2<T>(is_far<T>(top, c) ? (s - top) * c : __fmaf_rn(s, c, -base_of(top, c)));
 }
 // What a sum relative to `from` is multiplied by to be relative to `to`, the larger.
 template <typename T>
 __device__ __forceinline__ float rebase(float from, float to, float c) {
   if (from == -INFINITY) return 0.f;
-  return ex2<T>(is_far(to, c) ? (from - to) * c : __fsub_rn(base_of(from, c), base_of(to, c)));
+  return ex2<T>(is_far<T>(to, c) ? (from - to) * c : __fsub_rn(base_of(from, c), base_of(to, c)));
 }
 // 2^(top c - b), b's rounding: what a sum relative to the largest logit is multiplied by to be relative to b.
+template <typename T>
 __device__ __forceinline__ float rounding_of_base(float top, float c) {
-  return is_far(top, c) ? 1.f : exp2f(__fmaf_rn(top, c, -base_of(top, c)));
+  return is_far<T>(top, c) ? 1.f : exp2f(__fmaf_rn(top, c, -base_of(top, c)));
 }
 
 // The largest of `n` vectors of logits, NaN if one is.
@@ -544,7 +561,7 @@ __global__ void __maxnreg__(80)
       const float* const sk = sk0 + slot * plan.kp;
       const float top = h.result[slot][0], total = h.result[slot][1], unlisted = h.result[slot][2];
       const bool live = h.result[slot][3] != 0.f;
-      const float to_top = 1.f / rounding_of_base(top, c);
+      const float to_top = 1.f / rounding_of_base<T>(top, c);
       float l = 0.f;
       if (live) {
         const float log_total = logf(total * to_top), q_rest = unlisted / total;
@@ -589,7 +606,6 @@ __global__ void __maxnreg__(80)
   } else {   // ---------------------------------------------------------------- consumers
     const int part = 1 << plan.part, k_n = (int)a.d.topk;
     const float inv_t = 1.f / a.d.temperature, c = inv_t * 1.4426950408889634f;
-    const uint64_t cc = pair(c, c);
     uint16_t* const mine = mine0 + warp * plan.kp;
     Turn t;
     int n = 0, merges = 0;
@@ -735,16 +751,13 @@ __global__ void __maxnreg__(80)
               raise<T>(run, m, c);
               if (run.top != based) {
                 based = run.top;
-                minus = minus_base(run.top, c);
-                far = is_far(run.top, c);
+                minus = minus_base<T>(run.top, c);
+                far = is_far<T>(run.top, c);
               }
-              const uint64_t mm = pair(minus, minus);
               uint64_t e[kCount];
 #pragma unroll
               for (int k = 0; k < kCount; ++k) {
-                Chunk<T> x(w[k]);
-                if (far) x.template exponentials<true>(mm, cc);
-                else x.template exponentials<false>(mm, cc);
+                const Chunk<T> x(w[k], minus, c, far);
                 e[k] = x.v[0];
 #pragma unroll
                 for (int j = 1; j < Chunk<T>::kPairs; ++j) e[k] = add2(e[k], x.v[j]);
@@ -811,7 +824,7 @@ __global__ void __maxnreg__(80)
       float total = r.unlisted + r.listed;
       if (kMode == kGradient) {
         const float* st = a.stats + row * 3;
-        const float from_top = rounding_of_base(st[0], c);
+        const float from_top = rounding_of_base<T>(st[0], c);
         r = Sums{st[0], st[2] * from_top, 0.f};
         total = st[1] * from_top;
         live = live && !(total == 0.f);
@@ -831,9 +844,9 @@ __global__ void __maxnreg__(80)
         const float scale = h.teacher[slot][kWeight] * a.d.temperature * up, all = mass + rest;
         const float coef = scale * (rest != 0.f ? all - rest / q_rest : all) * inv;
         T* const dst = grad_at(row, begin) - s.lead;
-        const bool apart = (reinterpret_cast<uintptr_t>(dst) & 15) != 0, far = is_far(r.top, c);
-        const float minus = minus_base(r.top, c);
-        const uint64_t mm = pair(minus, minus), kk = pair(coef, coef);
+        const bool apart = (reinterpret_cast<uintptr_t>(dst) & 15) != 0, far = is_far<T>(r.top, c);
+        const float minus = minus_base<T>(r.top, c);
+        const uint64_t kk = pair(coef, coef);
         // The teacher's part of an entry's gradient; an id listed twice has the sum at each of its entries.
         auto entry_p = [&](int k) {
           if (kMode == kBoth && !repeated) return expf(lp[k]);
@@ -862,9 +875,7 @@ __global__ void __maxnreg__(80)
           }
           auto turn = [&](uint4 w) {
             if (!live) return make_uint4(0, 0, 0, 0);
-            Chunk<T> x(w);
-            if (far) x.template exponentials<true>(mm, cc);
-            else x.template exponentials<false>(mm, cc);
+            Chunk<T> x(w, minus, c, far);
 #pragma unroll
             for (int k = 0; k < Chunk<T>::kPairs; ++k) x.v[k] = mul2(x.v[k], kk);
             return x.packed();
