@@ -325,18 +325,21 @@ struct Slice {
   __device__ __forceinline__ bool inside(int place) const { return place >= lead && place < lead + n; }
 };
 
-// What the teacher warp reads of a row, a row ahead of its use: the entries of the first kAhead rounds
-// of 32 as they are in memory.
+// What the teacher warp reads of a row, some rows ahead of its use: the entries of the first kAhead rounds
+// of 32 as they are in memory.  Nothing is made of them before, so that all are in flight at once.
 constexpr int kAhead = 4;
 struct Fetched {
   float weight, lse;
-  long long id[kAhead];
+  uint2 id[kAhead];
   uint32_t logit[kAhead];
 };
-__device__ __forceinline__ long long raw_id(const DistillArgs& a, long long row, int k) {
+__device__ __forceinline__ uint2 raw_id(const DistillArgs& a, long long row, int k) {
   const long long i = row * a.d.ids_stride + k;
-  return a.d.id_bytes == 8 ? static_cast<const long long*>(a.top_ids)[i]
-                           : (long long)static_cast<const int*>(a.top_ids)[i];
+  return a.d.id_bytes == 8 ? static_cast<const uint2*>(a.top_ids)[i]
+                           : make_uint2(static_cast<const uint32_t*>(a.top_ids)[i], 0);
+}
+__device__ __forceinline__ long long id_of(const DistillArgs& a, uint2 raw) {
+  return a.d.id_bytes == 8 ? (long long)((unsigned long long)raw.y << 32 | raw.x) : (long long)(int)raw.x;
 }
 __device__ __forceinline__ uint32_t raw_logit(const DistillArgs& a, long long row, int k) {
   const long long i = row * a.d.top_stride + k;
@@ -349,17 +352,31 @@ __device__ __forceinline__ float logit_of(const DistillArgs& a, uint32_t raw) {
   return unpack2<false>(raw).x;
 }
 __device__ __forceinline__ void fetch(const DistillArgs& a, long long row, Fetched& f) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, k_n = (int)a.d.topk;
+  if (a.d.id_bytes == 8) {
+    const uint2* p = static_cast<const uint2*>(a.top_ids) + row * a.d.ids_stride + lane;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (lane + i * 32 < k_n) f.id[i] = p[i * 32];
+  } else {
+    const uint32_t* p = static_cast<const uint32_t*>(a.top_ids) + row * a.d.ids_stride + lane;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (lane + i * 32 < k_n) f.id[i].x = p[i * 32];
+  }
+  if (a.d.top_dtype == CBR_F32) {
+    const uint32_t* p = static_cast<const uint32_t*>(a.top_logits) + row * a.d.top_stride + lane;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (lane + i * 32 < k_n) f.logit[i] = p[i * 32];
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(a.top_logits) + row * a.d.top_stride + lane;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (lane + i * 32 < k_n) f.logit[i] = p[i * 32];
+  }
   f.weight = a.row_weight ? a.row_weight[row] : 1.f;
   f.lse = a.teacher_lse ? a.teacher_lse[row] : 0.f;
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    const int k = lane + i * 32;
-    if (k < (int)a.d.topk) {
-      f.id[i] = raw_id(a, row, k);
-      f.logit[i] = raw_logit(a, row, k);
-    }
-  }
 }
 
 // The teacher's distribution of a row, by one warp: `begun` is called once the ids and the row's state
@@ -370,7 +387,8 @@ __device__ void teach(const DistillArgs& a, long long row, const Fetched& f, flo
   const int lane = threadIdx.x & 31, k_n = (int)a.d.topk;
   float top = -INFINITY;
   bool any = false;
-  auto put = [&](int k, long long raw, uint32_t logit) {
+  auto put = [&](int k, uint2 raw_id, uint32_t logit) {
+    const long long raw = id_of(a, raw_id);
     const int id = raw >= 0 && raw < a.d.vocab ? (int)raw : kAbsent;
     const float x = id < 0 ? -INFINITY : logit_of(a, logit) * inv_t;
     ids[k] = id;
