@@ -60,13 +60,13 @@ struct Plan {
 struct Header {
   // chunk by chunk: copied in; worked through; copied out
   uint64_t full[kMaxBuffers], done[kMaxBuffers], free[kMaxBuffers];
-  // row by row: teacher's entries; its probabilities; no longer needed; row's sums; the consumers'
-  // own sums; the cluster's sums
+  // row by row: teacher's entries; its probabilities (kGradient: and the row's sums); no longer needed;
+  // row's sums; the consumers' own sums; the cluster's sums
   uint64_t t_full[kRows], m_full[kRows], t_free[kRows], r_full[kRows], c_full[2], x_full;
   float red[2][kMaxWarps][4];       // (largest, unlisted, listed) of each consumer
   float xch[kMaxCluster][4];        // and of each block of the cluster
   float teacher[kRows][4];          // mass, rest, weight, state
-  float result[kRows][4];           // of the row: largest, total, unlisted; live
+  float result[kRows][4];           // of the row: largest, total, unlisted; live (kGradient: dloss)
 };
 enum { kMass, kRest, kWeight, kState };
 enum { kDead, kEmpty, kLive };    // weight 0 (not even loaded), nothing to learn from, the rest
@@ -329,7 +329,7 @@ struct Slice {
 // of 32 as they are in memory.  Nothing is made of them before, so that all are in flight at once.
 constexpr int kAhead = 4;
 struct Fetched {
-  float weight, lse;
+  float weight, lse, stats[3], up;   // the last two: of kGradient
   uint2 id[kAhead];
   uint32_t logit[kAhead];
 };
@@ -351,6 +351,7 @@ __device__ __forceinline__ float logit_of(const DistillArgs& a, uint32_t raw) {
   if (a.d.top_dtype == CBR_BF16) return __uint_as_float(raw << 16);
   return unpack2<false>(raw).x;
 }
+template <int kMode>
 __device__ __forceinline__ void fetch(const DistillArgs& a, long long row, Fetched& f) {
   const int lane = threadIdx.x & 31, k_n = (int)a.d.topk;
   if (a.d.id_bytes == 8) {
@@ -377,6 +378,11 @@ __device__ __forceinline__ void fetch(const DistillArgs& a, long long row, Fetch
   }
   f.weight = a.row_weight ? a.row_weight[row] : 1.f;
   f.lse = a.teacher_lse ? a.teacher_lse[row] : 0.f;
+  if constexpr (kMode == kGradient) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) f.stats[i] = a.stats[row * 3 + i];
+    f.up = a.dloss ? a.dloss[row] : 1.f;
+  }
 }
 
 // The teacher's distribution of a row, by one warp: `begun` is called once the ids and the row's state
@@ -571,9 +577,10 @@ __global__ void __maxnreg__(80)
     const float inv_t = 1.f / a.d.temperature, c = inv_t * 1.4426950408889634f;
     // The loss of the block's n-th row, once its sums are there.
     auto settle = [&](long long row, int n) {
+      if (!kAcross) return true;
       const int slot = n % kRows;
       if (!__all_sync(0xffffffffu, mbar_wait(bar(&h.r_full[slot]), n / kRows & 1))) return ok = false;
-      if (!kAcross || rank) return true;
+      if (rank) return true;
       const int* const ids = ids0 + slot * plan.kp;
       const float* const lp = lp0 + slot * plan.kp;
       const float* const sk = sk0 + slot * plan.kp;
@@ -604,11 +611,11 @@ __global__ void __maxnreg__(80)
     const int start = warp - plan.warps - 2;
     int n = start;   // of the block's rows
     Fetched next;
-    if (first + n * step < items) fetch(a, row_of(first + n * step), next);
+    if (first + n * step < items) fetch<kMode>(a, row_of(first + n * step), next);
     for (long long i = first + n * step; ok && i < items; i += kTeachers * step, n += kTeachers) {
       const int slot = n % kRows;
       const Fetched now = next;
-      if (i + kTeachers * step < items) fetch(a, row_of(i + kTeachers * step), next);
+      if (i + kTeachers * step < items) fetch<kMode>(a, row_of(i + kTeachers * step), next);
       if (n >= kRows) {
         if (!settle(row_of(i - kRows * step), n - kRows)) break;
         ok = __all_sync(0xffffffffu, mbar_wait(bar(&h.t_free[slot]), (n / kRows & 1) ^ 1));
@@ -617,6 +624,13 @@ __global__ void __maxnreg__(80)
       teach(a, row_of(i), now, inv_t, ids0 + slot * plan.kp, lp0 + slot * plan.kp, h.teacher[slot], [&] {
         if (lane == 0) mbar_arrive(bar(&h.t_full[slot]));
       });
+      if (kMode == kGradient && lane == 0) {
+        const float from_top = rounding_of_base<T>(now.stats[0], c);
+        h.result[slot][0] = now.stats[0];
+        h.result[slot][1] = now.stats[1] * from_top;
+        h.result[slot][2] = now.stats[2] * from_top;
+        h.result[slot][3] = now.up;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(&h.m_full[slot]));
     }
@@ -840,15 +854,7 @@ __global__ void __maxnreg__(80)
         live = live && r.top != -INFINITY;
       }
       float total = r.unlisted + r.listed;
-      if (kMode == kGradient) {
-        const float* st = a.stats + row * 3;
-        const float from_top = rounding_of_base<T>(st[0], c);
-        r = Sums{st[0], st[2] * from_top, 0.f};
-        total = st[1] * from_top;
-        live = live && !(total == 0.f);
-        if (a.dloss) up = a.dloss[row];
-      }
-      if (threadIdx.x == 0) {
+      if (kAcross && threadIdx.x == 0) {
         h.result[slot][0] = r.top;
         h.result[slot][1] = total;
         h.result[slot][2] = r.unlisted;
@@ -857,6 +863,18 @@ __global__ void __maxnreg__(80)
       }
       if constexpr (kMode != kLoss) {
         if (!(ok = wait(bar(&h.m_full[slot]), n / kRows & 1))) break;
+        if (!kAcross) {
+          r = Sums{h.result[slot][0], h.result[slot][2], 0.f};
+          total = h.result[slot][1];
+          live = live && !(total == 0.f);
+          up = h.result[slot][3];
+          // an id listed twice, where the lanes hold all of the entries
+          repeated = count > 32;
+          if (live && !repeated) {
+            const uint32_t same = __match_any_sync(0xffffffffu, k0 >= 0 ? place0 : -1 - lane);
+            repeated = __any_sync(0xffffffffu, (same & (same - 1)) != 0);
+          }
+        }
         const float inv = 1.f / total, q_rest = r.unlisted * inv, mass = h.teacher[slot][kMass];
         const float rest = q_rest == 0.f ? 0.f : h.teacher[slot][kRest];
         const float scale = h.teacher[slot][kWeight] * a.d.temperature * up, all = mass + rest;
@@ -867,7 +885,7 @@ __global__ void __maxnreg__(80)
         const uint64_t kk = pair(coef, coef);
         // The teacher's part of an entry's gradient; an id listed twice has the sum at each of its entries.
         auto entry_p = [&](int k) {
-          if (kMode == kBoth && !repeated) return expf(lp[k]);
+          if (!repeated) return expf(lp[k]);
           float pk = 0.f;
           for (int m = 0; m < count; ++m)
             if (ids[mine[m]] == ids[k]) pk += expf(lp[mine[m]]);
