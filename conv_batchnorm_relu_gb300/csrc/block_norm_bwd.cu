@@ -2,11 +2,12 @@
 //
 // One pass: a team of threads holds a row of x_out, dh, dx_out and the branch in registers, up to the
 // stores of dx and dbranch, with coming rows' loads in flight meanwhile: a ring of rows in shared memory,
-// filled by bulk copies, where a block is a team and the rows are aligned; else the next row, in registers.
-// The parameters
-// of its columns and their gradients stay in registers over its rows; gate and post_weight are constant
-// over a gate's rows, so both take their gradients from one sum, of D e.  Blocks leave their sums in the
-// workspace, and a second kernel adds them in a fixed order.  Bound by HBM: six rows of the storage type.
+// filled by bulk copies, where a block is a team and the rows are aligned and of 16-bit elements; else the
+// next row, in registers.  The parameters of its columns and their gradients stay in registers over its
+// rows; gate and post_weight are constant over a gate's rows, so both take their gradients from one sum,
+// of D e.  Blocks leave their sums in the workspace, and a second kernel adds them in a fixed order.
+// Bound by HBM, six rows of the storage type: 32768x4096 bf16 in 265 us, 6.1 TB/s; narrow and unaligned
+// rows by their instructions (50176x64 f16: 16 us, 2.4 TB/s).
 //
 // The second norm's means enter the first's linearly.  For RMS, with p = branch_scale gate post_weight
 // and q = dx_out + r2 u: D = q - r2 mean(u c) c, so
@@ -401,8 +402,10 @@ int launch_kind(const BlockNormArgs& a, int team, int threads, int num_sms, cuda
   const long long most = (long long)std::min(fit, blocks_per_sm(a.d.dim)) * num_sms;
   const int teams = kBlock ? 1 : threads / team;
   p.team = team;
-  // Few rows a gate (a stretch would not give each team of a block a few rows): teams with runs of gates.
-  p.shared = !kBlock && a.gate && a.d.gate_rows >= 4 * teams;
+  // Few rows a gate: teams with runs of gates; 32, or as many as a block has teams: the block shares each.
+  // us, 50176x64 f16 with 8, 16, 32, 64 rows a gate: runs 18, 23, 39, 70 (fewer and fewer teams have one),
+  // shared 81, 48, 32, 26 (the teams' sums are added up once a gate).
+  p.shared = !kBlock && a.gate && a.d.gate_rows >= std::max(32, teams);
   if (p.shared) {
     p.blocks = (int)std::min<long long>(most, (a.d.rows + teams - 1) / teams);
     p.run = (a.d.rows + p.blocks - 1) / p.blocks;
@@ -431,25 +434,29 @@ int launch(const BlockNormArgs& a, int team, int threads, int num_sms, cudaStrea
              : launch_kind<T, kVec, kEpt, kBlock, kRing, false, kThreads, kFit>(a, team, threads, num_sms, st);
 }
 
+// us, what is taken first.  Narrow rows: teams of a warp or less in blocks of 128 threads at three an SM,
+// 168 registers each (50176x64 f16 16.2); 256 at two have 128 and spill (18.5); a block for each row: 57.
+// Wide rows: eight elements a thread, 16-bit rows through the ring (32768x4096 bf16 265, 8192x1024 31),
+// since without it too little is in flight (648, 45); 32-bit ones in registers, where the next row's four
+// parts are as much as the ring holds (8192x4096 135, with the ring 146).  16 elements a thread spill
+// (32768x4096: 791) and are left to rows that 512 threads cannot hold otherwise.  Rows of single 16-bit
+// elements: four a thread, for more threads on an SM (16384x1001 bf16 62, eight: 102); 32-bit ones keep
+// eight (73, four: 80).
 template <typename T, int kVec>
 int pick(const BlockNormArgs& a, int num_sms, cudaStream_t st) {
   const int dim = (int)a.d.dim;
-  if (dim <= 256) {   // eight elements a thread, a warp or less
+  auto threads_of = [&](int ept) { return ((dim + ept - 1) / ept + 31) / 32 * 32; };
+  if (dim <= 256) {
     int team = 1;
     while (team * 8 < dim) team *= 2;
-    return launch<T, kVec, 8, false, false, 256, 2>(a, team, 256, num_sms, st);
+    return launch<T, kVec, 8, false, false, 128, 3>(a, team, 128, num_sms, st);
   }
-  const int ept = dim <= 4096 ? 8 : dim <= 8192 ? 16 : 32;
-  const int threads = ((dim + ept - 1) / ept + 31) / 32 * 32;
-  if constexpr (kVec > 1) {
-    if (ept == 8) return launch<T, kVec, 8, true, true, 512, 1>(a, threads, threads, num_sms, st);
-    // the ring has to hold two rows
-    if (ept == 16 && sizeof(T) == 2) return launch<T, kVec, 16, true, true, 512, 1>(a, threads, threads, num_sms, st);
-  } else {
-    if (ept == 8) return launch<T, kVec, 8, true, false, 512, 1>(a, threads, threads, num_sms, st);
-  }
-  if (ept == 16) return launch<T, kVec, 16, true, false, 512, 1>(a, threads, threads, num_sms, st);
-  return launch<T, kVec, 32, true, false, 512, 1>(a, threads, threads, num_sms, st);
+  if constexpr (kVec == 1 && sizeof(T) == 2)
+    if (dim <= 2048) return launch<T, kVec, 4, true, false, 512, 1>(a, threads_of(4), threads_of(4), num_sms, st);
+  constexpr bool kRing = kVec > 1 && sizeof(T) == 2;
+  if (dim <= 4096) return launch<T, kVec, 8, true, kRing, 512, 1>(a, threads_of(8), threads_of(8), num_sms, st);
+  if (dim <= 8192) return launch<T, kVec, 16, true, kRing, 512, 1>(a, threads_of(16), threads_of(16), num_sms, st);
+  return launch<T, kVec, 32, true, false, 512, 1>(a, threads_of(32), threads_of(32), num_sms, st);
 }
 
 template <typename T>

@@ -19,6 +19,9 @@
 // 32-bit ones: 2^(s c - b), with b the largest logit's s c, rounded: one fused multiply-add whose product
 // and difference are exact, and b itself, being the same everywhere, drops out of every quotient; where
 // the largest is so low that b is not finite (a row masked with the type's lowest value), the difference.
+// Measured: 4096x131072 bf16 363 us, bound by data movement (with the second pass's reload from L2; the
+// kernel without its arithmetic takes as long); 2048x32000 55 us, of which a steady state at 86% of the
+// copy rate, 5 us until the first chunks are there, and the last round of rows, which not every block has.
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -39,10 +42,10 @@ enum Mode { kLoss, kBoth, kGradient };
 constexpr int kMaxWarps = 16;       // consumers
 constexpr int kMaxBuffers = 16;
 constexpr int kMaxCluster = 8;
-constexpr int kFewRows = 4;         // rows of a call whose rows are each shared by a cluster
+constexpr int kFewRows = 4;         // rows of a call whose rows are each shared by a cluster (make_plan)
 constexpr int kRows = 4;            // whose entries are held at once; a multiple of kTeachers
-constexpr int kBatch = 4;           // 16-byte vectors that a consumer has in hand at once
-constexpr int kTeachers = 2;        // warps, for a row each in turn
+constexpr int kBatch = 4;           // 16-byte vectors that a consumer has in hand at once (2: 57 us for 55)
+constexpr int kTeachers = 2;        // warps, for a row each in turn (one: 56 us for 55)
 constexpr int kOthers = 2 + kTeachers;  // warps that are not consumers
 constexpr int kAbsent = -(1 << 30); // the id of an absent entry
 
@@ -974,7 +977,8 @@ Plan make_plan(const DistillArgs& a, int elt) {
   const long long v = a.d.vocab;
   // A block for each row.  In calls of a few rows a cluster shares each, while a slice keeps 2 KB; its
   // sums are added in another order, so the rule goes by the rows alone and its bound is low: other calls
-  // give a row the same result whatever rows are beside it.
+  // give a row the same result whatever rows are beside it.  One or four rows of 131072 bf16: 8.1 us, a
+  // block each 19.8; of 32000: 7.5, 8.5.
   p.slices = 1;
   if (a.d.rows <= kFewRows)
     while (p.slices < kMaxCluster && v * elt / (2 * p.slices) >= 2048) p.slices *= 2;
@@ -982,7 +986,8 @@ Plan make_plan(const DistillArgs& a, int elt) {
   const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.d.logits_stride * elt % 16 == 0;
   p.ragged = !aligned || v * elt % 16 != 0;
   const int vectors = (int)(std::min<long long>(p.width, v) * elt + 15) / 16 + !aligned;
-  // Chunks of 32 KB for eight warps, two batches of vectors for each lane; smaller where the row is.
+  // Chunks of 32 KB for eight warps, two batches of vectors for each lane (2048x32000 bf16: 55 us; of 16
+  // KB, one batch between waits: 64); smaller where the row is.
   p.part = 8;
   p.warps = 8;
   while (p.warps > 1 && (p.warps << p.part) / 2 >= vectors) p.warps /= 2;
@@ -990,7 +995,8 @@ Plan make_plan(const DistillArgs& a, int elt) {
   const int chunk = p.warps << p.part << 4;
   p.kp = (int)((a.d.topk + 31) / 32 * 32);
   const int fixed = (int)((sizeof(Header) + 15) / 16 * 16 + (size_t)p.kp * (kRows * 12 + p.warps * 2) + 127) / 128 * 128;
-  // Two blocks an SM: while one waits for loads or for its sums, the other computes.
+  // Two blocks an SM: while one waits for loads or for its sums, the other computes (55 us; one block with
+  // twice the ring: 78).
   p.buffers = std::max(2, std::min((113 * 1024 - fixed) / chunk, kMaxBuffers));
   p.smem = fixed + p.buffers * chunk;
   return p;

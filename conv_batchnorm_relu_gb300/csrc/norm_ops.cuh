@@ -19,7 +19,8 @@ using namespace tok;
 template <typename T, int kVec, int kEpt>
 struct Row {
   static constexpr int kSteps = kEpt / kVec;
-  using Raw = std::conditional_t<kVec == 1, T, uint4>;
+  // single elements: a register each (16-bit ones in pairs would be packed, and waited for, at once)
+  using Raw = std::conditional_t<kVec == 1, uint32_t, uint4>;
   Raw raw[kSteps];
 
   static __device__ __forceinline__ int column(int step, int team) { return step * team * kVec; }
@@ -31,7 +32,11 @@ struct Row {
     for (int j = 0; j < kSteps; ++j) {
       const int c = column(j, team);
       if constexpr (kVec == 1) {
-        raw[j] = c < left ? p[c] : from_f<T>(0.f);
+        raw[j] = 0;
+        if (c < left) {
+          if constexpr (sizeof(T) == 4) asm volatile("ld.global.b32 %0, [%1];" : "=r"(raw[j]) : "l"(p + c));
+          else asm volatile("ld.global.u16 %0, [%1];" : "=r"(raw[j]) : "l"(p + c));
+        }
       } else {
         raw[j] = make_uint4(0, 0, 0, 0);
         if (c < left)
@@ -55,7 +60,9 @@ struct Row {
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) {
       if constexpr (kVec == 1) {
-        v[j] = to_f(raw[j]);
+        if constexpr (sizeof(T) == 4) v[j] = __uint_as_float(raw[j]);
+        else if constexpr (std::is_same_v<T, __nv_bfloat16>) v[j] = __uint_as_float(raw[j] << 16);
+        else v[j] = unpack2<false>(raw[j]).x;
       } else if constexpr (sizeof(T) == 4) {
         v[4 * j] = __uint_as_float(raw[j].x), v[4 * j + 1] = __uint_as_float(raw[j].y);
         v[4 * j + 2] = __uint_as_float(raw[j].z), v[4 * j + 3] = __uint_as_float(raw[j].w);

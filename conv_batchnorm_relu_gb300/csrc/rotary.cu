@@ -1,10 +1,12 @@
 // Rotary positions over several axes (formulas: include/cbr.h).
 //
 // A block takes a few consecutive tokens: the cosines and sines of their pairs once, into shared memory,
-// then the heads of q and k, a 16-byte vector (and, with pairs in halves, its partner) a thread and step;
+// then the heads of q and k, a 16-byte vector (and, with pairs in halves, its partner) a thread and step.
 // The angle is a product modulo 2^64 of the position and the frequency in turns, so it is reduced to one
 // turn without rounding; its top 32 bits, as a signed fraction of half a turn, go to sincospif.  Bound by
-// HBM: each element of q and k read and written once.
+// HBM, each element of q and k read and written once: 65536 tokens of 40 heads of 128 bf16 in 197 us, 6.8
+// TB/s; calls that fit in L2 by the index arithmetic of each vector (12544 tokens of 24 heads of 80 f16: 21
+// us, 4.6 TB/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -174,7 +176,8 @@ int launch(const RotaryArgs& a, int num_sms, cudaStream_t st) {
   p.heads = d.heads_q + d.heads_k;
   const long long per_token = (long long)p.heads * p.items;
   // About four items a thread, so that the table is a small part of a block's work, while there are
-  // blocks for every SM; at most 16 KB of table.
+  // blocks for every SM (us, the two calls above: 197 and 21; one item 197 and 23, eight 201 and 22; blocks
+  // of 256 threads 198 and 21); at most 16 KB of table.
   const long long all = d.batch * d.tokens;
   long long want = std::max(1ll, 4ll * kThreads / per_token);
   want = std::min(want, std::max(1ll, all / (4ll * num_sms)));
