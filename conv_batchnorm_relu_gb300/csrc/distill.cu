@@ -18,7 +18,8 @@
 // and masks kept the integer pipe busiest: 2048 rows of 32000 bf16 took 64.1 us with them, 58.4 without).
 // 32-bit ones: 2^(s c - b), with b the largest logit's s c, rounded: one fused multiply-add whose product
 // and difference are exact, and b itself, being the same everywhere, drops out of every quotient; where
-// the largest is so low that b is not finite (a row masked with the type's lowest value), the difference.
+// b is so large that its rounding would count (a row masked with -1e9 or the type's lowest value), the
+// difference as for 16-bit logits.
 // Measured: 4096x131072 bf16 363 us, bound by data movement (with the second pass's reload from L2; the
 // kernel without its arithmetic takes as long); 2048x32000 55 us, of which a steady state at 86% of the
 // copy rate, 5 us until the first chunks are there, and the last round of rows, which not every block has.
@@ -217,11 +218,14 @@ struct Chunk {
 };
 
 // The exponent's b (not to be fused with what it meets: it has to be the same everywhere), and whether
-// it is out of range.  16-bit logits have no b: the difference comes with their conversion to 32 bits.
+// exponentials are relative to the logit itself instead: where b's rounding may pass 2^-3, so that sums
+// relative to b stay within a tenth of those relative to the logit, and always for 16-bit logits, whose
+// difference comes with their conversion to 32 bits.
+constexpr float kFar = 4194304.f;   // 2^22
 __device__ __forceinline__ float base_of(float top, float c) { return __fmul_rn(top, c); }
 template <typename T>
 __device__ __forceinline__ bool is_far(float top, float c) {
-  return sizeof(T) == 2 || !(fabsf(base_of(top, c)) < 1e38f);
+  return sizeof(T) == 2 || !(fabsf(base_of(top, c)) < kFar);
 }
 template <typename T>
 __device__ __forceinline__ float minus_base(float top, float c) {
@@ -231,11 +235,14 @@ template <typename T>
 __device__ __forceinline__ float exponential(float s, float top, float c) {
   return ex2<T>(is_far<T>(top, c) ? (s - top) * c : __fmaf_rn(s, c, -base_of(top, c)));
 }
-// What a sum relative to `from` is multiplied by to be relative to `to`, the larger.
+// What a sum relative to `from` is multiplied by to be relative to `to`, the larger: either may be far.
 template <typename T>
 __device__ __forceinline__ float rebase(float from, float to, float c) {
   if (from == -INFINITY) return 0.f;
-  return ex2<T>(is_far<T>(to, c) ? (from - to) * c : __fsub_rn(base_of(from, c), base_of(to, c)));
+  float x;
+  if (is_far<T>(to, c)) x = is_far<T>(from, c) ? (from - to) * c : -__fmaf_rn(to, c, -base_of(from, c));
+  else x = is_far<T>(from, c) ? __fmaf_rn(from, c, -base_of(to, c)) : __fsub_rn(base_of(from, c), base_of(to, c));
+  return ex2<T>(x);
 }
 // 2^(top c - b), b's rounding: what a sum relative to the largest logit is multiplied by to be relative to b.
 template <typename T>
