@@ -396,7 +396,10 @@ __device__ __forceinline__ void fetch(const DistillArgs& a, long long row, Fetch
 }
 
 // The teacher's distribution of a row, by one warp: `begun` is called once the ids and the row's state
-// are there, which is all that the first pass needs.
+// are there, which is all that the first pass needs.  Without a log-sum-exp, log p is of differences from the
+// largest logit, before 1 / T, so its roundings go by how far the entries are from one another, not by how
+// large they are (a common offset of 300 at T = 2 cost 6e-6 of the loss when it went through t / T).  With one,
+// t / T carries its rounding along: the difference is good to its own.
 template <typename F>
 __device__ void teach(const DistillArgs& a, long long row, const Fetched& f, float inv_t, int* ids, float* lp, float* out,
                       F begun) {
@@ -406,7 +409,7 @@ __device__ void teach(const DistillArgs& a, long long row, const Fetched& f, flo
   auto put = [&](int k, uint2 raw_id, uint32_t logit) {
     const long long raw = id_of(a, raw_id);
     const int id = raw >= 0 && raw < a.d.vocab ? (int)raw : kAbsent;
-    const float x = id < 0 ? -INFINITY : logit_of(a, logit) * inv_t;
+    const float x = id < 0 ? -INFINITY : logit_of(a, logit);
     ids[k] = id;
     lp[k] = x;
     top = Max::of(top, x);
@@ -425,20 +428,28 @@ __device__ void teach(const DistillArgs& a, long long row, const Fetched& f, flo
   }
   __syncwarp();
   begun();
-  float norm = f.lse, mass = 0.f;
+  float mass = 1.f;
   if (!a.teacher_lse) {
     float s = 0.f;
-    for (int k = lane; k < k_n; k += 32) s += expf(lp[k] - top);   // 0 for an absent entry
-    norm = top + logf(warp_reduce<Sum>(s));
+    for (int k = lane; k < k_n; k += 32) {
+      const float l = (lp[k] - top) * inv_t;
+      lp[k] = l;
+      s += expf(l);   // 0 for an absent entry
+    }
+    const float norm = logf(warp_reduce<Sum>(s));
+    for (int k = lane; k < k_n; k += 32) lp[k] -= norm;
+  } else {
+    mass = 0.f;
+    for (int k = lane; k < k_n; k += 32) {
+      const float t = lp[k], x = t * inv_t, low = __fmaf_rn(-x, a.d.temperature, t) * inv_t;
+      const float l = (x - f.lse) + (fabsf(x) < INFINITY ? low : 0.f);   // an infinity leaves no remainder
+      lp[k] = l;
+      mass += expf(l);
+    }
+    mass = warp_reduce<Sum>(mass);
   }
-  for (int k = lane; k < k_n; k += 32) {
-    const float l = lp[k] - norm;
-    lp[k] = l;
-    if (a.teacher_lse) mass += expf(l);
-  }
-  if (a.teacher_lse) mass = warp_reduce<Sum>(mass);
   if (lane == 0) {
-    out[kMass] = a.teacher_lse ? mass : 1.f;
+    out[kMass] = mass;
     out[kRest] = a.teacher_lse ? fmaxf(0.f, 1.f - mass) : 0.f;
   }
 }
