@@ -59,6 +59,7 @@ struct Plan {
   int kp;           // room for entries
   int smem;
   bool ragged;      // a row may start or end inside a 16-byte vector
+  float c, c_low;   // log2(e) / T, and what its rounding left: that grows with the distance from the largest logit
 };
 
 struct Header {
@@ -67,10 +68,10 @@ struct Header {
   // row by row: teacher's entries; its probabilities (kGradient: and the row's sums); no longer needed;
   // row's sums; the consumers' own sums; the cluster's sums
   uint64_t t_full[kRows], m_full[kRows], t_free[kRows], r_full[kRows], c_full[2], x_full;
-  float red[2][kMaxWarps][4];       // (largest, unlisted, listed) of each consumer
+  float red[2][kMaxWarps][4];       // (largest and sum, unlisted and listed) of each consumer
   float xch[kMaxCluster][4];        // and of each block of the cluster
   float teacher[kRows][4];          // mass, rest, weight, state
-  float result[kRows][4];           // of the row: largest, total, unlisted; live (kGradient: dloss)
+  float result[kRows][4];           // of the row: largest, total, unlisted (as `share` has it); live (kGradient: dloss)
 };
 enum { kMass, kRest, kWeight, kState };
 enum { kDead, kEmpty, kLive };    // weight 0 (not even loaded), nothing to learn from, the rest
@@ -129,8 +130,9 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
                : "memory");
 }
 
-// 2^x.  With 16-bit logits results below 2^-126 are taken as 0 (below what f16 and the sums can
-// show; a bf16 gradient under 2^-126 becomes 0).  32-bit gradients keep their subnormal range.
+// 2^x.  With 16-bit logits results below 2^-126 are taken as 0: too little for a sum of exponentials
+// relative to its own largest, and a bf16 gradient that small, before its scale, becomes 0.  32-bit
+// gradients keep their subnormal range.
 template <typename T>
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -244,6 +246,11 @@ __device__ __forceinline__ float rebase(float from, float to, float c) {
   else x = is_far<T>(from, c) ? __fmaf_rn(from, c, -base_of(to, c)) : __fsub_rn(base_of(from, c), base_of(to, c));
   return ex2<T>(x);
 }
+// The logarithm to base 2 of what a sum relative to `from` is multiplied by to be relative to the logit `to`.
+template <typename T>
+__device__ __forceinline__ float exponent(float from, float to, float c) {
+  return is_far<T>(from, c) ? (from - to) * c : -__fmaf_rn(to, c, -base_of(from, c));
+}
 // 2^(top c - b), b's rounding: what a sum relative to the largest logit is multiplied by to be relative to b.
 template <typename T>
 __device__ __forceinline__ float rounding_of_base(float top, float c) {
@@ -277,10 +284,9 @@ __device__ __forceinline__ float largest(const uint4 (&w)[n]) {
   }
 }
 
-// A running (largest, sum of exponentials relative to it) pair, the sum in three parts: two of unlisted
-// words, one of listed.
+// A running (largest, sum of exponentials relative to it) of the unlisted words, the sum in two parts.
 struct Running {
-  float top = -INFINITY, listed = 0.f;
+  float top = -INFINITY;
   uint64_t sum = 0;
 };
 template <typename T>
@@ -288,28 +294,69 @@ __device__ __forceinline__ void raise(Running& r, float m, float c) {
   if (!(m <= r.top)) {   // NaN gets in, too, and stays
     m = Max::of(m, r.top);
     const float f = rebase<T>(r.top, m, c);
-    r.listed *= f;
     r.sum = m == m ? mul2(r.sum, pair(f, f)) : pair(m, m);
     r.top = m;
   }
 }
-// The same, merged over threads.
+// (largest, sum) of the unlisted words and of the listed ones, each sum relative to its own largest: the
+// unlisted mass has a logarithm even where it is nothing beside the listed one.
 struct Sums {
-  float top = -INFINITY, unlisted = 0.f, listed = 0.f;
+  float top = -INFINITY, unlisted = 0.f;
+  float top_listed = -INFINITY, listed = 0.f;
 };
-// The lanes' pairs as one.
+// The lanes' sums as one.
 template <typename T>
 __device__ __forceinline__ Sums merge_warp(Sums r, float c) {
-  const float m = warp_max(r.top);
-  const float f = rebase<T>(r.top, m, c);
-  uint64_t s = pair(r.unlisted * f, r.listed * f);
+  const float m = warp_max(r.top), n = warp_max(r.top_listed);
+  uint64_t s = pair(r.unlisted * rebase<T>(r.top, m, c), r.listed * rebase<T>(r.top_listed, n, c));
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     const float2 v = unpair(s);
     s = add2(s, pair(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
   }
   const float2 v = unpair(s);
-  return Sums{m, v.x, v.y};
+  return Sums{m, v.x, n, v.y};
+}
+
+// `rebase`, with the roundings of the exponent, which grow with the distance, put right: a row's unlisted
+// share is a result.
+template <typename T>
+__device__ __forceinline__ float rebase_far_down(float from, float to, float c, float c_low) {
+  const float f = rebase<T>(from, to, c);
+  if (is_far<T>(from, c) != is_far<T>(to, c)) return f;
+  const bool far = is_far<T>(to, c);
+  const float x = far ? from : base_of(from, c), y = far ? to : base_of(to, c);
+  const float d = __fsub_rn(x, y), z = __fsub_rn(d, x);
+  const float low = __fsub_rn(__fsub_rn(x, __fsub_rn(d, z)), __fadd_rn(y, z));   // d + low = x - y
+  const float r = far ? __fmaf_rn(d, c, -__fmul_rn(d, c)) + __fmaf_rn(d, c_low, low * c) : __fmaf_rn(from - to, c_low, low);
+  return f * (1.f + (fabsf(r) < 1.f ? r * 0.69314718f : 0.f));
+}
+// The unlisted words' part of a row's sum, relative to the row's largest logit `top`: as it is, or, where it
+// is below 2^-64 and a tail needs it, its logarithm to base 2 (negative), 0 below 2^-1074.  Words masked
+// with the type's lowest value are below that as are those at -infinity, and their row has no tail.
+constexpr float kFaint = 0x1p-64f, kLeast = -1074.f;
+template <typename T>
+__device__ __forceinline__ float share(const Sums& r, float top, float c, float c_low, bool tail) {
+  const float u = r.unlisted * rebase_far_down<T>(r.top, top, c, c_low);
+  if (!tail || u >= kFaint) return u;
+  const float l = log2f(r.unlisted) + exponent<T>(r.top, top, c);
+  return l < kLeast ? 0.f : l;
+}
+// What the gradients of unlisted words are made with where their share is small: exponentials relative to
+// `base`, near the largest of them, whose sum `sum` is near 1, and from there to the row's largest logit, `down`.
+// Factors of their exponentials relative to the row's largest would pass the range of 32 bits.
+constexpr float kSmall = 0x1p-20f;
+struct Base {
+  float base, sum, down;
+};
+template <typename T>
+__device__ __forceinline__ Base base_of_share(float share, float top, float c, float temperature) {
+  Base b;
+  const float l = share < 0.f ? share : log2f(share);
+  b.base = __fmaf_rn(l, temperature * 0.69314718f, top);
+  b.down = rebase<T>(b.base, top, c);
+  b.sum = share < 0.f ? exp2f(l - exponent<T>(b.base, top, c)) : share / b.down;
+  return b;
 }
 
 // Where a slice's elements lie in its chunks: element j at place lead + j, so that global and shared
@@ -595,7 +642,7 @@ __global__ void __maxnreg__(80)
       bulk_wait_group<0>();
     }
   } else if (warp >= plan.warps + 2) {   // ------------------------------------ teachers
-    const float inv_t = 1.f / a.d.temperature, c = inv_t * 1.4426950408889634f;
+    const float inv_t = 1.f / a.d.temperature, c = plan.c;
     // The loss of the block's n-th row, once its sums are there.
     auto settle = [&](long long row, int n) {
       if (!kAcross) return true;
@@ -605,26 +652,26 @@ __global__ void __maxnreg__(80)
       const int* const ids = ids0 + slot * plan.kp;
       const float* const lp = lp0 + slot * plan.kp;
       const float* const sk = sk0 + slot * plan.kp;
-      const float top = h.result[slot][0], total = h.result[slot][1], unlisted = h.result[slot][2];
+      const float top = h.result[slot][0], total = h.result[slot][1], part = h.result[slot][2];
       const bool live = h.result[slot][3] != 0.f;
       const float to_top = 1.f / rounding_of_base<T>(top, c);
       float l = 0.f;
       if (live) {
-        const float log_total = logf(total * to_top), q_rest = unlisted / total;
-        const float rest = q_rest == 0.f ? 0.f : h.teacher[slot][kRest];
+        const float log_total = logf(total * to_top);
+        const float rest = part == 0.f ? 0.f : h.teacher[slot][kRest];
         for (int k = lane; k < (int)a.d.topk; k += 32) {
           const float p = ids[k] >= 0 ? expf(lp[k]) : 0.f;
           if (!(p == 0.f)) l += p * (lp[k] - ((sk[k] - top) * inv_t - log_total));
         }
         l = warp_reduce<Sum>(l);
-        if (rest != 0.f) l += rest * (logf(rest) - logf(q_rest));
+        if (rest != 0.f) l += rest * (logf(rest) - (part < 0.f ? part * 0.69314718f - log_total : logf(part / total)));
       }
       if (lane == 0) {
         a.loss[row] = live ? l * h.teacher[slot][kWeight] * a.d.temperature * a.d.temperature : 0.f;
         if (a.stats) {
           a.stats[row * 3] = live ? top : 0.f;
           a.stats[row * 3 + 1] = live ? total * to_top : 0.f;
-          a.stats[row * 3 + 2] = live ? unlisted * to_top : 0.f;
+          a.stats[row * 3 + 2] = !live ? 0.f : part < 0.f ? part : part * to_top;
         }
       }
       return true;
@@ -649,7 +696,7 @@ __global__ void __maxnreg__(80)
         const float from_top = rounding_of_base<T>(now.stats[0], c);
         h.result[slot][0] = now.stats[0];
         h.result[slot][1] = now.stats[1] * from_top;
-        h.result[slot][2] = now.stats[2] * from_top;
+        h.result[slot][2] = now.stats[2] < 0.f ? now.stats[2] : now.stats[2] * from_top;
         h.result[slot][3] = now.up;
       }
       __syncwarp();
@@ -658,7 +705,7 @@ __global__ void __maxnreg__(80)
     for (int m = max(start, n - kRows); ok && m < n; m += kTeachers) settle(row_of(first + m * step), m);
   } else {   // ---------------------------------------------------------------- consumers
     const int part = 1 << plan.part, k_n = (int)a.d.topk;
-    const float inv_t = 1.f / a.d.temperature, c = inv_t * 1.4426950408889634f;
+    const float c = plan.c;
     uint16_t* const mine = mine0 + warp * plan.kp;
     Turn t;
     int n = 0, merges = 0;
@@ -784,8 +831,7 @@ __global__ void __maxnreg__(80)
       const bool two = kAcross && state != kDead;   // passes; else the second alone
       const int again = two ? again_of(chunks) : 0;
       Turn u = t;   // where the second pass begins: the first chunk that stays
-      float up = 1.f;
-      Sums r;
+      float up = 1.f, top = -INFINITY, total = 0.f, part_u = 0.f;   // of the row; the unlisted share
       if (two) {
         float based = -INFINITY, minus = 0.f;   // no base yet: every logit so far is -infinity
         bool far = false;
@@ -839,54 +885,66 @@ __global__ void __maxnreg__(80)
           if (q + 1 == again) u = t;
         }
         if (!ok) break;
+        const float2 f = unpair(run.sum);
+        Sums r{run.top, f.x + f.y};
         for (int i = lane, round = 0; i < count; i += 32, ++round) {   // the listed words, each id once
           const float v = sk[mine[i]];
           if (!live || (twice >> round & 1) || v == -INFINITY) continue;
-          raise<T>(run, v, c);
-          run.listed += exponential<T>(v, run.top, c);
+          if (!(v <= r.top_listed)) {
+            const float m = Max::of(v, r.top_listed);
+            r.listed *= rebase<T>(r.top_listed, m, c);
+            r.top_listed = m;
+          }
+          r.listed += exponential<T>(v, r.top_listed, c);
         }
-        const float2 f = unpair(run.sum);
-        r = merge_warp<T>(Sums{run.top, f.x + f.y, run.listed}, c);
+        r = merge_warp<T>(r, c);
         float(*const red)[4] = h.red[merges & 1];   // the last row's may still be read
         if (lane == 0) {
           red[warp][0] = r.top;
           red[warp][1] = r.unlisted;
-          red[warp][2] = r.listed;
+          red[warp][2] = r.top_listed;
+          red[warp][3] = r.listed;
           mbar_arrive(bar(&h.c_full[merges & 1]));
         }
         if (!(ok = wait(bar(&h.c_full[merges & 1]), merges >> 1 & 1))) break;
         ++merges;
         r = Sums{};
-        if (lane < plan.warps) r = Sums{red[lane][0], red[lane][1], red[lane][2]};
+        if (lane < plan.warps) r = Sums{red[lane][0], red[lane][1], red[lane][2], red[lane][3]};
         r = merge_warp<T>(r, c);
         if (across > 1 && live) {
           if (warp == 0 && lane < across) {
             const uint32_t to = map_to_rank(smem_u32(h.xch[rank]), lane);
             st_cluster(to, r.top);
             st_cluster(to + 4, r.unlisted);
-            st_cluster(to + 8, r.listed);
+            st_cluster(to + 8, r.top_listed);
+            st_cluster(to + 12, r.listed);
             arrive_cluster(map_to_rank(bar(&h.x_full), lane));
           }
           if (!(ok = __all_sync(0xffffffffu, wait_cluster(bar(&h.x_full), 0)))) break;
           r = Sums{};
-          if (lane < across) r = Sums{h.xch[lane][0], h.xch[lane][1], h.xch[lane][2]};
+          if (lane < across) r = Sums{h.xch[lane][0], h.xch[lane][1], h.xch[lane][2], h.xch[lane][3]};
           r = merge_warp<T>(r, c);
         }
-        live = live && r.top != -INFINITY;
+        top = Max::of(r.top, r.top_listed);
+        live = live && top != -INFINITY;
+        if (live) {
+          total = r.unlisted * rebase<T>(r.top, top, c) + r.listed * rebase<T>(r.top_listed, top, c);
+          part_u = share<T>(r, top, c, plan.c_low, a.teacher_lse != nullptr);
+        }
       }
-      float total = r.unlisted + r.listed;
       if (kAcross && threadIdx.x == 0) {
-        h.result[slot][0] = r.top;
+        h.result[slot][0] = top;
         h.result[slot][1] = total;
-        h.result[slot][2] = r.unlisted;
+        h.result[slot][2] = part_u;
         h.result[slot][3] = live ? 1.f : 0.f;
         mbar_arrive(bar(&h.r_full[slot]));
       }
       if constexpr (kMode != kLoss) {
         if (!(ok = wait(bar(&h.m_full[slot]), n / kRows & 1))) break;
         if (!kAcross) {
-          r = Sums{h.result[slot][0], h.result[slot][2], 0.f};
+          top = h.result[slot][0];
           total = h.result[slot][1];
+          part_u = h.result[slot][2];
           live = live && !(total == 0.f);
           up = h.result[slot][3];
           // an id listed twice, where the lanes hold all of the entries
@@ -896,13 +954,20 @@ __global__ void __maxnreg__(80)
             repeated = __any_sync(0xffffffffu, (same & (same - 1)) != 0);
           }
         }
-        const float inv = 1.f / total, q_rest = r.unlisted * inv, mass = h.teacher[slot][kMass];
-        const float rest = q_rest == 0.f ? 0.f : h.teacher[slot][kRest];
+        const float inv = 1.f / total, mass = h.teacher[slot][kMass];
+        const float rest = part_u == 0.f ? 0.f : h.teacher[slot][kRest];
         const float scale = h.teacher[slot][kWeight] * a.d.temperature * up, all = mass + rest;
-        const float coef = scale * (rest != 0.f ? all - rest / q_rest : all) * inv;
+        float base = top, coef;   // an unlisted word's gradient: coef times its exponential relative to base
+        if (rest != 0.f && part_u < kSmall) {
+          const Base b = base_of_share<T>(part_u, top, c, a.d.temperature);
+          base = b.base;
+          coef = scale * (all * inv * b.down - rest / b.sum);
+        } else {
+          coef = scale * (rest != 0.f ? all - rest / (part_u * inv) : all) * inv;
+        }
         T* const dst = grad_at(row, begin) - s.lead;
-        const bool apart = (reinterpret_cast<uintptr_t>(dst) & 15) != 0, far = is_far<T>(r.top, c);
-        const float minus = minus_base<T>(r.top, c);
+        const bool apart = (reinterpret_cast<uintptr_t>(dst) & 15) != 0, far = is_far<T>(base, c);
+        const float minus = minus_base<T>(base, c);
         const uint64_t kk = pair(coef, coef);
         // The teacher's part of an entry's gradient; an id listed twice has the sum at each of its entries.
         auto entry_p = [&](int k) {
@@ -913,7 +978,7 @@ __global__ void __maxnreg__(80)
           return pk;
         };
         auto entry_gradient = [&](float s, float pk) {
-          return from_f<T>(scale * (exponential<T>(s, r.top, c) * inv * all - pk));
+          return from_f<T>(scale * (exponential<T>(s, top, c) * inv * all - pk));
         };
         const float p0 = live && k0 >= 0 ? entry_p(k0) : 0.f;
         const T g0 = kMode == kBoth && live && k0 >= 0 ? entry_gradient(sk[k0], p0) : from_f<T>(0.f);
@@ -1003,6 +1068,9 @@ Plan make_plan(const DistillArgs& a, int elt) {
   p.width = (int)(((v + p.slices - 1) / p.slices + 127) / 128 * 128);
   const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.d.logits_stride * elt % 16 == 0;
   p.ragged = !aligned || v * elt % 16 != 0;
+  const double c = 1.4426950408889634 / (double)a.d.temperature;
+  p.c = (float)c;
+  p.c_low = (float)(c - (double)p.c);
   const int vectors = (int)(std::min<long long>(p.width, v) * elt + 15) / 16 + !aligned;
   // Chunks of 32 KB for eight warps, two batches of vectors for each lane (2048x32000 bf16: 55 us; of 16
   // KB, one batch between waits: 64); smaller where the row is.

@@ -349,7 +349,8 @@ int32_t cbr_profile_last_count(void);
  *   teacher_lse NULL: p = softmax of t / T over the present entries, no tail (p_rest = 0)
  *   teacher_lse set:  p_k = exp(t_k / T - teacher_lse[r]) (the log-sum-exp of t / T over the
  *                     teacher's whole vocabulary), p_rest = max(0, 1 - sum p_k), and q_rest is the
- *                     student's mass outside the listed ids; p_rest = 0 where q_rest is 0
+ *                     student's mass outside the listed ids; p_rest = 0 where q_rest is 0 (below
+ *                     2^-1074: e^-744, so words masked with the type's lowest value leave no tail)
  *   loss_r  = w_r T^2 (sum_k p_k (log p_k - log q_k) + p_rest (log p_rest - log q_rest))
  *   dlogits = dloss_r w_r T (q_v (sum p + p_rest) - sum over the entries of v of p_k
  *                            - [v is not listed] q_v p_rest / q_rest)
@@ -357,6 +358,8 @@ int32_t cbr_profile_last_count(void);
  * A row has loss 0, gradient 0 and statistics 0, whatever its other values (NaN included), if
  * w_r = 0; or no entry is present (teacher_lse NULL: none above -infinity); or no student logit
  * is above -infinity.  Other NaN and infinities go through the formulas, in their row alone.
+ * Of 16-bit logits, exponentials below 2^-126 of the largest logit's (with a tail: of the largest
+ * unlisted one's, for the unlisted words' share of it) count as 0, so a bf16 gradient that small is 0.
  */
 typedef struct {
   int64_t rows, vocab;      /* rows >= 0; 1 <= vocab <= 393216 */
@@ -374,8 +377,9 @@ typedef struct {
 /*
  * Loss.  logits [rows][vocab], top_ids and top_logits [rows][topk], teacher_lse [rows] fp32 or
  * NULL, row_weight [rows] fp32 or NULL -> loss [rows] fp32, stats [rows][3] fp32 (the largest
- * logit, the sum of exp((s - largest) / T) over the row and over its unlisted ids) for the
- * backward.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, DEVICE, CUDA.
+ * logit, the sum of exp((s - largest) / T) over the row and over its unlisted ids; with
+ * teacher_lse, the latter's logarithm to base 2 instead where it is below 2^-64, a negative
+ * number, and 0 below 2^-1074) for the backward.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, DEVICE, CUDA.
  */
 cbr_status_t cbr_distill_forward(const cbr_distill_desc_t* desc, const void* logits, const void* top_ids,
                                  const void* top_logits, const float* teacher_lse, const float* row_weight,

@@ -1,5 +1,5 @@
 """The distillation's numbers at the ends of their range: logits of any magnitude, teachers whose
-logits have a common offset."""
+logits have a common offset, unlisted words that hold next to nothing of the student's mass."""
 import math
 
 import pytest
@@ -99,3 +99,80 @@ def test_far_teachers_keep_their_bits(temperature):
     want["loss_bound"] = (p * (each_p * (1 + (log_p - log_q).abs()) + each_q) + mag * ref.rounds(k)).sum(1) * temperature ** 2
     got = tokens.distill_forward_backward(logits, ids, top, temperature=temperature)
     ref.close(got["loss"], want["loss"], want["loss_bound"], "loss")
+
+
+# ------------------------------------------------------------------------------- hardly any unlisted mass
+
+def faint(rows, vocab, k, dtype, seed, gap, temperature, pad):
+    """Students whose listed words stand gap * temperature above all others; the last columns are padding."""
+    logits, ids, top, lse = make(rows, vocab, k, dtype, seed, True)
+    lse = torch.logsumexp(top.float() / temperature, 1) + 0.1 + torch.rand(
+        rows, generator=torch.Generator().manual_seed(seed + 1)).cuda()
+    ids = (ids.long() % (vocab - pad)).to(ids.dtype)
+    logits.scatter_(1, ids.long(), (logits.float().gather(1, ids.long()) + gap * temperature).to(logits.dtype))
+    if pad:
+        logits[:, vocab - pad:] = -math.inf
+    return logits, ids, top, lse
+
+
+def faint_reference(logits, ids, top, lse, weight, temperature):
+    """The plain form, with bounds for a tail that is computed relative to its own largest word: an unlisted
+    word's share of the unlisted mass is off by the roundings of sums and by w for each unit of the exponents
+    that enter, and by an exponential lost below the normal range (2^-126 of the largest)."""
+    want = ref.distill(logits, ids, top, temperature, lse, weight)
+    z = logits.cpu().double() / temperature
+    r, v = z.shape
+    per = ref.rounds(v) + ref.rounds(ids.shape[1]) + 16 * ref.W
+    listed = torch.zeros(r, v, dtype=torch.bool).scatter_(1, ids.cpu().long(), True)
+    t = top.cpu().double() / temperature
+    p = torch.exp(t - lse.cpu().double()[:, None])
+    full = torch.zeros(r, v, dtype=torch.float64).scatter_add_(1, ids.cpu().long(), p)
+    log_q = torch.log_softmax(z, 1)
+    own = torch.softmax(z.masked_fill(listed, -math.inf), 1)
+    spread = (z.max(1, keepdim=True).values - z.masked_fill(listed, -math.inf).max(1, keepdim=True).values).abs()
+    size = (1 + log_q.abs().nan_to_num(0, 0, 0)) * per
+    bound = torch.exp(log_q) * size * (p.sum(1, keepdim=True) + 1) + full * (1 + t.abs().max(1, keepdim=True).values) * per
+    bound = bound + torch.where(listed, 0.0, own * (p.sum(1, keepdim=True) + 1) * (2 + spread) * (size + per)) + 2.0 ** -126
+    w = torch.ones(r, dtype=torch.float64) if weight is None else weight.cpu().double()
+    want["grad_bound"] = bound * w.abs()[:, None] * temperature
+    u = want["stats"][:, 2]
+    tail = u < 2.0 ** -64
+    want["stats"][:, 2] = torch.where(tail & (u > 0), torch.log2(u.clamp(min=1e-320)), u)
+    return want
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("gap", [20, 40, 60, 80, 90, 100, 130, 400, 700])
+@pytest.mark.parametrize("rows,vocab,k,pad", [(2, 4099, 20, 7), (6, 1000, 10, 100), (5, 300, 6, 0)], ids=lambda v: str(v))
+def test_a_tail_of_hardly_any_mass(rows, vocab, k, pad, gap, dtype):
+    """The loss has its logarithm and the unlisted words share its gradient, however small it is."""
+    temperature = 2.5
+    logits, ids, top, lse = faint(rows, vocab, k, dtype, 38 + gap, gap, temperature, pad)
+    for weight in (None, torch.full((rows,), 4096.0 / 3, device="cuda")):
+        want = faint_reference(logits, ids, top, lse, weight, temperature)
+        compare(logits, ids, top, lse, weight, temperature, want)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("scale", [1e9, 1e15, 1e22])
+def test_large_scales_of_a_faint_tail(scale, dtype):
+    """The factor of an unlisted word's exponential passes the range of 32 bits long before its gradient."""
+    logits, ids, top, lse = faint(6, 515, 8, dtype, 39, 35, 4.0, 15)
+    w = torch.full((6,), scale, device="cuda")
+    if dtype == "f16":
+        w.fill_(1024.0)
+    want = faint_reference(logits, ids, top, lse, w, 4.0)
+    compare(logits, ids, top, lse, w, 4.0, want)
+
+
+def test_no_tail_below_the_range():
+    """Words masked with a large negative number are as good as not there, as those at -infinity are."""
+    for dtype in DT:
+        logits, ids, top, lse = faint(6, 515, 8, dtype, 40, 10, 1.0, 15)
+        low, none = logits.clone(), logits.clone()
+        listed = torch.zeros_like(logits, dtype=torch.bool).scatter_(1, ids.long(), True)
+        low[~listed], none[~listed] = torch.finfo(DT[dtype]).min, -math.inf
+        a = tokens.distill_forward_backward(low, ids, top, teacher_lse=lse)
+        b = tokens.distill_forward_backward(none, ids, top, teacher_lse=lse)
+        assert torch.equal(a["loss"], b["loss"]) and torch.equal(a["dlogits"], b["dlogits"])
+        compare(low, ids, top, lse)
