@@ -327,6 +327,8 @@ def block_norm_backward(dx_out, dh, x_out, branch=None, post_weight=None, gate=N
                       residual_scale, branch_scale)
     if ws is None:
         ws = _new((block_norm_workspace_size(rows, dim, dt),), torch.uint8, dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        _bad(f"ws has to be contiguous on {dev}")
     _check(_load().cbr_block_norm_backward(
         desc, dxo_at, dh_at, xo_at, f_at, _vector(post_weight, dim, dev, "post_weight"), gate_at,
         _vector(pre_weight, dim, dev, "pre_weight"), _vector(stats, 4 * rows, dev, "stats"), dx.data_ptr(), df_at,
