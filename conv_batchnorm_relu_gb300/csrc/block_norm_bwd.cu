@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(kThreads, kFit)
   using R = Row<T, kVec, kEpt>;
   constexpr int kSums = kCenter ? 2 : 3;
   __shared__ float red[2][4][kMaxTeamWarps];
-  __shared__ float fold[kBlock ? 1 : kThreads * kEpt];
+  __shared__ __align__(16) float fold[kBlock ? 1 : kThreads * kEpt];   // R::put writes 16 bytes at a time
+  static_assert(__alignof__(fold) >= 16, "");
   __shared__ __align__(8) uint64_t full[kRing ? kMaxStages : 1];
   extern __shared__ __align__(128) uint8_t ring[];
   const int team = kBlock ? blockDim.x : plan.team, at = kBlock ? threadIdx.x : threadIdx.x & (team - 1);
