@@ -1,4 +1,5 @@
 // C ABI of the token operators (declared in include/cbr.h): argument checks and dispatch.
+#include <algorithm>
 #include <cmath>
 
 #include "cbr_internal.h"
@@ -9,8 +10,9 @@ namespace {
 
 constexpr int64_t kMaxVocab = 393216, kMaxTopk = 1024, kMaxDim = 16384;
 constexpr int kMaxHeadDim = 1024, kMaxAxes = 8;
-// Row counts and strides up to 2^40, so that no product of checked sizes leaves 64 bits.
-constexpr int64_t kMaxExtent = int64_t(1) << 40;
+// Row counts and strides up to 2^40, and an axis' steps times its stride up to 2^58 elements: a tensor's
+// axes together stay within 2^62 bytes.
+constexpr int64_t kMaxExtent = int64_t(1) << 40, kMaxReach = int64_t(1) << 58;
 
 bool known_dtype(int32_t t) { return t == CBR_F16 || t == CBR_BF16 || t == CBR_F32; }
 size_t elt(int32_t t) { return t == CBR_F32 ? 4 : 2; }
@@ -18,8 +20,10 @@ bool off(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a !=
 bool extent(int64_t v) { return v >= 0 && v <= kMaxExtent; }
 bool finite(float v) { return std::isfinite(v); }
 
+bool in_reach(int64_t stride, int64_t steps) { return steps <= 1 || stride <= kMaxReach / (steps - 1); }
+
 // A row stride: at least the row (any value will do where there is one row at most).
-bool row_stride(int64_t s, int64_t width, int64_t rows) { return extent(s) && (rows <= 1 || s >= width); }
+bool row_stride(int64_t s, int64_t width, int64_t rows) { return extent(s) && (rows <= 1 || s >= width) && in_reach(s, rows); }
 
 // An output that is an input must be it exactly.
 bool same_or_apart(const void* out, int64_t out_stride, const void* in, int64_t in_stride, int64_t rows) {
@@ -78,6 +82,11 @@ int check(const cbr_rotary_desc_t* d) {
   for (int i = 0; i < 3; ++i)
     if (!extent(d->q_stride[i]) || !extent(d->k_stride[i]) || !extent(d->q_out_stride[i]) ||
         !extent(d->k_out_stride[i]) || !extent(d->pos_stride[i]))
+      return CBR_ERR_INVALID_ARG;
+  const int64_t steps[3] = {d->batch, d->tokens, std::max(d->heads_q, d->heads_k)};
+  for (int i = 0; i < 3; ++i)
+    if (!in_reach(d->q_stride[i], steps[i]) || !in_reach(d->k_stride[i], steps[i]) || !in_reach(d->q_out_stride[i], steps[i]) ||
+        !in_reach(d->k_out_stride[i], steps[i]) || !in_reach(d->pos_stride[i], i < 2 ? steps[i] : d->axes))
       return CBR_ERR_INVALID_ARG;
   if (!known_dtype(d->dtype) || d->head_dim > kMaxHeadDim || d->axes > kMaxAxes || d->heads_q > 65536 ||
       d->heads_k > 65536)

@@ -334,8 +334,8 @@ int32_t cbr_profile_last_count(void);
  * map is a grid of tokens: norms around a gated residual block, rotary positions over several
  * axes, and a distillation loss from a teacher's top logits.  The conventions above hold (caller
  * owns every buffer, asynchronous on `stream`, host-side validation before anything is enqueued),
- * with these differences: strides are in elements and counted in 64 bits; a tensor need only be
- * aligned to its element; a call whose output is empty (no rows, no tokens) does nothing and
+ * with these differences: strides are in elements and counted in 64 bits (each up to 2^40, and up
+ * to 2^58 times the steps of its axis); a tensor need only be aligned to its element; a call whose output is empty (no rows, no tokens) does nothing and
  * returns CBR_OK; and device data is never trusted (an entry id outside the vocabulary is an
  * absent entry, an axis outside the position's axes is the last one).
  * Rows of one output may not overlap, and no output may overlap an input except where it says so.
