@@ -1,6 +1,7 @@
 // C ABI of the token operators (declared in include/cbr.h): argument checks and dispatch.
 #include <algorithm>
 #include <cmath>
+#include <utility>
 
 #include "cbr_internal.h"
 #include "token_ops.h"
@@ -94,12 +95,17 @@ int check(const cbr_rotary_desc_t* d) {
   return CBR_OK;
 }
 
-// The rows of an output must not share memory: no axis of several steps may stand still, or step
-// by less than a head.
+// The heads of an output must not share memory: taken by their strides, each axis of several steps
+// steps past all that the smaller ones reach.
 bool distinct(const cbr_rotary_desc_t& d, const int64_t* s, int32_t heads) {
-  const int64_t n[3] = {d.batch, d.tokens, heads};
-  for (int i = 0; i < 3; ++i)
-    if (n[i] > 1 && s[i] < d.head_dim) return false;
+  std::pair<int64_t, int64_t> axes[3] = {{s[0], d.batch}, {s[1], d.tokens}, {s[2], heads}};   // stride, steps
+  std::sort(axes, axes + 3);
+  int64_t reach = d.head_dim;
+  for (const auto& [stride, steps] : axes) {
+    if (steps <= 1) continue;
+    if (stride < reach) return false;
+    reach += stride * (steps - 1);
+  }
   return true;
 }
 

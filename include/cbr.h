@@ -480,7 +480,10 @@ typedef struct {
   int32_t layout, dtype;
 } cbr_rotary_desc_t;
 
-/* q_out may be q itself and k_out k itself (same address and strides). */
+/*
+ * q_out may be q itself and k_out k itself (same address and strides).  An output's axes may lie in any
+ * order in memory, each stepping past all that the smaller ones reach.
+ */
 cbr_status_t cbr_rotary_forward(const cbr_rotary_desc_t* desc, const void* q, const void* k,
                                 const int32_t* positions, const int64_t* freq, const uint8_t* axis, void* q_out,
                                 void* k_out, cbr_stream_t stream);

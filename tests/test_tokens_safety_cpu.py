@@ -28,3 +28,24 @@ def test_rows_times_strides_stay_in_64_bits(lib):  # noqa: F811
         assert rot(lib, rotary_desc(batch=FAR, n=1, **kw)) == 1, kw
     assert rot(lib, rotary_desc(n=1 << 19, q=(640, FAR, 64))) == 1
     assert rot(lib, rotary_desc(hq=65536, q=(FAR, 128, FAR))) in DEVICE_OR_OK
+
+
+# batch 2, 5 tokens, 2 heads of q and 1 of k, 64 wide
+@pytest.mark.parametrize("strides", [
+    (640, 64, 64),          # a token's second head is the next token's first
+    (640, 64, 320 - 64),    # the second head of the first token is the fifth token's first
+    (320, 128, 64),         # the second batch begins in the first one's third token
+    (192, 128, 64), (128, 128, 64), (640, 128, 128), (640, 96, 64)])
+def test_rotary_outputs_that_overlap_are_refused(lib, strides):  # noqa: F811
+    assert rot(lib, rotary_desc(qo=strides)) == 1
+
+
+@pytest.mark.parametrize("strides", [
+    (640, 128, 64), (640, 64, 320), (128, 256, 64), (64, 256, 128), (64, 128, 640), (1000, 200, 100), (10240, 1024, 512)])
+def test_rotary_outputs_in_any_order_of_axes_are_taken(lib, strides):  # noqa: F811
+    assert rot(lib, rotary_desc(qo=strides)) in DEVICE_OR_OK
+
+
+def test_axes_of_one_step_may_have_any_stride(lib):  # noqa: F811
+    assert rot(lib, rotary_desc(batch=1, n=1, hq=1, qo=(0, 0, 0), ko=(0, 1, 2))) in DEVICE_OR_OK
+    assert rot(lib, rotary_desc(batch=1, qo=(7, 128, 64))) in DEVICE_OR_OK
