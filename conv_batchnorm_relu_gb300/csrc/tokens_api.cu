@@ -34,7 +34,7 @@ bool same_or_apart(const void* out, int64_t out_stride, const void* in, int64_t 
 int check(const cbr_distill_desc_t* d) {
   if (!d) return CBR_ERR_INVALID_ARG;
   if (!extent(d->rows) || d->vocab < 1 || d->topk < 0 || !(d->temperature > 0.f) || !finite(d->temperature) ||
-      !finite(1.f / d->temperature) || (d->id_bytes != 4 && d->id_bytes != 8))
+      !finite(1.4426951f / d->temperature) || (d->id_bytes != 4 && d->id_bytes != 8))
     return CBR_ERR_INVALID_ARG;
   if (!known_dtype(d->dtype) || !known_dtype(d->top_dtype) || d->vocab > kMaxVocab || d->topk > kMaxTopk)
     return CBR_ERR_UNSUPPORTED;

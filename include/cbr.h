@@ -371,7 +371,7 @@ typedef struct {
   int32_t dtype;            /* of logits and dlogits */
   int32_t top_dtype;        /* of top_logits */
   int32_t id_bytes;         /* 4 (int32) or 8 (int64) */
-  float temperature;        /* > 0 */
+  float temperature;        /* > 0; log2(e) / temperature has to be finite */
 } cbr_distill_desc_t;
 
 /*

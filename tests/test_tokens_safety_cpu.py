@@ -49,3 +49,10 @@ def test_rotary_outputs_in_any_order_of_axes_are_taken(lib, strides):  # noqa: F
 def test_axes_of_one_step_may_have_any_stride(lib):  # noqa: F811
     assert rot(lib, rotary_desc(batch=1, n=1, hq=1, qo=(0, 0, 0), ko=(0, 1, 2))) in DEVICE_OR_OK
     assert rot(lib, rotary_desc(batch=1, qo=(7, 128, 64))) in DEVICE_OR_OK
+
+
+def test_temperatures_at_the_end_of_the_range(lib):  # noqa: F811
+    """The kernels' exponents have the factor log2(e) / T; where it is infinite a difference of 0 would be NaN."""
+    assert fb(lib, distill_desc(temp=4e-39)) == 1      # 1 / T is finite yet
+    assert fb(lib, distill_desc(temp=5e-39)) in DEVICE_OR_OK
+    assert fb(lib, distill_desc(temp=3e38)) in DEVICE_OR_OK
