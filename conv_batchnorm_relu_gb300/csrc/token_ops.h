@@ -9,6 +9,17 @@
 
 namespace cbr {
 
+// Runs the body of a C entry: a C++ exception (the caches of launch shapes take memory and a lock) ends in a
+// status, not in the caller.
+template <typename F>
+cbr_status_t guarded(F&& body) noexcept {
+  try {
+    return static_cast<cbr_status_t>(body());
+  } catch (...) {
+    return CBR_ERR_CUDA;
+  }
+}
+
 // The current device if this library runs on it (cbr_api.cu): its SM count and its error word.
 int device_for_call(int* num_sms, uint32_t** err);
 

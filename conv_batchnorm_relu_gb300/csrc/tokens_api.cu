@@ -143,75 +143,85 @@ extern "C" {
 cbr_status_t cbr_distill_forward(const cbr_distill_desc_t* desc, const void* logits, const void* top_ids,
                                  const void* top_logits, const float* teacher_lse, const float* row_weight,
                                  float* loss, float* stats, cbr_stream_t stream) {
-  if (const int e = check(desc)) return (cbr_status_t)e;
-  DistillArgs a{*desc, nullptr, logits, top_ids, top_logits, teacher_lse, row_weight, loss, stats, nullptr, nullptr};
-  return (cbr_status_t)run(a, true, false, false, reinterpret_cast<cudaStream_t>(stream));
+  return guarded([&]() -> int {
+    if (const int e = check(desc)) return e;
+    DistillArgs a{*desc, nullptr, logits, top_ids, top_logits, teacher_lse, row_weight, loss, stats, nullptr, nullptr};
+    return run(a, true, false, false, reinterpret_cast<cudaStream_t>(stream));
+  });
 }
 
 cbr_status_t cbr_distill_backward(const cbr_distill_desc_t* desc, const float* dloss, const void* logits,
                                   const void* top_ids, const void* top_logits, const float* teacher_lse,
                                   const float* row_weight, const float* stats, void* dlogits, cbr_stream_t stream) {
-  if (const int e = check(desc)) return (cbr_status_t)e;
-  DistillArgs a{*desc, dloss, logits, top_ids, top_logits, teacher_lse, row_weight, nullptr,
-                const_cast<float*>(stats), dlogits, nullptr};
-  return (cbr_status_t)run(a, true, true, true, reinterpret_cast<cudaStream_t>(stream));
+  return guarded([&]() -> int {
+    if (const int e = check(desc)) return e;
+    DistillArgs a{*desc, dloss, logits, top_ids, top_logits, teacher_lse, row_weight, nullptr,
+                  const_cast<float*>(stats), dlogits, nullptr};
+    return run(a, true, true, true, reinterpret_cast<cudaStream_t>(stream));
+  });
 }
 
 cbr_status_t cbr_distill_forward_backward(const cbr_distill_desc_t* desc, const void* logits, const void* top_ids,
                                           const void* top_logits, const float* teacher_lse,
                                           const float* row_weight, float* loss, float* stats, void* dlogits,
                                           cbr_stream_t stream) {
-  if (const int e = check(desc)) return (cbr_status_t)e;
-  DistillArgs a{*desc, nullptr, logits, top_ids, top_logits, teacher_lse, row_weight, loss, stats, dlogits, nullptr};
-  return (cbr_status_t)run(a, false, true, false, reinterpret_cast<cudaStream_t>(stream));
+  return guarded([&]() -> int {
+    if (const int e = check(desc)) return e;
+    DistillArgs a{*desc, nullptr, logits, top_ids, top_logits, teacher_lse, row_weight, loss, stats, dlogits, nullptr};
+    return run(a, false, true, false, reinterpret_cast<cudaStream_t>(stream));
+  });
 }
 
 cbr_status_t cbr_block_norm_forward(const cbr_block_norm_desc_t* desc, const void* x, const void* branch,
                                     const float* post_weight, const float* gate, const float* pre_weight,
                                     void* x_out, void* h, float* stats, cbr_stream_t stream) {
-  if (const int e = check(desc)) return (cbr_status_t)e;
-  const cbr_block_norm_desc_t& d = *desc;
-  // the join is there where its weight is: an empty branch may have no address
-  const bool join = post_weight != nullptr;
-  if (!join) gate = nullptr;
-  if (!(d.eps > 0.f) || !finite(d.eps) || !gate_rows_ok(d, gate)) return CBR_ERR_INVALID_ARG;
-  if ((!join && branch) || (!join && !pre_weight)) return CBR_ERR_INVALID_ARG;
-  if (!row_stride(d.x_stride, d.dim, d.rows) || (join && !row_stride(d.branch_stride, d.dim, d.rows)) ||
-      (join && !row_stride(d.x_out_stride, d.dim, d.rows)) || (pre_weight && !row_stride(d.h_stride, d.dim, d.rows)))
-    return CBR_ERR_INVALID_ARG;
-  if (d.rows == 0) return CBR_OK;
-  if (!x || (join && (!branch || !x_out)) || (pre_weight && !h)) return CBR_ERR_INVALID_ARG;
-  if (branch && (!same_or_apart(x_out, d.x_out_stride, x, d.x_stride, d.rows) ||
-                 !same_or_apart(x_out, d.x_out_stride, branch, d.branch_stride, d.rows)))
-    return CBR_ERR_INVALID_ARG;
-  if (pre_weight && (!same_or_apart(h, d.h_stride, branch ? branch : x, branch ? d.branch_stride : d.x_stride, d.rows) ||
-                     h == x_out || (branch && h == x)))
-    return CBR_ERR_INVALID_ARG;
-  const size_t e = elt(d.dtype);
-  if (off(x, e) || off(branch, e) || off(x_out, e) || off(h, e) || off(post_weight, 4) || off(gate, 4) ||
-      off(pre_weight, 4) || off(stats, 4))
-    return CBR_ERR_MISALIGNED;
-  BlockNormArgs a{};
-  int sms = 0;
-  uint32_t* err = nullptr;
-  if (const int s = device_for_call(&sms, &err)) return (cbr_status_t)s;
-  a.d = d;
-  a.x = x;
-  a.branch = branch;
-  a.post_weight = post_weight;
-  a.gate = gate;
-  a.pre_weight = pre_weight;
-  a.x_out = x_out;
-  a.h = h;
-  a.stats = stats;
-  return (cbr_status_t)launch_block_norm(a, sms, reinterpret_cast<cudaStream_t>(stream));
+  return guarded([&]() -> int {
+    if (const int e = check(desc)) return e;
+    const cbr_block_norm_desc_t& d = *desc;
+    // the join is there where its weight is: an empty branch may have no address
+    const bool join = post_weight != nullptr;
+    if (!join) gate = nullptr;
+    if (!(d.eps > 0.f) || !finite(d.eps) || !gate_rows_ok(d, gate)) return CBR_ERR_INVALID_ARG;
+    if ((!join && branch) || (!join && !pre_weight)) return CBR_ERR_INVALID_ARG;
+    if (!row_stride(d.x_stride, d.dim, d.rows) || (join && !row_stride(d.branch_stride, d.dim, d.rows)) ||
+        (join && !row_stride(d.x_out_stride, d.dim, d.rows)) || (pre_weight && !row_stride(d.h_stride, d.dim, d.rows)))
+      return CBR_ERR_INVALID_ARG;
+    if (d.rows == 0) return CBR_OK;
+    if (!x || (join && (!branch || !x_out)) || (pre_weight && !h)) return CBR_ERR_INVALID_ARG;
+    if (branch && (!same_or_apart(x_out, d.x_out_stride, x, d.x_stride, d.rows) ||
+                   !same_or_apart(x_out, d.x_out_stride, branch, d.branch_stride, d.rows)))
+      return CBR_ERR_INVALID_ARG;
+    if (pre_weight && (!same_or_apart(h, d.h_stride, branch ? branch : x, branch ? d.branch_stride : d.x_stride, d.rows) ||
+                       h == x_out || (branch && h == x)))
+      return CBR_ERR_INVALID_ARG;
+    const size_t e = elt(d.dtype);
+    if (off(x, e) || off(branch, e) || off(x_out, e) || off(h, e) || off(post_weight, 4) || off(gate, 4) ||
+        off(pre_weight, 4) || off(stats, 4))
+      return CBR_ERR_MISALIGNED;
+    BlockNormArgs a{};
+    int sms = 0;
+    uint32_t* err = nullptr;
+    if (const int s = device_for_call(&sms, &err)) return s;
+    a.d = d;
+    a.x = x;
+    a.branch = branch;
+    a.post_weight = post_weight;
+    a.gate = gate;
+    a.pre_weight = pre_weight;
+    a.x_out = x_out;
+    a.h = h;
+    a.stats = stats;
+    return launch_block_norm(a, sms, reinterpret_cast<cudaStream_t>(stream));
+  });
 }
 
 cbr_status_t cbr_block_norm_workspace_size(const cbr_block_norm_desc_t* desc, size_t* bytes) {
-  if (const int e = check(desc)) return (cbr_status_t)e;
-  if (!bytes) return CBR_ERR_INVALID_ARG;
-  *bytes = block_norm_part_floats(*desc) * sizeof(float);
-  return CBR_OK;
+  return guarded([&]() -> int {
+    if (const int e = check(desc)) return e;
+    if (!bytes) return CBR_ERR_INVALID_ARG;
+    *bytes = block_norm_part_floats(*desc) * sizeof(float);
+    return CBR_OK;
+  });
 }
 
 cbr_status_t cbr_block_norm_backward(const cbr_block_norm_desc_t* desc, const void* dx_out, const void* dh,
@@ -219,74 +229,80 @@ cbr_status_t cbr_block_norm_backward(const cbr_block_norm_desc_t* desc, const vo
                                      const float* gate, const float* pre_weight, const float* stats, void* dx,
                                      void* dbranch, float* dpost_weight, float* dgate, float* dpre_weight,
                                      void* ws, size_t ws_bytes, cbr_stream_t stream) {
-  if (const int e = check(desc)) return (cbr_status_t)e;
-  const cbr_block_norm_desc_t& d = *desc;
-  const bool join = post_weight != nullptr;
-  if (!join) gate = nullptr;
-  if (!gate_rows_ok(d, gate)) return CBR_ERR_INVALID_ARG;
-  if ((!join && branch) || (!join && !pre_weight)) return CBR_ERR_INVALID_ARG;
-  if ((dx_out && !row_stride(d.dx_out_stride, d.dim, d.rows)) || !row_stride(d.dx_stride, d.dim, d.rows) ||
-      (join && (!row_stride(d.branch_stride, d.dim, d.rows) || !row_stride(d.dbranch_stride, d.dim, d.rows))) ||
-      (pre_weight && (!row_stride(d.x_out_stride, d.dim, d.rows) || !row_stride(d.dh_stride, d.dim, d.rows))))
-    return CBR_ERR_INVALID_ARG;
-  if ((join && !dpost_weight) || (pre_weight && !dpre_weight)) return CBR_ERR_INVALID_ARG;
-  if (d.rows > 0) {
-    if (!dx || !stats || (!pre_weight && !dx_out) || (join && (!branch || !dbranch)) ||
-        (pre_weight && (!dh || !x_out)) || (gate && !dgate) || !ws)
+  return guarded([&]() -> int {
+    if (const int e = check(desc)) return e;
+    const cbr_block_norm_desc_t& d = *desc;
+    const bool join = post_weight != nullptr;
+    if (!join) gate = nullptr;
+    if (!gate_rows_ok(d, gate)) return CBR_ERR_INVALID_ARG;
+    if ((!join && branch) || (!join && !pre_weight)) return CBR_ERR_INVALID_ARG;
+    if ((dx_out && !row_stride(d.dx_out_stride, d.dim, d.rows)) || !row_stride(d.dx_stride, d.dim, d.rows) ||
+        (join && (!row_stride(d.branch_stride, d.dim, d.rows) || !row_stride(d.dbranch_stride, d.dim, d.rows))) ||
+        (pre_weight && (!row_stride(d.x_out_stride, d.dim, d.rows) || !row_stride(d.dh_stride, d.dim, d.rows))))
       return CBR_ERR_INVALID_ARG;
-    if ((dx_out && !same_or_apart(dx, d.dx_stride, dx_out, d.dx_out_stride, d.rows)) || dx == x_out || dx == dh ||
-        (branch && (!same_or_apart(dbranch, d.dbranch_stride, branch, d.branch_stride, d.rows) ||
-                    !same_or_apart(dbranch, d.dbranch_stride, dh, d.dh_stride, d.rows) || dbranch == dx ||
-                    dbranch == x_out || dbranch == dx_out || dx == branch)))
-      return CBR_ERR_INVALID_ARG;
-  }
-  const size_t e = elt(d.dtype);
-  if (off(dx_out, e) || off(dh, e) || off(x_out, e) || off(branch, e) || off(dx, e) || off(dbranch, e) ||
-      off(post_weight, 4) || off(gate, 4) || off(pre_weight, 4) || off(stats, 4) || off(dpost_weight, 4) ||
-      off(dgate, 4) || off(dpre_weight, 4) || off(ws, 16))
-    return CBR_ERR_MISALIGNED;
-  if (d.rows > 0 && ws_bytes < block_norm_part_floats(d) * sizeof(float)) return CBR_ERR_WORKSPACE;
-  int sms = 0;
-  uint32_t* err = nullptr;
-  if (const int s = device_for_call(&sms, &err)) return (cbr_status_t)s;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (d.rows == 0) {   // sums over no rows
-    if (join && cudaMemsetAsync(dpost_weight, 0, d.dim * 4, st) != cudaSuccess) return CBR_ERR_CUDA;
-    if (pre_weight && cudaMemsetAsync(dpre_weight, 0, d.dim * 4, st) != cudaSuccess) return CBR_ERR_CUDA;
-    return CBR_OK;
-  }
-  BlockNormArgs a{};
-  a.d = d;
-  a.x = x_out;
-  a.branch = branch;
-  a.post_weight = post_weight;
-  a.gate = gate;
-  a.pre_weight = pre_weight;
-  a.stats = const_cast<float*>(stats);
-  a.dx_out = dx_out;
-  a.dh = dh;
-  a.dx = dx;
-  a.dbranch = dbranch;
-  a.dpost_weight = dpost_weight;
-  a.dgate = dgate;
-  a.dpre_weight = dpre_weight;
-  a.part = static_cast<float*>(ws);
-  a.err = err;
-  return (cbr_status_t)launch_block_norm_backward(a, sms, st);
+    if ((join && !dpost_weight) || (pre_weight && !dpre_weight)) return CBR_ERR_INVALID_ARG;
+    if (d.rows > 0) {
+      if (!dx || !stats || (!pre_weight && !dx_out) || (join && (!branch || !dbranch)) ||
+          (pre_weight && (!dh || !x_out)) || (gate && !dgate) || !ws)
+        return CBR_ERR_INVALID_ARG;
+      if ((dx_out && !same_or_apart(dx, d.dx_stride, dx_out, d.dx_out_stride, d.rows)) || dx == x_out || dx == dh ||
+          (branch && (!same_or_apart(dbranch, d.dbranch_stride, branch, d.branch_stride, d.rows) ||
+                      !same_or_apart(dbranch, d.dbranch_stride, dh, d.dh_stride, d.rows) || dbranch == dx ||
+                      dbranch == x_out || dbranch == dx_out || dx == branch)))
+        return CBR_ERR_INVALID_ARG;
+    }
+    const size_t e = elt(d.dtype);
+    if (off(dx_out, e) || off(dh, e) || off(x_out, e) || off(branch, e) || off(dx, e) || off(dbranch, e) ||
+        off(post_weight, 4) || off(gate, 4) || off(pre_weight, 4) || off(stats, 4) || off(dpost_weight, 4) ||
+        off(dgate, 4) || off(dpre_weight, 4) || off(ws, 16))
+      return CBR_ERR_MISALIGNED;
+    if (d.rows > 0 && ws_bytes < block_norm_part_floats(d) * sizeof(float)) return CBR_ERR_WORKSPACE;
+    int sms = 0;
+    uint32_t* err = nullptr;
+    if (const int s = device_for_call(&sms, &err)) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (d.rows == 0) {   // sums over no rows
+      if (join && cudaMemsetAsync(dpost_weight, 0, d.dim * 4, st) != cudaSuccess) return CBR_ERR_CUDA;
+      if (pre_weight && cudaMemsetAsync(dpre_weight, 0, d.dim * 4, st) != cudaSuccess) return CBR_ERR_CUDA;
+      return CBR_OK;
+    }
+    BlockNormArgs a{};
+    a.d = d;
+    a.x = x_out;
+    a.branch = branch;
+    a.post_weight = post_weight;
+    a.gate = gate;
+    a.pre_weight = pre_weight;
+    a.stats = const_cast<float*>(stats);
+    a.dx_out = dx_out;
+    a.dh = dh;
+    a.dx = dx;
+    a.dbranch = dbranch;
+    a.dpost_weight = dpost_weight;
+    a.dgate = dgate;
+    a.dpre_weight = dpre_weight;
+    a.part = static_cast<float*>(ws);
+    a.err = err;
+    return launch_block_norm_backward(a, sms, st);
+  });
 }
 
 cbr_status_t cbr_rotary_forward(const cbr_rotary_desc_t* desc, const void* q, const void* k,
                                 const int32_t* positions, const int64_t* freq, const uint8_t* axis, void* q_out,
                                 void* k_out, cbr_stream_t stream) {
-  return (cbr_status_t)run(desc, q, k, positions, freq, axis, q_out, k_out, false,
-                           reinterpret_cast<cudaStream_t>(stream));
+  return guarded([&]() -> int {
+    return run(desc, q, k, positions, freq, axis, q_out, k_out, false,
+                             reinterpret_cast<cudaStream_t>(stream));
+  });
 }
 
 cbr_status_t cbr_rotary_backward(const cbr_rotary_desc_t* desc, const void* dq_out, const void* dk_out,
                                  const int32_t* positions, const int64_t* freq, const uint8_t* axis, void* dq,
                                  void* dk, cbr_stream_t stream) {
-  return (cbr_status_t)run(desc, dq_out, dk_out, positions, freq, axis, dq, dk, true,
-                           reinterpret_cast<cudaStream_t>(stream));
+  return guarded([&]() -> int {
+    return run(desc, dq_out, dk_out, positions, freq, axis, dq, dk, true,
+                             reinterpret_cast<cudaStream_t>(stream));
+  });
 }
 
 }  // extern "C"

@@ -56,3 +56,25 @@ def test_temperatures_at_the_end_of_the_range(lib):  # noqa: F811
     assert fb(lib, distill_desc(temp=4e-39)) == 1      # 1 / T is finite yet
     assert fb(lib, distill_desc(temp=5e-39)) in DEVICE_OR_OK
     assert fb(lib, distill_desc(temp=3e38)) in DEVICE_OR_OK
+
+
+def test_no_exception_leaves_an_entry(tmp_path):
+    """The guard around every entry's body: a status for what it returns, CBR_ERR_CUDA for what it throws."""
+    import os
+    import re
+    import shutil
+    import subprocess
+
+    from conv_batchnorm_relu_gb300 import build
+    src = tmp_path / "g.cpp"
+    src.write_text('#include <new>\n#include "token_ops.h"\nint main() {\n'
+                   '  if (cbr::guarded([] { return 3; }) != CBR_ERR_UNSUPPORTED) return 1;\n'
+                   '  if (cbr::guarded([]() -> int { throw std::bad_alloc(); }) != CBR_ERR_CUDA) return 2;\n'
+                   '  return 0;\n}\n')
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(shutil.which("nvcc") or build._nvcc()))), "include")
+    exe = str(tmp_path / "g")
+    subprocess.run(["g++", "-std=c++17", "-I", build.CSRC, "-I", cuda, str(src), "-o", exe], check=True)
+    assert subprocess.run([exe]).returncode == 0
+    text = open(os.path.join(build.CSRC, "tokens_api.cu")).read()
+    entries = re.findall(r"^cbr_status_t cbr_\w+\([^)]*\) \{\n(.*)$", text, re.M)
+    assert len(entries) == 8 and all(e.strip().startswith("return guarded(") for e in entries)
