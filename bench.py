@@ -230,25 +230,36 @@ def record_external(ev, stream):
         raise RuntimeError(f"cuEventRecordWithFlags failed ({rc})")
 
 
-def traffic_for(kernel: str, config_index: int):
+def source_sha256(source: str, csrc: str) -> str:
+    """Hash of a CUDA source of `csrc` and of the headers there that it includes, directly or not: what
+    its kernels are built from."""
+    import hashlib
+    import re
+    files, todo = set(), [source]
+    while todo:
+        fn = todo.pop()
+        if fn in files or not os.path.exists(os.path.join(csrc, fn)):
+            continue
+        files.add(fn)
+        with open(os.path.join(csrc, fn)) as f:
+            todo += re.findall(r'^\s*#\s*include\s+"([^"/]+)"', f.read(), re.M)
+    h = hashlib.sha256()
+    for fn in sorted(files):
+        with open(os.path.join(csrc, fn), "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()
+
+
+def traffic_for(kernel: str, config_index: int, csrc: str = os.path.join(ROOT, "conv_batchnorm_relu_gb300", "csrc")):
     """Per-launch DRAM bytes from a committed ncu summary of this workload, if it matches the
-    current source."""
+    current source of the kernel."""
     p = os.path.join(ROOT, "profiles", "traffic.json")
     if not os.path.exists(p):
         return None
-    import hashlib
     with open(p) as f:
         t = json.load(f)
     ent = t.get(f"config{config_index}", {}).get(kernel)
-    if not ent:
-        return None
-    h = hashlib.sha256()
-    csrc = os.path.join(ROOT, "conv_batchnorm_relu_gb300", "csrc")
-    for fn in sorted(os.listdir(csrc)):
-        if fn.endswith((".cu", ".cuh", ".h")):
-            with open(os.path.join(csrc, fn), "rb") as f:
-                h.update(f.read())
-    if ent.get("csrc_sha256") != h.hexdigest():
+    if not ent or ent.get("source_sha256") != source_sha256(ent["source"], csrc):
         return None
     return ent.get("bytes_per_launch")
 
