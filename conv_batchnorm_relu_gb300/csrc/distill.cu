@@ -1108,13 +1108,14 @@ int launch(const DistillArgs& a, int num_sms, cudaStream_t st) {
   cfg.gridDim = dim3(across);
   cfg.dynamicSmemBytes = p.smem;
   cfg.stream = st;
-  // how many clusters run at once: asked once for each launch shape
+  // how many clusters run at once: asked once for each launch shape and device
   static std::mutex mu;
-  static std::map<std::tuple<int, int, int>, int> at_once;
-  int clusters = 0;
+  static std::map<std::tuple<int, int, int, int>, int> at_once;
+  int clusters = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return CBR_ERR_CUDA;
   {
     std::lock_guard<std::mutex> lk(mu);
-    int& n = at_once[{threads, p.smem, across}];
+    int& n = at_once[{threads, p.smem, across, dev}];
     if (!n && cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
