@@ -1047,7 +1047,7 @@ __global__ void __maxnreg__(80)
       if (lane == 0) mbar_arrive(bar(&h.t_free[slot]));
     }
   }
-  if (!ok) report_error(a.err, kErrWaitHalo);
+  if (!ok) report_error(a.err, kErrWaitOperand);
   // no block leaves while another may still write to its shared memory
   if (across > 1) {
     __syncwarp();
