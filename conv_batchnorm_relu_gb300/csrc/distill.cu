@@ -40,7 +40,7 @@ using namespace tok;
 
 enum Mode { kLoss, kBoth, kGradient };
 
-constexpr int kMaxWarps = 16;       // consumers
+constexpr int kMaxWarps = 8;        // consumers
 constexpr int kMaxBuffers = 16;
 constexpr int kMaxCluster = 8;
 constexpr int kFewRows = 4;         // rows of a call whose rows are each shared by a cluster (make_plan)
@@ -501,7 +501,7 @@ __device__ void teach(const DistillArgs& a, long long row, const Fetched& f, flo
   }
 }
 
-// 80 registers: two blocks of 12 warps, or one of 20, on an SM.
+// 80 registers: two blocks of 12 warps on an SM.
 template <typename T, int kMode>
 __global__ void __maxnreg__(80)
     distill_kernel(const __grid_constant__ DistillArgs a, const __grid_constant__ Plan plan) {
@@ -1075,7 +1075,7 @@ Plan make_plan(const DistillArgs& a, int elt) {
   // Chunks of 32 KB for eight warps, two batches of vectors for each lane (2048x32000 bf16: 55 us; of 16
   // KB, one batch between waits: 64); smaller where the row is.
   p.part = 8;
-  p.warps = 8;
+  p.warps = kMaxWarps;
   while (p.warps > 1 && (p.warps << p.part) / 2 >= vectors) p.warps /= 2;
   while (p.part > 5 && (p.warps << p.part) / 2 >= vectors) --p.part;
   const int chunk = p.warps << p.part << 4;
@@ -1089,7 +1089,7 @@ Plan make_plan(const DistillArgs& a, int elt) {
 }
 
 template <typename T, int kMode>
-int launch(const DistillArgs& a, int num_sms, cudaStream_t st) {
+int launch(const DistillArgs& a, cudaStream_t st) {
   auto kernel = distill_kernel<T, kMode>;
   constexpr bool kAcross = kMode != kGradient;
   Plan p = make_plan(a, sizeof(T));
@@ -1133,21 +1133,21 @@ int launch(const DistillArgs& a, int num_sms, cudaStream_t st) {
 }
 
 template <typename T>
-int launch_of(const DistillArgs& a, bool backward, int num_sms, cudaStream_t st) {
-  if (backward) return launch<T, kGradient>(a, num_sms, st);
-  return a.dlogits ? launch<T, kBoth>(a, num_sms, st) : launch<T, kLoss>(a, num_sms, st);
+int launch_of(const DistillArgs& a, bool backward, cudaStream_t st) {
+  if (backward) return launch<T, kGradient>(a, st);
+  return a.dlogits ? launch<T, kBoth>(a, st) : launch<T, kLoss>(a, st);
 }
 
-int launch_any(const DistillArgs& a, bool backward, int num_sms, cudaStream_t st) {
-  if (a.d.dtype == CBR_F32) return launch_of<float>(a, backward, num_sms, st);
-  if (a.d.dtype == CBR_BF16) return launch_of<__nv_bfloat16>(a, backward, num_sms, st);
-  return launch_of<__half>(a, backward, num_sms, st);
+int launch_any(const DistillArgs& a, bool backward, cudaStream_t st) {
+  if (a.d.dtype == CBR_F32) return launch_of<float>(a, backward, st);
+  if (a.d.dtype == CBR_BF16) return launch_of<__nv_bfloat16>(a, backward, st);
+  return launch_of<__half>(a, backward, st);
 }
 
 }  // namespace
 
-int launch_distill(const DistillArgs& a, int num_sms, cudaStream_t st) { return launch_any(a, false, num_sms, st); }
+int launch_distill(const DistillArgs& a, cudaStream_t st) { return launch_any(a, false, st); }
 
-int launch_distill_backward(const DistillArgs& a, int num_sms, cudaStream_t st) { return launch_any(a, true, num_sms, st); }
+int launch_distill_backward(const DistillArgs& a, cudaStream_t st) { return launch_any(a, true, st); }
 
 }  // namespace cbr

@@ -1,4 +1,4 @@
-// Device helpers shared by the token operators: storage types, block reductions.
+// Device helpers shared by the token operators: storage types, sums and maxima over a warp.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -29,19 +29,10 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-// Element i of a buffer whose type is known at run time only (the teacher's short rows).
-__device__ __forceinline__ float load_as_float(const void* p, int dtype, long long i) {
-  if (dtype == CBR_F32) return static_cast<const float*>(p)[i];
-  if (dtype == CBR_BF16) return to_f(static_cast<const __nv_bfloat16*>(p)[i]);
-  return to_f(static_cast<const __half*>(p)[i]);
-}
-
 struct Sum {
-  static __device__ __forceinline__ float id() { return 0.f; }
   static __device__ __forceinline__ float of(float a, float b) { return a + b; }
 };
 struct Max {   // NaN if either is
-  static __device__ __forceinline__ float id() { return -INFINITY; }
   static __device__ __forceinline__ float of(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -61,18 +52,6 @@ __device__ __forceinline__ float warp_max(float v) {
   float r;
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
-}
-
-// Every thread of the block gets the result; `red` holds one float a warp (at most 32).
-template <typename Op>
-__device__ __forceinline__ float block_reduce(float v, float* red) {
-  v = warp_reduce<Op>(v);
-  __syncthreads();  // the last reduction's readers are done with red
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  const int warps = (blockDim.x + 31) >> 5;
-  v = (int)(threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : Op::id();
-  return warp_reduce<Op>(v);
 }
 
 // A place in a ring of buffers that are used in turn, and the parity of that use.

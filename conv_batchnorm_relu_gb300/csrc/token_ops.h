@@ -41,8 +41,8 @@ struct DistillArgs {
   uint32_t* err;
 };
 // Loss (and gradient, where dlogits is set) / gradient from the forward's stats (distill.cu).
-int launch_distill(const DistillArgs& a, int num_sms, cudaStream_t st);
-int launch_distill_backward(const DistillArgs& a, int num_sms, cudaStream_t st);
+int launch_distill(const DistillArgs& a, cudaStream_t st);
+int launch_distill_backward(const DistillArgs& a, cudaStream_t st);
 
 struct BlockNormArgs {
   cbr_block_norm_desc_t d;

@@ -58,7 +58,7 @@ int run(DistillArgs a, bool need_stats, bool need_grad, bool backward, cudaStrea
     return CBR_ERR_MISALIGNED;
   int sms = 0;
   if (const int e = device_for_call(&sms, &a.err)) return e;
-  return backward ? launch_distill_backward(a, sms, st) : launch_distill(a, sms, st);
+  return backward ? launch_distill_backward(a, st) : launch_distill(a, st);
 }
 
 int check(const cbr_block_norm_desc_t* d) {
