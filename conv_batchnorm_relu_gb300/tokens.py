@@ -61,6 +61,14 @@ def _bad(what: str, status: int = _INVALID):
     raise CBRError(status, what)
 
 
+def _pack(form: struct.Struct, *values) -> bytes:
+    """The descriptor; a number that its 32 bits cannot hold is refused like one that the library refuses."""
+    try:
+        return form.pack(*values)
+    except (struct.error, OverflowError) as e:
+        raise CBRError(_INVALID, f"arguments: {e}") from None
+
+
 def _dtype(t: torch.Tensor, what: str) -> int:
     code = _DTYPE.get(t.dtype)
     if code is None:
@@ -140,8 +148,8 @@ def _distill_args(logits, top_ids, top_logits, temperature, teacher_lse, row_wei
     s_id = _matrix(top_ids, (rows, k), top_ids.dtype, dev, "top_ids")
     s_top = _matrix(top_logits, (rows, k), top_logits.dtype, dev, "top_logits")
     s_out = vocab if dlogits is None else _matrix(dlogits, shape, logits.dtype, dev, "dlogits")
-    desc = _DISTILL.pack(rows, vocab, k, s, s_out, s_id, s_top, dtype, top_dtype, top_ids.element_size(),
-                         float(temperature))
+    desc = _pack(_DISTILL, rows, vocab, k, s, s_out, s_id, s_top, dtype, top_dtype, top_ids.element_size(),
+                 float(temperature))
     return desc, (logits.data_ptr(), top_ids.data_ptr(), top_logits.data_ptr(),
                   _vector(teacher_lse, rows, dev, "teacher_lse"), _vector(row_weight, rows, dev, "row_weight"))
 
@@ -258,8 +266,8 @@ def block_norm_forward(x, branch=None, post_weight=None, gate=None, pre_weight=N
     if want_stats:
         stats = _given(out, "stats", (rows, 4), torch.float32, dev)
     gate_rows, gate_at = _gate(gate, rows, dim, dev)
-    desc = _NORM.pack(rows, dim, gate_rows, s_x, s_f, s_xo, s_h, 0, 0, 0, 0, dtype, _kind(kind), eps, residual_scale,
-                      branch_scale)
+    desc = _pack(_NORM, rows, dim, gate_rows, s_x, s_f, s_xo, s_h, 0, 0, 0, 0, dtype, _kind(kind), eps, residual_scale,
+                 branch_scale)
     _check(_load().cbr_block_norm_forward(
         desc, x.data_ptr(), f_at, _vector(post_weight, dim, dev, "post_weight"), gate_at,
         _vector(pre_weight, dim, dev, "pre_weight"), xo_at, h_at, _vector(stats, 4 * rows, dev, "stats"),
@@ -275,7 +283,7 @@ def block_norm_workspace_size(rows: int, dim: int, dtype=torch.float16) -> int:
     size = _sizes.get(dim)
     if size is None:
         n = ctypes.c_size_t()
-        desc = _NORM.pack(rows, dim, 0, dim, dim, dim, dim, dim, dim, dim, dim, _DTYPE[dtype], 0, 1.0, 1.0, 1.0)
+        desc = _pack(_NORM, rows, dim, 0, dim, dim, dim, dim, dim, dim, dim, dim, _DTYPE[dtype], 0, 1.0, 1.0, 1.0)
         _check(_load().cbr_block_norm_workspace_size(desc, ctypes.byref(n)), "cbr_block_norm_workspace_size")
         size = _sizes[dim] = n.value
     return size
@@ -323,8 +331,8 @@ def block_norm_backward(dx_out, dh, x_out, branch=None, post_weight=None, gate=N
                 dgate.zero_()
     dx = _given(out, "dx", shape, dt, dev)
     s_dx = _matrix(dx, shape, dt, dev, "dx")
-    desc = _NORM.pack(rows, dim, gate_rows, dim, s_f, s_xo, dim, s_dxo, s_dh, s_dx, s_df, dtype, _kind(kind), 1.0,
-                      residual_scale, branch_scale)
+    desc = _pack(_NORM, rows, dim, gate_rows, dim, s_f, s_xo, dim, s_dxo, s_dh, s_dx, s_df, dtype, _kind(kind), 1.0,
+                 residual_scale, branch_scale)
     if ws is None:
         ws = _new((block_norm_workspace_size(rows, dim, dt),), torch.uint8, dev)
     elif ws.device != dev or not ws.is_contiguous():
@@ -428,7 +436,7 @@ def _rotary(f, q, k, positions, freq, axis, layout, out):
         sko, n, ko_at = _heads(k_out, batch, tokens, head_dim, dt, dev, "out[1]")
         if n != hk:
             _bad("out[1] has another number of heads")
-    desc = _ROTARY.pack(batch, tokens, *sq, *sk, *sqo, *sko, *sp, hq, hk, head_dim, 2 * pairs, p[-1], code, dtype)
+    desc = _pack(_ROTARY, batch, tokens, *sq, *sk, *sqo, *sko, *sp, hq, hk, head_dim, 2 * pairs, p[-1], code, dtype)
     _check(getattr(_load(), f)(desc, q_at, k_at, positions.data_ptr(), freq.data_ptr(), axis.data_ptr(), qo_at, ko_at,
                                _stream_of(dev)), f)
     return q_out, k_out

@@ -25,3 +25,19 @@ def test_a_workspace_elsewhere_or_shorter_than_it_looks_is_refused():
     for dtype, size in ((torch.uint8, 1), (torch.float32, 4)):
         got = call(torch.zeros(n // size, dtype=dtype, device="cuda"))
         assert torch.equal(got["dx"], want["dx"]) and torch.equal(got["dpre_weight"], want["dpre_weight"])
+
+
+@pytest.mark.parametrize("value", [1e39, -1e39, float("inf"), float("nan")])
+def test_numbers_that_32_bits_cannot_hold_are_refused(value):
+    x, w = torch.randn(3, 64, device="cuda"), torch.ones(64, device="cuda")
+    ids = torch.zeros(3, 1, dtype=torch.int32, device="cuda")
+    stats = torch.zeros(3, 4, device="cuda")
+    with pytest.raises(tokens.CBRError):
+        tokens.distill_forward(x, ids, x[:, :1], temperature=value)
+    with pytest.raises(tokens.CBRError):
+        tokens.block_norm_forward(x, pre_weight=w, eps=value)
+    for name in ("residual_scale", "branch_scale"):
+        with pytest.raises(tokens.CBRError):
+            tokens.block_norm_forward(x, x, w, None, w, **{name: value})
+        with pytest.raises(tokens.CBRError):
+            tokens.block_norm_backward(x, x, x, x, w, None, w, stats, **{name: value})
