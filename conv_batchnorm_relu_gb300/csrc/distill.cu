@@ -67,11 +67,11 @@ struct Header {
   uint64_t full[kMaxBuffers], done[kMaxBuffers], free[kMaxBuffers];
   // row by row: teacher's entries; its probabilities (kGradient: and the row's sums); no longer needed;
   // row's sums; the consumers' own sums; the cluster's sums
-  uint64_t t_full[kRows], m_full[kRows], t_free[kRows], r_full[kRows], c_full[2], x_full;
-  float red[2][kMaxWarps][4];       // (largest and sum, unlisted and listed) of each consumer
-  float xch[kMaxCluster][4];        // and of each block of the cluster
+  uint64_t t_full[kRows], m_full[kRows], t_free[kRows], r_full[kRows], c_full[2], x_full[2];
+  float red[2][kMaxWarps][4];       // (largest, unlisted, listed) of each consumer
+  float xch[2][kMaxCluster][4];     // and of each block of the cluster
   float teacher[kRows][4];          // mass, rest, weight, state
-  float result[kRows][4];           // of the row: largest, total, unlisted (as `share` has it); live (kGradient: dloss)
+  float result[kRows][4];           // of the row: largest, total, unlisted (as `dim_share` has it); live (kGradient: dloss)
 };
 enum { kMass, kRest, kWeight, kState };
 enum { kDead, kEmpty, kLive };    // weight 0 (not even loaded), nothing to learn from, the rest
@@ -237,14 +237,19 @@ template <typename T>
 __device__ __forceinline__ float exponential(float s, float top, float c) {
   return ex2<T>(is_far<T>(top, c) ? (s - top) * c : __fmaf_rn(s, c, -base_of(top, c)));
 }
-// What a sum relative to `from` is multiplied by to be relative to `to`, the larger: either may be far.
+// What a sum relative to `from` is multiplied by to be relative to `to`, the larger: either may be far, and
+// then the exponent is what is between a base and a logit.
 template <typename T>
 __device__ __forceinline__ float rebase(float from, float to, float c) {
-  if (from == -INFINITY) return 0.f;
-  float x;
-  if (is_far<T>(to, c)) x = is_far<T>(from, c) ? (from - to) * c : -__fmaf_rn(to, c, -base_of(from, c));
-  else x = is_far<T>(from, c) ? __fmaf_rn(from, c, -base_of(to, c)) : __fsub_rn(base_of(from, c), base_of(to, c));
-  return ex2<T>(x);
+  float e = (from - to) * c;
+  if constexpr (sizeof(T) == 4) {
+    const float x = base_of(from, c), y = base_of(to, c);
+    const bool near_x = fabsf(x) < kFar, near_y = fabsf(y) < kFar;
+    const float from_y = near_x ? __fsub_rn(x, y) : __fmaf_rn(from, c, -y);   // to near
+    const float to_x = -__fmaf_rn(to, c, -x);
+    e = near_y ? from_y : near_x ? to_x : e;
+  }
+  return from == -INFINITY ? 0.f : ex2<T>(e);
 }
 // The logarithm to base 2 of what a sum relative to `from` is multiplied by to be relative to the logit `to`.
 template <typename T>
@@ -284,9 +289,10 @@ __device__ __forceinline__ float largest(const uint4 (&w)[n]) {
   }
 }
 
-// A running (largest, sum of exponentials relative to it) of the unlisted words, the sum in two parts.
+// A running (largest, sum of exponentials relative to it) pair, the sum in three parts: two of unlisted
+// words, one of listed.
 struct Running {
-  float top = -INFINITY;
+  float top = -INFINITY, listed = 0.f;
   uint64_t sum = 0;
 };
 template <typename T>
@@ -294,28 +300,28 @@ __device__ __forceinline__ void raise(Running& r, float m, float c) {
   if (!(m <= r.top)) {   // NaN gets in, too, and stays
     m = Max::of(m, r.top);
     const float f = rebase<T>(r.top, m, c);
+    r.listed *= f;
     r.sum = m == m ? mul2(r.sum, pair(f, f)) : pair(m, m);
     r.top = m;
   }
 }
-// (largest, sum) of the unlisted words and of the listed ones, each sum relative to its own largest: the
-// unlisted mass has a logarithm even where it is nothing beside the listed one.
+// The same, merged over threads.
 struct Sums {
-  float top = -INFINITY, unlisted = 0.f;
-  float top_listed = -INFINITY, listed = 0.f;
+  float top = -INFINITY, unlisted = 0.f, listed = 0.f;
 };
 // The lanes' sums as one.
 template <typename T>
 __device__ __forceinline__ Sums merge_warp(Sums r, float c) {
-  const float m = warp_max(r.top), n = warp_max(r.top_listed);
-  uint64_t s = pair(r.unlisted * rebase<T>(r.top, m, c), r.listed * rebase<T>(r.top_listed, n, c));
+  const float m = warp_max(r.top);
+  const float f = rebase<T>(r.top, m, c);
+  uint64_t s = pair(r.unlisted * f, r.listed * f);
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     const float2 v = unpair(s);
     s = add2(s, pair(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
   }
   const float2 v = unpair(s);
-  return Sums{m, v.x, n, v.y};
+  return Sums{m, v.x, v.y};
 }
 
 // `rebase`, with the roundings of the exponent, which grow with the distance, put right: a row's unlisted
@@ -333,12 +339,13 @@ __device__ __forceinline__ float rebase_far_down(float from, float to, float c, 
 }
 // The unlisted words' part of a row's sum, relative to the row's largest logit `top`: as it is, or, where it
 // is below 2^-64 and a tail needs it, its logarithm to base 2 (negative), 0 below 2^-1074.  Words masked
-// with the type's lowest value are below that as are those at -infinity, and their row has no tail.
-constexpr float kFaint = 0x1p-64f, kLeast = -1074.f;
+// with the type's lowest value are below that as are those at -infinity, and their row has no tail.  From
+// 2^-32 down it is made from a sum of its own, relative to the largest unlisted logit: this is that.
+constexpr float kDim = 0x1p-32f, kFaint = 0x1p-64f, kLeast = -1074.f;
 template <typename T>
-__device__ __forceinline__ float share(const Sums& r, float top, float c, float c_low, bool tail) {
+__device__ __noinline__ float dim_share(Sums r, float top, float c, float c_low) {
   const float u = r.unlisted * rebase_far_down<T>(r.top, top, c, c_low);
-  if (!tail || u >= kFaint) return u;
+  if (u >= kFaint) return u;
   const float l = log2f(r.unlisted) + exponent<T>(r.top, top, c);
   return l < kLeast ? 0.f : l;
 }
@@ -350,7 +357,7 @@ struct Base {
   float base, sum, down;
 };
 template <typename T>
-__device__ __forceinline__ Base base_of_share(float share, float top, float c, float temperature) {
+__device__ __noinline__ Base base_of_share(float share, float top, float c, float temperature) {
   Base b;
   const float l = share < 0.f ? share : log2f(share);
   b.base = __fmaf_rn(l, temperature * 0.69314718f, top);
@@ -465,6 +472,7 @@ __device__ void teach(const DistillArgs& a, long long row, const Fetched& f, flo
 #pragma unroll
   for (int i = 0; i < kAhead; ++i)
     if (lane + i * 32 < k_n) put(lane + i * 32, f.id[i], f.logit[i]);
+#pragma unroll 1
   for (int k = lane + kAhead * 32; k < k_n; k += 32) put(k, raw_id(a, row, k), raw_logit(a, row, k));
   any = __any_sync(0xffffffffu, any);
   top = warp_max(top);
@@ -478,15 +486,18 @@ __device__ void teach(const DistillArgs& a, long long row, const Fetched& f, flo
   float mass = 1.f;
   if (!a.teacher_lse) {
     float s = 0.f;
+#pragma unroll 1
     for (int k = lane; k < k_n; k += 32) {
       const float l = (lp[k] - top) * inv_t;
       lp[k] = l;
       s += expf(l);   // 0 for an absent entry
     }
     const float norm = logf(warp_reduce<Sum>(s));
+#pragma unroll 1
     for (int k = lane; k < k_n; k += 32) lp[k] -= norm;
   } else {
     mass = 0.f;
+#pragma unroll 1
     for (int k = lane; k < k_n; k += 32) {
       const float t = lp[k], x = t * inv_t, low = __fmaf_rn(-x, a.d.temperature, t) * inv_t;
       const float l = (x - f.lse) + (fabsf(x) < INFINITY ? low : 0.f);   // an infinity leaves no remainder
@@ -501,7 +512,9 @@ __device__ void teach(const DistillArgs& a, long long row, const Fetched& f, flo
   }
 }
 
-// 80 registers: two blocks of 12 warps on an SM.
+// 80 registers: two blocks of 12 warps on an SM.  Loops stay rolled but for the vectors of a batch: unrolled,
+// a kernel of 100 KB of instructions (70 now) waited for them (the loss alone, 2048x32000 bf16: 34.5 us, 31.7
+// rolled; 32-bit 57.5, 55.3).
 template <typename T, int kMode>
 __global__ void __maxnreg__(80)
     distill_kernel(const __grid_constant__ DistillArgs a, const __grid_constant__ Plan plan) {
@@ -523,6 +536,7 @@ __global__ void __maxnreg__(80)
   const int across = kAcross ? plan.slices : 1;
   const int rank = across > 1 ? (int)(blockIdx.x % across) : 0;
   if (threadIdx.x == 0) {
+#pragma unroll 1
     for (int i = 0; i < buffers; ++i) {
       mbar_init(bar(&h.full[i]), 1);
       mbar_init(bar(&h.done[i]), plan.warps);
@@ -535,7 +549,7 @@ __global__ void __maxnreg__(80)
       mbar_init(bar(&h.r_full[i]), 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(bar(&h.c_full[i]), plan.warps);
-    mbar_init(bar(&h.x_full), across);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(&h.x_full[i]), across);
     fence_mbarrier_init();
   }
   if (across > 1) cluster_sync();
@@ -566,6 +580,7 @@ __global__ void __maxnreg__(80)
       Turn t;
       long long loads = 0;
       bool next_dead = first < items && dead_row(row_of(first));
+#pragma unroll 1
       for (long long i = first; ok && i < items; i += step) {
         const long long row = row_of(i);
         const bool dead = next_dead;
@@ -575,6 +590,7 @@ __global__ void __maxnreg__(80)
         const T* src = logits_at(row, begin);
         const Slice<T> s(src, slice_n(begin));
         const int chunks = chunks_of(s), again = dead ? 0 : again_of(chunks);
+#pragma unroll 1
         for (int q = 0; q < chunks + again; ++q) {
           // the buffer's last chunk was copied out before this one comes in
           if (loads >= buffers && !(ok = mbar_wait(bar(&h.free[t.slot]), t.parity ^ 1))) break;
@@ -593,6 +609,7 @@ __global__ void __maxnreg__(80)
         }
       }
       // no copy is in flight when the block ends, also where a wait ran out (else: all are complete)
+#pragma unroll 1
       for (long long l = max(0ll, loads - buffers); l < loads; ++l)
         ok &= mbar_wait(bar(&h.full[l % buffers]), (uint32_t)(l / buffers) & 1);
     }
@@ -607,6 +624,7 @@ __global__ void __maxnreg__(80)
         leaving = -1;
       };
       bool next_dead = first < items && dead_row(row_of(first));
+#pragma unroll 1
       for (long long i = first; ok && i < items; i += step) {
         const long long row = row_of(i);
         const bool dead = next_dead;
@@ -618,6 +636,7 @@ __global__ void __maxnreg__(80)
         const int passing = kMode == kLoss ? chunks : again, total = kMode == kLoss ? chunks : chunks + again;
         T* const dst = kMode == kLoss ? nullptr : grad_at(row, begin) - s.lead;
         const bool apart = (reinterpret_cast<uintptr_t>(dst) & 15) != 0;
+#pragma unroll 1
         for (int j = 0; j < total; ++j) {
           // the buffers go back as soon as they can, unless the next chunk is there already
           if (leaving >= 0 && !mbar_test(bar(&h.done[t.slot]), t.parity)) all_left();
@@ -659,6 +678,7 @@ __global__ void __maxnreg__(80)
       if (live) {
         const float log_total = logf(total * to_top);
         const float rest = part == 0.f ? 0.f : h.teacher[slot][kRest];
+#pragma unroll 1
         for (int k = lane; k < (int)a.d.topk; k += 32) {
           const float p = ids[k] >= 0 ? expf(lp[k]) : 0.f;
           if (!(p == 0.f)) l += p * (lp[k] - ((sk[k] - top) * inv_t - log_total));
@@ -680,6 +700,7 @@ __global__ void __maxnreg__(80)
     int n = start;   // of the block's rows
     Fetched next;
     if (first + n * step < items) fetch<kMode>(a, row_of(first + n * step), next);
+#pragma unroll 1
     for (long long i = first + n * step; ok && i < items; i += kTeachers * step, n += kTeachers) {
       const int slot = n % kRows;
       const Fetched now = next;
@@ -702,6 +723,7 @@ __global__ void __maxnreg__(80)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(&h.m_full[slot]));
     }
+#pragma unroll 1
     for (int m = max(start, n - kRows); ok && m < n; m += kTeachers) settle(row_of(first + m * step), m);
   } else {   // ---------------------------------------------------------------- consumers
     const int part = 1 << plan.part, k_n = (int)a.d.topk;
@@ -723,6 +745,7 @@ __global__ void __maxnreg__(80)
     };
     T next_edge = from_f<T>(0.f);
     if (plan.ragged && first < items) next_edge = edge_of(first);
+#pragma unroll 1
     for (long long i = first; i < items; i += step, ++n) {
       const long long row = row_of(i);
       const int begin = begin_of(i), slot = n % kRows;
@@ -745,6 +768,7 @@ __global__ void __maxnreg__(80)
       // This warp's entries.
       int count = 0;
       if (live) {
+#pragma unroll 1
         for (int k = lane; k < plan.kp; k += 32) {
           const int place = k < k_n ? ids[k] + shift : -1;
           const bool hit = s.inside(place) && is_mine(place);
@@ -759,6 +783,7 @@ __global__ void __maxnreg__(80)
       // Calls f(entry, place, round) for this warp's entries in chunk q.
       auto entries = [&](int q, auto f) {
         if (place0 >= 0 && place0 >> (chunk_bits + kLog) == q) f(k0, place0, 0);
+#pragma unroll 1
         for (int i = lane + 32, round = 1; i < count; i += 32, ++round) {
           const int k = mine[i], place = ids[k] + shift;
           if (place >> (chunk_bits + kLog) == q) f(k, place, round);
@@ -819,6 +844,7 @@ __global__ void __maxnreg__(80)
           entries(q, [&](int k, int place, int round) {
             if (!(found >> round & 1)) return;
             float v = __int_as_float(0x7fffffff);
+#pragma unroll 1
             for (int m = 0; m < count; ++m)
               if (ids[mine[m]] == ids[k] && __float_as_int(sk[mine[m]]) != 0x7fffffff) v = sk[mine[m]];
             sk[k] = v;
@@ -835,6 +861,7 @@ __global__ void __maxnreg__(80)
       if (two) {
         float based = -INFINITY, minus = 0.f;   // no base yet: every logit so far is -infinity
         bool far = false;
+#pragma unroll 1
         for (int q = 0; q < chunks; ++q) {
           if (!(ok = wait(bar(&h.full[t.slot]), t.parity))) break;
           if (live) {
@@ -865,12 +892,14 @@ __global__ void __maxnreg__(80)
               for (int k = 0; k < kCount; ++k) run.sum = add2(run.sum, e[k]);
             };
             int v = from + lane;
+#pragma unroll 1
             for (; v + (kBatch - 1) * 32 < to; v += kBatch * 32) {
               uint4 w[kBatch];
 #pragma unroll
               for (int k = 0; k < kBatch; ++k) w[k] = ld_shared_v4(at + (v + k * 32) * 16);
               add(w);
             }
+#pragma unroll 1
             for (; v < to; v += 32) {
               const uint4 w[1] = {ld_shared_v4(at + v * 16)};
               add(w);
@@ -886,51 +915,60 @@ __global__ void __maxnreg__(80)
         }
         if (!ok) break;
         const float2 f = unpair(run.sum);
-        Sums r{run.top, f.x + f.y};
+        const Sums own{run.top, f.x + f.y, 0.f};
+#pragma unroll 1
         for (int i = lane, round = 0; i < count; i += 32, ++round) {   // the listed words, each id once
           const float v = sk[mine[i]];
           if (!live || (twice >> round & 1) || v == -INFINITY) continue;
-          if (!(v <= r.top_listed)) {
-            const float m = Max::of(v, r.top_listed);
-            r.listed *= rebase<T>(r.top_listed, m, c);
-            r.top_listed = m;
-          }
-          r.listed += exponential<T>(v, r.top_listed, c);
+          raise<T>(run, v, c);
+          run.listed += exponential<T>(v, run.top, c);
         }
-        r = merge_warp<T>(r, c);
-        float(*const red)[4] = h.red[merges & 1];   // the last row's may still be read
-        if (lane == 0) {
-          red[warp][0] = r.top;
-          red[warp][1] = r.unlisted;
-          red[warp][2] = r.top_listed;
-          red[warp][3] = r.listed;
-          mbar_arrive(bar(&h.c_full[merges & 1]));
-        }
-        if (!(ok = wait(bar(&h.c_full[merges & 1]), merges >> 1 & 1))) break;
-        ++merges;
-        r = Sums{};
-        if (lane < plan.warps) r = Sums{red[lane][0], red[lane][1], red[lane][2], red[lane][3]};
-        r = merge_warp<T>(r, c);
-        if (across > 1 && live) {
-          if (warp == 0 && lane < across) {
-            const uint32_t to = map_to_rank(smem_u32(h.xch[rank]), lane);
-            st_cluster(to, r.top);
-            st_cluster(to + 4, r.unlisted);
-            st_cluster(to + 8, r.top_listed);
-            st_cluster(to + 12, r.listed);
-            arrive_cluster(map_to_rank(bar(&h.x_full), lane));
-          }
-          if (!(ok = __all_sync(0xffffffffu, wait_cluster(bar(&h.x_full), 0)))) break;
-          r = Sums{};
-          if (lane < across) r = Sums{h.xch[lane][0], h.xch[lane][1], h.xch[lane][2], h.xch[lane][3]};
+        const float2 g = unpair(run.sum);
+        Sums r{run.top, g.x + g.y, run.listed};
+        // The consumers' sums as one, and the cluster's, for everyone; where the unlisted share is dim, once
+        // more for the unlisted words alone.  A cluster's blocks may be one exchange apart: each has its barrier.
+#pragma unroll 1
+        for (int exchange = 0;; ++exchange) {
           r = merge_warp<T>(r, c);
+          float(*const red)[4] = h.red[merges & 1];   // the last merge's may still be read
+          if (lane == 0) {
+            red[warp][0] = r.top;
+            red[warp][1] = r.unlisted;
+            red[warp][2] = r.listed;
+            mbar_arrive(bar(&h.c_full[merges & 1]));
+          }
+          if (!(ok = wait(bar(&h.c_full[merges & 1]), merges >> 1 & 1))) break;
+          ++merges;
+          r = Sums{};
+          if (lane < plan.warps) r = Sums{red[lane][0], red[lane][1], red[lane][2]};
+          r = merge_warp<T>(r, c);
+          if (across > 1 && live) {
+            float(*const xch)[4] = h.xch[exchange];
+            if (warp == 0 && lane < across) {
+              const uint32_t to = map_to_rank(smem_u32(xch[rank]), lane);
+              st_cluster(to, r.top);
+              st_cluster(to + 4, r.unlisted);
+              st_cluster(to + 8, r.listed);
+              arrive_cluster(map_to_rank(bar(&h.x_full[exchange]), lane));
+            }
+            if (!(ok = __all_sync(0xffffffffu, wait_cluster(bar(&h.x_full[exchange]), 0)))) break;
+            r = Sums{};
+            if (lane < across) r = Sums{xch[lane][0], xch[lane][1], xch[lane][2]};
+            r = merge_warp<T>(r, c);
+          }
+          if (exchange == 0) {
+            top = r.top;
+            total = r.unlisted + r.listed;
+            part_u = r.unlisted;
+            live = live && top != -INFINITY;
+            if (!(a.teacher_lse && live && part_u < kDim)) break;   // the same for every consumer of the cluster
+            r = own;
+          } else {
+            part_u = dim_share<T>(r, top, c, plan.c_low);
+            break;
+          }
         }
-        top = Max::of(r.top, r.top_listed);
-        live = live && top != -INFINITY;
-        if (live) {
-          total = r.unlisted * rebase<T>(r.top, top, c) + r.listed * rebase<T>(r.top_listed, top, c);
-          part_u = share<T>(r, top, c, plan.c_low, a.teacher_lse != nullptr);
-        }
+        if (!ok) break;
       }
       if (kAcross && threadIdx.x == 0) {
         h.result[slot][0] = top;
@@ -973,6 +1011,7 @@ __global__ void __maxnreg__(80)
         auto entry_p = [&](int k) {
           if (!repeated) return expf(lp[k]);
           float pk = 0.f;
+#pragma unroll 1
           for (int m = 0; m < count; ++m)
             if (ids[mine[m]] == ids[k]) pk += expf(lp[mine[m]]);
           return pk;
@@ -982,6 +1021,7 @@ __global__ void __maxnreg__(80)
         };
         const float p0 = live && k0 >= 0 ? entry_p(k0) : 0.f;
         const T g0 = kMode == kBoth && live && k0 >= 0 ? entry_gradient(sk[k0], p0) : from_f<T>(0.f);
+#pragma unroll 1
         for (int j = 0; j < chunks; ++j) {
           const int q = j < chunks - again ? j + again : j - (chunks - again);   // those that stayed come first
           const bool came = !two || j >= chunks - again;
@@ -1004,6 +1044,7 @@ __global__ void __maxnreg__(80)
           };
           int v = from + lane;
           if (!apart)
+#pragma unroll 1
             for (; v + (kBatch - 1) * 32 < to; v += kBatch * 32) {
               uint4 w[kBatch];
 #pragma unroll
@@ -1011,6 +1052,7 @@ __global__ void __maxnreg__(80)
 #pragma unroll
               for (int k = 0; k < kBatch; ++k) st_shared_v4(at + (v + k * 32) * 16, turn(w[k]));
             }
+#pragma unroll 1
           for (; v < to; v += 32) {
             const uint4 w = turn(ld_shared_v4(at + v * 16));
             if (!apart) {
