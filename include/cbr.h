@@ -408,9 +408,10 @@ cbr_status_t cbr_distill_forward_backward(const cbr_distill_desc_t* desc, const 
  *   x_out = residual_scale x + branch_scale gate n     the join
  *   h     = (x_out - m2) r2 pre_weight                 the norm before the next block
  * with r = 1 / sqrt(mean((a - m)^2) + eps) over a row, m its mean (CBR_NORM_LAYER) or 0
- * (CBR_NORM_RMS).  h is computed from x_out before it is rounded.  Sums are kept in fp32: r is 0 for
- * a row whose squares pass its range, as for one with an infinity.  Either half may stand alone:
- * post_weight and branch NULL: h = norm of x (there is no x_out); pre_weight NULL: x_out only.
+ * (CBR_NORM_RMS); neither kind has a bias.  h is computed from x_out before it is rounded.  Sums are
+ * kept in fp32: r is 0 for a row whose squares pass its range, as for one with an infinity.  Either
+ * half may stand alone: post_weight and branch NULL: h = norm of x (there is no x_out); pre_weight
+ * NULL: x_out only.
  * gate [rows / gate_rows][dim]: one row for each gate_rows consecutive rows (gate_rows = rows: one
  * gate vector; 1: a gate for every row); NULL: no gate.  Weights, gate and their gradients are
  * fp32, the rest has the storage dtype.
