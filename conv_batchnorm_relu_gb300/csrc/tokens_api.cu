@@ -1,8 +1,8 @@
 // C ABI of the token operators (declared in include/cbr.h): argument checks and dispatch.
 #include <algorithm>
 #include <cmath>
-#include <utility>
 
+#include "api_checks.h"
 #include "cbr_internal.h"
 #include "token_ops.h"
 
@@ -11,25 +11,6 @@ namespace {
 
 constexpr int64_t kMaxVocab = 393216, kMaxTopk = 1024, kMaxDim = 16384;
 constexpr int kMaxHeadDim = 1024, kMaxAxes = 8;
-// Row counts and strides up to 2^40, and an axis' steps times its stride up to 2^58 elements: a tensor's
-// axes together stay within 2^62 bytes.
-constexpr int64_t kMaxExtent = int64_t(1) << 40, kMaxReach = int64_t(1) << 58;
-
-bool known_dtype(int32_t t) { return t == CBR_F16 || t == CBR_BF16 || t == CBR_F32; }
-size_t elt(int32_t t) { return t == CBR_F32 ? 4 : 2; }
-bool off(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
-bool extent(int64_t v) { return v >= 0 && v <= kMaxExtent; }
-bool finite(float v) { return std::isfinite(v); }
-
-bool in_reach(int64_t stride, int64_t steps) { return steps <= 1 || stride <= kMaxReach / (steps - 1); }
-
-// A row stride: at least the row (any value will do where there is one row at most).
-bool row_stride(int64_t s, int64_t width, int64_t rows) { return extent(s) && (rows <= 1 || s >= width) && in_reach(s, rows); }
-
-// An output that is an input must be it exactly.
-bool same_or_apart(const void* out, int64_t out_stride, const void* in, int64_t in_stride, int64_t rows) {
-  return out != in || !in || rows <= 1 || out_stride == in_stride;
-}
 
 int check(const cbr_distill_desc_t* d) {
   if (!d) return CBR_ERR_INVALID_ARG;
@@ -95,27 +76,11 @@ int check(const cbr_rotary_desc_t* d) {
   return CBR_OK;
 }
 
-// The heads of an output must not share memory: taken by their strides, each axis of several steps
-// steps past all that the smaller ones reach.
-bool distinct(const cbr_rotary_desc_t& d, const int64_t* s, int32_t heads) {
-  std::pair<int64_t, int64_t> axes[3] = {{s[0], d.batch}, {s[1], d.tokens}, {s[2], heads}};   // stride, steps
-  std::sort(axes, axes + 3);
-  int64_t reach = d.head_dim;
-  for (const auto& [stride, steps] : axes) {
-    if (steps <= 1) continue;
-    if (stride < reach) return false;
-    reach += stride * (steps - 1);
-  }
-  return true;
-}
-
-bool same(const int64_t* a, const int64_t* b) { return a[0] == b[0] && a[1] == b[1] && a[2] == b[2]; }
-
 int run(const cbr_rotary_desc_t* desc, const void* q, const void* k, const int32_t* positions, const int64_t* freq,
         const uint8_t* axis, void* q_out, void* k_out, bool backward, cudaStream_t st) {
   if (const int e = check(desc)) return e;
   const cbr_rotary_desc_t& d = *desc;
-  if ((d.heads_q && !distinct(d, d.q_out_stride, d.heads_q)) || (d.heads_k && !distinct(d, d.k_out_stride, d.heads_k)))
+  if ((d.heads_q && !distinct(d.q_out_stride, d.batch, d.tokens, d.heads_q, d.head_dim)) || (d.heads_k && !distinct(d.k_out_stride, d.batch, d.tokens, d.heads_k, d.head_dim)))
     return CBR_ERR_INVALID_ARG;
   if (d.batch == 0 || d.tokens == 0 || d.heads_q + d.heads_k == 0) return CBR_OK;
   if ((d.heads_q && (!q || !q_out)) || (d.heads_k && (!k || !k_out)) || !positions || !freq || !axis)

@@ -104,7 +104,7 @@ _empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None
 
 def _new(shape, dtype, dev) -> torch.Tensor:
     """A new contiguous tensor on the current device."""
-    if _empty_cuda is None:
+    if _empty_cuda is None or not shape:
         return torch.empty(shape, dtype=dtype, device=dev)
     strides = [1]
     for n in shape[:0:-1]:

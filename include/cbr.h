@@ -494,6 +494,113 @@ cbr_status_t cbr_rotary_backward(const cbr_rotary_desc_t* desc, const void* dq_o
                                  const int32_t* positions, const int64_t* freq, const uint8_t* axis, void* dq,
                                  void* dk, cbr_stream_t stream);
 
+/* ======================================================================= trunk operators
+ *
+ * Attention over a trunk's tokens, group norm with an activation over NHWC feature maps, and the
+ * clipping that ends a training step.  The token operators' conventions hold (strides in elements,
+ * device data is never trusted, an empty output is nothing to do); results repeat bit for bit.
+ */
+
+/*
+ * Attention.  q [batch][q_tokens][heads_q][head_dim], k and v [batch][k_tokens][heads_k][head_dim];
+ * heads_q = G heads_k, and query head h reads key head h / G.  Query i of sequence b sees key j if
+ *   j < key_lengths[b]              (NULL: k_tokens; taken into [0, k_tokens])
+ *   j <= query_start[b] + i         (causal only; NULL: 0.  The place of the sequence's first query
+ *                                    among its keys; may be negative)
+ *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp s_ij,  p_ij = exp(s_ij - lse_i),  o_i = sum_j p_ij v_j
+ * over the keys it sees.  A query that sees none has o = 0, lse = -infinity and dq = 0.  Keys and values
+ * from key_lengths on are not used, whatever stands there (NaN included).  Sums are kept in fp32; p and
+ * ds enter the second products rounded to the storage dtype, as q, k and v are.
+ * Types: CBR_F16 and CBR_BF16 (the products run on the tensor cores' 16-bit instructions).  head_dim: a
+ * multiple of 8 up to 128.  Addresses are 16-byte aligned and strides multiples of 8 elements (those of
+ * an axis with one step are not looked at).  An input may repeat over sequences or heads (stride 0).
+ */
+typedef struct {
+  int64_t batch, q_tokens, k_tokens;                               /* >= 0; tokens up to 2^30 */
+  int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];      /* elements between sequences, tokens, heads */
+  int64_t do_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];  /* backward */
+  int32_t heads_q, heads_k, head_dim;
+  int32_t causal, dtype;
+  float scale;                                                     /* finite, >= 0 */
+} cbr_attention_desc_t;
+
+/* Workspace bytes of the two calls for this desc (either pointer may be NULL). */
+cbr_status_t cbr_attention_workspace_size(const cbr_attention_desc_t* desc, size_t* fwd_bytes, size_t* bwd_bytes);
+
+/*
+ * Forward -> o [batch][q_tokens][heads_q][head_dim], lse [batch][heads_q][q_tokens] fp32, contiguous (NULL:
+ * not wanted).  o may not be q, k or v.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, WORKSPACE, DEVICE, CUDA.
+ */
+cbr_status_t cbr_attention_forward(const cbr_attention_desc_t* desc, const void* q, const void* k, const void* v,
+                                   const int32_t* key_lengths, const int32_t* query_start, void* o, float* lse,
+                                   void* ws, size_t ws_bytes, cbr_stream_t stream);
+
+/*
+ * Backward, from the gradient at o and the forward's o and lse; the probabilities are computed again.
+ *   D_i = do_i . o_i,  dp_ij = do_i . v_j,  ds_ij = p_ij (dp_ij - D_i)
+ *   dv_j = sum_i p_ij do_i,  dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
+ * dk and dv of a key head are summed over the query heads that read it; they are 0 from key_lengths on.
+ * No output may be an input.
+ */
+cbr_status_t cbr_attention_backward(const cbr_attention_desc_t* desc, const void* d_o, const void* q, const void* k,
+                                    const void* v, const void* o, const float* lse, const int32_t* key_lengths,
+                                    const int32_t* query_start, void* dq, void* dk, void* dv, void* ws,
+                                    size_t ws_bytes, cbr_stream_t stream);
+
+/*
+ * Group norm with an activation, channels last.  x [images][pixels][channels], the channels in `groups`
+ * groups of channels / groups neighbours; m and v are the mean and biased variance of a group's pixels of
+ * one image, r = 1 / sqrt(v + eps):
+ *   y = act(gamma (x - m) r + beta),   act(z) = z, max(0, z), or z / (1 + exp(-z))
+ * gamma, beta and their gradients are fp32 [channels]; both NULL: 1 and 0.  Statistics are fp32, merged
+ * from partial means and squared deviations, so a mean far from 0 costs no digits.
+ */
+typedef enum { CBR_ACT_NONE = 0, CBR_ACT_RELU = 1, CBR_ACT_SILU = 2 } cbr_act_t;
+typedef struct {
+  int64_t images, pixels;              /* >= 0; images up to 2^31 - 1, pixels up to 2^31 - 1 */
+  int64_t x_stride[2], y_stride[2];    /* elements between images and pixels (>= channels) */
+  int64_t dy_stride[2], dx_stride[2];  /* backward */
+  int32_t channels, groups;            /* channels: 1 .. 16384, a multiple of groups */
+  int32_t act, dtype;
+  float eps;                           /* > 0 (forward) */
+} cbr_group_norm_desc_t;
+
+/* Workspace bytes of the backward for this desc: the parameter gradients' partial sums. */
+cbr_status_t cbr_group_norm_workspace_size(const cbr_group_norm_desc_t* desc, size_t* bytes);
+
+/* Forward -> y, mean and rstd [images][groups] fp32.  y may be x itself (same strides). */
+cbr_status_t cbr_group_norm_forward(const cbr_group_norm_desc_t* desc, const void* x, const float* gamma,
+                                    const float* beta, void* y, float* mean, float* rstd, cbr_stream_t stream);
+
+/*
+ * Backward, from x and the forward's mean and rstd.  With xh = (x - m) r, z = gamma xh + beta,
+ * g = dy act'(z) (0 where z <= 0 for the ReLU), and means over a group's pixels of one image:
+ *   dx = r (gamma g - mean(gamma g) - xh mean(gamma g xh)),  dgamma = sum g xh,  dbeta = sum g
+ * dx may be dy itself (same strides); dgamma and dbeta are NULL where gamma is.
+ */
+cbr_status_t cbr_group_norm_backward(const cbr_group_norm_desc_t* desc, const void* dy, const void* x,
+                                     const float* gamma, const float* beta, const float* mean, const float* rstd,
+                                     void* dx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                                     cbr_stream_t stream);
+
+/*
+ * The norm of a set of gradients, and their clipping to it:
+ *   norm = unscale sqrt(sum of all squares),   scale = unscale min(1, max_norm / norm)   (norm 0: unscale)
+ *   out_i = scale grad_i
+ * unscale (finite, > 0) takes a loss scale off.  grads, outs, sizes and dtypes are host arrays of `count` device
+ * addresses, numbers of elements and types (f32, f16, bf16 in any mixture); the addresses are read before
+ * the call returns.  Gradients are contiguous and aligned to their element; an out may be its gradient (it is
+ * then not written where scale is 1) and may not overlap another gradient or out.  outs NULL: only norm
+ * and scale (max_norm may be infinity).  norm and scale are fp32 scalars.  Squares are summed so that none
+ * overflows or underflows: a norm past the range of fp32 reads as infinity, but scale goes by its value.  An
+ * infinite gradient makes scale 0 (max_norm finite), a NaN makes norm and scale NaN; gradients are scaled
+ * all the same.
+ */
+cbr_status_t cbr_clip_workspace_size(int64_t count, size_t* bytes);
+cbr_status_t cbr_clip_gradients(int64_t count, const void* const* grads, const int64_t* sizes, const int32_t* dtypes,
+                                void* const* outs, float max_norm, float unscale, float* norm, float* scale,
+                                void* ws, size_t ws_bytes, cbr_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
