@@ -137,16 +137,7 @@ int backward(const AttentionArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t attention_forward_ws(const cbr_attention_desc_t&) { return 0; }
 size_t attention_backward_ws(const cbr_attention_desc_t& d) { return (size_t)d.batch * d.heads_q * d.q_tokens * 4; }
-
-int launch_attention(const AttentionArgs& a, cudaStream_t st) {
-  const int64_t rows = a.d.batch * a.d.heads_q * a.d.q_tokens;
-  const unsigned grid = (unsigned)((rows + kWarps - 1) / kWarps);
-  if (a.d.dtype == CBR_BF16) query_kernel<__nv_bfloat16, false><<<grid, 32 * kWarps, 0, st>>>(a);
-  else query_kernel<__half, false><<<grid, 32 * kWarps, 0, st>>>(a);
-  return launched();
-}
 
 int launch_attention_backward(const AttentionArgs& a, cudaStream_t st) {
   return a.d.dtype == CBR_BF16 ? backward<__nv_bfloat16>(a, st) : backward<__half>(a, st);

@@ -1,0 +1,166 @@
+// What the attention kernels share: tiles, masks, the load of keys and values, TMEM rows.
+//
+// Every kernel works on tiles of 128 tokens of one head.  A tile in shared memory is kDim / 64 slabs of
+// [128 rows][128 bytes] in the 128-byte swizzle, as the tensor maps write them; it serves as a K-major
+// operand (rows along M or N, the head's elements along K) and as an MN-major one (rows along K).  Heads of
+// up to 64 (128) elements fill kDim = 64 (128); the maps fill the rest with zeros.
+#pragma once
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "cbr_internal.h"
+#include "common.cuh"
+#include "token_ops.cuh"
+#include "trunk_ops.h"
+
+namespace cbr {
+namespace att {
+
+constexpr int kTile = 128;
+constexpr int64_t kSms = 152;        // of the device that the rules on blocks are made for
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+__host__ __device__ constexpr int tile_bytes(int dim) { return kTile * dim * 2; }
+constexpr int kSlab = kTile * 128;   // bytes of a slab
+
+// exp2 in one instruction (relative error 2^-22); 0 below 2^-126.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A tensor map's coordinates of a head: rows of a tile are (token, packed head) pairs, `pack` neighbouring
+// query heads to a token, so that the heads that share a key head can share its tiles.  An axis that repeats
+// (stride 0) is one step in its map: its factor is 0 and its coordinate stays 0.
+struct Place {
+  int32_t head, batch;   // factors, 1 or 0
+};
+
+// Kernel parameters beside the maps.
+struct Params {
+  const int32_t* key_lengths;
+  const int32_t* query_start;
+  int32_t q_tokens, k_tokens, heads_q, heads_k, group, head_dim, causal;
+  int32_t pack;          // query heads in a tile's rows: 1 or the group
+  int32_t tile_tokens;   // queries in a tile: 128 / pack
+  int32_t tiles;         // tiles of queries that a block takes
+  int32_t q_blocks;      // blocks along the queries
+  int32_t splits;        // blocks that share a tile's keys
+  float scale;
+  Place q, k, v, d_o;
+  uint32_t* err;
+};
+
+// Keys of sequence b.
+__device__ __forceinline__ int keys_of(const Params& a, int b) {
+  return a.key_lengths ? min(max(a.key_lengths[b], 0), a.k_tokens) : a.k_tokens;
+}
+// The place of sequence b's first query, kept within a range in which sums of tokens (up to 2^29) cannot
+// overflow: beyond the last key, or so far before the first that no query sees one, all are alike.
+__device__ __forceinline__ int start_of(const Params& a, int b) {
+  return a.query_start ? min(max(a.query_start[b], -(1 << 30)), a.k_tokens) : 0;
+}
+
+// scale log2(e); above 0, so that a hidden score's -infinity stays one (10^-35 of a score is 0 beside 1).
+__device__ __forceinline__ float exponent_scale(const Params& a) { return fmaxf(a.scale * kLog2e, 1e-35f); }
+
+// A tile of keys or values (128 rows from `row` on of one head), by one thread: kDim / 64 boxes.
+template <int kDim>
+__device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap* map, const Place& p, int row, int head, int batch,
+                                          uint32_t bar) {
+  mbar_arrive_expect_tx(bar, tile_bytes(kDim));
+#pragma unroll
+  for (int i = 0; i < kDim / 64; ++i) tma_load_4d(dst + i * kSlab, map, 64 * i, row, head * p.head, batch * p.batch, bar);
+}
+
+// A tile of queries (or of what has their shape): `tile_tokens` tokens of `pack` heads; the rows that are left of the
+// 128 keep what they held.  head: counted in packs.
+template <int kDim>
+__device__ __forceinline__ void load_queries(uint32_t dst, const CUtensorMap* map, const Params& a, const Place& p, int token,
+                                             int head, int batch, uint32_t bar) {
+  mbar_arrive_expect_tx(bar, a.tile_tokens * a.pack * kDim * 2);
+#pragma unroll
+  for (int i = 0; i < kDim / 64; ++i)
+    tma_load_5d(dst + i * kSlab, map, 64 * i, 0, token, head * p.head, batch * p.batch, bar);
+}
+
+// Rows from `first` on of a tile set to zero by one warp, visible to the tensor cores afterwards.
+template <int kDim>
+__device__ __forceinline__ void clear_rows(uint32_t dst, int first, int lane) {
+  for (int c = first * 8 + lane; c < kTile * 8; c += 32)
+#pragma unroll
+    for (int i = 0; i < kDim / 64; ++i) st_shared_v4(dst + i * kSlab + c * 16, make_uint4(0, 0, 0, 0));
+  fence_proxy_async_smem();
+}
+
+// K-major and MN-major descriptors of a tile; a step of 16 along K is `k_step(k)` bytes further.
+__device__ __forceinline__ uint64_t k_major(uint32_t tile) { return make_sw128_desc(tile, 16, 1024, 0); }
+__device__ __forceinline__ uint64_t mn_major(uint32_t tile) { return make_sw128_desc(tile, kSlab, 1024, 0); }
+__device__ __forceinline__ constexpr uint64_t k_major_step(int k) { return (uint64_t)(((k >> 2) * kSlab + (k & 3) * 32) >> 4); }
+__device__ __forceinline__ constexpr uint64_t mn_major_step(int k) { return (uint64_t)((k * 2048) >> 4); }
+
+// 16-bit results of a row, eight at a time.
+template <bool BF16>
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack2<BF16>(v[0], v[1]), pack2<BF16>(v[2], v[3]), pack2<BF16>(v[4], v[5]), pack2<BF16>(v[6], v[7]));
+}
+
+// ---------------------------------------------------------------- host side
+
+// A map's axis: its steps and bytes between them; one that has a single step, or repeats, is one step.
+struct Axis {
+  uint64_t steps, bytes;
+};
+inline Axis axis(int64_t steps, int64_t stride) {
+  return steps <= 1 || stride == 0 ? Axis{1, 16} : Axis{(uint64_t)steps, (uint64_t)stride * 2};
+}
+inline bool map_of(CUtensorMap* map, const cbr_attention_desc_t& d, const void* p, int rank, const Axis* axes, const uint32_t* box) {
+  uint64_t dims[5] = {(uint64_t)d.head_dim}, strides[4];
+  for (int i = 1; i < rank; ++i) dims[i] = axes[i - 1].steps, strides[i - 1] = axes[i - 1].bytes;
+  return encode_tiled(map, d.dtype == CBR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, p, dims,
+                      strides, box);
+}
+
+// Keys or values: [batch][heads_k][tokens][head_dim], boxes of 128 tokens and 64 elements.
+inline bool key_map(CUtensorMap* map, const cbr_attention_desc_t& d, const void* p, const int64_t* s) {
+  const Axis axes[3] = {axis(std::max<int64_t>(d.k_tokens, 1), s[1]), axis(d.heads_k, s[2]), axis(d.batch, s[0])};
+  const uint32_t box[4] = {64, kTile, 1, 1};
+  return map_of(map, d, p, 4, axes, box);
+}
+
+// Queries, or what has their shape: [batch][heads_q / pack][tokens][pack][head_dim].
+inline bool query_map(CUtensorMap* map, const cbr_attention_desc_t& d, const void* p, const int64_t* s, int pack) {
+  const Axis axes[4] = {axis(pack, s[2]), axis(d.q_tokens, s[1]), axis(d.heads_q / pack, s[2] * pack), axis(d.batch, s[0])};
+  const uint32_t box[5] = {64, (uint32_t)pack, (uint32_t)(kTile / pack), 1, 1};
+  return map_of(map, d, p, 5, axes, box);
+}
+
+inline Place place(const int64_t* s) { return Place{s[2] != 0, s[0] != 0}; }
+
+inline Params params_of(const AttentionArgs& g, int pack) {
+  const cbr_attention_desc_t& d = g.d;
+  Params p{};
+  p.key_lengths = g.key_lengths;
+  p.query_start = g.query_start;
+  p.q_tokens = (int32_t)d.q_tokens;
+  p.k_tokens = (int32_t)d.k_tokens;
+  p.heads_q = d.heads_q;
+  p.heads_k = d.heads_k;
+  p.group = d.heads_q / d.heads_k;
+  p.head_dim = d.head_dim;
+  p.causal = d.causal;
+  p.pack = pack;
+  p.tile_tokens = kTile / pack;
+  p.scale = d.scale;
+  p.q = place(d.q_stride);
+  p.k = place(d.k_stride);
+  p.v = place(d.v_stride);
+  p.d_o = place(d.do_stride);
+  p.err = g.err;
+  return p;
+}
+
+}  // namespace att
+}  // namespace cbr

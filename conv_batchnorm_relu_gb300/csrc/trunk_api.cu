@@ -7,7 +7,7 @@
 namespace cbr {
 namespace {
 
-constexpr int64_t kMaxTokens = int64_t(1) << 30, kMaxBlocks = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxTokens = int64_t(1) << 29, kMaxBlocks = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxByteStride = int64_t(1) << 39;   // elements of 16 bits: what a tensor map can hold
 constexpr int kMaxAttentionDim = 128, kMaxHeads = 65536, kMaxChannels = 16384;
 constexpr int64_t kMaxTensors = int64_t(1) << 20;

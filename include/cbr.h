@@ -516,7 +516,7 @@ cbr_status_t cbr_rotary_backward(const cbr_rotary_desc_t* desc, const void* dq_o
  * an axis with one step are not looked at).  An input may repeat over sequences or heads (stride 0).
  */
 typedef struct {
-  int64_t batch, q_tokens, k_tokens;                               /* >= 0; tokens up to 2^30 */
+  int64_t batch, q_tokens, k_tokens;                               /* >= 0; tokens up to 2^29 */
   int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];      /* elements between sequences, tokens, heads */
   int64_t do_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];  /* backward */
   int32_t heads_q, heads_k, head_dim;
