@@ -76,11 +76,14 @@ __device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap* map, 
 }
 
 // A tile of queries (or of what has their shape): `tile_tokens` tokens of `pack` heads; the rows that are left of the
-// 128 keep what they held.  head: counted in packs.
+// 128 keep what they held.  head: counted in packs.  The barrier's thread has announced query_bytes() for each.
+template <int kDim>
+__device__ __forceinline__ uint32_t query_bytes(const Params& a) {
+  return a.tile_tokens * a.pack * kDim * 2;
+}
 template <int kDim>
 __device__ __forceinline__ void load_queries(uint32_t dst, const CUtensorMap* map, const Params& a, const Place& p, int token,
                                              int head, int batch, uint32_t bar) {
-  mbar_arrive_expect_tx(bar, a.tile_tokens * a.pack * kDim * 2);
 #pragma unroll
   for (int i = 0; i < kDim / 64; ++i)
     tma_load_5d(dst + i * kSlab, map, 64 * i, 0, token, head * p.head, batch * p.batch, bar);

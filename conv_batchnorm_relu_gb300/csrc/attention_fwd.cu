@@ -110,9 +110,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kLoadWarp) {
     if (last > begin) {
       if (lane == 0) {
+        mbar_arrive_expect_tx(bar_q, ((end[0] > begin) + (end[1] > begin)) * query_bytes<kDim>(a));
         for (int t = 0; t < 2; ++t)
           if (end[t] > begin)
-            load_queries<kDim>(sbase + L::kQ + t * tile_bytes(kDim), &map_q, a, a.q, token0 + t * a.tile_tokens, head, batch, bar_q + 0);
+            load_queries<kDim>(sbase + L::kQ + t * tile_bytes(kDim), &map_q, a, a.q, token0 + t * a.tile_tokens, head, batch, bar_q);
       }
       uint32_t it = 0;
       for (int j = begin; j < last && !__any_sync(0xffffffffu, *abort_flag); ++j) {

@@ -92,6 +92,17 @@ def test_few_queries_on_long_keys(tq, tk, hq, hk, dim, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("batch,tq,tk,hq,hk,dim,causal", [
+    (20, 300, 300, 8, 8, 64, True), (11, 260, 390, 24, 3, 128, True), (16, 513, 200, 12, 4, 80, False), (40, 129, 70, 4, 4, 32, True)])
+def test_many_heads(batch, tq, tk, hq, hk, dim, causal, dtype):
+    """More blocks than SMs, each with several tiles of queries, odd numbers of them and of rows in the last."""
+    g = torch.Generator().manual_seed(batch)
+    lengths = [int(torch.randint(0, tk + 1, (1,), generator=g)) for _ in range(batch)]
+    start = [int(torch.randint(-tq, tk, (1,), generator=g)) for _ in range(batch)] if causal else None
+    check(make(batch, tq, tk, hq, hk, dim, dtype, 20, lengths, start), causal)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("tq,tk,hq,hk,causal", [(3000, 40, 4, 1, False), (2100, 2100, 3, 1, True), (5000, 1, 1, 1, False)])
 def test_many_queries_on_few_keys(tq, tk, hq, hk, causal, dtype):
     check(make(1, tq, tk, hq, hk, 64, dtype, 8), causal)
