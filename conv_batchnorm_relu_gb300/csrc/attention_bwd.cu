@@ -1,0 +1,766 @@
+// Attention backward (declared in include/cbr.h) on the tensor cores: the probabilities are computed again.
+//
+// Three launches.  prepare_kernel takes D_i = do_i . o_i and the exponents' offsets.  query_kernel holds a tile
+// of 128 queries and walks over the keys: S = Q K^T, dP = dO V^T, dQ += dS K.  key_kernel holds a tile of 128
+// keys and walks over the queries of all heads that read it: S' = K Q^T, dP' = V dO^T, dV += P' dO,
+// dK += dS' Q.  Scores and dP are taken twice (seven products instead of five), and in return every sum
+// stays in TMEM to its end, in a fixed order: no atomics, no sums in memory.
+//   P and dS go from registers over their scores in TMEM and enter the second products from there.  Both tiles'
+// elements are shared by two warpgroups: a thread has a row and 64 of its 128 columns.
+//   f16: p is taken 2^12 times as large, and dS a power of two times as large that a bound on |do| |v| gives
+// for each key head, so that small ones keep their digits; the results are scaled back.
+//   Queries past the last one have the offset +infinity (p = 0), keys past theirs are cut off at the outputs.
+#include <algorithm>
+
+#include "attention.cuh"
+#include "cbr_internal.h"
+
+namespace cbr {
+namespace att {
+namespace {
+
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kThreads = 320;
+
+struct BackwardParams {
+  Params p;
+  const float* offset;    // [batch * packs][rows]: lse log2(e) - shift of a row, +infinity where p is 0
+  const float* delta;     // the same of D
+  const uint32_t* norms;  // f16: [batch][heads_k][2] bits of the largest |do|^2 and |v|^2
+  int64_t rows;           // of a pack of heads, a multiple of 128
+  void* out[2];           // dq; or dv, dk
+  int64_t stride[2][3];
+  float* part;            // splits > 1: [split][out][rows of the outputs][head_dim]
+  int64_t part_rows;
+};
+
+template <bool BF16>
+constexpr float kShift = BF16 ? 0.f : 12.f;
+
+// f16: the power of two that takes |dP - D| <= 2 max|do| max|v| to at most 2^14; 1 where that bound says nothing.
+template <bool BF16>
+__device__ __forceinline__ float ds_scale(const BackwardParams& f, int batch, int key_head) {
+  if constexpr (BF16) return 1.f;
+  const uint32_t* n = f.norms + 2 * ((int64_t)batch * f.p.heads_k + key_head);
+  const float bound = 2.f * sqrtf(__uint_as_float(n[0])) * sqrtf(__uint_as_float(n[1]));
+  if (!(bound > 0.f && bound < INFINITY)) return 1.f;
+  return __int_as_float((127 + 14 - (ilogbf(bound) + 1)) << 23);
+}
+
+// ---------------------------------------------------------------- D, offsets, bounds
+
+constexpr int kPrepareRows = 64;   // rows of a block of 256 threads, 16 lanes to a row
+
+struct PrepareParams {
+  BackwardParams f;
+  const void* d_o;
+  const void* o;
+  const void* v;
+  int64_t do_stride[3], o_stride[3], v_stride[3];
+  const float* lse;
+  float* offset;
+  float* delta;
+  uint32_t* norms;
+  int64_t query_blocks;   // blocks of queries; the others (f16) take values
+};
+
+__device__ __forceinline__ float half_warp_sum(float v) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// |a|^2 of a thread's eight elements, and a . b.
+template <bool BF16>
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
+  const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = unpack2<BF16>(x[i]), w = unpack2<BF16>(y[i]);
+    s = fmaf(u.x, w.x, s);
+    s = fmaf(u.y, w.y, s);
+  }
+  return s;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepareParams g) {
+  const Params& a = g.f.p;
+  __shared__ float largest[8];
+  const int lane = threadIdx.x & 15, sub = threadIdx.x >> 4, e = lane * 8;
+  const bool queries = blockIdx.x < g.query_blocks;
+  float most = 0.f;
+  int64_t batch, key_head;
+  if (queries) {
+    const int64_t packs = a.heads_q / a.pack, per = g.f.rows / kPrepareRows;
+    const int64_t at = blockIdx.x / per, first = blockIdx.x % per * kPrepareRows;
+    const int64_t head = at % packs;
+    batch = at / packs;
+    key_head = a.pack > 1 ? head : head / a.group;
+#pragma unroll
+    for (int r = 0; r < kPrepareRows / 16; ++r) {
+      const int64_t row = first + r * 16 + sub, token = row / a.pack, h = head * a.pack + row % a.pack;
+      const bool live = token < a.q_tokens;
+      uint4 u = make_uint4(0, 0, 0, 0), w = u;
+      if (live && e < a.head_dim) {
+        u = ld_global_nc_v4(static_cast<const uint16_t*>(g.d_o) + batch * g.do_stride[0] + token * g.do_stride[1] + h * g.do_stride[2] + e);
+        w = ld_global_nc_v4(static_cast<const uint16_t*>(g.o) + batch * g.o_stride[0] + token * g.o_stride[1] + h * g.o_stride[2] + e);
+      }
+      const float d = half_warp_sum(dot8<BF16>(u, w));
+      if constexpr (!BF16) most = tok::Max::of(most, half_warp_sum(dot8<BF16>(u, u)));
+      if (lane == 0) {
+        const float lse = live ? g.lse[(batch * a.heads_q + h) * a.q_tokens + token] : -INFINITY;
+        g.offset[at * g.f.rows + row] = lse == -INFINITY ? INFINITY : lse * kLog2e - kShift<BF16>;
+        g.delta[at * g.f.rows + row] = d;
+      }
+    }
+  } else {
+    const int64_t per = (a.k_tokens + kPrepareRows - 1) / kPrepareRows, at = (blockIdx.x - g.query_blocks) / per;
+    const int64_t first = (blockIdx.x - g.query_blocks) % per * kPrepareRows;
+    key_head = at % a.heads_k;
+    batch = at / a.heads_k;
+    const int keys = keys_of(a, (int)batch);
+#pragma unroll
+    for (int r = 0; r < kPrepareRows / 16; ++r) {
+      const int64_t row = first + r * 16 + sub;
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (row < keys && e < a.head_dim)
+        u = ld_global_nc_v4(static_cast<const uint16_t*>(g.v) + batch * g.v_stride[0] + row * g.v_stride[1] + key_head * g.v_stride[2] + e);
+      most = tok::Max::of(most, half_warp_sum(dot8<BF16>(u, u)));
+    }
+  }
+  if constexpr (!BF16) {
+    most = tok::warp_max(most);
+    if ((threadIdx.x & 31) == 0) largest[threadIdx.x >> 5] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < 8; ++i) most = tok::Max::of(most, largest[i]);
+      // bits of floats that are not negative are in their order, those of a NaN above all: the largest does not
+      // depend on the order of the blocks
+      atomicMax(g.norms + 2 * (batch * a.heads_k + key_head) + !queries, __float_as_uint(fabsf(most)));
+    }
+  }
+}
+
+// ---------------------------------------------------------------- a row's results
+
+// 32 columns of a row from TMEM, scaled: whole results in the storage type, parts of them in 32 bits.
+//   any: the accumulator was written (the same in the whole warp); use: the row has a result, else 0.
+template <bool BF16>
+__device__ __forceinline__ void store32(uint32_t taddr, int col, int dim, bool any, bool use, bool live, float scale, uint8_t* out,
+                                        float* part) {
+  uint32_t r[32];
+  float v[32];
+  if (any) {
+    tmem_ld32(taddr + col, r);
+    tmem_ld_wait();
+  }
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = any && use ? __uint_as_float(r[e]) * scale : 0.f;
+  if (!live) return;
+#pragma unroll
+  for (int e = 0; e < 32; e += 8) {
+    if (col + e >= dim) continue;
+    if (!part) {
+      st_global_v4(out + 2 * (col + e), pack8<BF16>(v + e));
+    } else {
+      *reinterpret_cast<float4*>(part + col + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+      *reinterpret_cast<float4*>(part + col + e + 4) = make_float4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]);
+    }
+  }
+}
+
+__device__ __forceinline__ uint8_t* row_of(const BackwardParams& f, int which, int64_t batch, int64_t token, int64_t head) {
+  return static_cast<uint8_t*>(f.out[which]) + 2 * (batch * f.stride[which][0] + token * f.stride[which][1] + head * f.stride[which][2]);
+}
+
+// ---------------------------------------------------------------- dQ
+
+template <int kDim>
+struct QuerySmem {
+  static constexpr int kK = 3, kV = 2;   // stages: a tile of keys stays for two products, one of values for one
+  static constexpr int kQ = 0, kDo = tile_bytes(kDim), kKeys = 2 * tile_bytes(kDim), kValues = kKeys + kK * tile_bytes(kDim);
+  static constexpr int kBar = kValues + kV * tile_bytes(kDim);
+  // Q and dO; K full, empty; V full, empty; scores, dS (two each); dP full, empty; dQ; tail; drain
+  static constexpr int kBars = 1 + 2 * kK + 2 * kV + 4 + 2 + 3, kTotal = kBar + kBars * 8 + 16 + 1024;
+};
+
+// Warps: 0-3 the first, 4-7 the second 64 columns of the 128 rows; 8 loads, 9 products.
+// TMEM: dQ at 0, S in two buffers at 128 and 256 (dS over them), dP at 384.
+template <int kDim, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    query_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+                 const __grid_constant__ BackwardParams f) {
+  using L = QuerySmem<kDim>;
+  constexpr uint32_t kTile_ = tile_bytes(kDim);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar_q = sbase + L::kBar, bar_kf = bar_q + 8, bar_ke = bar_kf + 8 * L::kK, bar_vf = bar_ke + 8 * L::kK;
+  const uint32_t bar_ve = bar_vf + 8 * L::kV, bar_s = bar_ve + 8 * L::kV, bar_ds = bar_s + 16, bar_dpf = bar_ds + 16;
+  const uint32_t bar_dpe = bar_dpf + 8, bar_dq = bar_dpe + 8, bar_tail = bar_dq + 8, bar_drain = bar_tail + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBar + L::kBars * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const Params& a = f.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int packs = a.heads_q / a.pack;
+  const int head = blockIdx.x % packs, batch = blockIdx.x / packs % (gridDim.x / packs / a.q_blocks);
+  const int block = a.q_blocks - 1 - blockIdx.x / (gridDim.x / a.q_blocks);   // the longest rows first
+  const int key_head = a.pack > 1 ? head : head / a.group;
+  const int token0 = block * a.tile_tokens;
+  const int keys = keys_of(a, batch), start = start_of(a, batch);
+  const int see = a.causal ? min(keys, max(0, start + min(token0 + a.tile_tokens, a.q_tokens))) : keys;
+  const int tiles = (see + kTile - 1) / kTile, share = (tiles + a.splits - 1) / a.splits;
+  const int first = min(tiles, (int)blockIdx.y * share), n = min(tiles, first + share) - first;
+
+  if (threadIdx.x == 0) {
+    for (uint32_t b = bar_q; b <= bar_drain; b += 8)
+      mbar_init(b, (b >= bar_ds && b < bar_dpf) || b == bar_dpe ? 8 : 1);   // dS, dP empty: one arrival for each row warp
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto give_up = [&](uint32_t bits) {
+    *abort_flag = 1;
+    report_error(a.err, bits);
+  };
+
+  if (warp == kLoadWarp) {
+    if (n > 0) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar_q, 2 * query_bytes<kDim>(a));
+        load_queries<kDim>(sbase + L::kQ, &map_q, a, a.q, token0, head, batch, bar_q);
+        load_queries<kDim>(sbase + L::kDo, &map_do, a, a.d_o, token0, head, batch, bar_q);
+      }
+      int kn = 0, vn = 0;   // tiles asked for
+      for (int j = 0; j < n && !__any_sync(0xffffffffu, *abort_flag); ++j) {
+        const int row = (first + j) * kTile;
+        const uint32_t ks = j % L::kK, vs = j % L::kV;
+        if (!__all_sync(0xffffffffu, mbar_wait_backoff(bar_ke + 8 * ks, ((j / L::kK) & 1) ^ 1, 32))) {
+          give_up(kErrWaitOperand);
+          break;
+        }
+        const bool tail = row + kTile > keys && keys < a.k_tokens;
+        const uint32_t dst = sbase + L::kKeys + ks * kTile_;
+        if (lane == 0) load_keys<kDim>(dst, &map_k, a.k, row, key_head, batch, tail ? bar_tail : bar_kf + 8 * ks);
+        if (tail) {
+          // keys behind the last one may be anything: dS is 0 there, and 0 times NaN is not
+          if (!__all_sync(0xffffffffu, mbar_wait(bar_tail, 0))) {
+            give_up(kErrWaitOperand);
+            break;
+          }
+          clear_rows<kDim>(dst, keys - row, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_kf + 8 * ks);
+        }
+        ++kn;
+        if (!__all_sync(0xffffffffu, mbar_wait_backoff(bar_ve + 8 * vs, ((j / L::kV) & 1) ^ 1, 32))) {
+          give_up(kErrWaitOperand);
+          break;
+        }
+        if (lane == 0) load_keys<kDim>(sbase + L::kValues + vs * kTile_, &map_v, a.v, row, key_head, batch, bar_vf + 8 * vs);
+        ++vn;
+        __syncwarp();
+      }
+      if (lane == 0) {   // never leave with a copy in flight
+        mbar_wait(bar_q, 0);
+        for (int i = max(0, kn - L::kK); i < kn; ++i) mbar_wait(bar_kf + 8 * (i % L::kK), (i / L::kK) & 1);
+        for (int i = max(0, vn - L::kV); i < vn; ++i) mbar_wait(bar_vf + 8 * (i % L::kV), (i / L::kV) & 1);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    if (n > 0) {
+      constexpr uint32_t kIdS = make_idesc_f16(128, 128, BF16, false, false), kIdQ = make_idesc_f16(128, kDim, BF16, false, true);
+      bool bad = false;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(bar, parity));
+        tc_fence_after();
+        return !bad;
+      };
+      auto product = [&](uint32_t d, uint32_t x, uint32_t y) {
+        const uint64_t xd = k_major(x), yd = k_major(y);
+#pragma unroll
+        for (int k = 0; k < kDim / 16; ++k) mma_f16_ss_warp(tmem + d, xd + k_major_step(k), yd + k_major_step(k), kIdS, k != 0);
+      };
+      auto scores = [&](int i) {
+        if (!wait(bar_kf + 8 * (i % L::kK), (i / L::kK) & 1)) return;
+        product(128 + (i & 1) * 128, sbase + L::kQ, sbase + L::kKeys + (i % L::kK) * kTile_);
+        mma_commit_warp(bar_s + 8 * (i & 1));
+      };
+      auto dp = [&](int i) {
+        if (!wait(bar_vf + 8 * (i % L::kV), (i / L::kV) & 1)) return;
+        product(384, sbase + L::kDo, sbase + L::kValues + (i % L::kV) * kTile_);
+        mma_commit_warp(bar_dpf);
+        mma_commit_warp(bar_ve + 8 * (i % L::kV));
+      };
+      if (wait(bar_q, 0)) scores(0);
+      if (!bad) dp(0);
+      if (!bad && n > 1) scores(1);
+      for (int j = 0; j < n && !bad; ++j) {
+        if (j + 1 < n) {
+          if (!wait(bar_dpe, j & 1)) break;
+          dp(j + 1);
+          if (bad) break;
+        }
+        if (!wait(bar_ds + 8 * (j & 1), (j >> 1) & 1)) break;
+        const uint64_t kd = mn_major(sbase + L::kKeys + (j % L::kK) * kTile_);
+        const uint32_t ds = tmem + 128 + (j & 1) * 128;
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)   // 64 columns of dS at the start of each half of its scores
+          mma_f16_ts_warp(tmem, ds + (k >> 2) * 64 + (k & 3) * 8, kd + mn_major_step(k), kIdQ, (k != 0) | (j != 0));
+        mma_commit_warp(bar_ke + 8 * (j % L::kK));
+        if (j + 2 < n) scores(j + 2);
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+      }
+      mma_commit_warp(bar_dq);
+      if (bad) give_up(kErrWaitMma);
+      mma_commit_warp(bar_drain);
+      mbar_wait(bar_drain, 0);
+    }
+  } else {
+    const int half = warp >> 2, row = threadIdx.x & 127;
+    const int token = token0 + row / a.pack;
+    const int q_head = a.pack > 1 ? head * a.pack + row % a.pack : head;
+    const bool live = row < a.tile_tokens * a.pack && token < a.q_tokens;
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const float c = exponent_scale(a), sc = ds_scale<BF16>(f, batch, key_head), sc2 = sc * ex2(-kShift<BF16>);
+    const int64_t at = ((int64_t)batch * packs + head) * f.rows + (int64_t)block * kTile + row;
+    const float offset = -f.offset[at], dsc = -f.delta[at] * sc2;
+    const int limit = a.causal ? min(keys, max(0, start + token + 1)) : keys;
+    const int least = a.causal ? min(keys, max(0, start + token0 + 1)) : keys;
+    bool bad = false;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t ts = trow + 128 + (j & 1) * 128 + half * 64;
+      const int key = (first + j) * kTile + half * 64;
+      const bool edge = key + 64 > least;
+      bad = !__all_sync(0xffffffffu, mbar_wait(bar_s + 8 * (j & 1), (j >> 1) & 1));
+      if (bad) break;
+      tc_fence_after();
+      uint32_t r[64];
+      float p[64];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) tmem_ld32(ts + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * i));
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 64; ++i) p[i] = ex2(fmaf(__uint_as_float(r[i]), c, offset));
+      bad = !__all_sync(0xffffffffu, mbar_wait(bar_dpf, j & 1));
+      if (bad) break;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) tmem_ld32(trow + 384 + half * 64 + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * i));
+      tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_dpe);
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (key + i >= limit) p[i] = 0.f, r[i] = 0u;
+      }
+      uint32_t ds[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        ds[i] = pack2<BF16>(p[2 * i] * fmaf(__uint_as_float(r[2 * i]), sc2, dsc), p[2 * i + 1] * fmaf(__uint_as_float(r[2 * i + 1]), sc2, dsc));
+      tmem_st32(ts, ds);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_ds + 8 * (j & 1));
+    }
+    if (!bad && n > 0) bad = !__all_sync(0xffffffffu, mbar_wait(bar_dq, 0));
+    if (bad) give_up(kErrWaitAccum);
+    tc_fence_after();
+    const int64_t out_row = ((int64_t)batch * a.heads_q + q_head) * a.q_tokens + token;
+    uint8_t* out = row_of(f, 0, batch, token, q_head);
+    float* part = a.splits > 1 ? f.part + (blockIdx.y * f.part_rows + out_row) * a.head_dim : nullptr;
+#pragma unroll 1
+    for (int i = half * (kDim / 2); i < (half + 1) * (kDim / 2); i += 32)
+      store32<BF16>(trow, i, a.head_dim, n > 0 && !bad, true, live, a.scale / sc, out, part);
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- dK, dV
+
+template <int kDim>
+struct KeySmem {
+  static constexpr int kK = 0, kV = tile_bytes(kDim), kQ = 2 * tile_bytes(kDim), kDo = 4 * tile_bytes(kDim);   // Q, dO: two stages
+  static constexpr int kRow = 6 * tile_bytes(kDim);   // two stages of 128 offsets and 128 D
+  static constexpr int kBar = kRow + 2 * 1024;
+  // K and V; Q full, empty; dO full, empty (two each); scores, p, dP, dS; out; drain
+  static constexpr int kBars = 1 + 8 + 4 + 2, kTotal = kBar + kBars * 8 + 16 + 1024;
+};
+
+// Rows are keys here, columns queries.  Warps as above.  TMEM: dV at 0, dK at 128, S at 256 (P over it), dP at 384
+// (dS over it).
+template <int kDim, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    key_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+               const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+               const __grid_constant__ BackwardParams f) {
+  using L = KeySmem<kDim>;
+  constexpr uint32_t kTile_ = tile_bytes(kDim);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar_kv = sbase + L::kBar, bar_qf = bar_kv + 8, bar_qe = bar_qf + 16, bar_of = bar_qe + 16, bar_oe = bar_of + 16;
+  const uint32_t bar_s = bar_oe + 16, bar_p = bar_s + 8, bar_dp = bar_p + 8, bar_ds = bar_dp + 8, bar_out = bar_ds + 8;
+  const uint32_t bar_drain = bar_out + 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBar + L::kBars * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const Params& a = f.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int key_tiles = (a.k_tokens + kTile - 1) / kTile;
+  const int key_head = blockIdx.x % a.heads_k, batch = blockIdx.x / a.heads_k % (gridDim.x / a.heads_k / key_tiles);
+  const int tile = blockIdx.x / (gridDim.x / key_tiles);   // causal: the first keys have the most queries, and come first
+  const int key0 = tile * kTile, keys = keys_of(a, batch), start = start_of(a, batch);
+  // tiles of queries: those from the first that sees one of the keys, of every pack of heads that reads them
+  const int q_tiles = (int)(f.rows / kTile);
+  const int q_first = a.causal ? (int)min((int64_t)q_tiles, (int64_t)min(max(0, key0 - start), a.q_tokens) * a.pack / kTile) : 0;
+  const int each = key0 < keys ? q_tiles - q_first : 0, all = each * (a.group / a.pack);
+  const int share = (all + a.splits - 1) / a.splits;
+  const int first = min(all, (int)blockIdx.y * share), n = min(all, first + share) - first;
+  const int head0 = a.pack > 1 ? key_head : key_head * a.group;   // the first pack of heads
+
+  if (threadIdx.x == 0) {
+    for (uint32_t b = bar_kv; b <= bar_drain; b += 8) mbar_init(b, b == bar_p || b == bar_ds ? 8 : b == bar_kv ? 2 : 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto give_up = [&](uint32_t bits) {
+    *abort_flag = 1;
+    report_error(a.err, bits);
+  };
+
+  if (warp == kLoadWarp) {
+    if (n > 0) {
+      if (lane == 0) {
+        load_keys<kDim>(sbase + L::kK, &map_k, a.k, key0, key_head, batch, bar_kv);
+        // (the barrier counts two arrivals: each of the loads announces its own bytes)
+        load_keys<kDim>(sbase + L::kV, &map_v, a.v, key0, key_head, batch, bar_kv);
+      }
+      int qn = 0, on = 0;   // tiles asked for
+      for (int j = 0; j < n && !__any_sync(0xffffffffu, *abort_flag); ++j) {
+        const int head = head0 + (first + j) / each, qt = q_first + (first + j) % each;
+        const uint32_t s = j & 1, parity = ((j >> 1) & 1) ^ 1;
+        if (!__all_sync(0xffffffffu, mbar_wait_backoff(bar_qe + 8 * s, parity, 32))) {
+          give_up(kErrWaitOperand);
+          break;
+        }
+        if (lane == 0) {
+          const int64_t at = ((int64_t)batch * (a.heads_q / a.pack) + head) * f.rows + (int64_t)qt * kTile;
+          mbar_arrive_expect_tx(bar_qf + 8 * s, query_bytes<kDim>(a) + 1024);
+          load_queries<kDim>(sbase + L::kQ + s * kTile_, &map_q, a, a.q, qt * a.tile_tokens, head, batch, bar_qf + 8 * s);
+          bulk_load_1d(sbase + L::kRow + s * 1024, f.offset + at, 512, bar_qf + 8 * s);
+          bulk_load_1d(sbase + L::kRow + s * 1024 + 512, f.delta + at, 512, bar_qf + 8 * s);
+        }
+        ++qn;
+        if (!__all_sync(0xffffffffu, mbar_wait_backoff(bar_oe + 8 * s, parity, 32))) {
+          give_up(kErrWaitOperand);
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar_of + 8 * s, query_bytes<kDim>(a));
+          load_queries<kDim>(sbase + L::kDo + s * kTile_, &map_do, a, a.d_o, qt * a.tile_tokens, head, batch, bar_of + 8 * s);
+        }
+        ++on;
+        __syncwarp();
+      }
+      if (lane == 0) {   // never leave with a copy in flight
+        mbar_wait(bar_kv, 0);
+        for (int i = max(0, qn - 2); i < qn; ++i) mbar_wait(bar_qf + 8 * (i & 1), (i >> 1) & 1);
+        for (int i = max(0, on - 2); i < on; ++i) mbar_wait(bar_of + 8 * (i & 1), (i >> 1) & 1);
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    if (n > 0) {
+      constexpr uint32_t kIdS = make_idesc_f16(128, 128, BF16, false, false), kIdK = make_idesc_f16(128, kDim, BF16, false, true);
+      bool bad = false;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(bar, parity));
+        tc_fence_after();
+        return !bad;
+      };
+      // keys (values) times queries (dO): a tile of scores
+      auto scores = [&](uint32_t d, uint32_t x, uint32_t y, uint32_t bar) {
+        const uint64_t xd = k_major(sbase + x), yd = k_major(sbase + y);
+#pragma unroll
+        for (int k = 0; k < kDim / 16; ++k) mma_f16_ss_warp(tmem + d, xd + k_major_step(k), yd + k_major_step(k), kIdS, k != 0);
+        mma_commit_warp(bar);
+      };
+      // what lies over the scores at `x` times queries (dO), added to the accumulator at `d`
+      auto gather = [&](uint32_t d, uint32_t x, uint32_t y, int j) {
+        const uint64_t yd = mn_major(sbase + y);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_f16_ts_warp(tmem + d, tmem + x + (k >> 2) * 64 + (k & 3) * 8, yd + mn_major_step(k), kIdK, (k != 0) | (j != 0));
+      };
+      if (wait(bar_kv, 0) && wait(bar_qf, 0)) scores(256, L::kK, L::kQ, bar_s);
+      if (!bad && wait(bar_of, 0)) scores(384, L::kV, L::kDo, bar_dp);
+      for (int j = 0; j < n && !bad; ++j) {
+        const uint32_t s = j & 1, next = s ^ 1, parity = ((j + 1) >> 1) & 1;
+        if (!wait(bar_p, j & 1)) break;
+        gather(0, 256, L::kDo + s * kTile_, j);
+        mma_commit_warp(bar_oe + 8 * s);
+        if (j + 1 < n) {
+          if (!wait(bar_qf + 8 * next, parity)) break;
+          scores(256, L::kK, L::kQ + next * kTile_, bar_s);
+        }
+        if (!wait(bar_ds, j & 1)) break;
+        gather(128, 384, L::kQ + s * kTile_, j);
+        mma_commit_warp(bar_qe + 8 * s);
+        if (j + 1 < n) {
+          if (!wait(bar_of + 8 * next, parity)) break;
+          scores(384, L::kV, L::kDo + next * kTile_, bar_dp);
+        }
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+      }
+      mma_commit_warp(bar_out);
+      if (bad) give_up(kErrWaitMma);
+      mma_commit_warp(bar_drain);
+      mbar_wait(bar_drain, 0);
+    }
+  } else {
+    const int half = warp >> 2, row = threadIdx.x & 127, key = key0 + row;
+    const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ts = trow + 256 + half * 64, tdp = trow + 384 + half * 64;
+    const float c = exponent_scale(a), sc = ds_scale<BF16>(f, batch, key_head), sc2 = sc * ex2(-kShift<BF16>);
+    bool bad = false;
+    for (int j = 0; j < n; ++j) {
+      const int qt = q_first + (first + j) % each;
+      // causal: the first of the tile's columns (queries, of several heads where packed) that sees this row's key
+      int hidden = 0;
+      if (a.causal) {
+        const int64_t from = (int64_t)max(0, key - start) * a.pack - (int64_t)qt * kTile - half * 64;
+        hidden = (int)max((int64_t)0, min((int64_t)64, from));
+      }
+      const bool edge = __any_sync(0xffffffffu, hidden > 0);
+      const float4* offset = reinterpret_cast<const float4*>(smem + L::kRow + (j & 1) * 1024) + half * 16;
+      const float4* delta = offset + 32;
+      bad = !__all_sync(0xffffffffu, mbar_wait(bar_qf + 8 * (j & 1), (j >> 1) & 1) && mbar_wait(bar_s, j & 1));
+      if (bad) break;
+      tc_fence_after();
+      uint32_t r[64];
+      float p[64];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) tmem_ld32(ts + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * i));
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float4 o = offset[i];
+        p[4 * i] = ex2(fmaf(__uint_as_float(r[4 * i]), c, -o.x));
+        p[4 * i + 1] = ex2(fmaf(__uint_as_float(r[4 * i + 1]), c, -o.y));
+        p[4 * i + 2] = ex2(fmaf(__uint_as_float(r[4 * i + 2]), c, -o.z));
+        p[4 * i + 3] = ex2(fmaf(__uint_as_float(r[4 * i + 3]), c, -o.w));
+      }
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (i < hidden) p[i] = 0.f;
+      }
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = pack2<BF16>(p[2 * i], p[2 * i + 1]);
+      tmem_st32(ts, w);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_p);
+      bad = !__all_sync(0xffffffffu, mbar_wait(bar_dp, j & 1));
+      if (bad) break;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) tmem_ld32(tdp + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * i));
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float4 d = delta[i];
+        const float x = (__uint_as_float(r[4 * i]) - d.x) * sc2 * p[4 * i], y = (__uint_as_float(r[4 * i + 1]) - d.y) * sc2 * p[4 * i + 1];
+        const float z = (__uint_as_float(r[4 * i + 2]) - d.z) * sc2 * p[4 * i + 2];
+        const float u = (__uint_as_float(r[4 * i + 3]) - d.w) * sc2 * p[4 * i + 3];
+        w[2 * i] = pack2<BF16>(x, y);
+        w[2 * i + 1] = pack2<BF16>(z, u);
+      }
+      tmem_st32(tdp, w);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_ds);
+    }
+    if (!bad && n > 0) bad = !__all_sync(0xffffffffu, mbar_wait(bar_out, 0));
+    if (bad) give_up(kErrWaitAccum);
+    tc_fence_after();
+    // the first warpgroup stores dV, the second dK
+    uint8_t* out = row_of(f, half, batch, key, key_head);
+    const int64_t out_row = ((int64_t)batch * a.heads_k + key_head) * a.k_tokens + key;
+    float* part = a.splits > 1 ? f.part + ((2 * blockIdx.y + half) * f.part_rows + out_row) * a.head_dim : nullptr;
+    const float scale = half ? a.scale / sc : ex2(-kShift<BF16>);
+#pragma unroll 1
+    for (int i = 0; i < kDim; i += 32)
+      store32<BF16>(trow + half * 128, i, a.head_dim, n > 0 && !bad, key < keys, key < a.k_tokens, scale, out, part);
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- parts
+
+// Parts added up in their order: a warp for each row of `outs` results of [batch][heads][tokens].
+template <bool BF16>
+__global__ void __launch_bounds__(128) sum_kernel(const __grid_constant__ BackwardParams f, int outs, int64_t heads, int64_t tokens) {
+  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, dim = f.p.head_dim;
+  if (at >= outs * f.part_rows) return;
+  const int64_t which = at / f.part_rows, row = at % f.part_rows;
+  using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
+  T* out = reinterpret_cast<T*>(row_of(f, (int)which, row / tokens / heads, row % tokens, row / tokens % heads));
+  for (int e = lane; e < dim; e += 32) {
+    float v = 0.f;
+    for (int s = 0; s < f.p.splits; ++s) v += f.part[((s * outs + which) * f.part_rows + row) * dim + e];
+    out[e] = tok::from_f<T>(v);
+  }
+}
+
+// ---------------------------------------------------------------- host side
+
+struct Shape {
+  int pack, query_splits, key_splits;
+  int64_t packs, rows, q_blocks, key_tiles;
+  size_t offsets, norms, parts;   // bytes of the workspace's regions
+};
+
+// Heads that share a key head are packed into a tile of queries where they fill it evenly.  Where blocks are fewer
+// than half the SMs their walk is shared, two tiles at least to each.
+Shape shape_of(const cbr_attention_desc_t& d, bool may_pack) {
+  Shape s{};
+  const int64_t group = d.heads_q / d.heads_k;
+  s.pack = may_pack && group <= kTile && (group & (group - 1)) == 0 ? (int)group : 1;
+  s.packs = d.heads_q / s.pack;
+  s.rows = (d.q_tokens * s.pack + kTile - 1) / kTile * kTile;
+  s.q_blocks = s.rows / kTile;
+  s.key_tiles = (d.k_tokens + kTile - 1) / kTile;
+  auto splits = [](int64_t blocks, int64_t walk) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kSms / std::max<int64_t>(blocks, 1), walk / 2));
+  };
+  s.query_splits = splits(s.q_blocks * s.packs * d.batch, s.key_tiles);
+  s.key_splits = splits(s.key_tiles * d.heads_k * d.batch, s.q_blocks * (group / s.pack));
+  s.offsets = (size_t)d.batch * s.packs * s.rows * 4;
+  s.norms = align256((size_t)d.batch * d.heads_k * 8);
+  const size_t q_part = s.query_splits > 1 ? (size_t)s.query_splits * d.batch * d.heads_q * d.q_tokens : 0;
+  const size_t k_part = s.key_splits > 1 ? (size_t)s.key_splits * 2 * d.batch * d.heads_k * d.k_tokens : 0;
+  s.parts = std::max(q_part, k_part) * d.head_dim * 4;   // one after the other
+  return s;
+}
+
+// (heads of q or dO that repeat have no axis to pack)
+bool may_pack(const cbr_attention_desc_t& d) { return d.q_stride[2] != 0 && d.do_stride[2] != 0; }
+
+size_t total(const Shape& s) { return 2 * align256(s.offsets) + s.norms + s.parts; }
+
+template <int kDim, bool BF16>
+int launch(const AttentionArgs& g, cudaStream_t st) {
+  const cbr_attention_desc_t& d = g.d;
+  const Shape s = shape_of(d, may_pack(d));
+  uint8_t* ws = static_cast<uint8_t*>(g.ws);
+  PrepareParams pre{};
+  BackwardParams& f = pre.f;
+  f.p = params_of(g, s.pack);
+  f.p.tiles = 1;
+  f.p.q_blocks = (int)s.q_blocks;
+  pre.offset = reinterpret_cast<float*>(ws);
+  pre.delta = reinterpret_cast<float*>(ws + align256(s.offsets));
+  pre.norms = reinterpret_cast<uint32_t*>(ws + 2 * align256(s.offsets));
+  f.offset = pre.offset;
+  f.delta = pre.delta;
+  f.norms = pre.norms;
+  f.rows = s.rows;
+  f.part = reinterpret_cast<float*>(ws + 2 * align256(s.offsets) + s.norms);
+  if (d.q_tokens && d.k_tokens) {
+    pre.d_o = g.d_o;
+    pre.o = g.o;
+    pre.v = g.v;
+    pre.lse = g.lse;
+    for (int i = 0; i < 3; ++i) pre.do_stride[i] = d.do_stride[i], pre.o_stride[i] = d.o_stride[i], pre.v_stride[i] = d.v_stride[i];
+    pre.query_blocks = d.batch * s.packs * (s.rows / kPrepareRows);
+    int64_t blocks = pre.query_blocks;
+    if constexpr (!BF16) {
+      if (cudaMemsetAsync(pre.norms, 0, (size_t)d.batch * d.heads_k * 8, st) != cudaSuccess) return CBR_ERR_CUDA;
+      blocks += d.batch * d.heads_k * ((d.k_tokens + kPrepareRows - 1) / kPrepareRows);
+    }
+    prepare_kernel<BF16><<<(unsigned)blocks, 256, 0, st>>>(pre);
+  }
+  // where one side is empty nothing is loaded, and the maps of the other stand in for its own
+  CUtensorMap q, k, v, d_o;
+  cbr_attention_desc_t e = d;
+  const void *pq = g.q, *pdo = g.d_o, *pk = g.k, *pv = g.v;
+  if (!d.q_tokens) {
+    e.q_tokens = 1, pq = pdo = g.k;
+    for (int i = 0; i < 3; ++i) e.q_stride[i] = e.do_stride[i] = 0;
+  }
+  if (!d.k_tokens) {
+    pk = pv = g.q;
+    for (int i = 0; i < 3; ++i) e.k_stride[i] = e.v_stride[i] = 0;
+  }
+  if (!query_map(&q, e, pq, e.q_stride, s.pack) || !query_map(&d_o, e, pdo, e.do_stride, s.pack) || !key_map(&k, e, pk, e.k_stride) ||
+      !key_map(&v, e, pv, e.v_stride))
+    return CBR_ERR_CUDA;
+  const auto by_query = &query_kernel<kDim, BF16>;
+  const auto by_key = &key_kernel<kDim, BF16>;
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(by_query), 227 * 1024) ||
+      !ensure_smem_attr(reinterpret_cast<const void*>(by_key), 227 * 1024))
+    return CBR_ERR_CUDA;
+  if (d.q_tokens) {
+    f.p.splits = s.query_splits;
+    f.out[0] = g.dq;
+    for (int i = 0; i < 3; ++i) f.stride[0][i] = d.dq_stride[i];
+    f.part_rows = d.batch * d.heads_q * d.q_tokens;
+    by_query<<<dim3((unsigned)(s.q_blocks * s.packs * d.batch), s.query_splits), kThreads, QuerySmem<kDim>::kTotal, st>>>(q, k, v, d_o, f);
+    if (s.query_splits > 1) sum_kernel<BF16><<<(unsigned)((f.part_rows + 3) / 4), 128, 0, st>>>(f, 1, d.heads_q, d.q_tokens);
+  }
+  if (d.k_tokens) {
+    f.p.splits = s.key_splits;
+    f.out[0] = g.dv;
+    f.out[1] = g.dk;
+    for (int i = 0; i < 3; ++i) f.stride[0][i] = d.dv_stride[i], f.stride[1][i] = d.dk_stride[i];
+    f.part_rows = d.batch * d.heads_k * d.k_tokens;
+    by_key<<<dim3((unsigned)(s.key_tiles * d.heads_k * d.batch), s.key_splits), kThreads, KeySmem<kDim>::kTotal, st>>>(q, k, v, d_o, f);
+    if (s.key_splits > 1) sum_kernel<BF16><<<(unsigned)((2 * f.part_rows + 3) / 4), 128, 0, st>>>(f, 2, d.heads_k, d.k_tokens);
+  }
+  return cudaGetLastError() == cudaSuccess ? CBR_OK : CBR_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace att
+
+size_t attention_backward_ws(const cbr_attention_desc_t& d) {
+  return std::max(att::total(att::shape_of(d, true)), att::total(att::shape_of(d, false)));
+}
+
+int launch_attention_backward(const AttentionArgs& a, cudaStream_t st) {
+  const bool bf16 = a.d.dtype == CBR_BF16;
+  if (a.d.head_dim > 64) return bf16 ? att::launch<128, true>(a, st) : att::launch<128, false>(a, st);
+  return bf16 ? att::launch<64, true>(a, st) : att::launch<64, false>(a, st);
+}
+
+}  // namespace cbr

@@ -352,11 +352,11 @@ struct Shape {
 // exponentials with the other's products; a block has an SM to itself, so one tile each is taken where two would
 // leave SMs without a block.  Where blocks are fewer than half the SMs the keys are shared among them, a few
 // tiles at least to each.
-Shape shape_of(const cbr_attention_desc_t& d) {
+// (Heads of q that repeat have no axis to pack.)
+Shape shape_of(const cbr_attention_desc_t& d, bool may_pack) {
   Shape s{};
   const int64_t group = d.heads_q / d.heads_k;
-  const bool repeats = d.q_stride[2] == 0;
-  s.pack = group > 1 && group <= kTile && !repeats && (kTile / group * group >= 112 || group * d.q_tokens <= kTile) ? (int)group : 1;
+  s.pack = group > 1 && group <= kTile && may_pack && (kTile / group * group >= 112 || group * d.q_tokens <= kTile) ? (int)group : 1;
   s.packs = d.heads_q / s.pack;
   const int64_t tiles = (d.q_tokens + kTile / s.pack - 1) / (kTile / s.pack);
   s.tiles = (tiles + 1) / 2 * s.packs * d.batch >= kSms ? 2 : 1;
@@ -400,12 +400,12 @@ int launch(const AttentionArgs& g, const Shape& s, cudaStream_t st) {
 }  // namespace att
 
 size_t attention_forward_ws(const cbr_attention_desc_t& d) {
-  const att::Shape s = att::shape_of(d);
-  return s.splits > 1 ? (size_t)s.splits * att::rows_of(d) * (d.head_dim + 1) * 4 : 0;
+  const int splits = std::max(att::shape_of(d, true).splits, att::shape_of(d, false).splits);
+  return splits > 1 ? (size_t)splits * att::rows_of(d) * (d.head_dim + 1) * 4 : 0;
 }
 
 int launch_attention(const AttentionArgs& a, cudaStream_t st) {
-  const att::Shape s = att::shape_of(a.d);
+  const att::Shape s = att::shape_of(a.d, a.d.q_stride[2] != 0);
   const bool bf16 = a.d.dtype == CBR_BF16;
   if (a.d.head_dim > 64) return bf16 ? att::launch<128, true>(a, s, st) : att::launch<128, false>(a, s, st);
   return bf16 ? att::launch<64, true>(a, s, st) : att::launch<64, false>(a, s, st);

@@ -20,9 +20,9 @@ int check(const cbr_attention_desc_t* d) {
   if ((d->dtype != CBR_F16 && d->dtype != CBR_BF16) || d->head_dim > kMaxAttentionDim || d->head_dim % 8 ||
       d->q_tokens > kMaxTokens || d->k_tokens > kMaxTokens || d->heads_q > kMaxHeads)
     return CBR_ERR_UNSUPPORTED;
-  // a block for each 128 queries (keys) of a head at the most
+  // the launches' blocks, one for each 64 queries (keys) of a head at the most, stay far below 2^31
   const int64_t tiles = std::max(d->q_tokens, d->k_tokens) / 128 + 1;
-  if (d->batch > kMaxBlocks / d->heads_q / tiles) return CBR_ERR_UNSUPPORTED;
+  if (d->batch > (int64_t(1) << 28) / d->heads_q / tiles) return CBR_ERR_UNSUPPORTED;
   return CBR_OK;
 }
 

@@ -91,7 +91,8 @@ def attention_backward(do, q, k, v, o, lse, scale, causal=False, lengths=None, s
         big = big.amax(1, keepdim=True)
         ds_low = 2.0 ** -30 * big * see
     e_p = p * (U[dt] + ep) + low
-    e_ds = ds.abs() * (U[dt] + ep + 4 * W) + p * (1 + ep) * edp + ds_low
+    # p itself is a 32-bit number: below 2^-126 its exponential is 0, so ds is off by that much of |dp - D|
+    e_ds = ds.abs() * (U[dt] + ep + 4 * W) + p * (1 + ep) * edp + ds_low + 2.0 ** -126 * (dp - delta).abs() * see
     nq, nk = tq * group, tk
     dv_b = e_p.transpose(-1, -2) @ do.abs() + mma(nq) * (p.transpose(-1, -2) @ do.abs())
     dq_b = scale * (e_ds @ k.abs() + mma(nk) * (ds.abs() @ k.abs()))
