@@ -9,7 +9,7 @@ namespace {
 
 constexpr int64_t kMaxTokens = int64_t(1) << 29, kMaxBlocks = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxByteStride = int64_t(1) << 39;   // elements of 16 bits: what a tensor map can hold
-constexpr int kMaxAttentionDim = 128, kMaxHeads = 65536, kMaxChannels = 16384;
+constexpr int kMaxAttentionDim = 128, kMaxHeads = 65536, kMaxChannels = 16384, kMaxGroups = 4096;
 constexpr int64_t kMaxTensors = int64_t(1) << 20;
 
 int check(const cbr_attention_desc_t* d) {
@@ -45,7 +45,7 @@ int check(const cbr_group_norm_desc_t* d) {
   if (d->images < 0 || d->pixels < 0 || d->channels < 1 || d->groups < 1 || d->channels % d->groups)
     return CBR_ERR_INVALID_ARG;
   if (d->act != CBR_ACT_NONE && d->act != CBR_ACT_RELU && d->act != CBR_ACT_SILU) return CBR_ERR_INVALID_ARG;
-  if (!known_dtype(d->dtype) || d->channels > kMaxChannels || d->images > kMaxBlocks || d->pixels > kMaxBlocks)
+  if (!known_dtype(d->dtype) || d->channels > kMaxChannels || d->groups > kMaxGroups || d->images > kMaxBlocks || d->pixels > kMaxBlocks)
     return CBR_ERR_UNSUPPORTED;
   return CBR_OK;
 }
@@ -161,17 +161,18 @@ cbr_status_t cbr_attention_backward(const cbr_attention_desc_t* desc, const void
   });
 }
 
-cbr_status_t cbr_group_norm_workspace_size(const cbr_group_norm_desc_t* desc, size_t* bytes) {
+cbr_status_t cbr_group_norm_workspace_size(const cbr_group_norm_desc_t* desc, size_t* fwd_bytes, size_t* bwd_bytes) {
   return guarded([&]() -> int {
     if (const int e = check(desc)) return e;
-    if (!bytes) return CBR_ERR_INVALID_ARG;
-    *bytes = group_norm_part_floats(*desc) * sizeof(float);
+    if (fwd_bytes) *fwd_bytes = group_norm_forward_floats(*desc) * sizeof(float);
+    if (bwd_bytes) *bwd_bytes = group_norm_backward_floats(*desc, true) * sizeof(float);
     return CBR_OK;
   });
 }
 
 cbr_status_t cbr_group_norm_forward(const cbr_group_norm_desc_t* desc, const void* x, const float* gamma,
-                                    const float* beta, void* y, float* mean, float* rstd, cbr_stream_t stream) {
+                                    const float* beta, void* y, float* mean, float* rstd, void* ws, size_t ws_bytes,
+                                    cbr_stream_t stream) {
   return guarded([&]() -> int {
     if (const int e = check(desc)) return e;
     const cbr_group_norm_desc_t& d = *desc;
@@ -180,7 +181,11 @@ cbr_status_t cbr_group_norm_forward(const cbr_group_norm_desc_t* desc, const voi
     if (d.images == 0 || d.pixels == 0) return CBR_OK;
     if (!x || !y || !mean || !rstd || (x == y && !same_map(d, d.x_stride, d.y_stride))) return CBR_ERR_INVALID_ARG;
     const size_t e = elt(d.dtype);
-    if (off(x, e) || off(y, e) || off(gamma, 4) || off(beta, 4) || off(mean, 4) || off(rstd, 4)) return CBR_ERR_MISALIGNED;
+    if (off(x, e) || off(y, e) || off(gamma, 4) || off(beta, 4) || off(mean, 4) || off(rstd, 4) || off(ws, 16))
+      return CBR_ERR_MISALIGNED;
+    const size_t need = group_norm_forward_floats(d) * sizeof(float);
+    if (need && !ws) return CBR_ERR_INVALID_ARG;
+    if (need && ws_bytes < need) return CBR_ERR_WORKSPACE;
     GroupNormArgs a{};
     uint32_t* err = nullptr;
     if (const int s = device_for_call(&a.num_sms, &err)) return s;
@@ -191,6 +196,7 @@ cbr_status_t cbr_group_norm_forward(const cbr_group_norm_desc_t* desc, const voi
     a.y = y;
     a.mean = mean;
     a.rstd = rstd;
+    a.part = static_cast<float*>(ws);
     return launch_group_norm(a, reinterpret_cast<cudaStream_t>(stream));
   });
 }
@@ -206,14 +212,16 @@ cbr_status_t cbr_group_norm_backward(const cbr_group_norm_desc_t* desc, const vo
         !gamma != !dgamma || !gamma != !dbeta)
       return CBR_ERR_INVALID_ARG;
     const bool empty = d.images == 0 || d.pixels == 0;
-    if (!empty && (!dy || !x || !mean || !rstd || !dx || (gamma && !ws) || dx == x ||
+    if (!empty && (!dy || !x || !mean || !rstd || !dx || dx == x ||
                    (dx == dy && !same_map(d, d.dx_stride, d.dy_stride))))
       return CBR_ERR_INVALID_ARG;
     const size_t e = elt(d.dtype);
     if (off(dy, e) || off(x, e) || off(dx, e) || off(gamma, 4) || off(beta, 4) || off(mean, 4) || off(rstd, 4) ||
         off(dgamma, 4) || off(dbeta, 4) || off(ws, 16))
       return CBR_ERR_MISALIGNED;
-    if (!empty && gamma && ws_bytes < group_norm_part_floats(d) * sizeof(float)) return CBR_ERR_WORKSPACE;
+    const size_t need = empty ? 0 : group_norm_backward_floats(d, gamma != nullptr) * sizeof(float);
+    if (need && !ws) return CBR_ERR_INVALID_ARG;
+    if (need && ws_bytes < need) return CBR_ERR_WORKSPACE;
     GroupNormArgs a{};
     uint32_t* err = nullptr;
     if (const int s = device_for_call(&a.num_sms, &err)) return s;

@@ -46,7 +46,8 @@ struct GroupNormArgs {
   float* part;
   int num_sms;
 };
-size_t group_norm_part_floats(const cbr_group_norm_desc_t& d);
+size_t group_norm_forward_floats(const cbr_group_norm_desc_t& d);
+size_t group_norm_backward_floats(const cbr_group_norm_desc_t& d, bool parameters);
 int launch_group_norm(const GroupNormArgs& a, cudaStream_t st);
 int launch_group_norm_backward(const GroupNormArgs& a, cudaStream_t st);
 

@@ -25,8 +25,8 @@ def _load() -> ctypes.CDLL:
     if _lib is None:
         lib = cbr.load()
         vp, d, size = ctypes.c_void_p, ctypes.c_char_p, ctypes.c_size_t
-        lib.cbr_group_norm_workspace_size.argtypes = [d, ctypes.POINTER(size)]
-        lib.cbr_group_norm_forward.argtypes = [d] + [vp] * 7
+        lib.cbr_group_norm_workspace_size.argtypes = [d, ctypes.POINTER(size), ctypes.POINTER(size)]
+        lib.cbr_group_norm_forward.argtypes = [d] + [vp] * 7 + [size, vp]
         lib.cbr_group_norm_backward.argtypes = [d] + [vp] * 10 + [size, vp]
         for f in ("cbr_group_norm_workspace_size", "cbr_group_norm_forward", "cbr_group_norm_backward"):
             getattr(lib, f).restype = ctypes.c_int32
@@ -70,12 +70,29 @@ def _shape(x: torch.Tensor, what: str):
     return x.shape[0], pixels, x.shape[-1]
 
 
-def group_norm_forward(x, gamma, beta, groups, *, eps=1e-5, act="none", out=None) -> dict:
+def _workspace(desc, ws, dev, backward: bool):
+    """The workspace (None: none is needed), its address and its bytes."""
+    if ws is not None:
+        if ws.device != dev or not ws.is_contiguous():
+            _bad(f"ws has to be contiguous on {dev}")
+        return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+    size = ctypes.c_size_t()
+    at = ctypes.byref(size)
+    _check(_load().cbr_group_norm_workspace_size(desc, None if backward else at, at if backward else None),
+           "cbr_group_norm_workspace_size")
+    if not size.value:
+        return None, None, 0
+    ws = _new((size.value,), torch.uint8, dev)
+    return ws, ws.data_ptr(), size.value
+
+
+def group_norm_forward(x, gamma, beta, groups, *, eps=1e-5, act="none", ws=None, out=None) -> dict:
     """cbr_group_norm_forward -> dict(y, mean [images][groups], rstd [images][groups]), the statistics fp32.
 
     x [images][...][channels] (an NHWC feature map; f32, f16 or bf16), whose pixels lie a fixed step apart; gamma
     and beta fp32 [channels], or both None; act "none", "relu" or "silu".  out may hold "y" (x itself, to save
-    its memory), "mean" and "rstd"."""
+    its memory), "mean" and "rstd".  ws: a workspace (:func:`group_norm_workspace_size`) to use instead of a new
+    one."""
     images, pixels, channels = _shape(x, "x")
     dev, dt = _device_of(x), x.dtype
     code = _dtype(x, "x")
@@ -86,9 +103,11 @@ def group_norm_forward(x, gamma, beta, groups, *, eps=1e-5, act="none", out=None
     mean = _given(out, "mean", (images, groups), torch.float32, dev)
     rstd = _given(out, "rstd", (images, groups), torch.float32, dev)
     desc = _pack(_DESC, images, pixels, *sx, *sy, 0, 0, 0, 0, channels, groups, _act(act), code, eps)
+    ws, ws_at, ws_n = _workspace(desc, ws, dev, False)
     _check(_load().cbr_group_norm_forward(
         desc, x_at, _vector(gamma, channels, dev, "gamma"), _vector(beta, channels, dev, "beta"), y_at,
-        _vector(mean, n, dev, "mean"), _vector(rstd, n, dev, "rstd"), _stream_of(dev)), "cbr_group_norm_forward")
+        _vector(mean, n, dev, "mean"), _vector(rstd, n, dev, "rstd"), ws_at, ws_n, _stream_of(dev)),
+        "cbr_group_norm_forward")
     return {"y": y, "mean": mean, "rstd": rstd}
 
 
@@ -96,8 +115,7 @@ def group_norm_backward(dy, x, gamma, beta, mean, rstd, groups, *, act="none", w
     """cbr_group_norm_backward -> dict(dx, dgamma, dbeta); the last two None without a gamma.
 
     dy: the gradient at y; mean and rstd from :func:`group_norm_forward`; the rest as there.  out may hold "dx" (dy
-    itself, to save its memory), "dgamma" and "dbeta".  ws: a workspace of :func:`group_norm_workspace_size`
-    bytes to use instead of a new one."""
+    itself, to save its memory), "dgamma" and "dbeta".  ws: as there."""
     images, pixels, channels = _shape(x, "x")
     dev, dt = _device_of(x), x.dtype
     code = _dtype(x, "x")
@@ -111,24 +129,19 @@ def group_norm_backward(dy, x, gamma, beta, mean, rstd, groups, *, act="none", w
         dgamma = _given(out, "dgamma", (channels,), torch.float32, dev)
         dbeta = _given(out, "dbeta", (channels,), torch.float32, dev)
     desc = _pack(_DESC, images, pixels, *sx, 0, 0, *sdy, *sdx, channels, groups, _act(act), code, 1.0)
-    if ws is None:
-        size = ctypes.c_size_t()
-        _check(_load().cbr_group_norm_workspace_size(desc, ctypes.byref(size)), "cbr_group_norm_workspace_size")
-        ws = _new((max(16, size.value),), torch.uint8, dev)
-    elif ws.device != dev or not ws.is_contiguous():
-        _bad(f"ws has to be contiguous on {dev}")
+    ws, ws_at, ws_n = _workspace(desc, ws, dev, True)
     _check(_load().cbr_group_norm_backward(
         desc, dy_at, x_at, _vector(gamma, channels, dev, "gamma"), _vector(beta, channels, dev, "beta"),
         _vector(mean, n, dev, "mean"), _vector(rstd, n, dev, "rstd"), dx_at, _vector(dgamma, channels, dev, "dgamma"),
-        _vector(dbeta, channels, dev, "dbeta"), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev)),
+        _vector(dbeta, channels, dev, "dbeta"), ws_at, ws_n, _stream_of(dev)),
         "cbr_group_norm_backward")
     return {"dx": dx, "dgamma": dgamma, "dbeta": dbeta}
 
 
-def group_norm_workspace_size(x, groups) -> int:
-    """Workspace bytes of :func:`group_norm_backward` for a map of x's shape."""
+def group_norm_workspace_size(x, groups) -> tuple[int, int]:
+    """Workspace bytes of (:func:`group_norm_forward`, :func:`group_norm_backward`) for a map of x's shape."""
     images, pixels, channels = _shape(x, "x")
-    size = ctypes.c_size_t()
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
     desc = _pack(_DESC, images, pixels, *([0] * 8), channels, groups, 0, _dtype(x, "x"), 1.0)
-    _check(_load().cbr_group_norm_workspace_size(desc, ctypes.byref(size)), "cbr_group_norm_workspace_size")
-    return size.value
+    _check(_load().cbr_group_norm_workspace_size(desc, ctypes.byref(f), ctypes.byref(b)), "cbr_group_norm_workspace_size")
+    return f.value, b.value

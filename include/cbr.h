@@ -560,17 +560,18 @@ typedef struct {
   int64_t images, pixels;              /* >= 0; images up to 2^31 - 1, pixels up to 2^31 - 1 */
   int64_t x_stride[2], y_stride[2];    /* elements between images and pixels (>= channels) */
   int64_t dy_stride[2], dx_stride[2];  /* backward */
-  int32_t channels, groups;            /* channels: 1 .. 16384, a multiple of groups */
+  int32_t channels, groups;            /* channels: 1 .. 16384, a multiple of groups; groups: 1 .. 4096 */
   int32_t act, dtype;
   float eps;                           /* > 0 (forward) */
 } cbr_group_norm_desc_t;
 
-/* Workspace bytes of the backward for this desc: the parameter gradients' partial sums. */
-cbr_status_t cbr_group_norm_workspace_size(const cbr_group_norm_desc_t* desc, size_t* bytes);
+/* Workspace bytes of the two calls for this desc (either pointer may be NULL). */
+cbr_status_t cbr_group_norm_workspace_size(const cbr_group_norm_desc_t* desc, size_t* fwd_bytes, size_t* bwd_bytes);
 
 /* Forward -> y, mean and rstd [images][groups] fp32.  y may be x itself (same strides). */
 cbr_status_t cbr_group_norm_forward(const cbr_group_norm_desc_t* desc, const void* x, const float* gamma,
-                                    const float* beta, void* y, float* mean, float* rstd, cbr_stream_t stream);
+                                    const float* beta, void* y, float* mean, float* rstd, void* ws, size_t ws_bytes,
+                                    cbr_stream_t stream);
 
 /*
  * Backward, from x and the forward's mean and rstd.  With xh = (x - m) r, z = gamma xh + beta,

@@ -174,7 +174,7 @@ def test_refusals():
         with pytest.raises(cbr.CBRError):
             gn.group_norm_forward(**args)
     o = gn.group_norm_forward(x, gamma, beta, 4)
-    n = gn.group_norm_workspace_size(x, 4)
+    n = gn.group_norm_workspace_size(x, 4)[1]
     for kw in (dict(dy=s["dy"].float()), dict(mean=o["mean"][:1]), dict(out={"dx": x}), dict(ws=torch.zeros(n - 1, dtype=torch.uint8, device="cuda")),
                dict(ws=torch.zeros(n, dtype=torch.uint8)), dict(gamma=None, beta=None, out={"dx": x})):
         args = {"dy": s["dy"], "x": x, "gamma": gamma, "beta": beta, "mean": o["mean"], "rstd": o["rstd"], "groups": 4, **kw}

@@ -44,8 +44,8 @@ def gn_desc(images=2, pixels=9, x=(144, 16), y=None, dy=None, dx=None, c=16, gro
     return group_norm._DESC.pack(images, pixels, *x, *(y or x), *(dy or x), *(dx or x), c, groups, act, dtype, eps)
 
 
-def gf(lib, desc, x=P, g=P, b=P, y=P + 4096, m=P, r=P):
-    return lib.cbr_group_norm_forward(desc, x, g, b, y, m, r, None)
+def gf(lib, desc, x=P, g=P, b=P, y=P + 4096, m=P, r=P, ws=P, size=FAR):
+    return lib.cbr_group_norm_forward(desc, x, g, b, y, m, r, ws, size, None)
 
 
 def gb(lib, desc, dy=P, x=P + 4096, g=P, b=P, m=P, r=P, dx=P + 8192, dg=P, db=P, ws=P, size=FAR):
@@ -119,7 +119,7 @@ def test_empty_calls_do_nothing(lib):
     (dict(images=-1), 1), (dict(pixels=-1), 1), (dict(c=0), 1), (dict(groups=0), 1), (dict(groups=3), 1), (dict(act=3), 1), (dict(act=-1), 1),
     (dict(eps=0.0), 1), (dict(eps=math.nan), 1), (dict(eps=math.inf), 1), (dict(dtype=3), 3), (dict(c=16388, x=(160000, 16388)), 3),
     (dict(images=1 << 31), 3), (dict(pixels=1 << 31), 3), (dict(x=(144, 15)), 1), (dict(x=(140, 16)), 1), (dict(y=(0, 16)), 1), (dict(x=(-144, 16)), 1),
-    (dict(y=(FAR + 1, 16)), 1)])
+    (dict(y=(FAR + 1, 16)), 1), (dict(c=8192, groups=8192, x=(80000, 8192)), 3)])
 def test_group_norm_descriptor_refusals(lib, kw, status):
     assert gf(lib, gn_desc(**kw)) == status
 
@@ -134,9 +134,14 @@ def test_group_norm_pointer_refusals(lib):
         assert gb(lib, d, **{k: None}) == 1, k
     assert gb(lib, d, dx=P + 4096) == 1 and gb(lib, d, dx=P + 1) == 2 and gb(lib, d, ws=P + 8) == 2
     assert gb(lib, gn_desc(dx=(160, 16)), dx=P) == 1
-    n = ctypes.c_size_t()
-    assert lib.cbr_group_norm_workspace_size(d, ctypes.byref(n)) == 0 and n.value > 0
-    assert gb(lib, d, size=n.value - 1) == 4 and lib.cbr_group_norm_workspace_size(d, None) == 1
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.cbr_group_norm_workspace_size(d, ctypes.byref(f), ctypes.byref(b)) == 0 and b.value > 0
+    assert gb(lib, d, size=b.value - 1) == 4 and gf(lib, d, ws=P + 8) == 2
+    assert lib.cbr_group_norm_workspace_size(d, None, None) == 0
+    # one image that no cluster holds: moments of its runs
+    big = gn_desc(images=1, pixels=1 << 20, c=64, x=(64 << 20, 64), groups=8)
+    assert lib.cbr_group_norm_workspace_size(big, ctypes.byref(f), ctypes.byref(b)) == 0 and f.value > 0
+    assert gf(lib, big, size=f.value - 1) == 4 and gf(lib, big, ws=None) == 1
 
 
 def test_clip_refusals(lib):
