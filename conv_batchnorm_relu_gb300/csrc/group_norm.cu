@@ -1,18 +1,21 @@
 // Group norm with an activation, channels last, forward and backward (declared in include/cbr.h).
 //
-// Bound by memory: x is read once and y written once where that can be.  A cluster of up to 16 blocks takes an
-// image, each block a run of its pixels: the block reads its run (16-byte vectors, a thread keeps its channels),
-// keeps it in shared memory and takes each channel's moments; the blocks exchange their groups' moments
-// through distributed shared memory; then each normalises what it holds and writes it.  Of an image that is
-// more than a cluster holds the rest is read again, mostly from L2.  The backward does the same with x and dy, and
-// the sums of g and g xh.  Where a few images are larger than that, clusters would leave most SMs idle: the
-// moments (sums) and the result are launches of their own, over runs of pixels on every SM.
+// Bound by memory: x is read once and y written once where that can be.  Maps that fit the shared memory of all SMs
+// at once go to clusters of up to 16 blocks: a cluster takes an image, each block a run of its pixels, which it reads
+// (16-byte vectors, a thread keeps its channels) and keeps; the blocks exchange their groups' moments through
+// distributed shared memory; then each normalises what it holds and writes it.  Small images are cut into slices
+// of whole groups instead, which need no exchange.
+//   Larger maps are a stream of tasks on a resident grid: the moments of an image's runs, and, some images later, their
+// results, which read x again from L2.  So HBM is read and written all the time, which clusters that load, wait and
+// store do not do (128x112x112x128 bf16 in clusters of 16: 298 us).
+//   The backward does the same with x and dy, and the sums of g and g xh.
 //   Moments: a thread sums its values' differences from its first one, and their squares, which costs no digits
 // where the mean is far from 0; means and squared deviations are merged by their counts.  All merges have a fixed
 // order.
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <climits>
 #include <mutex>
 #include <set>
 #include <utility>
@@ -28,7 +31,7 @@ namespace {
 
 using namespace tok;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kMaxCluster = 16;
+constexpr int kThreads = 256, kMaxCluster = 16;
 constexpr int64_t kSms = 152;   // of the device that the rules on blocks are made for
 
 struct Params {
@@ -45,20 +48,36 @@ struct Params {
   int64_t pixels;
   int64_t base;          // pixels of a run; the first `extra` runs have one more
   int extra;
-  int channels, groups, per, act;   // per: channels of a group
-  int keep;              // pixels of a run that stay in shared memory
+  int channels, groups, per, act;   // of a slice: blocks along y take slices of whole groups; per: channels of a group
+  int all_channels, all_groups;
+  int keep;              // pixels of a run that stay in shared memory: all of them (clusters), or none
   int runs;              // of an image, one to a block
   float eps;
 };
+
+// The parameters of this block's slice of the channels.
+template <typename T>
+__device__ __forceinline__ Params slice_of(Params a) {
+  const int c = blockIdx.y * a.channels, g = blockIdx.y * a.groups;
+  a.x = static_cast<const T*>(a.x) + c;
+  a.dy = static_cast<const T*>(a.dy) + c;
+  a.y = static_cast<T*>(a.y) + c;
+  if (a.gamma) a.gamma += c, a.beta += c;
+  a.mean += g;
+  a.rstd += g;
+  a.part += c;
+  a.group_part += 2 * g;
+  return a;
+}
 
 // kVec neighbouring channels of a pixel, as they are stored.
 template <typename T, int kVec>
 struct Vec {
   static constexpr int kBytes = kVec * (int)sizeof(T);
-  static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4;
+  static constexpr int kWords = kBytes < 4 ? 1 : kBytes / 4, kPairs = (kVec + 1) / 2;
   uint32_t w[kWords];
 
-  __device__ __forceinline__ void load(const T* p) {
+  __device__ __forceinline__ void load(const uint8_t* p) {
     if constexpr (kBytes == 16)
       asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
     else if constexpr (kBytes == 8)
@@ -68,71 +87,81 @@ struct Vec {
     else
       asm volatile("ld.global.u16 %0, [%1];" : "=r"(w[0]) : "l"(p));
   }
-  __device__ __forceinline__ void store(T* p) const {
+  // global to shared memory without registers; asynchronous where the width allows
+  static __device__ __forceinline__ void copy(uint32_t to, const uint8_t* p) {
+    if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+    else if constexpr (kBytes >= 4) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(p), "n"(kBytes) : "memory");
+    else asm volatile("{\n\t.reg .u16 h;\n\tld.global.u16 h, [%1];\n\tst.shared.u16 [%0], h;\n\t}" ::"r"(to), "l"(p) : "memory");
+  }
+  __device__ __forceinline__ void store(uint8_t* p) const {
     if constexpr (kBytes == 16) st_global_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
     else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
     else *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
   }
-  // to and from shared memory, `i` vectors from its start
-  __device__ __forceinline__ void put(uint8_t* s, int i) const {
-    uint8_t* p = s + (size_t)i * kBytes;
-    if constexpr (kBytes == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
-    else *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+  __device__ __forceinline__ void take(uint32_t from) {
+    if constexpr (kBytes == 16)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from));
+    else if constexpr (kBytes == 8)
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(from));
+    else if constexpr (kBytes == 4)
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(from));
+    else
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w[0]) : "r"(from));
   }
-  __device__ __forceinline__ void take(const uint8_t* s, int i) {
-    const uint8_t* p = s + (size_t)i * kBytes;
-    if constexpr (kBytes == 16) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else if constexpr (kBytes == 8) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      w[0] = v.x, w[1] = v.y;
-    } else if constexpr (kBytes == 4) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
+  // as pairs of 32-bit values (a single one: with 0)
+  __device__ __forceinline__ void get(float2 (&v)[kPairs]) const {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) v[i] = unpack2<std::is_same_v<T, __nv_bfloat16>>(w[i]);
     } else {
-      w[0] = *reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) v[i] = make_float2(__uint_as_float(w[2 * i]), kVec > 1 ? __uint_as_float(w[2 * i + (kVec > 1)]) : 0.f);
     }
   }
-  __device__ __forceinline__ void get(float (&v)[kVec]) const {
-    if constexpr (sizeof(T) == 4) {
+  __device__ __forceinline__ void set(const float2 (&v)[kPairs]) {
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) v[i] = __uint_as_float(w[i]);
+      for (int i = 0; i < kPairs; ++i) w[i] = pack2<std::is_same_v<T, __nv_bfloat16>>(v[i].x, v[i].y);
     } else {
 #pragma unroll
-      for (int i = 0; i < kVec; i += 2) {
-        const float2 f = unpack2<std::is_same_v<T, __nv_bfloat16>>(w[i / 2]);
-        v[i] = f.x;
-        if constexpr (kVec > 1) v[i + 1] = f.y;
-      }
-    }
-  }
-  __device__ __forceinline__ void set(const float (&v)[kVec]) {
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) w[i] = __float_as_uint(v[i]);
-    } else if constexpr (kVec == 1) {
-      w[0] = pack2<std::is_same_v<T, __nv_bfloat16>>(v[0], 0.f);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kVec; i += 2) w[i / 2] = pack2<std::is_same_v<T, __nv_bfloat16>>(v[i], v[i + 1]);
+      for (int i = 0; i < kVec; ++i) w[i] = __float_as_uint(i & 1 ? v[i / 2].y : v[i / 2].x);
     }
   }
 };
 
-// How a block's threads lie over its run: a thread has a column (kVec channels) and every `rows`th pixel.
+// Two 32-bit values in one instruction.
+__device__ __forceinline__ uint64_t bits(float2 v) { return (uint64_t)__float_as_uint(v.y) << 32 | __float_as_uint(v.x); }
+__device__ __forceinline__ float2 pair(uint64_t v) { return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return pair(d);
+}
+__device__ __forceinline__ float2 sub(float2 a, float2 b) {
+  uint64_t d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return pair(d);
+}
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return pair(d);
+}
+
+// How a block's threads lie over its run: a thread has a column (kVec channels) and every `rows`th pixel.  Threads behind
+// the last row have nothing to do.
 struct Lay {
-  int columns;   // vectors of a pixel
-  int across;    // of them at a time: the threads of a row
-  int rows;      // rows of threads; threads behind the last have nothing to do
+  int columns;   // vectors of a pixel, at most kThreads
+  int rows;      // of threads
+  int row, col;  // this thread's
   template <int kVec>
   static __device__ __forceinline__ Lay of(int channels) {
     Lay l;
     l.columns = channels / kVec;
-    l.across = min(l.columns, kThreads);
-    l.rows = kThreads / l.across;
+    l.rows = kThreads / l.columns;
+    l.row = threadIdx.x / l.columns;
+    l.col = threadIdx.x - l.row * l.columns;
     return l;
   }
 };
@@ -140,170 +169,395 @@ struct Lay {
 // The pixels of run `r` of an image.
 __device__ __forceinline__ int64_t run_begin(const Params& a, int r) { return a.base * r + min(r, a.extra); }
 __device__ __forceinline__ int run_length(const Params& a, int r) { return (int)a.base + (r < a.extra); }
-// Of `n` pixels, those of row `row` of `rows`.
-__device__ __forceinline__ int turns(int n, int row, int rows) { return row < n ? (n - row + rows - 1) / rows : 0; }
+// Of `n` pixels, those of this thread's row.
+__device__ __forceinline__ int turns(int n, const Lay& l) { return l.row < l.rows && l.row < n ? (n - l.row + l.rows - 1) / l.rows : 0; }
 
-__device__ __forceinline__ float act_of(float z, int act) {
-  if (act == CBR_ACT_RELU) return Max::of(z, 0.f);
-  if (act == CBR_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
+template <int kAct>
+__device__ __forceinline__ float act_of(float z) {
+  if constexpr (kAct == CBR_ACT_RELU) return Max::of(z, 0.f);
+  if constexpr (kAct == CBR_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
   return z;
 }
-__device__ __forceinline__ float act_slope(float z, float up, int act) {
-  if (act == CBR_ACT_RELU) return z > 0.f ? up : 0.f;
-  if (act == CBR_ACT_SILU) {
+template <int kAct>
+__device__ __forceinline__ float act_slope(float z, float up) {
+  if constexpr (kAct == CBR_ACT_RELU) return z > 0.f ? up : 0.f;
+  if constexpr (kAct == CBR_ACT_SILU) {
     const float s = __fdividef(1.f, 1.f + __expf(-z));
     return up * (s * fmaf(z, 1.f - s, 1.f));
   }
   return up;
 }
+// Runs the body made for the activation.
+template <typename Body>
+__device__ __forceinline__ void by_act(int act, Body body) {
+  if (act == CBR_ACT_RELU) body(std::integral_constant<int, CBR_ACT_RELU>{});
+  else if (act == CBR_ACT_SILU) body(std::integral_constant<int, CBR_ACT_SILU>{});
+  else body(std::integral_constant<int, CBR_ACT_NONE>{});
+}
 
-// What a channel is normalised with: z = (x - mean) scale + shift.
+// A thread's channels of an array in shared memory.
 template <int kVec>
-struct Channel {
-  float mean[kVec], scale[kVec], shift[kVec], rstd[kVec];
-  __device__ __forceinline__ void of(const Params& a, int c, const float* mean_of, const float* rstd_of) {
+__device__ __forceinline__ void take_channels(float2 (&v)[(kVec + 1) / 2], const float* p, int col) {
+  p += col * kVec;
+  if constexpr (kVec == 1) {
+    v[0] = make_float2(p[0], 0.f);
+  } else {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const int g = (c + i) / a.per;
-      mean[i] = mean_of[g];
-      rstd[i] = rstd_of[g];
-      scale[i] = a.gamma ? rstd[i] * a.gamma[c + i] : rstd[i];
-      shift[i] = a.gamma ? a.beta[c + i] : 0.f;
+    for (int i = 0; i < kVec / 4; ++i) {
+      const float4 u = reinterpret_cast<const float4*>(p)[i];
+      v[2 * i] = make_float2(u.x, u.y);
+      v[2 * i + 1] = make_float2(u.z, u.w);
+    }
+  }
+}
+
+// A thread's pixels of a column in kOps maps: global and shared-memory addresses of the first, and the steps to the next
+// ones.  Shared memory has `slots` places for them (a multiple of the batches), used in turn.
+template <int kOps>
+struct Way {
+  const uint8_t* at[kOps];
+  int64_t step[kOps];
+  uint32_t held[kOps], held_step;
+  int all, slots;
+};
+// By the maps read: pixels that a thread takes at a time, batches of them that it has asked for, blocks to an SM.  The
+// forward moves more and computes less: deeper rings (two blocks with 5 batches and three with 3: 176 and 182 us at
+// 128x112x112x128 bf16); the backward wants warps (101 and 95 us at 256x56x56x64 f16).
+template <int kOps>
+constexpr int kBatch = 4 / kOps;
+template <int kOps, int kBytes>
+constexpr int kAhead = kOps == 1 ? 5 : kBytes == 16 ? 3 : 6;
+template <int kOps>
+constexpr int kResident = kOps == 1 ? 2 : 3;
+
+// Reads a column through shared memory, some batches ahead from the start on.  A thread reads only what it has
+// copied itself, so it waits for its own copies alone.
+template <typename V, int kOps>
+struct Reader {
+  static constexpr int kBatch = gn::kBatch<kOps>;
+  Way<kOps> way;       // of the next pixel to ask for
+  uint32_t from[kOps];
+  int asked = 0, slot = 0;
+
+  __device__ __forceinline__ explicit Reader(const Way<kOps>& w) : way(w) {
+#pragma unroll
+    for (int o = 0; o < kOps; ++o) from[o] = w.held[o];
+#pragma unroll 1
+    for (int i = 0; i < kAhead<kOps, V::kBytes>; ++i) ask();
+  }
+  __device__ __forceinline__ void copy() {
+#pragma unroll
+    for (int o = 0; o < kOps; ++o) {
+      V::copy(way.held[o], way.at[o]);
+      way.held[o] += way.held_step;
+      way.at[o] += way.step[o];
+    }
+  }
+  __device__ __forceinline__ void ask() {
+    if (asked + kBatch <= way.all) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) copy();
+      asked += kBatch;
+      slot += kBatch;
+      if (slot == way.slots) {
+        slot = 0;
+#pragma unroll
+        for (int o = 0; o < kOps; ++o) way.held[o] -= way.slots * way.held_step;
+      }
+    } else {
+      for (; asked < way.all; ++asked) copy();   // the last ones: less than a batch, which a ring has room for
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // take() gets each pixel's vectors.
+  template <typename Take>
+  __device__ __forceinline__ void run(Take take) {
+    V v[kBatch][kOps];
+    int done = 0, at = 0;
+    auto fetch = [&](int b) {
+#pragma unroll
+      for (int o = 0; o < kOps; ++o) {
+        v[b][o].take(from[o]);
+        from[o] += way.held_step;
+      }
+    };
+#pragma unroll 1
+    for (; done + kBatch <= way.all; done += kBatch) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAhead<kOps, V::kBytes> - 1) : "memory");
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) fetch(b);
+      at += kBatch;
+      if (at == way.slots) {
+        at = 0;
+#pragma unroll
+        for (int o = 0; o < kOps; ++o) from[o] -= way.slots * way.held_step;
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) take(v[b]);
+      ask();   // into the places just read
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll 1
+    for (; done < way.all; ++done) {
+      fetch(0);
+      take(v[0]);
     }
   }
 };
 
-constexpr int kBatch = 4;   // a thread's loads in flight for each operand
+// Goes over a column that shared memory holds.
+template <typename V, int kOps, typename Take>
+__device__ __forceinline__ void reread(const Way<kOps>& way, Take take) {
+  constexpr int kBatch = gn::kBatch<kOps>;
+  V v[kBatch][kOps];
+  uint32_t from[kOps];
+  int done = 0;
+#pragma unroll
+  for (int o = 0; o < kOps; ++o) from[o] = way.held[o];
+  auto fetch = [&](int b) {
+#pragma unroll
+    for (int o = 0; o < kOps; ++o) {
+      v[b][o].take(from[o]);
+      from[o] += way.held_step;
+    }
+  };
+#pragma unroll 1
+  for (; done + kBatch <= way.all; done += kBatch) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) fetch(b);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) take(v[b]);
+  }
+#pragma unroll 1
+  for (; done < way.all; ++done) {
+    fetch(0);
+    take(v[0]);
+  }
+}
 
-// Shared memory: two values of each channel for each row of threads, two of each group twice, the kept pixels.
 template <int kVec>
-__host__ __device__ constexpr int table_floats(int channels) {
-  return channels > kThreads * kVec ? channels : kThreads * kVec;
+constexpr int kTable = kThreads * kVec;   // values of all channels in all rows of threads, at the most
+
+// Shared memory holds a run's pixels one after the other (a.keep of them, dy's behind x's), or, where a.keep is 0, a ring
+// for each thread: kAhead batches of vectors, a step of all threads apart.
+template <typename T, int kVec, int kOps>
+__device__ __forceinline__ Way<kOps> way_of(const Params& a, const Lay& l, const T* x, const T* dy, const uint8_t* kept, int n) {
+  using V = Vec<T, kVec>;
+  const int col = l.col;
+  Way<kOps> w;
+  const bool ring = a.keep == 0;
+  w.at[0] = reinterpret_cast<const uint8_t*>(x + l.row * a.x_stride[1] + (int64_t)col * kVec);
+  w.step[0] = l.rows * a.x_stride[1] * (int64_t)sizeof(T);
+  w.held[0] = smem_u32(kept) + (ring ? threadIdx.x : l.row * l.columns + col) * V::kBytes;
+  w.held_step = (ring ? kThreads : l.rows * l.columns) * V::kBytes;
+  w.slots = ring ? kAhead<kOps, V::kBytes> * kBatch<kOps> : INT_MAX;
+  w.all = turns(n, l);
+  if constexpr (kOps == 2) {
+    w.at[1] = reinterpret_cast<const uint8_t*>(dy + l.row * a.dy_stride[1] + (int64_t)col * kVec);
+    w.step[1] = l.rows * a.dy_stride[1] * (int64_t)sizeof(T);
+    w.held[1] = w.held[0] + (ring ? w.slots * w.held_step : a.keep * a.channels * (uint32_t)sizeof(T));
+  }
+  return w;
 }
 
 // ---------------------------------------------------------------- forward
 
-// A run's moments: `table` gets (mean, squared deviations) of every channel in every row of threads; `kept` the
-// first pixels.
+// A run's moments: `table` gets (mean, squared deviations) of every channel in every row of threads.
 template <typename T, int kVec>
-__device__ __forceinline__ void moments(const Params& a, const T* x, int n, float* table, uint8_t* kept) {
-  const Lay l = Lay::of<kVec>(a.channels);
-  const int row = threadIdx.x / l.across, size = table_floats<kVec>(a.channels);
-  if (row >= l.rows) return;
-  for (int col = threadIdx.x % l.across; col < l.columns; col += l.across) {
-    const T* p = x + (int64_t)col * kVec;
-    float first[kVec], s[kVec], q[kVec];
+__device__ __forceinline__ void moments(const Params& a, const Lay& l, const T* x, int n, float* table, const uint8_t* kept) {
+  using V = Vec<T, kVec>;
+  const Way<1> way = way_of<T, kVec, 1>(a, l, x, nullptr, kept, n);
+  if (way.all == 0) return;
+  Reader<V, 1> reader(way);
+  float2 first[V::kPairs], s[V::kPairs], q[V::kPairs];
+  V v;
+  v.load(way.at[0]);
+  v.get(first);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) first[i] = s[i] = q[i] = 0.f;
-    for (int at = row; at < n; at += l.rows * kBatch) {
-      Vec<T, kVec> v[kBatch];
+  for (int i = 0; i < V::kPairs; ++i) s[i] = q[i] = make_float2(0.f, 0.f);
+  reader.run([&](V (&v)[1]) {
+    float2 f[V::kPairs];
+    v[0].get(f);
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-        if (at + b * l.rows < n) v[b].load(p + (at + b * l.rows) * a.x_stride[1]);
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int pixel = at + b * l.rows;
-        if (pixel >= n) continue;
-        if (pixel < a.keep) v[b].put(kept, pixel * l.columns + col);
-        float f[kVec];
-        v[b].get(f);
-        if (pixel == row)
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) first[i] = f[i];
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const float d = f[i] - first[i];
-          s[i] += d;
-          q[i] = fmaf(d, d, q[i]);
-        }
-      }
+    for (int i = 0; i < V::kPairs; ++i) {
+      const float2 d = sub(f[i], first[i]);
+      s[i] = add(s[i], d);
+      q[i] = fma(d, d, q[i]);
     }
-    const int count = turns(n, row, l.rows);
-    if (count == 0) continue;
-    const float inv = 1.f / (float)count;
-    float* m = table + row * a.channels + col * kVec;
+  });
+  const float inv = 1.f / (float)way.all;
+  float* m = table + l.row * a.channels + l.col * kVec;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const float shift = s[i] * inv;
-      m[i] = first[i] + shift;
-      m[size + i] = q[i] - s[i] * shift;
-    }
+  for (int i = 0; i < kVec; ++i) {
+    const float si = i & 1 ? s[i / 2].y : s[i / 2].x, qi = i & 1 ? q[i / 2].y : q[i / 2].x;
+    m[i] = (i & 1 ? first[i / 2].y : first[i / 2].x) + si * inv;
+    m[kTable<kVec> + i] = qi - si * (si * inv);
   }
 }
 
-// The groups' moments of a run from its channels': a warp for each group.
-template <int kVec>
-__device__ __forceinline__ void group_moments(const Params& a, int n, const float* table, float2* groups) {
-  const Lay l = Lay::of<kVec>(a.channels);
-  const int size = table_floats<kVec>(a.channels), lane = threadIdx.x & 31;
-  for (int g = threadIdx.x >> 5; g < a.groups; g += kWarps) {
-    const float* m = table + g * a.per;
-    const float ref = n ? m[0] : 0.f;
-    float s = 0.f, q = 0.f;
-    for (int e = lane; e < l.rows * a.per; e += 32) {
-      const int row = e / a.per, at = row * a.channels + e % a.per, count = turns(n, row, l.rows);
-      if (count) s = fmaf((float)count, m[at] - ref, s);
-    }
-    const float mean = n ? ref + warp_reduce<Sum>(s) / ((float)n * (float)a.per) : 0.f;
-    for (int e = lane; e < l.rows * a.per; e += 32) {
-      const int row = e / a.per, at = row * a.channels + e % a.per, count = turns(n, row, l.rows);
-      if (count) q += fmaf((float)count * (m[at] - mean), m[at] - mean, m[size + at]);
-    }
-    q = warp_reduce<Sum>(q);
-    if (lane == 0) groups[g] = make_float2(mean, q);
+// How `many` sums of `terms` terms are shared out: 2^log lanes (at most a warp) to each.
+struct Team {
+  int log;
+  static __device__ __forceinline__ Team of(int many, int terms) {
+    // the largest power of two that is no more than the terms nor the threads there are for each sum
+    const int most = min(min(32, terms), max(1, kThreads / many));
+    return Team{31 - __clz(most)};
   }
+  __device__ __forceinline__ int lanes() const { return 1 << log; }
+  __device__ __forceinline__ int sub() const { return threadIdx.x & (lanes() - 1); }
+  __device__ __forceinline__ int first() const { return threadIdx.x >> log; }   // of the sums
+  __device__ __forceinline__ int teams() const { return kThreads >> log; }
+  __device__ __forceinline__ float sum(float v) const {
+    for (int o = lanes() >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  }
+};
+// Of the sums over a run: rows of threads into channels, channels into groups, runs into images.
+struct Teams {
+  Team channels, groups, runs;
+  static __device__ __forceinline__ Teams of(const Params& a, const Lay& l) {
+    return Teams{Team::of(a.channels, l.rows), Team::of(a.groups, a.per), Team::of(a.groups, a.runs)};
+  }
+};
+
+// The channels' moments of a run, from the rows of threads', into the first row's place.
+template <int kVec>
+__device__ __forceinline__ void channel_moments(const Params& a, const Lay& l, Team team, int n, float* table) {
+  const int lanes = team.lanes(), sub = team.sub();
+  const int base = n / l.rows, extra = n - base * l.rows, rows = min(n, l.rows);
+  const float inv = 1.f / (float)max(n, 1);
+  for (int first = 0; first < a.channels; first += team.teams()) {
+    const int c = first + team.first();
+    const bool in = c < a.channels;
+    const float* m = table + min(c, a.channels - 1);
+    const float ref = m[0];
+    float s = 0.f, q = 0.f;
+    for (int r = sub; r < rows; r += lanes) s = fmaf((float)(base + (r < extra)), m[r * a.channels] - ref, s);
+    const float mean = ref + team.sum(s) * inv;
+    for (int r = sub; r < rows; r += lanes) {
+      const float d = m[r * a.channels] - mean;
+      q += fmaf((float)(base + (r < extra)) * d, d, m[kTable<kVec> + r * a.channels]);
+    }
+    q = team.sum(q);
+    __syncwarp();
+    if (in && sub == 0) table[c] = n ? mean : 0.f, table[kTable<kVec> + c] = n ? q : 0.f;
+  }
+}
+
+// The groups' moments of a run from its channels', which have n values each.
+template <int kVec>
+__device__ __forceinline__ void group_moments(const Params& a, Team team, int n, const float* table, float2* groups) {
+  const int lanes = team.lanes(), sub = team.sub();
+  const float inv = 1.f / (float)a.per;
+  for (int first = 0; first < a.groups; first += team.teams()) {
+    const int g = first + team.first();
+    const float* m = table + min(g, a.groups - 1) * a.per;
+    const float ref = m[0];
+    float s = 0.f, q = 0.f;
+    for (int e = sub; e < a.per; e += lanes) s += m[e] - ref;
+    const float mean = ref + team.sum(s) * inv;
+    for (int e = sub; e < a.per; e += lanes) {
+      const float d = m[e] - mean;
+      q += fmaf((float)n * d, d, m[kTable<kVec> + e]);
+    }
+    q = team.sum(q);
+    if (g < a.groups && sub == 0) groups[g] = make_float2(mean, q);
+  }
+}
+
+// (count, mean, squared deviations) of two sets as one.
+__device__ __forceinline__ void merge_moments(float& n, float& mean, float& q, float n2, float mean2, float q2) {
+  if (n2 == 0.f) return;
+  const float d = mean2 - mean, share = n2 / (n + n2);
+  mean = fmaf(d, share, mean);
+  q += fmaf(d * d, n * share, q2);
+  n += n2;
 }
 
 __device__ __forceinline__ float rstd_of(float squares, float n, float eps) { return 1.f / sqrtf(fmaxf(squares, 0.f) / n + eps); }
 
-// A run normalised: the kept pixels from shared memory, the others read again.
-template <typename T, int kVec>
-__device__ __forceinline__ void normalise(const Params& a, const T* x, T* y, int n, const float* mean, const float* rstd, const uint8_t* kept) {
-  const Lay l = Lay::of<kVec>(a.channels);
-  const int row = threadIdx.x / l.across;
-  if (row >= l.rows) return;
-  for (int col = threadIdx.x % l.across; col < l.columns; col += l.across) {
-    Channel<kVec> c;
-    c.of(a, col * kVec, mean, rstd);
-    for (int at = row; at < n; at += l.rows * kBatch) {
-      Vec<T, kVec> v[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int pixel = at + b * l.rows;
-        if (pixel < a.keep && pixel < n) v[b].take(kept, pixel * l.columns + col);
-        else if (pixel < n) v[b].load(x + pixel * a.x_stride[1] + (int64_t)col * kVec);
-      }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int pixel = at + b * l.rows;
-        if (pixel >= n) continue;
-        float f[kVec];
-        v[b].get(f);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) f[i] = act_of(fmaf(f[i] - c.mean[i], c.scale[i], c.shift[i]), a.act);
-        v[b].set(f);
-        v[b].store(y + pixel * a.y_stride[1] + (int64_t)col * kVec);
-      }
-    }
-  }
+// Shared memory: two values of each channel for each row of threads; two of each group (a run's); two more (an image's);
+// five of each channel (what the results are computed with); the channels' groups; the kept pixels or rings.
+__host__ __device__ constexpr int64_t shared_bytes(int64_t table, int channels, int groups) {
+  return 8 * table + 16 * (((int64_t)groups + 1) & ~1) + 20 * (((int64_t)channels + 3) & ~3) + ((2 * (int64_t)channels + 15) & ~15);
 }
-
 template <typename T, int kVec>
 struct Shared {
   float* table;
   float2* groups;
-  float* stat;     // mean, then rstd; backward: the two means of a group
+  float* stat;        // mean, then rstd (backward: the two means) of each group
+  float* coef;        // mean, scale, shift (backward: and two more) of each channel, `step` apart
+  uint16_t* group;
   uint8_t* kept;
+  int step;
   __device__ __forceinline__ Shared(const Params& a, uint8_t* smem) {
+    const int even = (a.groups + 1) & ~1;
+    step = (a.channels + 3) & ~3;
     table = reinterpret_cast<float*>(smem);
-    groups = reinterpret_cast<float2*>(table + 2 * table_floats<kVec>(a.channels));
-    stat = reinterpret_cast<float*>(groups + a.groups);
-    kept = smem + ((8 * table_floats<kVec>(a.channels) + 16 * a.groups + 15) & ~15);
+    groups = reinterpret_cast<float2*>(table + 2 * kTable<kVec>);
+    stat = reinterpret_cast<float*>(groups + even);
+    coef = stat + 2 * even;
+    group = reinterpret_cast<uint16_t*>(coef + 5 * step);
+    kept = smem + shared_bytes(kTable<kVec>, a.channels, a.groups);
+  }
+  // the channels' groups, visible to the block after its next barrier
+  __device__ __forceinline__ void set_groups(const Params& a) const {
+    for (int c = threadIdx.x; c < a.channels; c += kThreads) group[c] = (uint16_t)(c / a.per);
+  }
+  // z = (x - mean) scale + shift
+  __device__ __forceinline__ void set_channels(const Params& a, const float* mean, const float* rstd) const {
+    for (int c = threadIdx.x; c < a.channels; c += kThreads) {
+      const int g = group[c];
+      coef[c] = mean[g];
+      coef[step + c] = a.gamma ? rstd[g] * a.gamma[c] : rstd[g];
+      coef[2 * step + c] = a.gamma ? a.beta[c] : 0.f;
+    }
+  }
+  // dx = scale g - rstd (mean_g + (x - mean) rstd mean_gx)
+  __device__ __forceinline__ void set_gradient(const Params& a, const float* rstd) const {
+    for (int c = threadIdx.x; c < a.channels; c += kThreads) {
+      const int g = group[c];
+      const float r = -rstd[g];
+      coef[3 * step + c] = r * stat[g];
+      coef[4 * step + c] = r * rstd[g] * stat[a.groups + g];
+    }
   }
 };
 
+// A run normalised: what shared memory holds (kHeld), or read again.  ready() brings the coefficients, the whole block
+// in step, after the first loads.
+template <typename T, int kVec, bool kHeld, typename Ready>
+__device__ __forceinline__ void normalise(const Params& a, const Lay& l, const Shared<T, kVec>& s, const T* x, T* y, int n, Ready ready) {
+  using V = Vec<T, kVec>;
+  std::conditional_t<kHeld, Way<1>, Reader<V, 1>> source(way_of<T, kVec, 1>(a, l, x, nullptr, s.kept, n));
+  ready();
+  float2 mean[V::kPairs], scale[V::kPairs], shift[V::kPairs];
+  take_channels<kVec>(mean, s.coef, l.col);
+  take_channels<kVec>(scale, s.coef + s.step, l.col);
+  take_channels<kVec>(shift, s.coef + 2 * s.step, l.col);
+  uint8_t* out = reinterpret_cast<uint8_t*>(y + l.row * a.y_stride[1] + l.col * kVec);
+  const int64_t out_step = l.rows * a.y_stride[1] * (int64_t)sizeof(T);
+  by_act(a.act, [&](auto act) {
+    auto make = [&](V (&v)[1]) {
+      float2 f[V::kPairs];
+      v[0].get(f);
+#pragma unroll
+      for (int i = 0; i < V::kPairs; ++i) {
+        f[i] = fma(sub(f[i], mean[i]), scale[i], shift[i]);
+        f[i] = make_float2(act_of<decltype(act)::value>(f[i].x), act_of<decltype(act)::value>(f[i].y));
+      }
+      v[0].set(f);
+      v[0].store(out);
+      out += out_step;
+    };
+    if constexpr (kHeld) reread<V, 1>(source, make);
+    else source.run(make);
+  });
+}
+
 template <typename T, int kVec>
-__global__ void __launch_bounds__(kThreads, 2) cluster_forward_kernel(const __grid_constant__ Params a) {
+__global__ void __launch_bounds__(kThreads, 2) cluster_forward_kernel(const __grid_constant__ Params whole) {
+  const Params a = slice_of<T>(whole);
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint8_t smem[];
   const Shared<T, kVec> s(a, smem);
@@ -312,9 +566,14 @@ __global__ void __launch_bounds__(kThreads, 2) cluster_forward_kernel(const __gr
   const int64_t image = blockIdx.x / a.runs;
   const int n = run_length(a, run);
   const T* x = static_cast<const T*>(a.x) + image * a.x_stride[0] + run_begin(a, run) * a.x_stride[1];
-  moments<T, kVec>(a, x, n, s.table, s.kept);
+  const Lay l = Lay::of<kVec>(a.channels);
+  const Teams teams = Teams::of(a, l);
+  s.set_groups(a);
+  moments<T, kVec>(a, l, x, n, s.table, s.kept);
   __syncthreads();
-  group_moments<kVec>(a, n, s.table, s.groups);
+  channel_moments<kVec>(a, l, teams.channels, n, s.table);
+  __syncthreads();
+  group_moments<kVec>(a, teams.groups, n, s.table, s.groups);
   cluster.sync();
   const float total = (float)a.pixels * (float)a.per;
   for (int g = threadIdx.x; g < a.groups; g += kThreads) {
@@ -335,200 +594,148 @@ __global__ void __launch_bounds__(kThreads, 2) cluster_forward_kernel(const __gr
     const float rstd = rstd_of(q, total, a.eps);
     s.stat[g] = mean;
     s.stat[a.groups + g] = rstd;
-    if (run == 0) a.mean[image * a.groups + g] = mean, a.rstd[image * a.groups + g] = rstd;
+    if (run == 0) a.mean[image * a.all_groups + g] = mean, a.rstd[image * a.all_groups + g] = rstd;
   }
   __syncthreads();
   cluster.barrier_arrive();   // the other blocks' moments are not read any more
-  normalise<T, kVec>(a, x, static_cast<T*>(a.y) + image * a.y_stride[0] + run_begin(a, run) * a.y_stride[1], n, s.stat, s.stat + a.groups, s.kept);
-  cluster.barrier_wait();
-}
-
-// Few large images: every run's moments, [image][run][group], then the images', then the result.
-template <typename T, int kVec>
-__global__ void __launch_bounds__(kThreads, 2) moments_kernel(const __grid_constant__ Params a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  const Shared<T, kVec> s(a, smem);
-  const int run = blockIdx.x % a.runs;
-  const int64_t image = blockIdx.x / a.runs;
-  const int n = run_length(a, run);
-  moments<T, kVec>(a, static_cast<const T*>(a.x) + image * a.x_stride[0] + run_begin(a, run) * a.x_stride[1], n, s.table, s.kept);
+  s.set_channels(a, s.stat, s.stat + a.groups);
   __syncthreads();
-  group_moments<kVec>(a, n, s.table, reinterpret_cast<float2*>(a.group_part) + (int64_t)blockIdx.x * a.groups);
-}
-
-// A warp for each group of an image.
-__global__ void __launch_bounds__(128) merge_moments_kernel(const __grid_constant__ Params a, int64_t images) {
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (at >= images * a.groups) return;
-  const float2* m = reinterpret_cast<const float2*>(a.group_part) + at / a.groups * a.runs * a.groups + at % a.groups;
-  const float ref = m[0].x, total = (float)a.pixels * (float)a.per;
-  float sum = 0.f, q = 0.f;
-  for (int r = lane; r < a.runs; r += 32) sum = fmaf((float)run_length(a, r) * (float)a.per, m[(int64_t)r * a.groups].x - ref, sum);
-  const float mean = ref + warp_reduce<Sum>(sum) / total;
-  for (int r = lane; r < a.runs; r += 32) {
-    const float2 v = m[(int64_t)r * a.groups];
-    q += fmaf((float)run_length(a, r) * (float)a.per * (v.x - mean), v.x - mean, v.y);
-  }
-  q = warp_reduce<Sum>(q);
-  if (lane == 0) a.mean[at] = mean, a.rstd[at] = rstd_of(q, total, a.eps);
-}
-
-// Runs in the opposite order to the moments', whose last ones are still in L2.
-template <typename T, int kVec>
-__global__ void __launch_bounds__(kThreads, 2) normalise_kernel(const __grid_constant__ Params a) {
-  const int block = gridDim.x - 1 - blockIdx.x, run = block % a.runs;
-  const int64_t image = block / a.runs;
-  normalise<T, kVec>(a, static_cast<const T*>(a.x) + image * a.x_stride[0] + run_begin(a, run) * a.x_stride[1],
-                     static_cast<T*>(a.y) + image * a.y_stride[0] + run_begin(a, run) * a.y_stride[1], run_length(a, run), a.mean + image * a.groups,
-                     a.rstd + image * a.groups, nullptr);
+  normalise<T, kVec, true>(a, l, s, x, static_cast<T*>(a.y) + image * a.y_stride[0] + run_begin(a, run) * a.y_stride[1], n, [] {});
+  cluster.barrier_wait();
 }
 
 // ---------------------------------------------------------------- backward
 
-// A run's sums of g and g xh: `table` gets them of every channel in every row of threads.
-template <typename T, int kVec>
-__device__ __forceinline__ void sums(const Params& a, int64_t image, const T* x, const T* dy, int n, float* table, uint8_t* kept) {
-  const Lay l = Lay::of<kVec>(a.channels);
-  const int row = threadIdx.x / l.across, size = table_floats<kVec>(a.channels);
-  if (row >= l.rows) return;
-  uint8_t* kept_dy = kept + (size_t)a.keep * a.channels * sizeof(T);
-  for (int col = threadIdx.x % l.across; col < l.columns; col += l.across) {
-    Channel<kVec> c;
-    c.of(a, col * kVec, a.mean + image * a.groups, a.rstd + image * a.groups);
-    float s[kVec], sx[kVec];
+// A run's sums of g and g xh: `table` gets them (the second still to be multiplied by rstd) of every channel in every row
+// of threads.  ready() as above.
+template <typename T, int kVec, typename Ready>
+__device__ __forceinline__ void sums(const Params& a, const Lay& l, const Shared<T, kVec>& s, const T* x, const T* dy, int n, Ready ready) {
+  using V = Vec<T, kVec>;
+  Reader<V, 2> reader(way_of<T, kVec, 2>(a, l, x, dy, s.kept, n));
+  ready();
+  float2 mean[V::kPairs], scale[V::kPairs], shift[V::kPairs], sum[V::kPairs], sum_x[V::kPairs];
+  take_channels<kVec>(mean, s.coef, l.col);
+  take_channels<kVec>(scale, s.coef + s.step, l.col);
+  take_channels<kVec>(shift, s.coef + 2 * s.step, l.col);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) s[i] = sx[i] = 0.f;
-    for (int at = row; at < n; at += l.rows * kBatch) {
-      Vec<T, kVec> v[kBatch], u[kBatch];
+  for (int i = 0; i < V::kPairs; ++i) sum[i] = sum_x[i] = make_float2(0.f, 0.f);
+  by_act(a.act, [&](auto act) {
+    reader.run([&](V (&v)[2]) {
+      float2 f[V::kPairs], up[V::kPairs];
+      v[0].get(f);
+      v[1].get(up);
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-        if (at + b * l.rows < n) {
-          v[b].load(x + (at + b * l.rows) * a.x_stride[1] + (int64_t)col * kVec);
-          u[b].load(dy + (at + b * l.rows) * a.dy_stride[1] + (int64_t)col * kVec);
-        }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int pixel = at + b * l.rows;
-        if (pixel >= n) continue;
-        if (pixel < a.keep) {
-          v[b].put(kept, pixel * l.columns + col);
-          u[b].put(kept_dy, pixel * l.columns + col);
-        }
-        float f[kVec], up[kVec];
-        v[b].get(f);
-        u[b].get(up);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const float d = f[i] - c.mean[i], g = act_slope(fmaf(d, c.scale[i], c.shift[i]), up[i], a.act);
-          s[i] += g;
-          sx[i] = fmaf(g, d * c.rstd[i], sx[i]);
-        }
+      for (int i = 0; i < V::kPairs; ++i) {
+        const float2 d = sub(f[i], mean[i]), z = fma(d, scale[i], shift[i]);
+        const float2 g = make_float2(act_slope<decltype(act)::value>(z.x, up[i].x), act_slope<decltype(act)::value>(z.y, up[i].y));
+        sum[i] = add(sum[i], g);
+        sum_x[i] = fma(g, d, sum_x[i]);
       }
-    }
-    float* t = table + row * a.channels + col * kVec;
+    });
+  });
+  if (l.row >= l.rows) return;
+  float* t = s.table + l.row * a.channels + l.col * kVec;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) t[i] = s[i], t[size + i] = sx[i];
+  for (int i = 0; i < kVec; ++i) {
+    t[i] = i & 1 ? sum[i / 2].y : sum[i / 2].x;
+    t[kTable<kVec> + i] = i & 1 ? sum_x[i / 2].y : sum_x[i / 2].x;
   }
 }
 
-// The rows of threads added up, into the first row's place.
+// The channels' sums of a run, from the rows of threads', into the first row's place.
 template <int kVec>
-__device__ __forceinline__ void channel_sums(const Params& a, float* table) {
-  const Lay l = Lay::of<kVec>(a.channels);
-  const int size = table_floats<kVec>(a.channels);
-  for (int c = threadIdx.x; c < a.channels; c += kThreads) {
+__device__ __forceinline__ void channel_sums(const Params& a, const Lay& l, Team team, float* table, const uint16_t* group, const float* rstd) {
+  const int lanes = team.lanes(), sub = team.sub();
+  for (int first = 0; first < a.channels; first += team.teams()) {
+    const int c = first + team.first();
+    const float* t = table + min(c, a.channels - 1);
     float s = 0.f, sx = 0.f;
-    for (int r = 0; r < l.rows; ++r) s += table[r * a.channels + c], sx += table[size + r * a.channels + c];
-    table[c] = s;
-    table[size + c] = sx;
+    for (int r = sub; r < l.rows; r += lanes) s += t[r * a.channels], sx += t[kTable<kVec> + r * a.channels];
+    s = team.sum(s);
+    sx = team.sum(sx);
+    __syncwarp();
+    if (c < a.channels && sub == 0) table[c] = s, table[kTable<kVec> + c] = sx * rstd[group[c]];
   }
 }
 
-// The groups' sums of gamma g and gamma g xh of a run: a warp for each group.
+// The groups' sums of gamma g and gamma g xh of a run.
 template <int kVec>
-__device__ __forceinline__ void group_sums(const Params& a, const float* table, float2* groups) {
-  const int size = table_floats<kVec>(a.channels), lane = threadIdx.x & 31;
-  for (int g = threadIdx.x >> 5; g < a.groups; g += kWarps) {
+__device__ __forceinline__ void group_sums(const Params& a, Team team, const float* table, float2* groups) {
+  const int lanes = team.lanes(), sub = team.sub();
+  for (int first = 0; first < a.groups; first += team.teams()) {
+    const int g = first + team.first(), at = min(g, a.groups - 1) * a.per;
     float s = 0.f, sx = 0.f;
-    for (int e = lane; e < a.per; e += 32) {
-      const int c = g * a.per + e;
-      const float w = a.gamma ? a.gamma[c] : 1.f;
-      s = fmaf(w, table[c], s);
-      sx = fmaf(w, table[size + c], sx);
+    for (int e = sub; e < a.per; e += lanes) {
+      const float w = a.gamma ? a.gamma[at + e] : 1.f;
+      s = fmaf(w, table[at + e], s);
+      sx = fmaf(w, table[kTable<kVec> + at + e], sx);
     }
-    s = warp_reduce<Sum>(s);
-    sx = warp_reduce<Sum>(sx);
-    if (lane == 0) groups[g] = make_float2(s, sx);
+    s = team.sum(s);
+    sx = team.sum(sx);
+    if (g < a.groups && sub == 0) groups[g] = make_float2(s, sx);
   }
 }
 
-// A run's dx, from the means of gamma g and gamma g xh over its image's groups.
-template <typename T, int kVec>
-__device__ __forceinline__ void gradient(const Params& a, int64_t image, const T* x, const T* dy, T* dx, int n, const float* mean_g,
-                                         const float* mean_gx, const uint8_t* kept) {
-  const Lay l = Lay::of<kVec>(a.channels);
-  const int row = threadIdx.x / l.across;
-  if (row >= l.rows) return;
-  const uint8_t* kept_dy = kept + (size_t)a.keep * a.channels * sizeof(T);
-  for (int col = threadIdx.x % l.across; col < l.columns; col += l.across) {
-    Channel<kVec> c;
-    c.of(a, col * kVec, a.mean + image * a.groups, a.rstd + image * a.groups);
-    float m[kVec], mx[kVec];
+// A run's dx, from the means of gamma g and gamma g xh over its image's groups; kHeld and ready() as above.
+template <typename T, int kVec, bool kHeld, typename Ready>
+__device__ __forceinline__ void gradient(const Params& a, const Lay& l, const Shared<T, kVec>& s, const T* x, const T* dy, T* dx, int n,
+                                         Ready ready) {
+  using V = Vec<T, kVec>;
+  std::conditional_t<kHeld, Way<2>, Reader<V, 2>> source(way_of<T, kVec, 2>(a, l, x, dy, s.kept, n));
+  ready();
+  float2 mean[V::kPairs], scale[V::kPairs], shift[V::kPairs], m[V::kPairs], mx[V::kPairs];
+  take_channels<kVec>(mean, s.coef, l.col);
+  take_channels<kVec>(scale, s.coef + s.step, l.col);
+  take_channels<kVec>(shift, s.coef + 2 * s.step, l.col);
+  take_channels<kVec>(m, s.coef + 3 * s.step, l.col);
+  take_channels<kVec>(mx, s.coef + 4 * s.step, l.col);
+  uint8_t* out = reinterpret_cast<uint8_t*>(dx + l.row * a.y_stride[1] + l.col * kVec);
+  const int64_t out_step = l.rows * a.y_stride[1] * (int64_t)sizeof(T);
+  by_act(a.act, [&](auto act) {
+    auto make = [&](V (&v)[2]) {
+      float2 f[V::kPairs], up[V::kPairs];
+      v[0].get(f);
+      v[1].get(up);
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-      const int g = (col * kVec + i) / a.per;
-      m[i] = c.rstd[i] * mean_g[g];
-      mx[i] = c.rstd[i] * mean_gx[g];
-    }
-    for (int at = row; at < n; at += l.rows * kBatch) {
-      Vec<T, kVec> v[kBatch], u[kBatch];
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int pixel = at + b * l.rows;
-        if (pixel < a.keep && pixel < n) {
-          v[b].take(kept, pixel * l.columns + col);
-          u[b].take(kept_dy, pixel * l.columns + col);
-        } else if (pixel < n) {
-          v[b].load(x + pixel * a.x_stride[1] + (int64_t)col * kVec);
-          u[b].load(dy + pixel * a.dy_stride[1] + (int64_t)col * kVec);
-        }
+      for (int i = 0; i < V::kPairs; ++i) {
+        const float2 d = sub(f[i], mean[i]), z = fma(d, scale[i], shift[i]);
+        const float2 g = make_float2(act_slope<decltype(act)::value>(z.x, up[i].x), act_slope<decltype(act)::value>(z.y, up[i].y));
+        f[i] = fma(g, scale[i], fma(d, mx[i], m[i]));
       }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int pixel = at + b * l.rows;
-        if (pixel >= n) continue;
-        float f[kVec], up[kVec];
-        v[b].get(f);
-        u[b].get(up);
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          const float d = f[i] - c.mean[i], g = act_slope(fmaf(d, c.scale[i], c.shift[i]), up[i], a.act);
-          f[i] = fmaf(g, c.scale[i], -fmaf(d * c.rstd[i], mx[i], m[i]));
-        }
-        v[b].set(f);
-        v[b].store(dx + pixel * a.y_stride[1] + (int64_t)col * kVec);
-      }
-    }
-  }
+      v[0].set(f);
+      v[0].store(out);
+      out += out_step;
+    };
+    if constexpr (kHeld) reread<V, 2>(source, make);
+    else source.run(make);
+  });
 }
 
 template <typename T, int kVec>
-__global__ void __launch_bounds__(kThreads, 2) cluster_backward_kernel(const __grid_constant__ Params a) {
+__global__ void __launch_bounds__(kThreads, 2) cluster_backward_kernel(const __grid_constant__ Params whole) {
+  const Params a = slice_of<T>(whole);
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint8_t smem[];
   const Shared<T, kVec> s(a, smem);
   const cg::cluster_group cluster = cg::this_cluster();
-  const int run = (int)cluster.block_rank(), size = table_floats<kVec>(a.channels);
+  const int run = (int)cluster.block_rank();
   const int64_t image = blockIdx.x / a.runs, begin = run_begin(a, run);
   const int n = run_length(a, run);
   const T* x = static_cast<const T*>(a.x) + image * a.x_stride[0] + begin * a.x_stride[1];
   const T* dy = static_cast<const T*>(a.dy) + image * a.dy_stride[0] + begin * a.dy_stride[1];
-  sums<T, kVec>(a, image, x, dy, n, s.table, s.kept);
+  const Lay l = Lay::of<kVec>(a.channels);
+  const Teams teams = Teams::of(a, l);
+  const float *mean = a.mean + image * a.all_groups, *rstd = a.rstd + image * a.all_groups;
+  s.set_groups(a);
+  sums<T, kVec>(a, l, s, x, dy, n, [&] {
+    __syncthreads();
+    s.set_channels(a, mean, rstd);
+    __syncthreads();
+  });
   __syncthreads();
-  channel_sums<kVec>(a, s.table);
+  channel_sums<kVec>(a, l, teams.channels, s.table, s.group, rstd);
   __syncthreads();
-  group_sums<kVec>(a, s.table, s.groups);
+  group_sums<kVec>(a, teams.groups, s.table, s.groups);
   cluster.sync();
   const float inv = 1.f / ((float)a.pixels * (float)a.per);
   for (int g = threadIdx.x; g < a.groups; g += kThreads) {
@@ -552,117 +759,383 @@ __global__ void __launch_bounds__(kThreads, 2) cluster_backward_kernel(const __g
       for (int r = 0; r < a.runs; ++r) {
         const float* t = cluster.map_shared_rank(s.table, r);
         v += t[c];
-        vx += t[size + c];
+        vx += t[kTable<kVec> + c];
       }
-      a.part[2 * image * a.channels + c] = vx;
-      a.part[(2 * image + 1) * a.channels + c] = v;
+      a.part[2 * image * a.all_channels + c] = vx;
+      a.part[(2 * image + 1) * a.all_channels + c] = v;
     }
   }
   __syncthreads();
   cluster.barrier_arrive();   // the other blocks' sums are not read any more
-  gradient<T, kVec>(a, image, x, dy, static_cast<T*>(a.y) + image * a.y_stride[0] + begin * a.y_stride[1], n, s.stat, s.stat + a.groups, s.kept);
+  s.set_gradient(a, rstd);
+  __syncthreads();
+  gradient<T, kVec, true>(a, l, s, x, dy, static_cast<T*>(a.y) + image * a.y_stride[0] + begin * a.y_stride[1], n, [] {});
   cluster.barrier_wait();
 }
 
-template <typename T, int kVec>
-__global__ void __launch_bounds__(kThreads, 2) sums_kernel(const __grid_constant__ Params a) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  const Shared<T, kVec> s(a, smem);
-  const int run = blockIdx.x % a.runs, size = table_floats<kVec>(a.channels);
-  const int64_t image = blockIdx.x / a.runs, begin = run_begin(a, run);
-  sums<T, kVec>(a, image, static_cast<const T*>(a.x) + image * a.x_stride[0] + begin * a.x_stride[1],
-                static_cast<const T*>(a.dy) + image * a.dy_stride[0] + begin * a.dy_stride[1], run_length(a, run), s.table, s.kept);
-  __syncthreads();
-  channel_sums<kVec>(a, s.table);
-  __syncthreads();
-  group_sums<kVec>(a, s.table, reinterpret_cast<float2*>(a.group_part) + (int64_t)blockIdx.x * a.groups);
-  if (a.gamma)
-    for (int c = threadIdx.x; c < a.channels; c += kThreads) {
-      a.part[2 * (int64_t)blockIdx.x * a.channels + c] = s.table[size + c];
-      a.part[(2 * (int64_t)blockIdx.x + 1) * a.channels + c] = s.table[c];
+// ---------------------------------------------------------------- maps larger than the clusters' shared memory
+
+template <typename T, int kVec, int kOps>
+__host__ __device__ constexpr int ring_bytes() {
+  return kOps * kAhead<kOps, Vec<T, kVec>::kBytes> * kBatch<kOps> * kThreads * Vec<T, kVec>::kBytes;
+}
+
+// Tasks in one order, dealt out to the blocks in turn.  Step s of them has the moments (sums) of image s, run by run; the
+// merge of image s - half's moments; and the results of image s - lag, run by run.  A block takes its tasks in that
+// order, so whatever one waits for is done or being done by a block that waits for less; `lag` is such that it is
+// nearly always done, and that what is read again is in L2.
+struct Stream {
+  Params a;
+  uint32_t* counts;   // of each image's runs whose moments are there, then one for each image: 1 when they are merged
+  float* means;       // backward: the images' two means of each group
+  uint32_t images, half, lag;
+  uint32_t* err;
+};
+enum Kind { kMoments, kMerge, kResult };
+struct Task {
+  Kind kind;
+  uint32_t image, run;
+  static __device__ __forceinline__ Task of(const Stream& f, uint32_t i) {
+    const uint32_t runs = f.a.runs;
+    // steps of the same size: before the first merge, before the first result, with all three, without moments, with
+    // results alone
+    uint32_t step = 0, size = runs, n = f.half * runs;
+    bool first = true, merge = false;
+    if (i >= n) {
+      i -= n, step = f.half, size = runs + 1, n = (f.lag - f.half) * size, merge = true;
+      if (i >= n) {
+        i -= n, step = f.lag, size = 2 * runs + 1, n = (f.images - f.lag) * size;
+        if (i >= n) {
+          i -= n, step = f.images, size = runs + 1, n = f.half * size, first = false;
+          if (i >= n) i -= n, step = f.images + f.half, size = runs, merge = false;
+        }
+      }
     }
-}
-
-// The images' means of gamma g and gamma g xh, behind the runs' sums: a warp for each group of an image.
-__global__ void __launch_bounds__(128) merge_sums_kernel(const __grid_constant__ Params a, int64_t images) {
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (at >= images * a.groups) return;
-  const float2* m = reinterpret_cast<const float2*>(a.group_part) + at / a.groups * a.runs * a.groups + at % a.groups;
-  float s = 0.f, sx = 0.f;
-  for (int r = lane; r < a.runs; r += 32) {
-    const float2 v = m[(int64_t)r * a.groups];
-    s += v.x;
-    sx += v.y;
+    const uint32_t past = i / size;
+    i -= past * size;
+    step += past;
+    if (first) {
+      if (i < runs) return Task{kMoments, step, i};
+      i -= runs;
+    }
+    if (merge) {
+      if (i == 0) return Task{kMerge, step - f.half, 0};
+      --i;
+    }
+    return Task{kResult, step - f.lag, i};
   }
-  s = warp_reduce<Sum>(s);
-  sx = warp_reduce<Sum>(sx);
-  const float inv = 1.f / ((float)a.pixels * (float)a.per);
-  float* means = a.group_part + 2 * images * a.runs * a.groups + 2 * (at / a.groups) * a.groups + at % a.groups;
-  if (lane == 0) means[0] = s * inv, means[a.groups] = sx * inv;
+  static __host__ __device__ uint32_t total(uint32_t images, uint32_t runs) { return images * (2 * runs + 1); }
+};
+
+// Waits until a count has been reached; a wait that runs out is reported.
+__device__ __forceinline__ void wait_for(const Stream& f, const uint32_t* count, uint32_t n) {
+  if (ld_acquire_gpu(count) >= n) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (ld_acquire_gpu(count) < n) {
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      report_error(f.err, kErrWaitOperand);
+      return;
+    }
+    __nanosleep(100);
+  }
+}
+// After a barrier of the block: what it has written is there for those who see the count.
+__device__ __forceinline__ void tell(uint32_t* count) {
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(count, 1u);
+  }
 }
 
-template <typename T, int kVec>
-__global__ void __launch_bounds__(kThreads, 2) gradient_kernel(const __grid_constant__ Params a) {
-  const int block = gridDim.x - 1 - blockIdx.x, run = block % a.runs;
-  const int64_t image = block / a.runs, begin = run_begin(a, run);
-  const float* means = a.group_part + 2 * (int64_t)gridDim.x * a.groups + 2 * image * a.groups;
-  gradient<T, kVec>(a, image, static_cast<const T*>(a.x) + image * a.x_stride[0] + begin * a.x_stride[1],
-                    static_cast<const T*>(a.dy) + image * a.dy_stride[0] + begin * a.dy_stride[1],
-                    static_cast<T*>(a.y) + image * a.y_stride[0] + begin * a.y_stride[1], run_length(a, run), means, means + a.groups, nullptr);
+// The image's moments (backward: means) from its runs'.  What other blocks have written comes through L2, kFew of a lane's
+// values at a time.
+template <bool kBack>
+__device__ __forceinline__ void merge_runs(const Params& a, Team team, const float2* part, float* mean, float* second) {
+  constexpr int kFew = kBack ? 8 : 16;
+  const int lanes = team.lanes(), sub = team.sub();
+  const float total = (float)a.pixels * (float)a.per;
+  for (int first = 0; first < a.groups; first += team.teams()) {
+    const int g = first + team.first();
+    const float2* m = part + min(g, a.groups - 1);
+    float n = 0.f, s = 0.f, q = 0.f;   // forward: count, mean, squared deviations
+    for (int r = sub; r < a.runs; r += kFew * lanes) {
+      float2 v[kFew];
+#pragma unroll
+      for (int i = 0; i < kFew; ++i)
+        if (r + i * lanes < a.runs) v[i] = __ldcg(m + (int64_t)(r + i * lanes) * a.groups);
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        if (r + i * lanes >= a.runs) continue;
+        if constexpr (kBack) s += v[i].x, q += v[i].y;
+        else merge_moments(n, s, q, (float)run_length(a, r + i * lanes) * (float)a.per, v[i].x, v[i].y);
+      }
+    }
+    if constexpr (kBack) {
+      s = team.sum(s) / total;
+      q = team.sum(q) / total;
+    } else {
+      for (int o = 1; o < lanes; o *= 2) {
+        const float n2 = __shfl_xor_sync(0xffffffffu, n, o), s2 = __shfl_xor_sync(0xffffffffu, s, o), q2 = __shfl_xor_sync(0xffffffffu, q, o);
+        // the lower lane's first, so that both get the same
+        if (sub & o) {
+          float n1 = n2, s1 = s2, q1 = q2;
+          merge_moments(n1, s1, q1, n, s, q);
+          n = n1, s = s1, q = q1;
+        } else {
+          merge_moments(n, s, q, n2, s2, q2);
+        }
+      }
+      q = rstd_of(q, total, a.eps);
+    }
+    if (g < a.groups && sub == 0) mean[g] = s, second[g] = q;
+  }
 }
 
-// dgamma and dbeta: `rows` rows of [dgamma's channels][dbeta's], added up by eight rows of threads that take turns, then
+template <typename T, int kVec, bool kBack>
+__global__ void __launch_bounds__(kThreads, kResident<1 + kBack>) stream_kernel(const __grid_constant__ Stream f) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const Params& a = f.a;
+  const Shared<T, kVec> s(a, smem);
+  const Lay l = Lay::of<kVec>(a.channels);
+  const Teams teams = Teams::of(a, l);
+  s.set_groups(a);
+  // the block's own sums of the parameters' gradients, behind the rings
+  float* own = reinterpret_cast<float*>(s.kept + ring_bytes<T, kVec, 1 + kBack>());
+  if constexpr (kBack)
+    for (int c = threadIdx.x; c < 2 * a.channels; c += kThreads) own[c] = 0.f;
+  __syncthreads();
+  const uint32_t runs = a.runs, all = Task::total(f.images, runs);
+  for (uint32_t i = blockIdx.x; i < all; i += gridDim.x) {
+    const Task task = Task::of(f, i);
+    const uint32_t image = task.image;
+    const int run = (int)task.run, n = run_length(a, run);
+    const int64_t begin = run_begin(a, run), at = (int64_t)image * a.groups;
+    const T* x = static_cast<const T*>(a.x) + image * a.x_stride[0] + begin * a.x_stride[1];
+    const T* dy = kBack ? static_cast<const T*>(a.dy) + image * a.dy_stride[0] + begin * a.dy_stride[1] : nullptr;
+    float2* part = reinterpret_cast<float2*>(a.group_part) + at * runs;
+    const float *mean = a.mean + at, *rstd = a.rstd + at;
+    if (task.kind == kMoments) {
+      if constexpr (kBack) {
+        sums<T, kVec>(a, l, s, x, dy, n, [&] {
+          __syncthreads();   // the task before may have its coefficients yet to read
+          s.set_channels(a, mean, rstd);
+          __syncthreads();
+        });
+      } else {
+        moments<T, kVec>(a, l, x, n, s.table, s.kept);
+      }
+      __syncthreads();
+      if constexpr (kBack) channel_sums<kVec>(a, l, teams.channels, s.table, s.group, rstd);
+      else channel_moments<kVec>(a, l, teams.channels, n, s.table);
+      __syncthreads();
+      if constexpr (kBack) {
+        for (int c = threadIdx.x; c < a.channels; c += kThreads) {
+          own[c] += s.table[kTable<kVec> + c];
+          own[a.channels + c] += s.table[c];
+        }
+        group_sums<kVec>(a, teams.groups, s.table, part + run * a.groups);
+      } else {
+        group_moments<kVec>(a, teams.groups, n, s.table, part + run * a.groups);
+      }
+      __syncthreads();
+      tell(f.counts + image);
+    } else if (task.kind == kMerge) {
+      wait_for(f, f.counts + image, runs);
+      merge_runs<kBack>(a, teams.runs, part, kBack ? f.means + 2 * at : a.mean + at, kBack ? f.means + 2 * at + a.groups : a.rstd + at);
+      __syncthreads();
+      tell(f.counts + f.images + image);
+    } else {
+      auto ready = [&] {
+        wait_for(f, f.counts + f.images + image, 1);
+        __syncthreads();   // the task before may have its coefficients yet to read
+        // what another block has written comes through L2
+        const float *first = kBack ? f.means + 2 * at : mean, *second = kBack ? f.means + 2 * at + a.groups : rstd;
+        for (int g = threadIdx.x; g < a.groups; g += kThreads) s.stat[g] = __ldcg(first + g), s.stat[a.groups + g] = __ldcg(second + g);
+        __syncthreads();
+        if constexpr (kBack) {
+          s.set_channels(a, mean, rstd);
+          s.set_gradient(a, rstd);
+        } else {
+          s.set_channels(a, s.stat, s.stat + a.groups);
+        }
+        __syncthreads();
+      };
+      T* y = static_cast<T*>(a.y) + image * a.y_stride[0] + begin * a.y_stride[1];
+      if constexpr (kBack) gradient<T, kVec, false>(a, l, s, x, dy, y, n, ready);
+      else normalise<T, kVec, false>(a, l, s, x, y, n, ready);
+    }
+  }
+  __syncthreads();
+  if constexpr (kBack) {
+    if (a.gamma)
+      for (int c = threadIdx.x; c < 2 * a.channels; c += kThreads) a.part[2 * (int64_t)blockIdx.x * a.channels + c] = own[c];
+  }
+}
+
+// ---------------------------------------------------------------- more channels than a block has columns for
+
+// Pixels of more than 256 vectors (2048 channels; less where they do not divide into vectors): a block for each group of
+// an image, which reads it three times (backward: twice).
+__device__ float block_sum(float v) {
+  __shared__ float part[kThreads / 32];
+  v = warp_reduce<Sum>(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int i = 0; i < kThreads / 32; ++i) s += part[i];
+  return s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) wide_forward_kernel(const __grid_constant__ Params a) {
+  const int64_t image = blockIdx.x / a.groups, count = a.pixels * a.per;
+  const int c0 = blockIdx.x % a.groups * a.per;
+  const T* x = static_cast<const T*>(a.x) + image * a.x_stride[0] + c0;
+  T* y = static_cast<T*>(a.y) + image * a.y_stride[0] + c0;
+  const float ref = to_f(x[0]);
+  float s = 0.f, q = 0.f;
+  for (int64_t i = threadIdx.x; i < count; i += kThreads) s += to_f(x[i / a.per * a.x_stride[1] + i % a.per]) - ref;
+  const float mean = ref + block_sum(s) / (float)count;
+  for (int64_t i = threadIdx.x; i < count; i += kThreads) {
+    const float d = to_f(x[i / a.per * a.x_stride[1] + i % a.per]) - mean;
+    q = fmaf(d, d, q);
+  }
+  const float rstd = rstd_of(block_sum(q), (float)count, a.eps);
+  if (threadIdx.x == 0) a.mean[blockIdx.x] = mean, a.rstd[blockIdx.x] = rstd;
+  by_act(a.act, [&](auto act) {
+    for (int64_t i = threadIdx.x; i < count; i += kThreads) {
+      const int c = (int)(i % a.per);
+      const float scale = a.gamma ? rstd * a.gamma[c0 + c] : rstd, shift = a.gamma ? a.beta[c0 + c] : 0.f;
+      const float z = fmaf(to_f(x[i / a.per * a.x_stride[1] + c]) - mean, scale, shift);
+      y[i / a.per * a.y_stride[1] + c] = from_f<T>(act_of<decltype(act)::value>(z));
+    }
+  });
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) wide_backward_kernel(const __grid_constant__ Params a) {
+  const int64_t image = blockIdx.x / a.groups;
+  const int c0 = blockIdx.x % a.groups * a.per;
+  const T* x = static_cast<const T*>(a.x) + image * a.x_stride[0] + c0;
+  const T* dy = static_cast<const T*>(a.dy) + image * a.dy_stride[0] + c0;
+  T* dx = static_cast<T*>(a.y) + image * a.y_stride[0] + c0;
+  const float mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
+  by_act(a.act, [&](auto act) {
+    float scale = 0.f, d = 0.f;
+    auto slope = [&](int64_t p, int c) {
+      scale = a.gamma ? rstd * a.gamma[c0 + c] : rstd;
+      d = to_f(x[p * a.x_stride[1] + c]) - mean;
+      return act_slope<decltype(act)::value>(fmaf(d, scale, a.gamma ? a.beta[c0 + c] : 0.f), to_f(dy[p * a.dy_stride[1] + c]));
+    };
+    float u = 0.f, ux = 0.f;
+    for (int c = 0; c < a.per; ++c) {
+      float s = 0.f, sx = 0.f;
+      for (int64_t p = threadIdx.x; p < a.pixels; p += kThreads) {
+        const float g = slope(p, c);
+        s += g;
+        sx = fmaf(g, d, sx);
+      }
+      s = block_sum(s);
+      sx = block_sum(sx) * rstd;
+      const float w = a.gamma ? a.gamma[c0 + c] : 1.f;
+      u = fmaf(w, s, u);
+      ux = fmaf(w, sx, ux);
+      if (a.gamma && threadIdx.x == 0) {
+        a.part[2 * image * a.channels + c0 + c] = sx;
+        a.part[(2 * image + 1) * a.channels + c0 + c] = s;
+      }
+    }
+    const float inv = 1.f / ((float)a.pixels * (float)a.per), m = -rstd * (u * inv), mx = -rstd * rstd * (ux * inv);
+    for (int64_t i = threadIdx.x; i < a.pixels * a.per; i += kThreads) {
+      const int c = (int)(i % a.per);
+      const float g = slope(i / a.per, c);
+      dx[i / a.per * a.y_stride[1] + c] = from_f<T>(fmaf(g, scale, fmaf(d, mx, m)));
+    }
+  });
+}
+
+// dgamma and dbeta: `rows` rows of [dgamma's channels][dbeta's], added up by 32 rows of threads that take turns, then
 // in their order.
-__global__ void __launch_bounds__(256) parameters_kernel(const float* part, int64_t rows, int channels, float* dgamma, float* dbeta) {
-  __shared__ float sum[8][33];
+__global__ void __launch_bounds__(1024) parameters_kernel(const float* part, int64_t rows, int channels, float* dgamma, float* dbeta) {
+  __shared__ float sum[32][33];
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < 2 * channels) {
 #pragma unroll 8
-    for (int64_t r = row; r < rows; r += 8) s += part[r * 2 * channels + c];
+    for (int64_t r = row; r < rows; r += 32) s += part[r * 2 * channels + c];
   }
   sum[row][lane] = s;
   __syncthreads();
-  if (row || c >= 2 * channels) return;
-#pragma unroll
-  for (int r = 1; r < 8; ++r) s += sum[r][lane];
-  if (c < channels) dgamma[c] = s;
-  else dbeta[c - channels] = s;
+  // a warp for each channel now
+  s = warp_reduce<Sum>(sum[lane][row]);
+  const int mine = blockIdx.x * 32 + row;
+  if (lane || mine >= 2 * channels) return;
+  if (mine < channels) dgamma[mine] = s;
+  else dbeta[mine - channels] = s;
 }
 
 // ---------------------------------------------------------------- host side
 
-// How a call is laid out.  cluster: runs is a cluster's blocks, one to a run; else the runs of an image, all on their
-// own.
+// How a call is laid out.  cluster: runs is a cluster's blocks, one to a run; else the runs of an image, tasks of
+// a grid of at most kStreamBlocks.
 struct Plan {
   bool cluster;
   int runs;
+  int slices;       // of the channels, blocks of their own (with one run)
+  int64_t lag;
   int64_t budget;   // bytes of shared memory for a block
 };
+constexpr int64_t kStreamBlocks = 3 * 192;   // of a stream's grid, at the most
+constexpr int64_t kRunBytes = 192 * 1024, kShortRun = 32 * 1024, kMostRuns = 1024;
 
 // Shared memory beside the kept pixels, with the widest vectors that a type has.
 int64_t table_bytes(const cbr_group_norm_desc_t& d) {
-  return 8 * (int64_t)std::max(d.channels, kThreads * (d.dtype == CBR_F32 ? 4 : 8)) + 16 * (int64_t)d.groups + 16;
+  return shared_bytes(kThreads * (d.dtype == CBR_F32 ? 4 : 8), d.channels, d.groups);
 }
 
 Plan plan_of(const cbr_group_norm_desc_t& d, bool backward) {
   Plan p{};
+  if (d.channels > kThreads * (d.dtype == CBR_F32 ? 4 : 8)) {
+    p.cluster = true;   // by groups
+    p.runs = p.slices = 1;
+    return p;
+  }
   const int64_t table = table_bytes(d), images = std::max<int64_t>(d.images, 1);
   // two blocks to an SM, so that one loads while the other stores; wide tables leave room for one
-  p.budget = table <= 48 * 1024 ? 112 * 1024 : 226 * 1024;
-  const int64_t image = d.pixels * d.channels * (d.dtype == CBR_F32 ? 4 : 2) * (backward ? 2 : 1), room = p.budget - table;
-  int64_t need = 1;
-  while (need < kMaxCluster && need * room < image) need *= 2;
-  // an image in 16 blocks that hold a part of it, where images alone keep the SMs busy
-  p.cluster = need * room >= image || images * kMaxCluster >= 2 * kSms;
+  p.budget = table + 8 * d.channels <= 64 * 1024 ? 112 * 1024 : 226 * 1024;
+  const int64_t elt = d.dtype == CBR_F32 ? 4 : 2, pixel = d.channels * elt * (backward ? 2 : 1), image = d.pixels * pixel;
+  const int64_t room = p.budget - table;
+  p.slices = 1;
+  // A small map of few images: slices of whole groups need no exchange.  Their pixels are at least 64 bytes wide and
+  // whole vectors, and a block has at most 32 KB, which it reads in one go.
+  for (int s = d.groups; s > 1 && images < kSms; --s) {
+    const int64_t width = d.channels / s * elt;
+    if (d.groups % s || width < 64 || width % 16 || images * s > 2 * kSms) continue;
+    if (image / s <= 32 * 1024) {
+      p.cluster = true;
+      p.runs = 1;
+      p.slices = s;
+      return p;
+    }
+    break;   // fewer slices are larger yet
+  }
+  // What fits the shared memory of all SMs at once goes to clusters.
+  int64_t need = std::max<int64_t>(1, (image + room - 1) / room);
+  p.cluster = need <= kMaxCluster && images * need <= 2 * kSms && (d.pixels + need - 1) / need * pixel <= room;
   if (p.cluster) {
     // more blocks while SMs are without one, and a run keeps a few KB
-    while (need < kMaxCluster && images * need <= kSms && image / (2 * need) >= 4096) need *= 2;
+    while (2 * need <= kMaxCluster && images * need <= kSms && image / (2 * need) >= 4096) need *= 2;
     p.runs = (int)need;
-  } else {
-    p.runs = (int)std::max<int64_t>(1, std::min<int64_t>(d.pixels, (4 * kSms + images - 1) / images));
+    return p;
   }
+  // Runs of 192 KB, whose reading a run's fixed cost (the merges, a few us) is small beside; shorter ones where that
+  // leaves blocks without a few tasks each.
+  const int64_t blocks = kSms * (backward ? kResident<2> : kResident<1>);
+  const int64_t run = std::min(kRunBytes, std::max(kShortRun, image * images / (2 * kSms * 4)));
+  p.runs = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(d.pixels, kMostRuns), (image + run - 1) / run));
+  // a result is this many images behind: the tasks between are at least those in flight
+  p.lag = std::min<int64_t>(images, (blocks + 2 * p.runs - 1) / (2 * p.runs) + 1);
   return p;
 }
 
@@ -700,29 +1173,34 @@ int launch(const GroupNormArgs& g, bool backward, cudaStream_t st) {
     a.y_stride[i] = backward ? d.dx_stride[i] : d.y_stride[i];
   }
   a.pixels = d.pixels;
-  a.channels = d.channels;
-  a.groups = d.groups;
+  a.all_channels = d.channels;
+  a.all_groups = d.groups;
+  a.channels = d.channels / plan.slices;
+  a.groups = d.groups / plan.slices;
   a.per = d.channels / d.groups;
   a.act = d.act;
   a.runs = plan.runs;
   a.base = d.pixels / plan.runs;
   a.extra = (int)(d.pixels % plan.runs);
   a.eps = d.eps;
-  if (d.images > 0x7fffffff / plan.runs || d.images > 0x7fffffff / d.groups) return CBR_ERR_UNSUPPORTED;
-  const int64_t rows = plan.cluster ? d.images : d.images * plan.runs;
+  if (d.images > 0x7fffffff / (2 * plan.runs + 1) || d.images > 0x7fffffff / d.groups) return CBR_ERR_UNSUPPORTED;
   a.part = g.part;
-  a.group_part = g.part + (backward ? 2 * rows * d.channels : 0);
-  const int64_t fixed = ((8 * (int64_t)table_floats<kVec>(d.channels) + 16 * (int64_t)d.groups + 15) & ~int64_t(15));
-  const int64_t pixel = (int64_t)d.channels * sizeof(T) * (backward ? 2 : 1);
-  const unsigned blocks = (unsigned)(d.images * plan.runs);
-  if (plan.cluster) {
-    const int64_t longest = (d.pixels + plan.runs - 1) / plan.runs;
-    a.keep = (int)std::min<int64_t>(longest, std::max<int64_t>(0, (plan.budget - fixed) / pixel));
+  const int64_t fixed = shared_bytes(kTable<kVec>, a.channels, a.groups);
+  const int64_t pixel = (int64_t)a.channels * sizeof(T) * (backward ? 2 : 1);
+  const int64_t longest = (d.pixels + plan.runs - 1) / plan.runs;
+  int64_t rows = d.images;
+  if (d.channels / kVec > kThreads) {
+    const auto kern = backward ? &wide_backward_kernel<T> : &wide_forward_kernel<T>;
+    a.channels = d.channels;
+    a.groups = d.groups;
+    kern<<<(unsigned)(d.images * d.groups), kThreads, 0, st>>>(a);
+  } else if (plan.cluster) {
+    a.keep = (int)longest;
     const auto kern = backward ? &cluster_backward_kernel<T, kVec> : &cluster_forward_kernel<T, kVec>;
     if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), 227 * 1024)) return CBR_ERR_CUDA;
     if (plan.runs > 8 && !allow_wide_cluster(reinterpret_cast<const void*>(kern))) return CBR_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(blocks);
+    cfg.gridDim = dim3((unsigned)(d.images * plan.runs), (unsigned)plan.slices);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = (size_t)(fixed + a.keep * pixel);
     cfg.stream = st;
@@ -737,20 +1215,35 @@ int launch(const GroupNormArgs& g, bool backward, cudaStream_t st) {
       return CBR_ERR_CUDA;
     }
   } else {
-    const unsigned warps = (unsigned)((d.images * d.groups + 3) / 4);
-    const auto first = backward ? &sums_kernel<T, kVec> : &moments_kernel<T, kVec>;
-    if (!ensure_smem_attr(reinterpret_cast<const void*>(first), 227 * 1024)) return CBR_ERR_CUDA;
-    first<<<blocks, kThreads, (size_t)fixed, st>>>(a);
-    if (backward) {
-      merge_sums_kernel<<<warps, 128, 0, st>>>(a, d.images);
-      gradient_kernel<T, kVec><<<blocks, kThreads, 0, st>>>(a);
-    } else {
-      merge_moments_kernel<<<warps, 128, 0, st>>>(a, d.images);
-      normalise_kernel<T, kVec><<<blocks, kThreads, 0, st>>>(a);
+    Stream f{};
+    const int64_t own = backward ? 8 * (int64_t)a.channels : 0;
+    // [groups' moments of every run][the images' means][parameters' sums of every block][counts]
+    a.group_part = g.part;
+    f.means = a.group_part + 2 * d.images * plan.runs * a.groups;
+    a.part = f.means + (backward ? 2 * d.images * a.groups : 0);
+    f.counts = reinterpret_cast<uint32_t*>(a.part + (backward ? 2 * kStreamBlocks * a.channels : 0));
+    f.a = a;
+    f.images = (uint32_t)d.images;
+    f.lag = (uint32_t)plan.lag;
+    f.half = (uint32_t)(plan.lag + 1) / 2;
+    f.err = g.err;
+    if (cudaMemsetAsync(f.counts, 0, (size_t)d.images * 8, st) != cudaSuccess) return CBR_ERR_CUDA;
+    const auto kern = backward ? &stream_kernel<T, kVec, true> : &stream_kernel<T, kVec, false>;
+    const int smem = (int)(fixed + (backward ? ring_bytes<T, kVec, 2>() : ring_bytes<T, kVec, 1>()) + own);
+    if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), 227 * 1024)) return CBR_ERR_CUDA;
+    const int fit = blocks_that_fit(reinterpret_cast<const void*>(kern), kThreads, smem);
+    if (fit < 1) return CBR_ERR_CUDA;
+    rows = std::min<int64_t>(std::min<int64_t>(kStreamBlocks, (int64_t)fit * g.num_sms), (int64_t)Task::total((uint32_t)d.images, (uint32_t)plan.runs));
+    // blocks wait for one another's runs: all of them have to be there at once
+    void* args[] = {&f};
+    if (cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3((unsigned)rows), dim3(kThreads), args, (size_t)smem, st) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return CBR_ERR_CUDA;
     }
   }
   if (backward && g.gamma)
-    parameters_kernel<<<(2 * d.channels + 31) / 32, 256, 0, st>>>(g.part, rows, d.channels, g.dgamma, g.dbeta);
+    parameters_kernel<<<(2 * d.channels + 31) / 32, 1024, 0, st>>>(a.part, rows, d.channels, g.dgamma, g.dbeta);
   return cudaGetLastError() == cudaSuccess ? CBR_OK : CBR_ERR_CUDA;
 }
 
@@ -768,8 +1261,10 @@ int dispatch(const GroupNormArgs& g, bool backward, cudaStream_t st) {
     }
     return true;
   };
+  // The backward of 8 channels a thread does not fit the registers of three blocks to an SM (100 us and more, 8-byte vectors
+  // 94 at 256x56x56x64 f16); it is left to pixels with more vectors than a block has threads.
   if constexpr (sizeof(T) == 2)
-    if (fits(8)) return launch<T, 8>(g, backward, st);
+    if ((!backward || d.channels > 4 * kThreads) && fits(8)) return launch<T, 8>(g, backward, st);
   if (fits(4)) return launch<T, 4>(g, backward, st);
   return launch<T, 1>(g, backward, st);
 }
@@ -784,12 +1279,15 @@ int dispatch(const GroupNormArgs& g, bool backward, cudaStream_t st) {
 
 size_t group_norm_forward_floats(const cbr_group_norm_desc_t& d) {
   const gn::Plan p = gn::plan_of(d, false);
-  return p.cluster ? 0 : (size_t)d.images * p.runs * 2 * d.groups;
+  return p.cluster ? 0 : (size_t)d.images * (2 * (size_t)p.runs * d.groups + 2);
 }
 size_t group_norm_backward_floats(const cbr_group_norm_desc_t& d, bool parameters) {
   const gn::Plan p = gn::plan_of(d, true);
-  if (p.cluster) return parameters ? (size_t)d.images * 2 * d.channels : 0;
-  return (size_t)d.images * p.runs * 2 * (d.channels + d.groups) + (size_t)d.images * 2 * d.groups;
+  // by images: clusters, and what goes by groups for its many channels
+  const size_t by_image = parameters ? (size_t)d.images * 2 * d.channels : 0;
+  if (p.cluster) return by_image;
+  const size_t stream = (size_t)d.images * (2 * ((size_t)p.runs + 1) * d.groups + 2) + 2 * (size_t)gn::kStreamBlocks * d.channels;
+  return std::max(stream, d.channels > gn::kThreads ? by_image : 0);
 }
 int launch_group_norm(const GroupNormArgs& a, cudaStream_t st) { return gn::dispatch(a, false, st); }
 int launch_group_norm_backward(const GroupNormArgs& a, cudaStream_t st) { return gn::dispatch(a, true, st); }

@@ -187,8 +187,7 @@ cbr_status_t cbr_group_norm_forward(const cbr_group_norm_desc_t* desc, const voi
     if (need && !ws) return CBR_ERR_INVALID_ARG;
     if (need && ws_bytes < need) return CBR_ERR_WORKSPACE;
     GroupNormArgs a{};
-    uint32_t* err = nullptr;
-    if (const int s = device_for_call(&a.num_sms, &err)) return s;
+    if (const int s = device_for_call(&a.num_sms, &a.err)) return s;
     a.d = d;
     a.x = x;
     a.gamma = gamma;
@@ -223,8 +222,7 @@ cbr_status_t cbr_group_norm_backward(const cbr_group_norm_desc_t* desc, const vo
     if (need && !ws) return CBR_ERR_INVALID_ARG;
     if (need && ws_bytes < need) return CBR_ERR_WORKSPACE;
     GroupNormArgs a{};
-    uint32_t* err = nullptr;
-    if (const int s = device_for_call(&a.num_sms, &err)) return s;
+    if (const int s = device_for_call(&a.num_sms, &a.err)) return s;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (empty) {   // sums over no pixels
       if (gamma && (cudaMemsetAsync(dgamma, 0, d.channels * 4, st) != cudaSuccess ||

@@ -45,6 +45,7 @@ struct GroupNormArgs {
   float* dbeta;
   float* part;
   int num_sms;
+  uint32_t* err;
 };
 size_t group_norm_forward_floats(const cbr_group_norm_desc_t& d);
 size_t group_norm_backward_floats(const cbr_group_norm_desc_t& d, bool parameters);
