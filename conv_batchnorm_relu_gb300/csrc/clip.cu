@@ -1,8 +1,11 @@
 // The norm of a set of gradients and their clipping (declared in include/cbr.h).
 //
-// Two kernels: every block's part of the sum of squares, then (after it, on the stream) the scale from all
-// parts and the scaled gradients.  The tensors' addresses travel in the launches' own parameters, kMost at
-// a time, so a call keeps nothing on the device and can be captured.
+// Bound by memory: every gradient is read for the norm, and read and written for the result, as far as L2 does not
+// hold it.  Two kernels: every block's part of the sum of squares, then (after it, on the stream) the scale from all
+// parts and the scaled gradients, from the last tensors to the first, whose ends are still in L2.  The tensors'
+// addresses travel in the launches' own parameters, so a call keeps nothing on the device and can be captured.
+//   A tile is 32 KB that start on a 16-byte boundary at or before the tensor's first element; a thread loads its next
+// tile's vectors before it works on the last ones.
 #include <algorithm>
 
 #include "common.cuh"
@@ -15,107 +18,197 @@ namespace {
 using namespace tok;
 
 constexpr int kThreads = 512;
-constexpr int kBlocks = 304;       // parts of the sum for each launch
-constexpr int kMost = 512;         // tensors in one launch's parameters
-constexpr int kTile = 8192;        // elements that a block takes at a time
-constexpr int kEpt = kTile / kThreads;
+constexpr int kBlocks = 304;              // two to an SM: parts of the sum for each launch
+constexpr int kMost = 512, kFew = 64;     // tensors in one launch's parameters (14 and 2 KB)
+constexpr int kVectors = 4;               // 16-byte vectors of a thread in a tile
+constexpr int kTileBytes = kThreads * kVectors * 16;
 
 template <int N>
 struct Table {
   const void* grad[N];
   void* out[N];
   int64_t size[N];
-  int64_t tile[N + 1];   // the tensor's first tile
+  uint32_t tile[N + 1];   // the tensor's first tile
   uint8_t dtype[N];
-  int count;
+  int32_t count;
 };
 
-// A thread's sum of squares is taken over few elements in fp32 and added up in fp64, whose range no sum
-// of squares of fp32 values leaves.  Where the fp32 sum is too large or too small to be exact it is taken
-// again, of the elements times a power of two.
-__device__ __forceinline__ double squares(const float (&v)[kEpt]) {
+// A thread's sum of squares is taken over one vector's values in each of four places in fp32 and added up in fp64, whose
+// range no sum of squares of fp32 values leaves.  Where the fp32 sum is too large or too small to be exact it is taken
+// again, of the values times a power of two.
+template <int n>
+__device__ __forceinline__ double squares(const float (&v)[n]) {
   float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < kEpt; ++i) s = fmaf(v[i], v[i], s);
+  for (int i = 0; i < n; ++i) s = fmaf(v[i], v[i], s);
   if (s > 0x1p100f || s < 0x1p-80f) {
     const float f = s > 1.f ? 0x1p-100f : 0x1p100f;
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kEpt; ++i) s = fmaf(v[i] * f, v[i] * f, s);
+    for (int i = 0; i < n; ++i) s = fmaf(v[i] * f, v[i] * f, s);
     return (double)s * (f > 1.f ? 0x1p-200 : 0x1p200);
   }
   return s;
 }
 
-__device__ double block_sum(double v) {
-  __shared__ double part[kThreads / 32];
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.0;
-  for (int i = 0; i < kThreads / 32; ++i) v += part[i];
   return v;
 }
 
+// Where a tile lies: its tensor, and the index (from the 16-byte boundary on) of its first element.
+struct Spot {
+  int tensor;
+  int64_t first;
+};
+
 template <int N>
-__device__ __forceinline__ int tensor_of(const Table<N>& t, int64_t tile) {
+__device__ __forceinline__ Spot spot_of(const Table<N>& t, uint32_t tile) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (t.tile[mid] <= tile) lo = mid;
     else hi = mid - 1;
   }
-  return lo;
+  const int elements = kTileBytes / (t.dtype[lo] == CBR_F32 ? 4 : 2);
+  return Spot{lo, (int64_t)(tile - t.tile[lo]) * elements};
 }
 
-template <typename T>
-__device__ __forceinline__ void load(float (&v)[kEpt], const void* p, int64_t at, int64_t size) {
-#pragma unroll
-  for (int i = 0; i < kEpt; ++i) {
-    const int64_t e = at + i * kThreads + threadIdx.x;
-    v[i] = e < size ? to_f(static_cast<const T*>(p)[e]) : 0.f;
-  }
-}
+// A thread's vectors of a tile as they are stored; what is not of the tensor is 0.
+struct Raw {
+  uint4 v[kVectors];
 
-template <typename T>
-__device__ __forceinline__ void store(const float (&v)[kEpt], float f, void* p, int64_t at, int64_t size) {
+  template <typename T>
+  __device__ __forceinline__ void load(const void* grad, int64_t size, int64_t first) {
+    constexpr int kPer = 16 / sizeof(T);
+    const int skip = (int)(reinterpret_cast<uintptr_t>(grad) & 15) / (int)sizeof(T);
+    const T* base = static_cast<const T*>(grad) - skip;
 #pragma unroll
-  for (int i = 0; i < kEpt; ++i) {
-    const int64_t e = at + i * kThreads + threadIdx.x;
-    if (e < size) static_cast<T*>(p)[e] = from_f<T>(v[i] * f);
+    for (int i = 0; i < kVectors; ++i) {
+      const int64_t e = first + ((int64_t)i * kThreads + threadIdx.x) * kPer;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (e >= skip && e + kPer <= skip + size) {
+        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w) : "l"(base + e));
+      } else if (e + kPer > skip && e < skip + size) {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          if (e + k < skip || e + k >= skip + size) continue;
+          if constexpr (sizeof(T) == 4) w[k] = *reinterpret_cast<const uint32_t*>(base + e + k);
+          else w[k / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(base + e + k) << (16 * (k & 1));
+        }
+        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
   }
-}
+  template <int N>
+  __device__ __forceinline__ void load(const Table<N>& t, const Spot& s) {
+    if (t.dtype[s.tensor] == CBR_F32) load<float>(t.grad[s.tensor], t.size[s.tensor], s.first);
+    else load<__half>(t.grad[s.tensor], t.size[s.tensor], s.first);   // (16 bits of either type)
+  }
+  template <typename T>
+  static __device__ __forceinline__ void values(const uint4& u, float (&f)[16 / sizeof(T)]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (sizeof(T) == 4) {
+        f[k] = __uint_as_float(w[k]);
+      } else {
+        const float2 p = unpack2<std::is_same_v<T, __nv_bfloat16>>(w[k]);
+        f[2 * k] = p.x, f[2 * k + 1] = p.y;
+      }
+    }
+  }
+  template <typename T>
+  __device__ __forceinline__ double sum() const {
+    double s = 0.0;
+    if constexpr (sizeof(T) == 4) {   // four vectors' 16 values at once
+      float f[4 * kVectors];
+#pragma unroll
+      for (int i = 0; i < kVectors; ++i) values<T>(v[i], *reinterpret_cast<float(*)[4]>(f + 4 * i));
+      s = squares(f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVectors; i += 2) {
+        float f[16];
+        values<T>(v[i], *reinterpret_cast<float(*)[8]>(f));
+        values<T>(v[i + 1], *reinterpret_cast<float(*)[8]>(f + 8));
+        s += squares(f);
+      }
+    }
+    return s;
+  }
+  // The scaled values to `out`, which lies as its gradient does (whole vectors) or not (single elements).
+  template <typename T>
+  __device__ __forceinline__ void store(float scale, const void* grad, void* out, int64_t size, int64_t first) const {
+    constexpr int kPer = 16 / sizeof(T);
+    const int skip = (int)(reinterpret_cast<uintptr_t>(grad) & 15) / (int)sizeof(T);
+    const bool alike = ((reinterpret_cast<uintptr_t>(grad) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    T* base = static_cast<T*>(out) - skip;
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) {
+      const int64_t e = first + ((int64_t)i * kThreads + threadIdx.x) * kPer;
+      if (e + kPer <= skip || e >= skip + size) continue;
+      float f[kPer];
+      values<T>(v[i], f);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) f[k] *= scale;
+      if (alike && e >= skip && e + kPer <= skip + size) {
+        uint4 u;
+        if constexpr (sizeof(T) == 4) {
+          u = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        } else {
+          constexpr bool kBf16 = std::is_same_v<T, __nv_bfloat16>;
+          u = make_uint4(pack2<kBf16>(f[0], f[1]), pack2<kBf16>(f[2], f[3]), pack2<kBf16>(f[4], f[5]), pack2<kBf16>(f[6], f[7]));
+        }
+        st_global_v4(base + e, u);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+          if (e + k >= skip && e + k < skip + size) base[e + k] = from_f<T>(f[k]);
+      }
+    }
+  }
+};
 
 template <int N>
-__device__ __forceinline__ void load_tile(float (&v)[kEpt], const Table<N>& t, int i, int64_t at) {
-  if (t.dtype[i] == CBR_F32) load<float>(v, t.grad[i], at, t.size[i]);
-  else if (t.dtype[i] == CBR_BF16) load<__nv_bfloat16>(v, t.grad[i], at, t.size[i]);
-  else load<__half>(v, t.grad[i], at, t.size[i]);
-}
-
-template <int N>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Table<N> t, double* part) {
+__global__ void __launch_bounds__(kThreads, 2) norm_kernel(const __grid_constant__ Table<N> t, double* part) {
+  __shared__ double sums[kThreads / 32];
+  const uint32_t tiles = t.tile[t.count];
   double sum = 0.0;
-  for (int64_t tile = blockIdx.x; tile < t.tile[t.count]; tile += gridDim.x) {
-    const int i = tensor_of(t, tile);
-    float v[kEpt];
-    load_tile(v, t, i, (tile - t.tile[i]) * kTile);
-    sum += squares(v);
+  Raw next;
+  Spot at{}, after{};
+  if (blockIdx.x < tiles) {
+    after = spot_of(t, blockIdx.x);
+    next.load(t, after);
   }
-  sum = block_sum(sum);
-  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+  for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const Raw raw = next;
+    at = after;
+    if (tile + gridDim.x < tiles) {
+      after = spot_of(t, tile + gridDim.x);
+      next.load(t, after);
+    }
+    const int type = t.dtype[at.tensor];
+    sum += type == CBR_F32 ? raw.sum<float>() : type == CBR_BF16 ? raw.sum<__nv_bfloat16>() : raw.sum<__half>();
+  }
+  sum = warp_sum(sum);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    sum = warp_sum(threadIdx.x < kThreads / 32 ? sums[threadIdx.x] : 0.0);
+    if (threadIdx.x == 0) part[blockIdx.x] = sum;
+  }
 }
 
-// Every block adds the parts up in the same order; the first one of the call writes the norm and the scale.
-__device__ float scale_of(const double* part, int parts, float max_norm, float unscale, float* norm_out, float* scale_out,
-                          bool write) {
+// Every block adds the parts up in the same order, in one warp; the first block of the call writes norm and scale.  The
+// scale goes by the norm before it is rounded: one that is subnormal in fp32 has few digits, one past its range none.
+__device__ __forceinline__ float scale_of(const double* part, int parts, float max_norm, float unscale, float* norm_out, float* scale_out,
+                                          bool write) {
   double s = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
-  s = block_sum(s);
-  // the scale goes by the norm before it is rounded: one that is subnormal in fp32 has few digits, one past
-  // its range none
+  for (int i = threadIdx.x; i < parts; i += 32) s += part[i];
+  s = warp_sum(s);
   const double exact = sqrt(s) * (double)unscale;
   const float norm = (float)exact;
   const float scale = exact > max_norm    ? (float)((double)max_norm / exact * (double)unscale)
@@ -126,56 +219,83 @@ __device__ float scale_of(const double* part, int parts, float max_norm, float u
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     scale_kernel(const __grid_constant__ Table<N> t, const double* part, int parts, float max_norm, float unscale,
                  float* norm_out, float* scale_out, int first) {
-  const float f = scale_of(part, parts, max_norm, unscale, norm_out, scale_out, first && blockIdx.x == 0);
-  for (int64_t tile = blockIdx.x; tile < t.tile[t.count]; tile += gridDim.x) {
-    const int i = tensor_of(t, tile);
+  __shared__ float shared_scale;
+  const uint32_t tiles = t.tile[t.count];
+  Raw next;
+  Spot at{}, after{};
+  if (blockIdx.x < tiles) {
+    after = spot_of(t, tiles - 1 - blockIdx.x);
+    next.load(t, after);
+  }
+  if (threadIdx.x < 32) {
+    const float f = scale_of(part, parts, max_norm, unscale, norm_out, scale_out, first && blockIdx.x == 0);
+    if (threadIdx.x == 0) shared_scale = f;
+  }
+  __syncthreads();
+  const float f = shared_scale;
+  for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const Raw raw = next;
+    at = after;
+    if (tile + gridDim.x < tiles) {
+      after = spot_of(t, tiles - 1 - tile - gridDim.x);
+      if (!(f == 1.f && t.out[after.tensor] == t.grad[after.tensor])) next.load(t, after);
+    }
+    const int i = at.tensor, type = t.dtype[i];
     if (f == 1.f && t.out[i] == t.grad[i]) continue;
-    const int64_t at = (tile - t.tile[i]) * kTile;
-    float v[kEpt];
-    load_tile(v, t, i, at);
-    if (t.dtype[i] == CBR_F32) store<float>(v, f, t.out[i], at, t.size[i]);
-    else if (t.dtype[i] == CBR_BF16) store<__nv_bfloat16>(v, f, t.out[i], at, t.size[i]);
-    else store<__half>(v, f, t.out[i], at, t.size[i]);
+    if (type == CBR_F32) raw.store<float>(f, t.grad[i], t.out[i], t.size[i], at.first);
+    else if (type == CBR_BF16) raw.store<__nv_bfloat16>(f, t.grad[i], t.out[i], t.size[i], at.first);
+    else raw.store<__half>(f, t.grad[i], t.out[i], t.size[i], at.first);
   }
 }
 
+// The tensors from `first` on; false where they are more than 2^32 tiles.
 template <int N>
-Table<N> table(const ClipArgs& a, int64_t first) {
-  Table<N> t;
+bool table(const ClipArgs& a, int64_t first, Table<N>& t) {
   t.count = (int)std::min<int64_t>(N, a.count - first);
   int64_t tile = 0;
   for (int i = 0; i < t.count; ++i) {
+    const int64_t n = a.sizes[first + i], elt = a.dtypes[first + i] == CBR_F32 ? 4 : 2;
     t.grad[i] = a.grads[first + i];
     t.out[i] = a.outs ? a.outs[first + i] : nullptr;
-    t.size[i] = a.sizes[first + i];
+    t.size[i] = n;
     t.dtype[i] = (uint8_t)a.dtypes[first + i];
-    t.tile[i] = tile;
-    tile += (t.size[i] + kTile - 1) / kTile;
+    t.tile[i] = (uint32_t)tile;
+    const int64_t skip = static_cast<int64_t>(reinterpret_cast<uintptr_t>(t.grad[i]) & 15);
+    tile += n ? (n * elt + skip + kTileBytes - 1) / kTileBytes : 0;
+    if (tile >= (int64_t(1) << 32) - kBlocks) return false;
   }
-  t.tile[t.count] = tile;
-  return t;
+  t.tile[t.count] = (uint32_t)tile;
+  return true;
 }
 
 int64_t launches(int64_t count) { return std::max<int64_t>(1, (count + kMost - 1) / kMost); }
+
+template <int N>
+int launch(const ClipArgs& a, cudaStream_t st) {
+  const int64_t n = launches(a.count);
+  const int parts = (int)(n * kBlocks);
+  Table<N> t;
+  for (int64_t l = 0; l < n; ++l)
+    if (!table<N>(a, l * N, t)) return CBR_ERR_UNSUPPORTED;
+  for (int64_t l = 0; l < n; ++l) {
+    if (n > 1) table<N>(a, l * N, t);
+    norm_kernel<N><<<kBlocks, kThreads, 0, st>>>(t, a.part + l * kBlocks);
+  }
+  for (int64_t l = a.outs ? n - 1 : 0; l >= 0; --l) {
+    if (n > 1) table<N>(a, l * N, t);
+    if (!a.outs) t.tile[t.count] = 0;
+    scale_kernel<N><<<a.outs ? kBlocks : 1, kThreads, 0, st>>>(t, a.part, parts, a.max_norm, a.unscale, a.norm, a.scale, l == 0);
+  }
+  return cudaGetLastError() == cudaSuccess ? CBR_OK : CBR_ERR_CUDA;
+}
 
 }  // namespace
 
 size_t clip_part_doubles(int64_t count) { return (size_t)launches(count) * kBlocks; }
 
-int launch_clip(const ClipArgs& a, cudaStream_t st) {
-  const int64_t n = launches(a.count);
-  const int parts = (int)(n * kBlocks);
-  for (int64_t l = 0; l < n; ++l)
-    norm_kernel<kMost><<<kBlocks, kThreads, 0, st>>>(table<kMost>(a, l * kMost), a.part + l * kBlocks);
-  for (int64_t l = 0; l < (a.outs ? n : 1); ++l) {
-    Table<kMost> t = table<kMost>(a, l * kMost);
-    if (!a.outs) t.tile[t.count] = 0;
-    scale_kernel<kMost><<<kBlocks, kThreads, 0, st>>>(t, a.part, parts, a.max_norm, a.unscale, a.norm, a.scale, l == 0);
-  }
-  return cudaGetLastError() == cudaSuccess ? CBR_OK : CBR_ERR_CUDA;
-}
+int launch_clip(const ClipArgs& a, cudaStream_t st) { return a.count <= kFew ? launch<kFew>(a, st) : launch<kMost>(a, st); }
 
 }  // namespace cbr

@@ -31,11 +31,16 @@ def _load() -> ctypes.CDLL:
     return _lib
 
 
+# A call is over many tensors: their attributes through map, without a line of Python for each.
+_T = torch.Tensor
+_dtype_of, _is_cuda = _T.dtype.__get__, _T.is_cuda.__get__
+
+
 def _addresses(tensors, dev, what: str) -> array:
-    for t in tensors:
-        if t.device != dev or not t.is_contiguous():
-            _bad(f"{what} have to be contiguous on {dev}")
-    return array("Q", [t.data_ptr() for t in tensors])
+    if not all(map(_T.is_contiguous, tensors)) or not all(map(_is_cuda, tensors)) or \
+            any(map(dev.index.__ne__, map(_T.get_device, tensors))):
+        _bad(f"{what} have to be contiguous on {dev}")
+    return array("Q", map(_T.data_ptr, tensors))
 
 
 def _run(grads, outs, max_norm, unscale, ws, out):
@@ -45,21 +50,20 @@ def _run(grads, outs, max_norm, unscale, ws, out):
         _bad("gradients have to be CUDA tensors")
     dev, n = _device_of(grads[0]), len(grads)
     at = _addresses(grads, dev, "gradients")
+    dtypes, sizes = list(map(_dtype_of, grads)), array("q", map(_T.numel, grads))
+    try:
+        types = array("i", map(_DTYPE.__getitem__, dtypes))
+    except KeyError as e:
+        _bad(f"gradients: {e}", _UNSUPPORTED)
     out_at = at
     if outs is not grads and outs is not None:
         if len(outs) != n:
             _bad(f"{len(outs)} outs for {n} gradients")
         out_at = _addresses(outs, dev, "outs")
-        for g, o in zip(grads, outs):
-            if o.dtype != g.dtype or o.shape != g.shape:
-                _bad("an out has to have its gradient's type and shape")
-    try:
-        types = array("i", [_DTYPE[g.dtype] for g in grads])
-    except KeyError as e:
-        _bad(f"gradients: {e}", _UNSUPPORTED)
-    sizes = array("q", [g.numel() for g in grads])
-    norm = _given(out, "norm", (), torch.float32, dev)
-    scale = _given(out, "scale", (), torch.float32, dev)
+        if list(map(_dtype_of, outs)) != dtypes or array("q", map(_T.numel, outs)) != sizes:
+            _bad("an out has to have its gradient's type and number of elements")
+    norm = _given(out, "norm", (1,), torch.float32, dev)
+    scale = _given(out, "scale", (1,), torch.float32, dev)
     if ws is None:
         ws = _new((clip_workspace_size(n),), torch.uint8, dev)
     elif ws.device != dev or not ws.is_contiguous():
@@ -69,14 +73,20 @@ def _run(grads, outs, max_norm, unscale, ws, out):
         out_at.buffer_info()[0] if outs is not None else None, max_norm, unscale, _vector(norm, 1, dev, "norm"),
         _vector(scale, 1, dev, "scale"), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev)),
         "cbr_clip_gradients")
-    return norm, scale
+    return norm.view(()), scale.view(())
+
+
+_sizes: dict = {}   # clip_workspace_size's answers
 
 
 def clip_workspace_size(count: int) -> int:
     """Workspace bytes of the calls below for `count` tensors."""
-    size = ctypes.c_size_t()
-    _check(_load().cbr_clip_workspace_size(count, ctypes.byref(size)), "cbr_clip_workspace_size")
-    return size.value
+    known = _sizes.get(count)
+    if known is None:
+        size = ctypes.c_size_t()
+        _check(_load().cbr_clip_workspace_size(count, ctypes.byref(size)), "cbr_clip_workspace_size")
+        known = _sizes[count] = size.value
+    return known
 
 
 def gradient_norm(grads, *, unscale=1.0, ws=None) -> torch.Tensor:
@@ -90,7 +100,7 @@ def clip_gradients(grads, max_norm, *, unscale=1.0, ws=None, out=None, scalars=N
         norm = unscale * sqrt(sum of all squares),  scale = unscale * min(1, max_norm / norm)
 
     grads: contiguous tensors (f32, f16, bf16 in any mixture).  unscale takes a loss scale off.  out: tensors
-    of the same shapes and types to write instead of the gradients.  scalars: {"norm": ..., "scale": ...} to
+    of the same sizes and types to write instead of the gradients.  scalars: {"norm": ..., "scale": ...} to
     write.  ws: a workspace of :func:`clip_workspace_size` bytes to use instead of a new one.  An infinite
     gradient makes the scale 0, a NaN makes it NaN; a step that is to be skipped then can look at "norm"."""
     grads = list(grads)
