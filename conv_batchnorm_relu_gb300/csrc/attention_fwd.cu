@@ -18,15 +18,15 @@ namespace cbr {
 namespace att {
 namespace {
 
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kThreads = 320;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kThreads = 384;   // three warpgroups: the last two warps only give their registers
 constexpr float kMove = 8.f;   // how far a score may pass the running maximum, as an exponent of 2
 
 template <int kDim>
 struct Smem {
   static constexpr int kStages = kDim == 128 ? 5 : 8;   // of keys and values in turn
   static constexpr int kQ = 0, kKv = 2 * tile_bytes(kDim), kBar = kKv + kStages * tile_bytes(kDim);
-  // barriers: Q; K/V full, empty; scores full, p full, O full for each query tile; tail; drain
-  static constexpr int kBars = 1 + 2 * kStages + 6 + 2, kTotal = kBar + kBars * 8 + 16 + 1024;
+  // barriers: Q; K/V full, empty; scores full, p full (two halves), O full for each query tile; tail; drain
+  static constexpr int kBars = 1 + 2 * kStages + 8 + 2, kTotal = kBar + kBars * 8 + 16 + 1024;
 };
 
 struct ForwardParams {
@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar_q = sbase + L::kBar, bar_full = bar_q + 8, bar_empty = bar_full + 8 * L::kStages;
-  const uint32_t bar_s = bar_empty + 8 * L::kStages, bar_p = bar_s + 16, bar_o = bar_p + 16, bar_tail = bar_o + 16;
+  const uint32_t bar_s = bar_empty + 8 * L::kStages, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_tail = bar_o + 16;
   const uint32_t bar_drain = bar_tail + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBar + L::kBars * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -86,7 +86,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_s + 8 * t, 1);
-      mbar_init(bar_p + 8 * t, 4);
+      mbar_init(bar_p + 16 * t, 4);
+      mbar_init(bar_p + 16 * t + 8, 4);
       mbar_init(bar_o + 8 * t, 1);
     }
     mbar_init(bar_tail, 1);
@@ -107,6 +108,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     report_error(a.err, bits);
   };
 
+  if (warp >= 8) {
+  give_registers<80>();
   if (warp == kLoadWarp) {
     if (last > begin) {
       if (lane == 0) {
@@ -175,13 +178,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         full(v_at);
         for (int t = 0; t < 2 && !bad; ++t) {
           if (j >= end[t]) continue;
-          bad = !__all_sync(0xffffffffu, mbar_wait(bar_p + 8 * t, ph));
-          if (bad) break;
-          tc_fence_after();
           const uint64_t vd = mn_major(sbase + L::kKv + (v_at % L::kStages) * tile_bytes(kDim));
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_f16_ts_warp(tmem + 256 + t * kDim, tmem + t * 128 + k * 8, vd + mn_major_step(k), kIdO, (k != 0) | (j != begin));
+          for (int half = 0; half < 2; ++half) {
+            if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(bar_p + 16 * t + 8 * half, ph));
+            if (bad) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+              mma_f16_ts_warp(tmem + 256 + t * kDim, tmem + t * 128 + k * 8, vd + mn_major_step(k), kIdO, (k != 0) | (j != begin));
+          }
+          if (bad) break;
           if (j + 1 < end[t]) {
             if (t == 0 || end[0] <= j + 1) full(k_next);
             if (bad) break;
@@ -200,7 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit_warp(bar_drain);
       mbar_wait(bar_drain, 0);
     }
+  }
   } else {
+    take_registers<208>();
     const int t = warp >> 2, row = threadIdx.x & 127;
     const int token = token0 + t * a.tile_tokens + row / a.pack;
     const int q_head = a.pack > 1 ? head * a.pack + row % a.pack : head;
@@ -232,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int i = 0; i < 128; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(r[i]));
-      const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      for (int i = 0; i < 128; i += 2) top[i / 2 & 3] = max3(top[i / 2 & 3], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+      const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]);
       const bool move = (most - m) * c > kMove && m != -INFINITY;
       if (__any_sync(0xffffffffu, move)) {
         // O is complete up to the tile before: its products were issued before these scores'
@@ -252,25 +261,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (m == -INFINITY) m = most;
       const float base = kShift - (m == -INFINITY ? 0.f : m * c);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t c2 = pair(c, c), base2 = pair(base, base);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2; ++i) {   // the products start with the first half while the second is worked on
         uint32_t p[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-          const float x = ex2(fmaf(__uint_as_float(r[64 * i + 2 * e]), c, base));
-          const float y = ex2(fmaf(__uint_as_float(r[64 * i + 2 * e + 1]), c, base));
-          sum[(2 * e) & 3] += x;
-          sum[(2 * e + 1) & 3] += y;
-          p[e] = pack2<BF16>(x, y);
+          const uint64_t x = fma2(pair(r[64 * i + 2 * e], r[64 * i + 2 * e + 1]), c2, base2);
+          const float lo = ex2(low(x)), hi = ex2(high(x));
+          sum[e & 1] = add2(sum[e & 1], pair(lo, hi));
+          p[e] = pack2<BF16>(lo, hi);
         }
         tmem_st32(ts + 32 * i, p);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p + 16 * t + 8 * i);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_p + 8 * t);
+      const uint64_t both = add2(sum[0], sum[1]);
+      l += low(both) + high(both);
     }
     const bool any = end[t] > begin && !bad;
     if (any && !mbar_wait(bar_o + 8 * t, 0)) give_up(kErrWaitAccum);

@@ -33,12 +33,11 @@ def _load() -> ctypes.CDLL:
 
 # A call is over many tensors: their attributes through map, without a line of Python for each.
 _T = torch.Tensor
-_dtype_of, _is_cuda = _T.dtype.__get__, _T.is_cuda.__get__
+_dtype_of = _T.dtype.__get__
 
 
 def _addresses(tensors, dev, what: str) -> array:
-    if not all(map(_T.is_contiguous, tensors)) or not all(map(_is_cuda, tensors)) or \
-            any(map(dev.index.__ne__, map(_T.get_device, tensors))):
+    if not all(map(_T.is_contiguous, tensors)) or any(map(dev.index.__ne__, map(_T.get_device, tensors))):
         _bad(f"{what} have to be contiguous on {dev}")
     return array("Q", map(_T.data_ptr, tensors))
 
