@@ -9,7 +9,7 @@
 // elements are shared by two warpgroups: a thread has a row and 64 of its 128 columns.
 //   f16: p is taken 2^12 times as large, and dS a power of two times as large that a bound on |do| |v| gives
 // for each key head, so that small ones keep their digits; the results are scaled back.
-//   Queries past the last one have the offset +infinity (p = 0), keys past theirs are cut off at the outputs.
+//   Queries past the last one have the offset -infinity (p = 0), keys past theirs are cut off at the outputs.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -23,8 +23,8 @@ constexpr int kLoadWarp = 8, kMmaWarp = 9, kThreads = 320;
 
 struct BackwardParams {
   Params p;
-  const float* offset;    // [batch * packs][rows]: lse log2(e) - shift of a row, +infinity where p is 0
-  const float* delta;     // the same of D
+  const float* offset;    // [batch * packs][rows]: shift - lse log2(e) of a row, -infinity where p is 0
+  const float* delta;     // the same of -D
   const uint32_t* norms;  // f16: [batch][heads_k][2] bits of the largest |do|^2 and |v|^2
   int64_t rows;           // of a pack of heads, a multiple of 128
   void* out[2];           // dq; or dv, dk
@@ -48,7 +48,7 @@ __device__ __forceinline__ float ds_scale(const BackwardParams& f, int batch, in
 
 // ---------------------------------------------------------------- D, offsets, bounds
 
-constexpr int kPrepareRows = 64;   // rows of a block of 256 threads, 16 lanes to a row
+constexpr int kPrepareRows = 64, kTurns = kPrepareRows / 16;   // rows of a block of 256 threads, 16 lanes to a row
 
 struct PrepareParams {
   BackwardParams f;
@@ -97,21 +97,28 @@ __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ Pr
     const int64_t head = at % packs;
     batch = at / packs;
     key_head = a.pack > 1 ? head : head / a.group;
+    uint4 u[kTurns], w[kTurns];
+    float lse[kTurns];
 #pragma unroll
-    for (int r = 0; r < kPrepareRows / 16; ++r) {
+    for (int r = 0; r < kTurns; ++r) {
       const int64_t row = first + r * 16 + sub, token = row / a.pack, h = head * a.pack + row % a.pack;
-      const bool live = token < a.q_tokens;
-      uint4 u = make_uint4(0, 0, 0, 0), w = u;
-      if (live && e < a.head_dim) {
-        u = ld_global_nc_v4(static_cast<const uint16_t*>(g.d_o) + batch * g.do_stride[0] + token * g.do_stride[1] + h * g.do_stride[2] + e);
-        w = ld_global_nc_v4(static_cast<const uint16_t*>(g.o) + batch * g.o_stride[0] + token * g.o_stride[1] + h * g.o_stride[2] + e);
+      u[r] = w[r] = make_uint4(0, 0, 0, 0);
+      lse[r] = -INFINITY;
+      if (token >= a.q_tokens) continue;
+      if (e < a.head_dim) {
+        u[r] = ld_global_nc_v4(static_cast<const uint16_t*>(g.d_o) + batch * g.do_stride[0] + token * g.do_stride[1] + h * g.do_stride[2] + e);
+        w[r] = ld_global_nc_v4(static_cast<const uint16_t*>(g.o) + batch * g.o_stride[0] + token * g.o_stride[1] + h * g.o_stride[2] + e);
       }
-      const float d = half_warp_sum(dot8<BF16>(u, w));
-      if constexpr (!BF16) most = tok::Max::of(most, half_warp_sum(dot8<BF16>(u, u)));
+      if (lane == 0) lse[r] = g.lse[(batch * a.heads_q + h) * a.q_tokens + token];
+    }
+#pragma unroll
+    for (int r = 0; r < kTurns; ++r) {
+      const float d = half_warp_sum(dot8<BF16>(u[r], w[r]));
+      if constexpr (!BF16) most = tok::Max::of(most, half_warp_sum(dot8<BF16>(u[r], u[r])));
       if (lane == 0) {
-        const float lse = live ? g.lse[(batch * a.heads_q + h) * a.q_tokens + token] : -INFINITY;
-        g.offset[at * g.f.rows + row] = lse == -INFINITY ? INFINITY : lse * kLog2e - kShift<BF16>;
-        g.delta[at * g.f.rows + row] = d;
+        const int64_t to = at * g.f.rows + first + r * 16 + sub;
+        g.offset[to] = lse[r] == -INFINITY ? -INFINITY : kShift<BF16> - lse[r] * kLog2e;
+        g.delta[to] = -d;
       }
     }
   } else {
@@ -120,14 +127,16 @@ __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ Pr
     key_head = at % a.heads_k;
     batch = at / a.heads_k;
     const int keys = keys_of(a, (int)batch);
+    uint4 u[kTurns];
 #pragma unroll
-    for (int r = 0; r < kPrepareRows / 16; ++r) {
+    for (int r = 0; r < kTurns; ++r) {
       const int64_t row = first + r * 16 + sub;
-      uint4 u = make_uint4(0, 0, 0, 0);
+      u[r] = make_uint4(0, 0, 0, 0);
       if (row < keys && e < a.head_dim)
-        u = ld_global_nc_v4(static_cast<const uint16_t*>(g.v) + batch * g.v_stride[0] + row * g.v_stride[1] + key_head * g.v_stride[2] + e);
-      most = tok::Max::of(most, half_warp_sum(dot8<BF16>(u, u)));
+        u[r] = ld_global_nc_v4(static_cast<const uint16_t*>(g.v) + batch * g.v_stride[0] + row * g.v_stride[1] + key_head * g.v_stride[2] + e);
     }
+#pragma unroll
+    for (int r = 0; r < kTurns; ++r) most = tok::Max::of(most, half_warp_sum(dot8<BF16>(u[r], u[r])));
   }
   if constexpr (!BF16) {
     most = tok::warp_max(most);
@@ -334,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float c = exponent_scale(a), sc = ds_scale<BF16>(f, batch, key_head), sc2 = sc * ex2(-kShift<BF16>);
     const int64_t at = ((int64_t)batch * packs + head) * f.rows + (int64_t)block * kTile + row;
-    const float offset = -f.offset[at], dsc = -f.delta[at] * sc2;
+    const float offset = f.offset[at], dsc = f.delta[at] * sc2;
+    const uint64_t c2 = pair(c, c), offset2 = pair(offset, offset), sc22 = pair(sc2, sc2), dsc2 = pair(dsc, dsc);
     const int limit = a.causal ? min(keys, max(0, start + token + 1)) : keys;
     const int least = a.causal ? min(keys, max(0, start + token0 + 1)) : keys;
     bool bad = false;
@@ -351,7 +361,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 2; ++i) tmem_ld32(ts + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * i));
       tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 64; ++i) p[i] = ex2(fmaf(__uint_as_float(r[i]), c, offset));
+      for (int i = 0; i < 64; i += 2) {
+        const uint64_t x = fma2(pair(r[i], r[i + 1]), c2, offset2);
+        p[i] = ex2(low(x));
+        p[i + 1] = ex2(high(x));
+      }
       bad = !__all_sync(0xffffffffu, mbar_wait(bar_dpf, j & 1));
       if (bad) break;
       tc_fence_after();
@@ -368,8 +382,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint32_t ds[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        ds[i] = pack2<BF16>(p[2 * i] * fmaf(__uint_as_float(r[2 * i]), sc2, dsc), p[2 * i + 1] * fmaf(__uint_as_float(r[2 * i + 1]), sc2, dsc));
+      for (int i = 0; i < 32; ++i) {
+        const uint64_t x = mul2(pair(p[2 * i], p[2 * i + 1]), fma2(pair(r[2 * i], r[2 * i + 1]), sc22, dsc2));
+        ds[i] = pack2<BF16>(low(x), high(x));
+      }
       tmem_st32(ts, ds);
       tmem_st_wait();
       tc_fence_before();
@@ -545,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t ts = trow + 256 + half * 64, tdp = trow + 384 + half * 64;
     const float c = exponent_scale(a), sc = ds_scale<BF16>(f, batch, key_head), sc2 = sc * ex2(-kShift<BF16>);
+    const uint64_t c2 = pair(c, c), sc22 = pair(sc2, sc2);
     bool bad = false;
     for (int j = 0; j < n; ++j) {
       const int qt = q_first + (first + j) % each;
@@ -567,11 +584,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float4 o = offset[i];
-        p[4 * i] = ex2(fmaf(__uint_as_float(r[4 * i]), c, -o.x));
-        p[4 * i + 1] = ex2(fmaf(__uint_as_float(r[4 * i + 1]), c, -o.y));
-        p[4 * i + 2] = ex2(fmaf(__uint_as_float(r[4 * i + 2]), c, -o.z));
-        p[4 * i + 3] = ex2(fmaf(__uint_as_float(r[4 * i + 3]), c, -o.w));
+        const float4 o = offset[i];   // negative
+        const uint64_t x = fma2(pair(r[4 * i], r[4 * i + 1]), c2, pair(o.x, o.y));
+        const uint64_t y = fma2(pair(r[4 * i + 2], r[4 * i + 3]), c2, pair(o.z, o.w));
+        p[4 * i] = ex2(low(x));
+        p[4 * i + 1] = ex2(high(x));
+        p[4 * i + 2] = ex2(low(y));
+        p[4 * i + 3] = ex2(high(y));
       }
       if (edge) {
 #pragma unroll
@@ -594,12 +613,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float4 d = delta[i];
-        const float x = (__uint_as_float(r[4 * i]) - d.x) * sc2 * p[4 * i], y = (__uint_as_float(r[4 * i + 1]) - d.y) * sc2 * p[4 * i + 1];
-        const float z = (__uint_as_float(r[4 * i + 2]) - d.z) * sc2 * p[4 * i + 2];
-        const float u = (__uint_as_float(r[4 * i + 3]) - d.w) * sc2 * p[4 * i + 3];
-        w[2 * i] = pack2<BF16>(x, y);
-        w[2 * i + 1] = pack2<BF16>(z, u);
+        const float4 d = delta[i];   // negative
+        uint64_t x = add2(pair(r[4 * i], r[4 * i + 1]), pair(d.x, d.y)), y = add2(pair(r[4 * i + 2], r[4 * i + 3]), pair(d.z, d.w));
+        if constexpr (!BF16) x = mul2(x, sc22), y = mul2(y, sc22);
+        x = mul2(x, pair(p[4 * i], p[4 * i + 1]));
+        y = mul2(y, pair(p[4 * i + 2], p[4 * i + 3]));
+        w[2 * i] = pack2<BF16>(low(x), high(x));
+        w[2 * i + 1] = pack2<BF16>(low(y), high(y));
       }
       tmem_st32(tdp, w);
       tmem_st_wait();
