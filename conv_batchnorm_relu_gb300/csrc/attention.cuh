@@ -102,39 +102,46 @@ __device__ __forceinline__ int start_of(const Params& a, int b) {
 // scale log2(e); above 0, so that a hidden score's -infinity stays one (10^-35 of a score is 0 beside 1).
 __device__ __forceinline__ float exponent_scale(const Params& a) { return fmaxf(a.scale * kLog2e, 1e-35f); }
 
-// A tile of keys or values (128 rows from `row` on of one head), by one thread: kDim / 64 boxes.
-template <int kDim>
+// A tile of keys or values (kRows rows from `row` on of one head), by one thread, in boxes of kBox rows and 64 elements.
+template <int kDim, int kRows = kTile, int kBox = kRows>
 __device__ __forceinline__ void load_keys(uint32_t dst, const CUtensorMap* map, const Place& p, int row, int head, int batch,
                                           uint32_t bar) {
-  mbar_arrive_expect_tx(bar, tile_bytes(kDim));
+  mbar_arrive_expect_tx(bar, kRows * kDim * 2);
 #pragma unroll
-  for (int i = 0; i < kDim / 64; ++i) tma_load_4d(dst + i * kSlab, map, 64 * i, row, head * p.head, batch * p.batch, bar);
+  for (int i = 0; i < kDim / 64; ++i)
+#pragma unroll
+    for (int r = 0; r < kRows; r += kBox)
+      tma_load_4d(dst + (i * kRows + r) * 128, map, 64 * i, row + r, head * p.head, batch * p.batch, bar);
 }
 
-// A tile of queries (or of what has their shape): `tile_tokens` tokens of `pack` heads; the rows that are left of the
-// 128 keep what they held.  head: counted in packs.  The barrier's thread has announced query_bytes() for each.
-template <int kDim>
+// A tile of queries (or of what has their shape), kRows rows of tokens and the `pack` heads of each, in boxes of kBox rows;
+// where the pack does not divide them, the rows that are left keep what they held.  head: counted in packs.  The
+// barrier's thread has announced query_bytes() for each.
+template <int kDim, int kRows = kTile>
 __device__ __forceinline__ uint32_t query_bytes(const Params& a) {
-  return a.tile_tokens * a.pack * kDim * 2;
+  return (kRows == kTile ? a.tile_tokens * a.pack : kRows) * kDim * 2;
 }
-template <int kDim>
+template <int kDim, int kRows = kTile, int kBox = kRows>
 __device__ __forceinline__ void load_queries(uint32_t dst, const CUtensorMap* map, const Params& a, const Place& p, int token,
                                              int head, int batch, uint32_t bar) {
 #pragma unroll
   for (int i = 0; i < kDim / 64; ++i)
-    tma_load_5d(dst + i * kSlab, map, 64 * i, 0, token, head * p.head, batch * p.batch, bar);
+#pragma unroll
+    for (int r = 0; r < kRows; r += kBox)
+      tma_load_5d(dst + (i * kRows + r) * 128, map, 64 * i, 0, token + r / a.pack, head * p.head, batch * p.batch, bar);
 }
 
 // Rows from `first` on of a tile set to zero by one warp, visible to the tensor cores afterwards.
-template <int kDim>
+template <int kDim, int kRows = kTile>
 __device__ __forceinline__ void clear_rows(uint32_t dst, int first, int lane) {
-  for (int c = first * 8 + lane; c < kTile * 8; c += 32)
+  for (int c = first * 8 + lane; c < kRows * 8; c += 32)
 #pragma unroll
-    for (int i = 0; i < kDim / 64; ++i) st_shared_v4(dst + i * kSlab + c * 16, make_uint4(0, 0, 0, 0));
+    for (int i = 0; i < kDim / 64; ++i) st_shared_v4(dst + i * kRows * 128 + c * 16, make_uint4(0, 0, 0, 0));
   fence_proxy_async_smem();
 }
 
-// K-major and MN-major descriptors of a tile; a step of 16 along K is `k_step(k)` bytes further.
+// K-major and MN-major descriptors of a tile, and how much further a step of 16 along K is.  (Tiles of 64 rows have one
+// slab: heads of 64.)
 __device__ __forceinline__ uint64_t k_major(uint32_t tile) { return make_sw128_desc(tile, 16, 1024, 0); }
 __device__ __forceinline__ uint64_t mn_major(uint32_t tile) { return make_sw128_desc(tile, kSlab, 1024, 0); }
 __device__ __forceinline__ constexpr uint64_t k_major_step(int k) { return (uint64_t)(((k >> 2) * kSlab + (k & 3) * 32) >> 4); }
@@ -162,17 +169,17 @@ inline bool map_of(CUtensorMap* map, const cbr_attention_desc_t& d, const void* 
                       strides, box);
 }
 
-// Keys or values: [batch][heads_k][tokens][head_dim], boxes of 128 tokens and 64 elements.
-inline bool key_map(CUtensorMap* map, const cbr_attention_desc_t& d, const void* p, const int64_t* s) {
+// Keys or values: [batch][heads_k][tokens][head_dim], boxes of `rows` tokens and 64 elements.
+inline bool key_map(CUtensorMap* map, const cbr_attention_desc_t& d, const void* p, const int64_t* s, int rows = kTile) {
   const Axis axes[3] = {axis(std::max<int64_t>(d.k_tokens, 1), s[1]), axis(d.heads_k, s[2]), axis(d.batch, s[0])};
-  const uint32_t box[4] = {64, kTile, 1, 1};
+  const uint32_t box[4] = {64, (uint32_t)rows, 1, 1};
   return map_of(map, d, p, 4, axes, box);
 }
 
 // Queries, or what has their shape: [batch][heads_q / pack][tokens][pack][head_dim].
-inline bool query_map(CUtensorMap* map, const cbr_attention_desc_t& d, const void* p, const int64_t* s, int pack) {
+inline bool query_map(CUtensorMap* map, const cbr_attention_desc_t& d, const void* p, const int64_t* s, int pack, int rows = kTile) {
   const Axis axes[4] = {axis(pack, s[2]), axis(d.q_tokens, s[1]), axis(d.heads_q / pack, s[2] * pack), axis(d.batch, s[0])};
-  const uint32_t box[5] = {64, (uint32_t)pack, (uint32_t)(kTile / pack), 1, 1};
+  const uint32_t box[5] = {64, (uint32_t)pack, (uint32_t)(rows / pack), 1, 1};
   return map_of(map, d, p, 5, axes, box);
 }
 

@@ -19,7 +19,17 @@ namespace cbr {
 namespace att {
 namespace {
 
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kThreads = 320;
+// By the head: kN, the tokens that a step of a walk takes (what stays has 128), and the warps.  Warps 0-3 (and 4-7) have the
+// 128 rows of a tile of scores, 64 columns of each to a thread; one loads, one issues the products.  Heads of 64 take
+// half of TMEM, and two blocks to an SM, one's start and end over the other's walk (16x784 tokens, 12 heads of 64: query
+// kernel 99 us, key kernel 141 with one block and kN = 128).
+template <int kDim>
+struct Form {
+  static constexpr int kN = kDim, kRowWarps = kN / 16, kHalves = kN / 64, kThreads = 32 * (kRowWarps + 2), kBlocks = 128 / kDim;
+  static constexpr int kLoadWarp = kRowWarps, kMmaWarp = kRowWarps + 1;
+  static constexpr int kStep = kN * kDim * 2;   // bytes of a step's tile
+  static constexpr uint32_t kColumns = 4 * kN;  // of TMEM, in quarters
+};
 
 struct BackwardParams {
   Params p;
@@ -48,7 +58,11 @@ __device__ __forceinline__ float ds_scale(const BackwardParams& f, int batch, in
 
 // ---------------------------------------------------------------- D, offsets, bounds
 
-constexpr int kPrepareRows = 64, kTurns = kPrepareRows / 16;   // rows of a block of 256 threads, 16 lanes to a row
+constexpr int kTurns = 4;   // rows of a thread in a block of 256
+template <int kDim>
+constexpr int kLanes = kDim / 8;                             // of a row
+template <int kDim>
+constexpr int kPrepareRows = kTurns * 256 / kLanes<kDim>;    // of a block: 64 or 128
 
 struct PrepareParams {
   BackwardParams f;
@@ -63,9 +77,10 @@ struct PrepareParams {
   int64_t query_blocks;   // blocks of queries; the others (f16) take values
 };
 
-__device__ __forceinline__ float half_warp_sum(float v) {
+template <int kDim>
+__device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = kLanes<kDim> / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -83,25 +98,27 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b) {
   return s;
 }
 
-template <bool BF16>
+template <int kDim, bool BF16>
 __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepareParams g) {
   const Params& a = g.f.p;
   __shared__ float largest[8];
-  const int lane = threadIdx.x & 15, sub = threadIdx.x >> 4, e = lane * 8;
+  constexpr int kSubs = 256 / kLanes<kDim>;
+  const int lane = threadIdx.x % kLanes<kDim>, sub = threadIdx.x / kLanes<kDim>, e = lane * 8;
   const bool queries = blockIdx.x < g.query_blocks;
   float most = 0.f;
   int64_t batch, key_head;
   if (queries) {
-    const int64_t packs = a.heads_q / a.pack, per = g.f.rows / kPrepareRows;
-    const int64_t at = blockIdx.x / per, first = blockIdx.x % per * kPrepareRows;
-    const int64_t head = at % packs;
-    batch = at / packs;
+    const uint32_t packs = a.heads_q / a.pack, per = (uint32_t)(g.f.rows / kPrepareRows<kDim>), place = blockIdx.x / per;
+    const int64_t at = place, first = (int64_t)(blockIdx.x - place * per) * kPrepareRows<kDim>;
+    const uint32_t head = place % packs;
+    batch = place / packs;
+    const int shift = 31 - __clz(a.pack);   // a power of two
     key_head = a.pack > 1 ? head : head / a.group;
     uint4 u[kTurns], w[kTurns];
     float lse[kTurns];
 #pragma unroll
     for (int r = 0; r < kTurns; ++r) {
-      const int64_t row = first + r * 16 + sub, token = row / a.pack, h = head * a.pack + row % a.pack;
+      const int64_t row = first + r * kSubs + sub, token = row >> shift, h = (head << shift) + (row & (a.pack - 1));
       u[r] = w[r] = make_uint4(0, 0, 0, 0);
       lse[r] = -INFINITY;
       if (token >= a.q_tokens) continue;
@@ -113,30 +130,31 @@ __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ Pr
     }
 #pragma unroll
     for (int r = 0; r < kTurns; ++r) {
-      const float d = half_warp_sum(dot8<BF16>(u[r], w[r]));
-      if constexpr (!BF16) most = tok::Max::of(most, half_warp_sum(dot8<BF16>(u[r], u[r])));
+      const float d = row_sum<kDim>(dot8<BF16>(u[r], w[r]));
+      if constexpr (!BF16) most = tok::Max::of(most, row_sum<kDim>(dot8<BF16>(u[r], u[r])));
       if (lane == 0) {
-        const int64_t to = at * g.f.rows + first + r * 16 + sub;
+        const int64_t to = at * g.f.rows + first + r * kSubs + sub;
         g.offset[to] = lse[r] == -INFINITY ? -INFINITY : kShift<BF16> - lse[r] * kLog2e;
         g.delta[to] = -d;
       }
     }
   } else {
-    const int64_t per = (a.k_tokens + kPrepareRows - 1) / kPrepareRows, at = (blockIdx.x - g.query_blocks) / per;
-    const int64_t first = (blockIdx.x - g.query_blocks) % per * kPrepareRows;
-    key_head = at % a.heads_k;
-    batch = at / a.heads_k;
+    const uint32_t per = (a.k_tokens + kPrepareRows<kDim> - 1) / kPrepareRows<kDim>, block = blockIdx.x - (uint32_t)g.query_blocks;
+    const uint32_t place = block / per;
+    const int64_t first = (int64_t)(block - place * per) * kPrepareRows<kDim>;
+    key_head = place % a.heads_k;
+    batch = place / a.heads_k;
     const int keys = keys_of(a, (int)batch);
     uint4 u[kTurns];
 #pragma unroll
     for (int r = 0; r < kTurns; ++r) {
-      const int64_t row = first + r * 16 + sub;
+      const int64_t row = first + r * kSubs + sub;
       u[r] = make_uint4(0, 0, 0, 0);
       if (row < keys && e < a.head_dim)
         u[r] = ld_global_nc_v4(static_cast<const uint16_t*>(g.v) + batch * g.v_stride[0] + row * g.v_stride[1] + key_head * g.v_stride[2] + e);
     }
 #pragma unroll
-    for (int r = 0; r < kTurns; ++r) most = tok::Max::of(most, half_warp_sum(dot8<BF16>(u[r], u[r])));
+    for (int r = 0; r < kTurns; ++r) most = tok::Max::of(most, row_sum<kDim>(dot8<BF16>(u[r], u[r])));
   }
   if constexpr (!BF16) {
     most = tok::warp_max(most);
@@ -188,21 +206,21 @@ __device__ __forceinline__ uint8_t* row_of(const BackwardParams& f, int which, i
 template <int kDim>
 struct QuerySmem {
   static constexpr int kK = 3, kV = 2;   // stages: a tile of keys stays for two products, one of values for one
-  static constexpr int kQ = 0, kDo = tile_bytes(kDim), kKeys = 2 * tile_bytes(kDim), kValues = kKeys + kK * tile_bytes(kDim);
-  static constexpr int kBar = kValues + kV * tile_bytes(kDim);
+  static constexpr int kQ = 0, kDo = tile_bytes(kDim), kKeys = 2 * tile_bytes(kDim), kValues = kKeys + kK * Form<kDim>::kStep;
+  static constexpr int kBar = kValues + kV * Form<kDim>::kStep;
   // Q and dO; K full, empty; V full, empty; scores, dS (two each); dP full, empty; dQ; tail; drain
   static constexpr int kBars = 1 + 2 * kK + 2 * kV + 4 + 2 + 3, kTotal = kBar + kBars * 8 + 16 + 1024;
 };
 
-// Warps: 0-3 the first, 4-7 the second 64 columns of the 128 rows; 8 loads, 9 products.
-// TMEM: dQ at 0, S in two buffers at 128 and 256 (dS over them), dP at 384.
+// TMEM by quarters: dQ, S in two buffers (dS over them), dP.
 template <int kDim, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Form<kDim>::kThreads, Form<kDim>::kBlocks)
     query_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
                  const __grid_constant__ BackwardParams f) {
   using L = QuerySmem<kDim>;
-  constexpr uint32_t kTile_ = tile_bytes(kDim);
+  using F = Form<kDim>;
+  constexpr int kN = F::kN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -221,17 +239,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int token0 = block * a.tile_tokens;
   const int keys = keys_of(a, batch), start = start_of(a, batch);
   const int see = a.causal ? min(keys, max(0, start + min(token0 + a.tile_tokens, a.q_tokens))) : keys;
-  const int tiles = (see + kTile - 1) / kTile, share = (tiles + a.splits - 1) / a.splits;
+  const int tiles = (see + kN - 1) / kN, share = (tiles + a.splits - 1) / a.splits;
   const int first = min(tiles, (int)blockIdx.y * share), n = min(tiles, first + share) - first;
 
   if (threadIdx.x == 0) {
     for (uint32_t b = bar_q; b <= bar_drain; b += 8)
-      mbar_init(b, (b >= bar_ds && b < bar_dpf) || b == bar_dpe ? 8 : 1);   // dS, dP empty: one arrival for each row warp
+      mbar_init(b, (b >= bar_ds && b < bar_dpf) || b == bar_dpe ? F::kRowWarps : 1);   // dS, dP empty: one arrival for each row warp
     *abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == F::kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), F::kColumns);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -243,31 +261,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     report_error(a.err, bits);
   };
 
-  if (warp == kLoadWarp) {
+  if (warp == F::kLoadWarp) {
     if (n > 0) {
       if (lane == 0) {
         mbar_arrive_expect_tx(bar_q, 2 * query_bytes<kDim>(a));
-        load_queries<kDim>(sbase + L::kQ, &map_q, a, a.q, token0, head, batch, bar_q);
-        load_queries<kDim>(sbase + L::kDo, &map_do, a, a.d_o, token0, head, batch, bar_q);
+        load_queries<kDim, kTile, kN>(sbase + L::kQ, &map_q, a, a.q, token0, head, batch, bar_q);
+        load_queries<kDim, kTile, kN>(sbase + L::kDo, &map_do, a, a.d_o, token0, head, batch, bar_q);
       }
       int kn = 0, vn = 0;   // tiles asked for
       for (int j = 0; j < n && !__any_sync(0xffffffffu, *abort_flag); ++j) {
-        const int row = (first + j) * kTile;
+        const int row = (first + j) * kN;
         const uint32_t ks = j % L::kK, vs = j % L::kV;
         if (!__all_sync(0xffffffffu, mbar_wait_backoff(bar_ke + 8 * ks, ((j / L::kK) & 1) ^ 1, 32))) {
           give_up(kErrWaitOperand);
           break;
         }
-        const bool tail = row + kTile > keys && keys < a.k_tokens;
-        const uint32_t dst = sbase + L::kKeys + ks * kTile_;
-        if (lane == 0) load_keys<kDim>(dst, &map_k, a.k, row, key_head, batch, tail ? bar_tail : bar_kf + 8 * ks);
+        const bool tail = row + kN > keys && keys < a.k_tokens;
+        const uint32_t dst = sbase + L::kKeys + ks * F::kStep;
+        if (lane == 0) load_keys<kDim, kN>(dst, &map_k, a.k, row, key_head, batch, tail ? bar_tail : bar_kf + 8 * ks);
         if (tail) {
           // keys behind the last one may be anything: dS is 0 there, and 0 times NaN is not
           if (!__all_sync(0xffffffffu, mbar_wait(bar_tail, 0))) {
             give_up(kErrWaitOperand);
             break;
           }
-          clear_rows<kDim>(dst, keys - row, lane);
+          clear_rows<kDim, kN>(dst, keys - row, lane);
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_kf + 8 * ks);
         }
@@ -276,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           give_up(kErrWaitOperand);
           break;
         }
-        if (lane == 0) load_keys<kDim>(sbase + L::kValues + vs * kTile_, &map_v, a.v, row, key_head, batch, bar_vf + 8 * vs);
+        if (lane == 0) load_keys<kDim, kN>(sbase + L::kValues + vs * F::kStep, &map_v, a.v, row, key_head, batch, bar_vf + 8 * vs);
         ++vn;
         __syncwarp();
       }
@@ -286,9 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = max(0, vn - L::kV); i < vn; ++i) mbar_wait(bar_vf + 8 * (i % L::kV), (i / L::kV) & 1);
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == F::kMmaWarp) {
     if (n > 0) {
-      constexpr uint32_t kIdS = make_idesc_f16(128, 128, BF16, false, false), kIdQ = make_idesc_f16(128, kDim, BF16, false, true);
+      constexpr uint32_t kIdS = make_idesc_f16(128, kN, BF16, false, false), kIdQ = make_idesc_f16(128, kDim, BF16, false, true);
       bool bad = false;
       auto wait = [&](uint32_t bar, uint32_t parity) {
         if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -302,12 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto scores = [&](int i) {
         if (!wait(bar_kf + 8 * (i % L::kK), (i / L::kK) & 1)) return;
-        product(128 + (i & 1) * 128, sbase + L::kQ, sbase + L::kKeys + (i % L::kK) * kTile_);
+        product(kN + (i & 1) * kN, sbase + L::kQ, sbase + L::kKeys + (i % L::kK) * F::kStep);
         mma_commit_warp(bar_s + 8 * (i & 1));
       };
       auto dp = [&](int i) {
         if (!wait(bar_vf + 8 * (i % L::kV), (i / L::kV) & 1)) return;
-        product(384, sbase + L::kDo, sbase + L::kValues + (i % L::kV) * kTile_);
+        product(3 * kN, sbase + L::kDo, sbase + L::kValues + (i % L::kV) * F::kStep);
         mma_commit_warp(bar_dpf);
         mma_commit_warp(bar_ve + 8 * (i % L::kV));
       };
@@ -321,10 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (bad) break;
         }
         if (!wait(bar_ds + 8 * (j & 1), (j >> 1) & 1)) break;
-        const uint64_t kd = mn_major(sbase + L::kKeys + (j % L::kK) * kTile_);
-        const uint32_t ds = tmem + 128 + (j & 1) * 128;
+        const uint64_t kd = mn_major(sbase + L::kKeys + (j % L::kK) * F::kStep);
+        const uint32_t ds = tmem + kN + (j & 1) * kN;
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)   // 64 columns of dS at the start of each half of its scores
+        for (int k = 0; k < kN / 16; ++k)   // 64 columns of dS at the start of each half of its scores
           mma_f16_ts_warp(tmem, ds + (k >> 2) * 64 + (k & 3) * 8, kd + mn_major_step(k), kIdQ, (k != 0) | (j != 0));
         mma_commit_warp(bar_ke + 8 * (j % L::kK));
         if (j + 2 < n) scores(j + 2);
@@ -349,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int least = a.causal ? min(keys, max(0, start + token0 + 1)) : keys;
     bool bad = false;
     for (int j = 0; j < n; ++j) {
-      const uint32_t ts = trow + 128 + (j & 1) * 128 + half * 64;
-      const int key = (first + j) * kTile + half * 64;
+      const uint32_t ts = trow + kN + (j & 1) * kN + half * 64;
+      const int key = (first + j) * kN + half * 64;
       const bool edge = key + 64 > least;
       bad = !__all_sync(0xffffffffu, mbar_wait(bar_s + 8 * (j & 1), (j >> 1) & 1));
       if (bad) break;
@@ -370,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (bad) break;
       tc_fence_after();
 #pragma unroll
-      for (int i = 0; i < 2; ++i) tmem_ld32(trow + 384 + half * 64 + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * i));
+      for (int i = 0; i < 2; ++i) tmem_ld32(trow + 3 * kN + half * 64 + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * i));
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
@@ -399,34 +417,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* out = row_of(f, 0, batch, token, q_head);
     float* part = a.splits > 1 ? f.part + (blockIdx.y * f.part_rows + out_row) * a.head_dim : nullptr;
 #pragma unroll 1
-    for (int i = half * (kDim / 2); i < (half + 1) * (kDim / 2); i += 32)
+    for (int i = half * 64; i < (half + 1) * 64; i += 32)
       store32<BF16>(trow, i, a.head_dim, n > 0 && !bad, true, live, a.scale / sc, out, part);
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == F::kMmaWarp) tmem_dealloc(tmem, F::kColumns);
 }
 
 // ---------------------------------------------------------------- dK, dV
 
 template <int kDim>
 struct KeySmem {
-  static constexpr int kK = 0, kV = tile_bytes(kDim), kQ = 2 * tile_bytes(kDim), kDo = 4 * tile_bytes(kDim);   // Q, dO: two stages
-  static constexpr int kRow = 6 * tile_bytes(kDim);   // two stages of 128 offsets and 128 D
-  static constexpr int kBar = kRow + 2 * 1024;
+  static constexpr int kStep = Form<kDim>::kStep, kRowStep = Form<kDim>::kN * 8;
+  static constexpr int kK = 0, kV = tile_bytes(kDim), kQ = 2 * tile_bytes(kDim), kDo = kQ + 2 * kStep;   // Q, dO: two stages
+  static constexpr int kRow = kDo + 2 * kStep;   // two stages of offsets and D
+  static constexpr int kBar = kRow + 2 * kRowStep;
   // K and V; Q full, empty; dO full, empty (two each); scores, p, dP, dS; out; drain
   static constexpr int kBars = 1 + 8 + 4 + 2, kTotal = kBar + kBars * 8 + 16 + 1024;
 };
 
-// Rows are keys here, columns queries.  Warps as above.  TMEM: dV at 0, dK at 128, S at 256 (P over it), dP at 384
-// (dS over it).
+// Rows are keys here, columns queries.  TMEM by quarters: dV, dK, S (P over it), dP (dS over it).
 template <int kDim, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Form<kDim>::kThreads, Form<kDim>::kBlocks)
     key_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
                const __grid_constant__ BackwardParams f) {
   using L = KeySmem<kDim>;
-  constexpr uint32_t kTile_ = tile_bytes(kDim);
+  using F = Form<kDim>;
+  constexpr int kN = F::kN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -443,20 +462,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tile = blockIdx.x / (gridDim.x / key_tiles);   // causal: the first keys have the most queries, and come first
   const int key0 = tile * kTile, keys = keys_of(a, batch), start = start_of(a, batch);
   // tiles of queries: those from the first that sees one of the keys, of every pack of heads that reads them
-  const int q_tiles = (int)(f.rows / kTile);
-  const int q_first = a.causal ? (int)min((int64_t)q_tiles, (int64_t)min(max(0, key0 - start), a.q_tokens) * a.pack / kTile) : 0;
+  const int q_tiles = (int)(f.rows / kN);
+  const int q_first = a.causal ? (int)min((int64_t)q_tiles, (int64_t)min(max(0, key0 - start), a.q_tokens) * a.pack / kN) : 0;
   const int each = key0 < keys ? q_tiles - q_first : 0, all = each * (a.group / a.pack);
   const int share = (all + a.splits - 1) / a.splits;
   const int first = min(all, (int)blockIdx.y * share), n = min(all, first + share) - first;
   const int head0 = a.pack > 1 ? key_head : key_head * a.group;   // the first pack of heads
 
   if (threadIdx.x == 0) {
-    for (uint32_t b = bar_kv; b <= bar_drain; b += 8) mbar_init(b, b == bar_p || b == bar_ds ? 8 : b == bar_kv ? 2 : 1);
+    for (uint32_t b = bar_kv; b <= bar_drain; b += 8) mbar_init(b, b == bar_p || b == bar_ds ? F::kRowWarps : b == bar_kv ? 2 : 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == F::kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), F::kColumns);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -468,12 +487,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     report_error(a.err, bits);
   };
 
-  if (warp == kLoadWarp) {
+  if (warp == F::kLoadWarp) {
     if (n > 0) {
       if (lane == 0) {
-        load_keys<kDim>(sbase + L::kK, &map_k, a.k, key0, key_head, batch, bar_kv);
+        load_keys<kDim, kTile, kN>(sbase + L::kK, &map_k, a.k, key0, key_head, batch, bar_kv);
         // (the barrier counts two arrivals: each of the loads announces its own bytes)
-        load_keys<kDim>(sbase + L::kV, &map_v, a.v, key0, key_head, batch, bar_kv);
+        load_keys<kDim, kTile, kN>(sbase + L::kV, &map_v, a.v, key0, key_head, batch, bar_kv);
       }
       int qn = 0, on = 0;   // tiles asked for
       for (int j = 0; j < n && !__any_sync(0xffffffffu, *abort_flag); ++j) {
@@ -484,11 +503,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (lane == 0) {
-          const int64_t at = ((int64_t)batch * (a.heads_q / a.pack) + head) * f.rows + (int64_t)qt * kTile;
-          mbar_arrive_expect_tx(bar_qf + 8 * s, query_bytes<kDim>(a) + 1024);
-          load_queries<kDim>(sbase + L::kQ + s * kTile_, &map_q, a, a.q, qt * a.tile_tokens, head, batch, bar_qf + 8 * s);
-          bulk_load_1d(sbase + L::kRow + s * 1024, f.offset + at, 512, bar_qf + 8 * s);
-          bulk_load_1d(sbase + L::kRow + s * 1024 + 512, f.delta + at, 512, bar_qf + 8 * s);
+          const int64_t at = ((int64_t)batch * (a.heads_q / a.pack) + head) * f.rows + (int64_t)qt * kN;
+          mbar_arrive_expect_tx(bar_qf + 8 * s, query_bytes<kDim, kN>(a) + L::kRowStep);
+          load_queries<kDim, kN>(sbase + L::kQ + s * F::kStep, &map_q, a, a.q, qt * (kN / a.pack), head, batch, bar_qf + 8 * s);
+          bulk_load_1d(sbase + L::kRow + s * L::kRowStep, f.offset + at, L::kRowStep / 2, bar_qf + 8 * s);
+          bulk_load_1d(sbase + L::kRow + s * L::kRowStep + L::kRowStep / 2, f.delta + at, L::kRowStep / 2, bar_qf + 8 * s);
         }
         ++qn;
         if (!__all_sync(0xffffffffu, mbar_wait_backoff(bar_oe + 8 * s, parity, 32))) {
@@ -496,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar_of + 8 * s, query_bytes<kDim>(a));
-          load_queries<kDim>(sbase + L::kDo + s * kTile_, &map_do, a, a.d_o, qt * a.tile_tokens, head, batch, bar_of + 8 * s);
+          mbar_arrive_expect_tx(bar_of + 8 * s, query_bytes<kDim, kN>(a));
+          load_queries<kDim, kN>(sbase + L::kDo + s * F::kStep, &map_do, a, a.d_o, qt * (kN / a.pack), head, batch, bar_of + 8 * s);
         }
         ++on;
         __syncwarp();
@@ -508,9 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = max(0, on - 2); i < on; ++i) mbar_wait(bar_of + 8 * (i & 1), (i >> 1) & 1);
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == F::kMmaWarp) {
     if (n > 0) {
-      constexpr uint32_t kIdS = make_idesc_f16(128, 128, BF16, false, false), kIdK = make_idesc_f16(128, kDim, BF16, false, true);
+      constexpr uint32_t kIdS = make_idesc_f16(128, kN, BF16, false, false), kIdK = make_idesc_f16(128, kDim, BF16, false, true);
       bool bad = false;
       auto wait = [&](uint32_t bar, uint32_t parity) {
         if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -528,26 +547,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto gather = [&](uint32_t d, uint32_t x, uint32_t y, int j) {
         const uint64_t yd = mn_major(sbase + y);
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
+        for (int k = 0; k < kN / 16; ++k)
           mma_f16_ts_warp(tmem + d, tmem + x + (k >> 2) * 64 + (k & 3) * 8, yd + mn_major_step(k), kIdK, (k != 0) | (j != 0));
       };
-      if (wait(bar_kv, 0) && wait(bar_qf, 0)) scores(256, L::kK, L::kQ, bar_s);
-      if (!bad && wait(bar_of, 0)) scores(384, L::kV, L::kDo, bar_dp);
+      if (wait(bar_kv, 0) && wait(bar_qf, 0)) scores(2 * kN, L::kK, L::kQ, bar_s);
+      if (!bad && wait(bar_of, 0)) scores(3 * kN, L::kV, L::kDo, bar_dp);
       for (int j = 0; j < n && !bad; ++j) {
         const uint32_t s = j & 1, next = s ^ 1, parity = ((j + 1) >> 1) & 1;
         if (!wait(bar_p, j & 1)) break;
-        gather(0, 256, L::kDo + s * kTile_, j);
+        gather(0, 2 * kN, L::kDo + s * F::kStep, j);
         mma_commit_warp(bar_oe + 8 * s);
         if (j + 1 < n) {
           if (!wait(bar_qf + 8 * next, parity)) break;
-          scores(256, L::kK, L::kQ + next * kTile_, bar_s);
+          scores(2 * kN, L::kK, L::kQ + next * F::kStep, bar_s);
         }
         if (!wait(bar_ds, j & 1)) break;
-        gather(128, 384, L::kQ + s * kTile_, j);
+        gather(kN, 3 * kN, L::kQ + s * F::kStep, j);
         mma_commit_warp(bar_qe + 8 * s);
         if (j + 1 < n) {
           if (!wait(bar_of + 8 * next, parity)) break;
-          scores(384, L::kV, L::kDo + next * kTile_, bar_dp);
+          scores(3 * kN, L::kV, L::kDo + next * F::kStep, bar_dp);
         }
         if (__any_sync(0xffffffffu, *abort_flag)) break;
       }
@@ -559,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const int half = warp >> 2, row = threadIdx.x & 127, key = key0 + row;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = trow + 256 + half * 64, tdp = trow + 384 + half * 64;
+    const uint32_t ts = trow + 2 * kN + half * 64, tdp = trow + 3 * kN + half * 64;
     const float c = exponent_scale(a), sc = ds_scale<BF16>(f, batch, key_head), sc2 = sc * ex2(-kShift<BF16>);
     const uint64_t c2 = pair(c, c), sc22 = pair(sc2, sc2);
     bool bad = false;
@@ -568,12 +587,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // causal: the first of the tile's columns (queries, of several heads where packed) that sees this row's key
       int hidden = 0;
       if (a.causal) {
-        const int64_t from = (int64_t)max(0, key - start) * a.pack - (int64_t)qt * kTile - half * 64;
+        const int64_t from = (int64_t)max(0, key - start) * a.pack - (int64_t)qt * kN - half * 64;
         hidden = (int)max((int64_t)0, min((int64_t)64, from));
       }
       const bool edge = __any_sync(0xffffffffu, hidden > 0);
-      const float4* offset = reinterpret_cast<const float4*>(smem + L::kRow + (j & 1) * 1024) + half * 16;
-      const float4* delta = offset + 32;
+      const float4* offset = reinterpret_cast<const float4*>(smem + L::kRow + (j & 1) * L::kRowStep) + half * 16;
+      const float4* delta = offset + kN / 4;
       bad = !__all_sync(0xffffffffu, mbar_wait(bar_qf + 8 * (j & 1), (j >> 1) & 1) && mbar_wait(bar_s, j & 1));
       if (bad) break;
       tc_fence_after();
@@ -630,18 +649,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!bad && n > 0) bad = !__all_sync(0xffffffffu, mbar_wait(bar_out, 0));
     if (bad) give_up(kErrWaitAccum);
     tc_fence_after();
-    // the first warpgroup stores dV, the second dK
-    uint8_t* out = row_of(f, half, batch, key, key_head);
-    const int64_t out_row = ((int64_t)batch * a.heads_k + key_head) * a.k_tokens + key;
-    float* part = a.splits > 1 ? f.part + ((2 * blockIdx.y + half) * f.part_rows + out_row) * a.head_dim : nullptr;
-    const float scale = half ? a.scale / sc : ex2(-kShift<BF16>);
+    // with two warpgroups the first stores dV, the second dK
 #pragma unroll 1
-    for (int i = 0; i < kDim; i += 32)
-      store32<BF16>(trow + half * 128, i, a.head_dim, n > 0 && !bad, key < keys, key < a.k_tokens, scale, out, part);
+    for (int which = half; which < 2; which += F::kHalves) {
+      uint8_t* out = row_of(f, which, batch, key, key_head);
+      const int64_t out_row = ((int64_t)batch * a.heads_k + key_head) * a.k_tokens + key;
+      float* part = a.splits > 1 ? f.part + ((2 * blockIdx.y + which) * f.part_rows + out_row) * a.head_dim : nullptr;
+      const float scale = which ? a.scale / sc : ex2(-kShift<BF16>);
+#pragma unroll 1
+      for (int i = 0; i < kDim; i += 32)
+        store32<BF16>(trow + which * kN, i, a.head_dim, n > 0 && !bad, key < keys, key < a.k_tokens, scale, out, part);
+    }
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == F::kMmaWarp) tmem_dealloc(tmem, F::kColumns);
 }
 
 // ---------------------------------------------------------------- parts
@@ -675,16 +697,17 @@ struct Shape {
 Shape shape_of(const cbr_attention_desc_t& d, bool may_pack) {
   Shape s{};
   const int64_t group = d.heads_q / d.heads_k;
-  s.pack = may_pack && group <= kTile && (group & (group - 1)) == 0 ? (int)group : 1;
+  const int step = d.head_dim > 64 ? 128 : 64, blocks_to_sm = 128 / step;
+  s.pack = may_pack && group <= step && (group & (group - 1)) == 0 ? (int)group : 1;
   s.packs = d.heads_q / s.pack;
   s.rows = (d.q_tokens * s.pack + kTile - 1) / kTile * kTile;
   s.q_blocks = s.rows / kTile;
   s.key_tiles = (d.k_tokens + kTile - 1) / kTile;
-  auto splits = [](int64_t blocks, int64_t walk) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kSms / std::max<int64_t>(blocks, 1), walk / 2));
+  auto splits = [&](int64_t blocks, int64_t walk) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kSms * blocks_to_sm / std::max<int64_t>(blocks, 1), walk / step / 2));
   };
-  s.query_splits = splits(s.q_blocks * s.packs * d.batch, s.key_tiles);
-  s.key_splits = splits(s.key_tiles * d.heads_k * d.batch, s.q_blocks * (group / s.pack));
+  s.query_splits = splits(s.q_blocks * s.packs * d.batch, d.k_tokens);
+  s.key_splits = splits(s.key_tiles * d.heads_k * d.batch, s.rows * (group / s.pack));
   s.offsets = (size_t)d.batch * s.packs * s.rows * 4;
   s.norms = align256((size_t)d.batch * d.heads_k * 8);
   const size_t q_part = s.query_splits > 1 ? (size_t)s.query_splits * d.batch * d.heads_q * d.q_tokens : 0;
@@ -722,13 +745,13 @@ int launch(const AttentionArgs& g, cudaStream_t st) {
     pre.v = g.v;
     pre.lse = g.lse;
     for (int i = 0; i < 3; ++i) pre.do_stride[i] = d.do_stride[i], pre.o_stride[i] = d.o_stride[i], pre.v_stride[i] = d.v_stride[i];
-    pre.query_blocks = d.batch * s.packs * (s.rows / kPrepareRows);
+    pre.query_blocks = d.batch * s.packs * (s.rows / kPrepareRows<kDim>);
     int64_t blocks = pre.query_blocks;
     if constexpr (!BF16) {
       if (cudaMemsetAsync(pre.norms, 0, (size_t)d.batch * d.heads_k * 8, st) != cudaSuccess) return CBR_ERR_CUDA;
-      blocks += d.batch * d.heads_k * ((d.k_tokens + kPrepareRows - 1) / kPrepareRows);
+      blocks += d.batch * d.heads_k * ((d.k_tokens + kPrepareRows<kDim> - 1) / kPrepareRows<kDim>);
     }
-    prepare_kernel<BF16><<<(unsigned)blocks, 256, 0, st>>>(pre);
+    prepare_kernel<kDim, BF16><<<(unsigned)blocks, 256, 0, st>>>(pre);
   }
   // where one side is empty nothing is loaded, and the maps of the other stand in for its own
   CUtensorMap q, k, v, d_o;
@@ -742,8 +765,9 @@ int launch(const AttentionArgs& g, cudaStream_t st) {
     pk = pv = g.q;
     for (int i = 0; i < 3; ++i) e.k_stride[i] = e.v_stride[i] = 0;
   }
-  if (!query_map(&q, e, pq, e.q_stride, s.pack) || !query_map(&d_o, e, pdo, e.do_stride, s.pack) || !key_map(&k, e, pk, e.k_stride) ||
-      !key_map(&v, e, pv, e.v_stride))
+  constexpr int kN = Form<kDim>::kN, kThreads = Form<kDim>::kThreads;
+  if (!query_map(&q, e, pq, e.q_stride, s.pack, kN) || !query_map(&d_o, e, pdo, e.do_stride, s.pack, kN) ||
+      !key_map(&k, e, pk, e.k_stride, kN) || !key_map(&v, e, pv, e.v_stride, kN))
     return CBR_ERR_CUDA;
   const auto by_query = &query_kernel<kDim, BF16>;
   const auto by_key = &key_kernel<kDim, BF16>;
