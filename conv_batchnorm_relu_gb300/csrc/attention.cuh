@@ -45,7 +45,6 @@ struct Params {
   int32_t q_tokens, k_tokens, heads_q, heads_k, group, head_dim, causal;
   int32_t pack;          // query heads in a tile's rows: 1 or the group
   int32_t tile_tokens;   // queries in a tile: 128 / pack
-  int32_t tiles;         // tiles of queries that a block takes
   int32_t q_blocks;      // blocks along the queries
   int32_t splits;        // blocks that share a tile's keys
   float scale;

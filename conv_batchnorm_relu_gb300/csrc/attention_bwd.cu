@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(Form<kDim>::kThreads, Form<kDim>::kBlocks)
 
 // ---------------------------------------------------------------- parts
 
-// Parts added up in their order: a warp for each row of `outs` results of [batch][heads][tokens].
+// Parts added up in their order: a warp for each row of `outs` results of [batch][heads][tokens], four elements to a lane.
 template <bool BF16>
 __global__ void __launch_bounds__(128) sum_kernel(const __grid_constant__ BackwardParams f, int outs, int64_t heads, int64_t tokens) {
   const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -677,11 +677,16 @@ __global__ void __launch_bounds__(128) sum_kernel(const __grid_constant__ Backwa
   const int64_t which = at / f.part_rows, row = at % f.part_rows;
   using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
   T* out = reinterpret_cast<T*>(row_of(f, (int)which, row / tokens / heads, row % tokens, row / tokens % heads));
-  for (int e = lane; e < dim; e += 32) {
-    float v = 0.f;
-    for (int s = 0; s < f.p.splits; ++s) v += f.part[((s * outs + which) * f.part_rows + row) * dim + e];
-    out[e] = tok::from_f<T>(v);
+  if (4 * lane >= dim) return;
+  const float4* part = reinterpret_cast<const float4*>(f.part + (which * f.part_rows + row) * dim + 4 * lane);
+  const int64_t step = outs * f.part_rows * dim / 4;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = 0; s < f.p.splits; ++s) {
+    const float4 u = part[s * step];
+    v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
   }
+  reinterpret_cast<uint2*>(out)[lane] = make_uint2(pack2<BF16>(v.x, v.y), pack2<BF16>(v.z, v.w));
 }
 
 // ---------------------------------------------------------------- host side
@@ -692,8 +697,8 @@ struct Shape {
   size_t offsets, norms, parts;   // bytes of the workspace's regions
 };
 
-// Heads that share a key head are packed into a tile of queries where they fill it evenly.  Where blocks are fewer
-// than half the SMs their walk is shared, two tiles at least to each.
+// Heads that share a key head are packed into a tile of queries where they fill it evenly.  Where blocks leave
+// SMs idle a long walk is shared among several, four steps at least to each.
 Shape shape_of(const cbr_attention_desc_t& d, bool may_pack) {
   Shape s{};
   const int64_t group = d.heads_q / d.heads_k;
@@ -704,7 +709,8 @@ Shape shape_of(const cbr_attention_desc_t& d, bool may_pack) {
   s.q_blocks = s.rows / kTile;
   s.key_tiles = (d.k_tokens + kTile - 1) / kTile;
   auto splits = [&](int64_t blocks, int64_t walk) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kSms * blocks_to_sm / std::max<int64_t>(blocks, 1), walk / step / 2));
+    if (walk < 12 * step) return 1;   // the sum of the parts costs about as much as a few steps
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kSms * blocks_to_sm / std::max<int64_t>(blocks, 1), walk / step / 4));
   };
   s.query_splits = splits(s.q_blocks * s.packs * d.batch, d.k_tokens);
   s.key_splits = splits(s.key_tiles * d.heads_k * d.batch, s.rows * (group / s.pack));
@@ -729,7 +735,6 @@ int launch(const AttentionArgs& g, cudaStream_t st) {
   PrepareParams pre{};
   BackwardParams& f = pre.f;
   f.p = params_of(g, s.pack);
-  f.p.tiles = 1;
   f.p.q_blocks = (int)s.q_blocks;
   pre.offset = reinterpret_cast<float*>(ws);
   pre.delta = reinterpret_cast<float*>(ws + align256(s.offsets));

@@ -18,15 +18,24 @@ namespace cbr {
 namespace att {
 namespace {
 
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kThreads = 384;   // three warpgroups: the last two warps only give their registers
 constexpr float kMove = 8.f;   // how far a score may pass the running maximum, as an exponent of 2
 
-template <int kDim>
+// By the tiles of queries that a block takes.  Two: the block has an SM to itself, and its row warps take registers from
+// the others (two warps only give theirs).  One: half of TMEM, two blocks to an SM, one's exponentials over the
+// other's products.
+template <int kTiles>
+struct Form {
+  static constexpr int kRowWarps = 4 * kTiles, kLoadWarp = kRowWarps, kMmaWarp = kRowWarps + 1;
+  static constexpr int kThreads = kTiles == 2 ? 384 : 192, kBlocks = 3 - kTiles;
+  static constexpr uint32_t kColumns = 256 * kTiles, kO = 128 * kTiles;   // of TMEM: all, and where O is
+};
+
+template <int kDim, int kTiles>
 struct Smem {
-  static constexpr int kStages = kDim == 128 ? 5 : 8;   // of keys and values in turn
-  static constexpr int kQ = 0, kKv = 2 * tile_bytes(kDim), kBar = kKv + kStages * tile_bytes(kDim);
+  static constexpr int kStages = kTiles == 2 ? (kDim == 128 ? 5 : 8) : (kDim == 128 ? 2 : 5);   // of keys and values in turn
+  static constexpr int kQ = 0, kKv = kTiles * tile_bytes(kDim), kBar = kKv + kStages * tile_bytes(kDim);
   // barriers: Q; K/V full, empty; scores full, p full (two halves), O full for each query tile; tail; drain
-  static constexpr int kBars = 1 + 2 * kStages + 8 + 2, kTotal = kBar + kBars * 8 + 16 + 1024;
+  static constexpr int kBars = 1 + 2 * kStages + 4 * kTiles + 2, kTotal = kBar + kBars * 8 + 16 + 1024;
 };
 
 struct ForwardParams {
@@ -38,17 +47,18 @@ struct ForwardParams {
   float* part_lse;       // [split][row]: log2 of the partial sums
 };
 
-template <int kDim, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kDim, int kTiles, bool BF16>
+__global__ void __launch_bounds__(Form<kTiles>::kThreads, Form<kTiles>::kBlocks)
     forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ ForwardParams f) {
-  using L = Smem<kDim>;
+  using L = Smem<kDim, kTiles>;
+  using F = Form<kTiles>;
   constexpr float kShift = BF16 ? 0.f : 6.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar_q = sbase + L::kBar, bar_full = bar_q + 8, bar_empty = bar_full + 8 * L::kStages;
-  const uint32_t bar_s = bar_empty + 8 * L::kStages, bar_p = bar_s + 16, bar_o = bar_p + 32, bar_tail = bar_o + 16;
+  const uint32_t bar_s = bar_empty + 8 * L::kStages, bar_p = bar_s + 8 * kTiles, bar_o = bar_p + 16 * kTiles, bar_tail = bar_o + 8 * kTiles;
   const uint32_t bar_drain = bar_tail + 8;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBar + L::kBars * 8);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -60,23 +70,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int head = blockIdx.x % packs, batch = blockIdx.x / packs % (gridDim.x / packs / a.q_blocks);
   const int block = a.q_blocks - 1 - blockIdx.x / (gridDim.x / a.q_blocks);
   const int key_head = a.pack > 1 ? head : head / a.group;
-  const int token0 = block * a.tiles * a.tile_tokens;
+  const int token0 = block * kTiles * a.tile_tokens;
   const int keys = keys_of(a, batch), start = start_of(a, batch);
   // tiles of keys that each query tile needs: those that its last query sees
-  int end[2], widest = 0;
+  int end[kTiles], widest = 0;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
+  for (int t = 0; t < kTiles; ++t) {
     const int first = token0 + t * a.tile_tokens;
     int see = 0;
-    if (t < a.tiles && first < a.q_tokens)
+    if (first < a.q_tokens)
       see = a.causal ? min(keys, max(0, start + min(first + a.tile_tokens, a.q_tokens))) : keys;
     end[t] = (see + kTile - 1) / kTile;
     widest = max(widest, end[t]);
   }
   const int share = (widest + a.splits - 1) / a.splits, begin = blockIdx.y * share;
 #pragma unroll
-  for (int t = 0; t < 2; ++t) end[t] = max(begin, min(end[t], begin + share));
-  const int last = max(end[0], end[1]);
+  for (int t = 0; t < kTiles; ++t) end[t] = max(begin, min(end[t], begin + share));
+  const int last = max(end[0], end[kTiles - 1]);
 
   if (threadIdx.x == 0) {
     mbar_init(bar_q, 1);
@@ -84,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_full + 8 * i, 1);
       mbar_init(bar_empty + 8 * i, 1);
     }
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < kTiles; ++t) {
       mbar_init(bar_s + 8 * t, 1);
       mbar_init(bar_p + 16 * t, 4);
       mbar_init(bar_p + 16 * t + 8, 4);
@@ -95,8 +105,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == F::kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), F::kColumns);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -108,13 +118,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     report_error(a.err, bits);
   };
 
-  if (warp >= 8) {
-  give_registers<80>();
-  if (warp == kLoadWarp) {
+  if (warp >= F::kRowWarps) {
+  if constexpr (kTiles == 2) give_registers<80>();
+  if (warp == F::kLoadWarp) {
     if (last > begin) {
       if (lane == 0) {
-        mbar_arrive_expect_tx(bar_q, ((end[0] > begin) + (end[1] > begin)) * query_bytes<kDim>(a));
-        for (int t = 0; t < 2; ++t)
+        int tiles = 0;
+        for (int t = 0; t < kTiles; ++t) tiles += end[t] > begin;
+        mbar_arrive_expect_tx(bar_q, tiles * query_bytes<kDim>(a));
+        for (int t = 0; t < kTiles; ++t)
           if (end[t] > begin)
             load_queries<kDim>(sbase + L::kQ + t * tile_bytes(kDim), &map_q, a, a.q, token0 + t * a.tile_tokens, head, batch, bar_q);
       }
@@ -150,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait(bar_full + 8 * (i % L::kStages), (i / L::kStages) & 1);
       }
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == F::kMmaWarp) {
     if (last > begin) {
       constexpr uint32_t kIdS = make_idesc_f16(128, 128, BF16, false, false), kIdO = make_idesc_f16(128, kDim, BF16, false, true);
       bool bad = !__all_sync(0xffffffffu, mbar_wait(bar_q, 0));
@@ -169,14 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit_warp(bar_s + 8 * t);
       };
       full(0);
-      for (int t = 0; t < 2 && !bad; ++t)
+      for (int t = 0; t < kTiles && !bad; ++t)
         if (end[t] > begin) scores(t, 0);
       if (!bad) mma_commit_warp(bar_empty);
       for (int j = begin; j < last && !bad; ++j) {
         const uint32_t v_at = done + 1, k_next = done + 2;
         const uint32_t ph = (j - begin) & 1;
         full(v_at);
-        for (int t = 0; t < 2 && !bad; ++t) {
+        for (int t = 0; t < kTiles && !bad; ++t) {
           if (j >= end[t]) continue;
           const uint64_t vd = mn_major(sbase + L::kKv + (v_at % L::kStages) * tile_bytes(kDim));
 #pragma unroll
@@ -186,9 +198,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int k = 4 * half; k < 4 * half + 4; ++k)
-              mma_f16_ts_warp(tmem + 256 + t * kDim, tmem + t * 128 + k * 8, vd + mn_major_step(k), kIdO, (k != 0) | (j != begin));
+              mma_f16_ts_warp(tmem + F::kO + t * kDim, tmem + t * 128 + k * 8, vd + mn_major_step(k), kIdO, (k != 0) | (j != begin));
           }
           if (bad) break;
+          if (t == kTiles - 1 || j >= end[kTiles - 1]) mma_commit_warp(bar_empty + 8 * (v_at % L::kStages));
           if (j + 1 < end[t]) {
             if (t == 0 || end[0] <= j + 1) full(k_next);
             if (bad) break;
@@ -198,7 +211,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (bad) break;
-        mma_commit_warp(bar_empty + 8 * (v_at % L::kStages));
         if (j + 1 < last) mma_commit_warp(bar_empty + 8 * (k_next % L::kStages));
         done += 2;
         if (__any_sync(0xffffffffu, *abort_flag)) break;
@@ -209,13 +221,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   } else {
-    take_registers<208>();
+    if constexpr (kTiles == 2) take_registers<208>();
     const int t = warp >> 2, row = threadIdx.x & 127;
     const int token = token0 + t * a.tile_tokens + row / a.pack;
     const int q_head = a.pack > 1 ? head * a.pack + row % a.pack : head;
-    const bool live = t < a.tiles && row < a.tile_tokens * a.pack && token < a.q_tokens;
+    const bool live = row < a.tile_tokens * a.pack && token < a.q_tokens;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = trow + t * 128, to = trow + 256 + t * kDim;
+    const uint32_t ts = trow + t * 128, to = trow + F::kO + t * kDim;
     const float c = exponent_scale(a);
     // the first key that this query does not see, and one for the whole tile
     const int limit = a.causal ? min(keys, max(0, start + token + 1)) : keys;
@@ -321,36 +333,58 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == F::kMmaWarp) tmem_dealloc(tmem, F::kColumns);
 }
 
-// The parts of a query's result, joined in their order: a warp for each query.
+constexpr int kMostSplits = 64;
+
+// The parts of a query's result, joined in their order: a warp for each query, four elements to a lane.
 template <bool BF16>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ ForwardParams f, int64_t rows) {
   const Params& a = f.p;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
-  float most = -INFINITY, sum = 0.f;
-  for (int s = 0; s < a.splits; ++s) most = tok::Max::of(most, f.part_lse[s * rows + row]);
-  const float base = most == -INFINITY ? 0.f : most;
-  float v[kTile / 32] = {};
-  for (int s = 0; s < a.splits; ++s) {
-    const float w = ex2(f.part_lse[s * rows + row] - base);
-    sum += w;
+  // the weights by lanes, at most kMostSplits
+  float lse[kMostSplits / 32], most = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kTile / 32; ++i)
-      if (lane + 32 * i < a.head_dim) v[i] = fmaf(w, f.part_o[(s * rows + row) * a.head_dim + lane + 32 * i], v[i]);
+  for (int i = 0; i < kMostSplits / 32; ++i) {
+    lse[i] = lane + 32 * i < a.splits ? f.part_lse[(lane + 32 * i) * rows + row] : -INFINITY;
+    most = tok::Max::of(most, lse[i]);
+  }
+  most = tok::warp_max(most);
+  const float base = most == -INFINITY ? 0.f : most;
+#pragma unroll
+  for (int i = 0; i < kMostSplits / 32; ++i) sum += lse[i] = ex2(lse[i] - base);
+  sum = tok::warp_reduce<tok::Sum>(sum);
+  const bool in = 4 * lane < a.head_dim;
+  const float4* part = reinterpret_cast<const float4*>(f.part_o + row * a.head_dim + (in ? 4 * lane : 0));
+  const int64_t step = rows * a.head_dim / 4;
+  float v[4] = {};
+#pragma unroll
+  for (int i = 0; i < kMostSplits / 32; ++i) {
+    for (int first = 32 * i; first < min(a.splits, 32 * i + 32); first += 8) {   // eight loads at a time
+      float4 o[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) o[s] = first + s < a.splits ? part[(first + s) * step] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const float w = __shfl_sync(0xffffffffu, lse[i], (first + s) & 31);
+        v[0] = fmaf(w, o[s].x, v[0]);
+        v[1] = fmaf(w, o[s].y, v[1]);
+        v[2] = fmaf(w, o[s].z, v[2]);
+        v[3] = fmaf(w, o[s].w, v[3]);
+      }
+    }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t token = row % a.q_tokens, h = row / a.q_tokens % a.heads_q, b = row / a.q_tokens / a.heads_q;
-  using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
-  T* out = static_cast<T*>(f.o) + b * f.o_stride[0] + token * f.o_stride[1] + h * f.o_stride[2];
-#pragma unroll
-  for (int i = 0; i < kTile / 32; ++i)
-    if (lane + 32 * i < a.head_dim) out[lane + 32 * i] = tok::from_f<T>(v[i] * inv);
+  uint8_t* out = static_cast<uint8_t*>(f.o) + 2 * (b * f.o_stride[0] + token * f.o_stride[1] + h * f.o_stride[2] + 4 * lane);
+  if (in) *reinterpret_cast<uint2*>(out) = make_uint2(pack2<BF16>(v[0] * inv, v[1] * inv), pack2<BF16>(v[2] * inv, v[3] * inv));
   if (f.lse && lane == 0) f.lse[row] = (base + log2f(sum)) * kLn2;
 }
+
+int64_t rows_of(const cbr_attention_desc_t& d) { return d.batch * d.heads_q * d.q_tokens; }
 
 struct Shape {
   int pack, tiles, splits;
@@ -360,8 +394,8 @@ struct Shape {
 // How the queries are laid over blocks.  Heads that share a key head are packed into a tile where that leaves at
 // most an eighth of its rows empty, or where all the queries there are fit one tile.  Two tiles to a block overlap one's
 // exponentials with the other's products; a block has an SM to itself, so one tile each is taken where two would
-// leave SMs without a block.  Where blocks are fewer than half the SMs the keys are shared among them, a few
-// tiles at least to each.
+// leave SMs without a block.  Where blocks leave SMs idle a long walk over the keys is shared among
+// several.
 // (Heads of q that repeat have no axis to pack.)
 Shape shape_of(const cbr_attention_desc_t& d, bool may_pack) {
   Shape s{};
@@ -372,18 +406,20 @@ Shape shape_of(const cbr_attention_desc_t& d, bool may_pack) {
   s.tiles = (tiles + 1) / 2 * s.packs * d.batch >= kSms ? 2 : 1;
   s.q_blocks = (tiles + s.tiles - 1) / s.tiles;
   const int64_t blocks = s.q_blocks * s.packs * d.batch, key_tiles = (d.k_tokens + kTile - 1) / kTile;
-  s.splits = (int)std::max<int64_t>(1, std::min<int64_t>(kSms / std::max<int64_t>(blocks, 1), key_tiles / 2));
+  // A tile takes a block that is alone about 1.4 us; the join 3 us for a few rows, 6 for ten thousand (8 tiles of one row:
+  // 14.6 us in one block, 10.3 in four; 7 tiles of 9408 rows: 12.4 and, in three, 17).
+  const bool few = rows_of(d) <= 2048;
+  if (s.tiles == 1 && key_tiles >= (few ? 6 : 12))
+    s.splits = (int)std::min<int64_t>({2 * kSms / std::max<int64_t>(blocks, 1), key_tiles / (few ? 2 : 4), kMostSplits});
+  s.splits = std::max(1, s.splits);
   return s;
 }
 
-int64_t rows_of(const cbr_attention_desc_t& d) { return d.batch * d.heads_q * d.q_tokens; }
-
-template <int kDim, bool BF16>
+template <int kDim, int kTiles, bool BF16>
 int launch(const AttentionArgs& g, const Shape& s, cudaStream_t st) {
   const cbr_attention_desc_t& d = g.d;
   ForwardParams f{};
   f.p = params_of(g, s.pack);
-  f.p.tiles = s.tiles;
   f.p.q_blocks = (int)s.q_blocks;
   f.p.splits = s.splits;
   f.o = g.o;
@@ -399,9 +435,9 @@ int launch(const AttentionArgs& g, const Shape& s, cudaStream_t st) {
   if (!query_map(&q, d, g.q, d.q_stride, s.pack) || !key_map(&k, d, d.k_tokens ? g.k : g.q, d.k_tokens ? d.k_stride : d.q_stride) ||
       !key_map(&v, d, d.k_tokens ? g.v : g.q, d.k_tokens ? d.v_stride : d.q_stride))
     return CBR_ERR_CUDA;
-  const auto kern = &forward_kernel<kDim, BF16>;
+  const auto kern = &forward_kernel<kDim, kTiles, BF16>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), 227 * 1024)) return CBR_ERR_CUDA;
-  kern<<<dim3((unsigned)(s.q_blocks * s.packs * d.batch), s.splits), kThreads, Smem<kDim>::kTotal, st>>>(q, k, v, f);
+  kern<<<dim3((unsigned)(s.q_blocks * s.packs * d.batch), s.splits), Form<kTiles>::kThreads, Smem<kDim, kTiles>::kTotal, st>>>(q, k, v, f);
   if (s.splits > 1) join_kernel<BF16><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(f, rows);
   return cudaGetLastError() == cudaSuccess ? CBR_OK : CBR_ERR_CUDA;
 }
@@ -416,9 +452,14 @@ size_t attention_forward_ws(const cbr_attention_desc_t& d) {
 
 int launch_attention(const AttentionArgs& a, cudaStream_t st) {
   const att::Shape s = att::shape_of(a.d, a.d.q_stride[2] != 0);
-  const bool bf16 = a.d.dtype == CBR_BF16;
-  if (a.d.head_dim > 64) return bf16 ? att::launch<128, true>(a, s, st) : att::launch<128, false>(a, s, st);
-  return bf16 ? att::launch<64, true>(a, s, st) : att::launch<64, false>(a, s, st);
+  auto by_type = [&](auto dim, auto tiles) {
+    constexpr int kDim = decltype(dim)::value, kTiles = decltype(tiles)::value;
+    return a.d.dtype == CBR_BF16 ? att::launch<kDim, kTiles, true>(a, s, st) : att::launch<kDim, kTiles, false>(a, s, st);
+  };
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  if (a.d.head_dim > 64) return s.tiles == 2 ? by_type(std::integral_constant<int, 128>{}, Two{}) : by_type(std::integral_constant<int, 128>{}, One{});
+  return s.tiles == 2 ? by_type(std::integral_constant<int, 64>{}, Two{}) : by_type(std::integral_constant<int, 64>{}, One{});
 }
 
 }  // namespace cbr
