@@ -1,9 +1,9 @@
 // Attention backward (declared in include/cbr.h) on the tensor cores: the probabilities are computed again.
 //
-// Three launches.  prepare_kernel takes D_i = do_i . o_i and the exponents' offsets.  query_kernel holds a tile
-// of 128 queries and walks over the keys: S = Q K^T, dP = dO V^T, dQ += dS K.  key_kernel holds a tile of 128
-// keys and walks over the queries of all heads that read it: S' = K Q^T, dP' = V dO^T, dV += P' dO,
-// dK += dS' Q.  Scores and dP are taken twice (seven products instead of five), and in return every sum
+// Two launches.  prepare_kernel takes D_i = do_i . o_i and the exponents' offsets.  backward_kernel has blocks of two
+// kinds.  One holds a tile of 128 queries and walks over the keys: S = Q K^T, dP = dO V^T, dQ += dS K.  The other
+// holds a tile of 128 keys and walks over the queries of all heads that read it: S' = K Q^T, dP' = V dO^T,
+// dV += P' dO, dK += dS' Q.  Scores and dP are taken twice (seven products instead of five), and in return every sum
 // stays in TMEM to its end, in a fixed order: no atomics, no sums in memory.
 //   P and dS go from registers over their scores in TMEM and enter the second products from there.  Both tiles'
 // elements are shared by two warpgroups: a thread has a row and 64 of its 128 columns.
@@ -31,16 +31,24 @@ struct Form {
   static constexpr uint32_t kColumns = 4 * kN;  // of TMEM, in quarters
 };
 
+// Where a kind of block puts its results.
+struct Results {
+  void* out[2];
+  int64_t stride[2][3];
+  float* part;            // splits > 1: [split][out][rows of the outputs][head_dim]
+  int64_t part_rows;
+  int32_t splits;
+  int32_t blocks;         // of one split
+};
+
 struct BackwardParams {
   Params p;
   const float* offset;    // [batch * packs][rows]: shift - lse log2(e) of a row, -infinity where p is 0
   const float* delta;     // the same of -D
   const uint32_t* norms;  // f16: [batch][heads_k][2] bits of the largest |do|^2 and |v|^2
   int64_t rows;           // of a pack of heads, a multiple of 128
-  void* out[2];           // dq; or dv, dk
-  int64_t stride[2][3];
-  float* part;            // splits > 1: [split][out][rows of the outputs][head_dim]
-  int64_t part_rows;
+  int64_t batch;
+  Results queries, keys;  // dq; dv, dk
 };
 
 template <bool BF16>
@@ -197,7 +205,7 @@ __device__ __forceinline__ void store32(uint32_t taddr, int col, int dim, bool a
   }
 }
 
-__device__ __forceinline__ uint8_t* row_of(const BackwardParams& f, int which, int64_t batch, int64_t token, int64_t head) {
+__device__ __forceinline__ uint8_t* row_of(const Results& f, int which, int64_t batch, int64_t token, int64_t head) {
   return static_cast<uint8_t*>(f.out[which]) + 2 * (batch * f.stride[which][0] + token * f.stride[which][1] + head * f.stride[which][2]);
 }
 
@@ -214,10 +222,8 @@ struct QuerySmem {
 
 // TMEM by quarters: dQ, S in two buffers (dS over them), dP.
 template <int kDim, bool BF16>
-__global__ void __launch_bounds__(Form<kDim>::kThreads, Form<kDim>::kBlocks)
-    query_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
-                 const __grid_constant__ BackwardParams f) {
+__device__ __forceinline__ void by_queries(const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v, const CUtensorMap& map_do,
+                                           const BackwardParams& f, const Results& out, const int index, const int split) {
   using L = QuerySmem<kDim>;
   using F = Form<kDim>;
   constexpr int kN = F::kN;
@@ -233,14 +239,14 @@ __global__ void __launch_bounds__(Form<kDim>::kThreads, Form<kDim>::kBlocks)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   const int packs = a.heads_q / a.pack;
-  const int head = blockIdx.x % packs, batch = blockIdx.x / packs % (gridDim.x / packs / a.q_blocks);
-  const int block = a.q_blocks - 1 - blockIdx.x / (gridDim.x / a.q_blocks);   // the longest rows first
+  const int head = index % packs, batch = index / packs % (int)f.batch;
+  const int block = a.q_blocks - 1 - index / (packs * (int)f.batch);   // the longest rows first
   const int key_head = a.pack > 1 ? head : head / a.group;
   const int token0 = block * a.tile_tokens;
   const int keys = keys_of(a, batch), start = start_of(a, batch);
   const int see = a.causal ? min(keys, max(0, start + min(token0 + a.tile_tokens, a.q_tokens))) : keys;
-  const int tiles = (see + kN - 1) / kN, share = (tiles + a.splits - 1) / a.splits;
-  const int first = min(tiles, (int)blockIdx.y * share), n = min(tiles, first + share) - first;
+  const int tiles = (see + kN - 1) / kN, share = (tiles + out.splits - 1) / out.splits;
+  const int first = min(tiles, split * share), n = min(tiles, first + share) - first;
 
   if (threadIdx.x == 0) {
     for (uint32_t b = bar_q; b <= bar_drain; b += 8)
@@ -414,11 +420,11 @@ __global__ void __launch_bounds__(Form<kDim>::kThreads, Form<kDim>::kBlocks)
     if (bad) give_up(kErrWaitAccum);
     tc_fence_after();
     const int64_t out_row = ((int64_t)batch * a.heads_q + q_head) * a.q_tokens + token;
-    uint8_t* out = row_of(f, 0, batch, token, q_head);
-    float* part = a.splits > 1 ? f.part + (blockIdx.y * f.part_rows + out_row) * a.head_dim : nullptr;
+    uint8_t* to = row_of(out, 0, batch, token, q_head);
+    float* part = out.splits > 1 ? out.part + (split * out.part_rows + out_row) * a.head_dim : nullptr;
 #pragma unroll 1
     for (int i = half * 64; i < (half + 1) * 64; i += 32)
-      store32<BF16>(trow, i, a.head_dim, n > 0 && !bad, true, live, a.scale / sc, out, part);
+      store32<BF16>(trow, i, a.head_dim, n > 0 && !bad, true, live, a.scale / sc, to, part);
     tc_fence_before();
   }
   __syncthreads();
@@ -439,10 +445,8 @@ struct KeySmem {
 
 // Rows are keys here, columns queries.  TMEM by quarters: dV, dK, S (P over it), dP (dS over it).
 template <int kDim, bool BF16>
-__global__ void __launch_bounds__(Form<kDim>::kThreads, Form<kDim>::kBlocks)
-    key_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-               const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
-               const __grid_constant__ BackwardParams f) {
+__device__ __forceinline__ void by_keys(const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v, const CUtensorMap& map_do,
+                                        const BackwardParams& f, const Results& out, const int index, const int split) {
   using L = KeySmem<kDim>;
   using F = Form<kDim>;
   constexpr int kN = F::kN;
@@ -457,16 +461,15 @@ __global__ void __launch_bounds__(Form<kDim>::kThreads, Form<kDim>::kBlocks)
   const Params& a = f.p;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const int key_tiles = (a.k_tokens + kTile - 1) / kTile;
-  const int key_head = blockIdx.x % a.heads_k, batch = blockIdx.x / a.heads_k % (gridDim.x / a.heads_k / key_tiles);
-  const int tile = blockIdx.x / (gridDim.x / key_tiles);   // causal: the first keys have the most queries, and come first
+  const int key_head = index % a.heads_k, batch = index / a.heads_k % (int)f.batch;
+  const int tile = index / (a.heads_k * (int)f.batch);   // causal: the first keys have the most queries, and come first
   const int key0 = tile * kTile, keys = keys_of(a, batch), start = start_of(a, batch);
   // tiles of queries: those from the first that sees one of the keys, of every pack of heads that reads them
   const int q_tiles = (int)(f.rows / kN);
   const int q_first = a.causal ? (int)min((int64_t)q_tiles, (int64_t)min(max(0, key0 - start), a.q_tokens) * a.pack / kN) : 0;
   const int each = key0 < keys ? q_tiles - q_first : 0, all = each * (a.group / a.pack);
-  const int share = (all + a.splits - 1) / a.splits;
-  const int first = min(all, (int)blockIdx.y * share), n = min(all, first + share) - first;
+  const int share = (all + out.splits - 1) / out.splits;
+  const int first = min(all, split * share), n = min(all, first + share) - first;
   const int head0 = a.pack > 1 ? key_head : key_head * a.group;   // the first pack of heads
 
   if (threadIdx.x == 0) {
@@ -652,13 +655,13 @@ __global__ void __launch_bounds__(Form<kDim>::kThreads, Form<kDim>::kBlocks)
     // with two warpgroups the first stores dV, the second dK
 #pragma unroll 1
     for (int which = half; which < 2; which += F::kHalves) {
-      uint8_t* out = row_of(f, which, batch, key, key_head);
+      uint8_t* to = row_of(out, which, batch, key, key_head);
       const int64_t out_row = ((int64_t)batch * a.heads_k + key_head) * a.k_tokens + key;
-      float* part = a.splits > 1 ? f.part + ((2 * blockIdx.y + which) * f.part_rows + out_row) * a.head_dim : nullptr;
+      float* part = out.splits > 1 ? out.part + ((2 * split + which) * out.part_rows + out_row) * a.head_dim : nullptr;
       const float scale = which ? a.scale / sc : ex2(-kShift<BF16>);
 #pragma unroll 1
       for (int i = 0; i < kDim; i += 32)
-        store32<BF16>(trow + which * kN, i, a.head_dim, n > 0 && !bad, key < keys, key < a.k_tokens, scale, out, part);
+        store32<BF16>(trow + which * kN, i, a.head_dim, n > 0 && !bad, key < keys, key < a.k_tokens, scale, to, part);
     }
     tc_fence_before();
   }
@@ -666,13 +669,27 @@ __global__ void __launch_bounds__(Form<kDim>::kThreads, Form<kDim>::kBlocks)
   if (warp == F::kMmaWarp) tmem_dealloc(tmem, F::kColumns);
 }
 
+// Blocks of both kinds in one launch, so that neither's last ones leave SMs idle: those by keys, whose walks over several
+// heads' queries are the longest, come first.
+template <int kDim, bool BF16>
+__global__ void __launch_bounds__(Form<kDim>::kThreads, Form<kDim>::kBlocks)
+    backward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_do,
+                    const __grid_constant__ BackwardParams f) {
+  const int by_key = f.keys.blocks * f.keys.splits, i = (int)blockIdx.x - by_key;
+  if (i < 0)
+    by_keys<kDim, BF16>(map_q, map_k, map_v, map_do, f, f.keys, blockIdx.x % f.keys.blocks, blockIdx.x / f.keys.blocks);
+  else
+    by_queries<kDim, BF16>(map_q, map_k, map_v, map_do, f, f.queries, i % f.queries.blocks, i / f.queries.blocks);
+}
+
 // ---------------------------------------------------------------- parts
 
 // Parts added up in their order: a warp for each row of `outs` results of [batch][heads][tokens], four elements to a lane.
 template <bool BF16>
-__global__ void __launch_bounds__(128) sum_kernel(const __grid_constant__ BackwardParams f, int outs, int64_t heads, int64_t tokens) {
+__global__ void __launch_bounds__(128) sum_kernel(const __grid_constant__ Results f, int dim, int outs, int64_t heads, int64_t tokens) {
   const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, dim = f.p.head_dim;
+  const int lane = threadIdx.x & 31;
   if (at >= outs * f.part_rows) return;
   const int64_t which = at / f.part_rows, row = at % f.part_rows;
   using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
@@ -682,7 +699,7 @@ __global__ void __launch_bounds__(128) sum_kernel(const __grid_constant__ Backwa
   const int64_t step = outs * f.part_rows * dim / 4;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int s = 0; s < f.p.splits; ++s) {
+  for (int s = 0; s < f.splits; ++s) {
     const float4 u = part[s * step];
     v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
   }
@@ -694,7 +711,7 @@ __global__ void __launch_bounds__(128) sum_kernel(const __grid_constant__ Backwa
 struct Shape {
   int pack, query_splits, key_splits;
   int64_t packs, rows, q_blocks, key_tiles;
-  size_t offsets, norms, parts;   // bytes of the workspace's regions
+  size_t offsets, norms, q_parts, parts;   // bytes of the workspace's regions; q_parts is the first of the parts
 };
 
 // Heads that share a key head are packed into a tile of queries where they fill it evenly.  Where blocks leave
@@ -708,17 +725,19 @@ Shape shape_of(const cbr_attention_desc_t& d, bool may_pack) {
   s.rows = (d.q_tokens * s.pack + kTile - 1) / kTile * kTile;
   s.q_blocks = s.rows / kTile;
   s.key_tiles = (d.k_tokens + kTile - 1) / kTile;
-  auto splits = [&](int64_t blocks, int64_t walk) {
+  const int64_t blocks = s.q_blocks * s.packs * d.batch + s.key_tiles * d.heads_k * d.batch;
+  auto splits = [&](int64_t walk) {
     if (walk < 12 * step) return 1;   // the sum of the parts costs about as much as a few steps
     return (int)std::max<int64_t>(1, std::min<int64_t>(kSms * blocks_to_sm / std::max<int64_t>(blocks, 1), walk / step / 4));
   };
-  s.query_splits = splits(s.q_blocks * s.packs * d.batch, d.k_tokens);
-  s.key_splits = splits(s.key_tiles * d.heads_k * d.batch, s.rows * (group / s.pack));
+  s.query_splits = splits(d.k_tokens);
+  s.key_splits = splits(s.rows * (group / s.pack));
   s.offsets = (size_t)d.batch * s.packs * s.rows * 4;
   s.norms = align256((size_t)d.batch * d.heads_k * 8);
   const size_t q_part = s.query_splits > 1 ? (size_t)s.query_splits * d.batch * d.heads_q * d.q_tokens : 0;
   const size_t k_part = s.key_splits > 1 ? (size_t)s.key_splits * 2 * d.batch * d.heads_k * d.k_tokens : 0;
-  s.parts = std::max(q_part, k_part) * d.head_dim * 4;   // one after the other
+  s.q_parts = q_part * d.head_dim * 4;
+  s.parts = s.q_parts + k_part * d.head_dim * 4;
   return s;
 }
 
@@ -743,7 +762,7 @@ int launch(const AttentionArgs& g, cudaStream_t st) {
   f.delta = pre.delta;
   f.norms = pre.norms;
   f.rows = s.rows;
-  f.part = reinterpret_cast<float*>(ws + 2 * align256(s.offsets) + s.norms);
+  f.batch = d.batch;
   if (d.q_tokens && d.k_tokens) {
     pre.d_o = g.d_o;
     pre.o = g.o;
@@ -774,28 +793,20 @@ int launch(const AttentionArgs& g, cudaStream_t st) {
   if (!query_map(&q, e, pq, e.q_stride, s.pack, kN) || !query_map(&d_o, e, pdo, e.do_stride, s.pack, kN) ||
       !key_map(&k, e, pk, e.k_stride, kN) || !key_map(&v, e, pv, e.v_stride, kN))
     return CBR_ERR_CUDA;
-  const auto by_query = &query_kernel<kDim, BF16>;
-  const auto by_key = &key_kernel<kDim, BF16>;
-  if (!ensure_smem_attr(reinterpret_cast<const void*>(by_query), 227 * 1024) ||
-      !ensure_smem_attr(reinterpret_cast<const void*>(by_key), 227 * 1024))
-    return CBR_ERR_CUDA;
-  if (d.q_tokens) {
-    f.p.splits = s.query_splits;
-    f.out[0] = g.dq;
-    for (int i = 0; i < 3; ++i) f.stride[0][i] = d.dq_stride[i];
-    f.part_rows = d.batch * d.heads_q * d.q_tokens;
-    by_query<<<dim3((unsigned)(s.q_blocks * s.packs * d.batch), s.query_splits), kThreads, QuerySmem<kDim>::kTotal, st>>>(q, k, v, d_o, f);
-    if (s.query_splits > 1) sum_kernel<BF16><<<(unsigned)((f.part_rows + 3) / 4), 128, 0, st>>>(f, 1, d.heads_q, d.q_tokens);
-  }
-  if (d.k_tokens) {
-    f.p.splits = s.key_splits;
-    f.out[0] = g.dv;
-    f.out[1] = g.dk;
-    for (int i = 0; i < 3; ++i) f.stride[0][i] = d.dv_stride[i], f.stride[1][i] = d.dk_stride[i];
-    f.part_rows = d.batch * d.heads_k * d.k_tokens;
-    by_key<<<dim3((unsigned)(s.key_tiles * d.heads_k * d.batch), s.key_splits), kThreads, KeySmem<kDim>::kTotal, st>>>(q, k, v, d_o, f);
-    if (s.key_splits > 1) sum_kernel<BF16><<<(unsigned)((2 * f.part_rows + 3) / 4), 128, 0, st>>>(f, 2, d.heads_k, d.k_tokens);
-  }
+  uint8_t* parts = ws + 2 * align256(s.offsets) + s.norms;
+  f.queries = Results{{g.dq, nullptr}, {}, reinterpret_cast<float*>(parts), d.batch * d.heads_q * d.q_tokens, s.query_splits,
+                      (int)(s.q_blocks * s.packs * d.batch)};
+  f.keys = Results{{g.dv, g.dk}, {}, reinterpret_cast<float*>(parts + s.q_parts), d.batch * d.heads_k * d.k_tokens, s.key_splits,
+                   (int)(s.key_tiles * d.heads_k * d.batch)};
+  for (int i = 0; i < 3; ++i) f.queries.stride[0][i] = d.dq_stride[i], f.keys.stride[0][i] = d.dv_stride[i], f.keys.stride[1][i] = d.dk_stride[i];
+  const auto kern = &backward_kernel<kDim, BF16>;
+  if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), 227 * 1024)) return CBR_ERR_CUDA;
+  constexpr int kSmem = std::max(QuerySmem<kDim>::kTotal, KeySmem<kDim>::kTotal);
+  kern<<<(unsigned)(f.keys.blocks * f.keys.splits + f.queries.blocks * f.queries.splits), kThreads, kSmem, st>>>(q, k, v, d_o, f);
+  if (s.query_splits > 1)
+    sum_kernel<BF16><<<(unsigned)((f.queries.part_rows + 3) / 4), 128, 0, st>>>(f.queries, d.head_dim, 1, d.heads_q, d.q_tokens);
+  if (s.key_splits > 1)
+    sum_kernel<BF16><<<(unsigned)((2 * f.keys.part_rows + 3) / 4), 128, 0, st>>>(f.keys, d.head_dim, 2, d.heads_k, d.k_tokens);
   return cudaGetLastError() == cudaSuccess ? CBR_OK : CBR_ERR_CUDA;
 }
 

@@ -79,28 +79,31 @@ __device__ __forceinline__ Spot spot_of(const Table<N>& t, uint32_t tile) {
 struct Raw {
   uint4 v[kVectors];
 
+  // The vector at index e, counted from the 16-byte boundary `skip` elements before the tensor.
+  template <typename T>
+  static __device__ __forceinline__ uint4 vector(const T* base, int skip, int64_t size, int64_t e) {
+    constexpr int kPer = 16 / sizeof(T);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (e >= skip && e + kPer <= skip + size) {
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(base + e));
+    } else if (e + kPer > skip && e < skip + size) {
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        if (e + k < skip || e + k >= skip + size) continue;
+        if constexpr (sizeof(T) == 4) w[k] = *reinterpret_cast<const uint32_t*>(base + e + k);
+        else w[k / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(base + e + k) << (16 * (k & 1));
+      }
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return v;
+  }
   template <typename T>
   __device__ __forceinline__ void load(const void* grad, int64_t size, int64_t first) {
-    constexpr int kPer = 16 / sizeof(T);
     const int skip = (int)(reinterpret_cast<uintptr_t>(grad) & 15) / (int)sizeof(T);
     const T* base = static_cast<const T*>(grad) - skip;
 #pragma unroll
-    for (int i = 0; i < kVectors; ++i) {
-      const int64_t e = first + ((int64_t)i * kThreads + threadIdx.x) * kPer;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (e >= skip && e + kPer <= skip + size) {
-        asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w) : "l"(base + e));
-      } else if (e + kPer > skip && e < skip + size) {
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          if (e + k < skip || e + k >= skip + size) continue;
-          if constexpr (sizeof(T) == 4) w[k] = *reinterpret_cast<const uint32_t*>(base + e + k);
-          else w[k / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(base + e + k) << (16 * (k & 1));
-        }
-        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
+    for (int i = 0; i < kVectors; ++i) v[i] = vector<T>(base, skip, size, first + ((int64_t)i * kThreads + threadIdx.x) * (16 / sizeof(T)));
   }
   template <int N>
   __device__ __forceinline__ void load(const Table<N>& t, const Spot& s) {
@@ -139,35 +142,69 @@ struct Raw {
     }
     return s;
   }
-  // The scaled values to `out`, which lies as its gradient does (whole vectors) or not (single elements).
+  template <typename T>
+  static __device__ __forceinline__ uint4 scaled(const uint4& u, float scale) {
+    float f[16 / sizeof(T)];
+    values<T>(u, f);
+#pragma unroll
+    for (int k = 0; k < 16 / (int)sizeof(T); ++k) f[k] *= scale;
+    if constexpr (sizeof(T) == 4) {
+      return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else {
+      constexpr bool kBf16 = std::is_same_v<T, __nv_bfloat16>;
+      return make_uint4(pack2<kBf16>(f[0], f[1]), pack2<kBf16>(f[2], f[3]), pack2<kBf16>(f[4], f[5]), pack2<kBf16>(f[6], f[7]));
+    }
+  }
+  // 16 bytes to the tensor's elements from e on, one by one those that it has.
+  template <typename T>
+  static __device__ __forceinline__ void put(T* base, int skip, int64_t size, int64_t e, const uint4& u, int count = 16 / sizeof(T)) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 16 / (int)sizeof(T); ++k) {
+      if (k >= count || e + k < skip || e + k >= skip + size) continue;
+      if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(base)[e + k] = w[k];
+      else reinterpret_cast<uint16_t*>(base)[e + k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
+    }
+  }
+  // The scaled values to `out`.  Where its 16-byte boundaries are others than the gradient's, a thread's store is the end
+  // of its vector and the beginning of the next one's, which the next lane has (the last lane's is loaded again).
   template <typename T>
   __device__ __forceinline__ void store(float scale, const void* grad, void* out, int64_t size, int64_t first) const {
     constexpr int kPer = 16 / sizeof(T);
     const int skip = (int)(reinterpret_cast<uintptr_t>(grad) & 15) / (int)sizeof(T);
-    const bool alike = ((reinterpret_cast<uintptr_t>(grad) ^ reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+    const T* source = static_cast<const T*>(grad) - skip;
     T* base = static_cast<T*>(out) - skip;
+    const int off = (int)(reinterpret_cast<uintptr_t>(base) & 15);   // bytes
+    const int later = (16 - off) / (int)sizeof(T);                   // elements to the next boundary
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) {
       const int64_t e = first + ((int64_t)i * kThreads + threadIdx.x) * kPer;
-      if (e + kPer <= skip || e >= skip + size) continue;
-      float f[kPer];
-      values<T>(v[i], f);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) f[k] *= scale;
-      if (alike && e >= skip && e + kPer <= skip + size) {
-        uint4 u;
-        if constexpr (sizeof(T) == 4) {
-          u = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-        } else {
-          constexpr bool kBf16 = std::is_same_v<T, __nv_bfloat16>;
-          u = make_uint4(pack2<kBf16>(f[0], f[1]), pack2<kBf16>(f[2], f[3]), pack2<kBf16>(f[4], f[5]), pack2<kBf16>(f[6], f[7]));
-        }
-        st_global_v4(base + e, u);
-      } else {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-          if (e + k >= skip && e + k < skip + size) base[e + k] = from_f<T>(f[k]);
+      const uint4 u = scaled<T>(v[i], scale);
+      if (off == 0) {
+        if (e >= skip && e + kPer <= skip + size) st_global_v4(base + e, u);
+        else put<T>(base, skip, size, e, u);
+        continue;
       }
+      uint4 n;
+      n.x = __shfl_down_sync(0xffffffffu, u.x, 1);
+      n.y = __shfl_down_sync(0xffffffffu, u.y, 1);
+      n.z = __shfl_down_sync(0xffffffffu, u.z, 1);
+      n.w = __shfl_down_sync(0xffffffffu, u.w, 1);
+      if ((threadIdx.x & 31) == 31) n = scaled<T>(vector<T>(source, skip, size, e + kPer), scale);
+      // bytes [16 - off, 32 - off) of (u, n): whole words, then the rest of a word
+      uint32_t w[8] = {u.x, u.y, u.z, u.w, n.x, n.y, n.z, n.w};
+      const int words = (16 - off) >> 2, rest = ((16 - off) & 3) * 8;
+      if (words & 1)
+#pragma unroll
+        for (int k = 0; k < 7; ++k) w[k] = w[k + 1];
+      if (words & 2)
+#pragma unroll
+        for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+      const uint4 s = make_uint4(__funnelshift_r(w[0], w[1], rest), __funnelshift_r(w[1], w[2], rest), __funnelshift_r(w[2], w[3], rest),
+                                 __funnelshift_r(w[3], w[4], rest));
+      if (e == 0) put<T>(base, skip, size, 0, u, later);   // what lies before the first boundary
+      if (e + later >= skip && e + later + kPer <= skip + size) st_global_v4(base + e + later, s);
+      else put<T>(base, skip, size, e + later, s);
     }
   }
 };

@@ -61,8 +61,8 @@ def _run(grads, outs, max_norm, unscale, ws, out):
         out_at = _addresses(outs, dev, "outs")
         if list(map(_dtype_of, outs)) != dtypes or array("q", map(_T.numel, outs)) != sizes:
             _bad("an out has to have its gradient's type and number of elements")
-    norm = _given(out, "norm", (1,), torch.float32, dev)
-    scale = _given(out, "scale", (1,), torch.float32, dev)
+    norm = _given(out, "norm", (), torch.float32, dev)
+    scale = _given(out, "scale", (), torch.float32, dev)
     if ws is None:
         ws = _new((clip_workspace_size(n),), torch.uint8, dev)
     elif ws.device != dev or not ws.is_contiguous():
@@ -72,7 +72,7 @@ def _run(grads, outs, max_norm, unscale, ws, out):
         out_at.buffer_info()[0] if outs is not None else None, max_norm, unscale, _vector(norm, 1, dev, "norm"),
         _vector(scale, 1, dev, "scale"), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev)),
         "cbr_clip_gradients")
-    return norm.view(()), scale.view(())
+    return norm, scale
 
 
 _sizes: dict = {}   # clip_workspace_size's answers

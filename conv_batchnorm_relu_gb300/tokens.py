@@ -104,8 +104,10 @@ _empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None
 
 def _new(shape, dtype, dev) -> torch.Tensor:
     """A new contiguous tensor on the current device."""
-    if _empty_cuda is None or not shape:
+    if _empty_cuda is None:
         return torch.empty(shape, dtype=dtype, device=dev)
+    if not shape:
+        return _empty_cuda((), (), dtype)
     strides = [1]
     for n in shape[:0:-1]:
         strides.append(strides[-1] * (n or 1))
