@@ -974,85 +974,163 @@ __global__ void __launch_bounds__(kThreads, kResident<1 + kBack>) stream_kernel(
 
 // ---------------------------------------------------------------- more channels than a block has columns for
 
-// Pixels of more than 256 vectors (2048 channels; less where they do not divide into vectors): a block for each group of
-// an image, which reads it three times (backward: twice).
-__device__ float block_sum(float v) {
-  __shared__ float part[kThreads / 32];
-  v = warp_reduce<Sum>(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.f;
-  for (int i = 0; i < kThreads / 32; ++i) s += part[i];
-  return s;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads) wide_forward_kernel(const __grid_constant__ Params a) {
-  const int64_t image = blockIdx.x / a.groups, count = a.pixels * a.per;
-  const int c0 = blockIdx.x % a.groups * a.per;
-  const T* x = static_cast<const T*>(a.x) + image * a.x_stride[0] + c0;
-  T* y = static_cast<T*>(a.y) + image * a.y_stride[0] + c0;
-  const float ref = to_f(x[0]);
-  float s = 0.f, q = 0.f;
-  for (int64_t i = threadIdx.x; i < count; i += kThreads) s += to_f(x[i / a.per * a.x_stride[1] + i % a.per]) - ref;
-  const float mean = ref + block_sum(s) / (float)count;
-  for (int64_t i = threadIdx.x; i < count; i += kThreads) {
-    const float d = to_f(x[i / a.per * a.x_stride[1] + i % a.per]) - mean;
-    q = fmaf(d, d, q);
-  }
-  const float rstd = rstd_of(block_sum(q), (float)count, a.eps);
-  if (threadIdx.x == 0) a.mean[blockIdx.x] = mean, a.rstd[blockIdx.x] = rstd;
-  by_act(a.act, [&](auto act) {
-    for (int64_t i = threadIdx.x; i < count; i += kThreads) {
-      const int c = (int)(i % a.per);
-      const float scale = a.gamma ? rstd * a.gamma[c0 + c] : rstd, shift = a.gamma ? a.beta[c0 + c] : 0.f;
-      const float z = fmaf(to_f(x[i / a.per * a.x_stride[1] + c]) - mean, scale, shift);
-      y[i / a.per * a.y_stride[1] + c] = from_f<T>(act_of<decltype(act)::value>(z));
+// Pixels of more than 256 vectors (2048 channels of 16 bits; 256 where they do not divide into vectors): moments (sums) of
+// every channel of every run, [image][run][2][channels]; the images' groups from them; the results, which read x again.
+template <typename T, int kVec, bool kBack>
+__global__ void __launch_bounds__(kThreads) wide_sums_kernel(const __grid_constant__ Params a) {
+  using V = Vec<T, kVec>;
+  const int run = blockIdx.x % a.runs, n = run_length(a, run);
+  const int64_t image = blockIdx.x / a.runs, begin = run_begin(a, run);
+  float* part = a.part + 2 * (int64_t)blockIdx.x * a.channels;
+  for (int col = threadIdx.x; col < a.channels / kVec; col += kThreads) {
+    const T* x = static_cast<const T*>(a.x) + image * a.x_stride[0] + begin * a.x_stride[1] + (int64_t)col * kVec;
+    const T* dy = kBack ? static_cast<const T*>(a.dy) + image * a.dy_stride[0] + begin * a.dy_stride[1] + (int64_t)col * kVec : nullptr;
+    float2 mean[V::kPairs], scale[V::kPairs], shift[V::kPairs], s[V::kPairs], q[V::kPairs];
+    [[maybe_unused]] float rstd[kVec];
+    V v;
+    [[maybe_unused]] V u;
+    v.load(reinterpret_cast<const uint8_t*>(x));
+    v.get(mean);   // forward: the first value
+#pragma unroll
+    for (int i = 0; i < V::kPairs; ++i) s[i] = q[i] = make_float2(0.f, 0.f);
+    if constexpr (kBack) {
+      float m[2 * V::kPairs] = {}, c[2 * V::kPairs] = {}, h[2 * V::kPairs] = {};
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const int64_t ch = col * kVec + i, g = image * a.groups + ch / a.per;
+        m[i] = a.mean[g];
+        rstd[i] = a.rstd[g];
+        c[i] = a.gamma ? rstd[i] * a.gamma[ch] : rstd[i];
+        h[i] = a.gamma ? a.beta[ch] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < V::kPairs; ++i)
+        mean[i] = make_float2(m[2 * i], m[2 * i + 1]), scale[i] = make_float2(c[2 * i], c[2 * i + 1]), shift[i] = make_float2(h[2 * i], h[2 * i + 1]);
     }
-  });
+    by_act(a.act, [&](auto act) {
+#pragma unroll 4
+      for (int p = 0; p < n; ++p) {
+        float2 f[V::kPairs];
+        [[maybe_unused]] float2 up[V::kPairs];
+        v.load(reinterpret_cast<const uint8_t*>(x + p * a.x_stride[1]));
+        v.get(f);
+        if constexpr (kBack) {
+          u.load(reinterpret_cast<const uint8_t*>(dy + p * a.dy_stride[1]));
+          u.get(up);
+        }
+#pragma unroll
+        for (int i = 0; i < V::kPairs; ++i) {
+          const float2 d = sub(f[i], mean[i]);
+          float2 g = d;
+          if constexpr (kBack) {
+            const float2 z = fma(d, scale[i], shift[i]);
+            g = make_float2(act_slope<decltype(act)::value>(z.x, up[i].x), act_slope<decltype(act)::value>(z.y, up[i].y));
+          }
+          s[i] = add(s[i], g);
+          q[i] = fma(g, d, q[i]);
+        }
+      }
+    });
+    const float inv = 1.f / (float)n;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const float si = i & 1 ? s[i / 2].y : s[i / 2].x, qi = i & 1 ? q[i / 2].y : q[i / 2].x;
+      const int c = col * kVec + i;
+      part[c] = kBack ? qi * rstd[i] : (i & 1 ? mean[i / 2].y : mean[i / 2].x) + si * inv;
+      part[a.channels + c] = kBack ? si : qi - si * (si * inv);
+    }
+  }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) wide_backward_kernel(const __grid_constant__ Params a) {
+// A block for each group of an image.
+template <bool kBack>
+__global__ void __launch_bounds__(kThreads) wide_merge_kernel(const __grid_constant__ Params a, float* means) {
+  __shared__ float3 sets[kThreads / 32];
   const int64_t image = blockIdx.x / a.groups;
   const int c0 = blockIdx.x % a.groups * a.per;
-  const T* x = static_cast<const T*>(a.x) + image * a.x_stride[0] + c0;
-  const T* dy = static_cast<const T*>(a.dy) + image * a.dy_stride[0] + c0;
-  T* dx = static_cast<T*>(a.y) + image * a.y_stride[0] + c0;
-  const float mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
-  by_act(a.act, [&](auto act) {
-    float scale = 0.f, d = 0.f;
-    auto slope = [&](int64_t p, int c) {
-      scale = a.gamma ? rstd * a.gamma[c0 + c] : rstd;
-      d = to_f(x[p * a.x_stride[1] + c]) - mean;
-      return act_slope<decltype(act)::value>(fmaf(d, scale, a.gamma ? a.beta[c0 + c] : 0.f), to_f(dy[p * a.dy_stride[1] + c]));
-    };
-    float u = 0.f, ux = 0.f;
-    for (int c = 0; c < a.per; ++c) {
-      float s = 0.f, sx = 0.f;
-      for (int64_t p = threadIdx.x; p < a.pixels; p += kThreads) {
-        const float g = slope(p, c);
-        s += g;
-        sx = fmaf(g, d, sx);
-      }
-      s = block_sum(s);
-      sx = block_sum(sx) * rstd;
-      const float w = a.gamma ? a.gamma[c0 + c] : 1.f;
-      u = fmaf(w, s, u);
-      ux = fmaf(w, sx, ux);
-      if (a.gamma && threadIdx.x == 0) {
-        a.part[2 * image * a.channels + c0 + c] = sx;
-        a.part[(2 * image + 1) * a.channels + c0 + c] = s;
+  const float total = (float)a.pixels * (float)a.per;
+  float n = 0.f, s = 0.f, q = 0.f;
+  for (int r = 0; r < a.runs; ++r) {
+    const float* part = a.part + 2 * (image * a.runs + r) * a.channels + c0;
+    for (int c = threadIdx.x; c < a.per; c += kThreads) {
+      const float first = part[c], second = part[a.channels + c];
+      if constexpr (kBack) {
+        const float w = a.gamma ? a.gamma[c0 + c] : 1.f;
+        s = fmaf(w, second, s);
+        q = fmaf(w, first, q);
+      } else {
+        merge_moments(n, s, q, (float)run_length(a, r), first, second);
       }
     }
-    const float inv = 1.f / ((float)a.pixels * (float)a.per), m = -rstd * (u * inv), mx = -rstd * rstd * (ux * inv);
-    for (int64_t i = threadIdx.x; i < a.pixels * a.per; i += kThreads) {
-      const int c = (int)(i % a.per);
-      const float g = slope(i / a.per, c);
-      dx[i / a.per * a.y_stride[1] + c] = from_f<T>(fmaf(g, scale, fmaf(d, mx, m)));
+  }
+  auto merge = [&](float n2, float s2, float q2) {
+    if constexpr (kBack) s += s2, q += q2;
+    else merge_moments(n, s, q, n2, s2, q2);
+  };
+  for (int o = 1; o < 32; o *= 2) {   // the lower lane's first; the first lane's is the warp's
+    const float n2 = __shfl_down_sync(0xffffffffu, n, o), s2 = __shfl_down_sync(0xffffffffu, s, o), q2 = __shfl_down_sync(0xffffffffu, q, o);
+    merge(n2, s2, q2);
+  }
+  if ((threadIdx.x & 31) == 0) sets[threadIdx.x >> 5] = make_float3(n, s, q);
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int w = 1; w < kThreads / 32; ++w) merge(sets[w].x, sets[w].y, sets[w].z);
+  if constexpr (kBack) {
+    means[2 * image * a.groups + blockIdx.x % a.groups] = s / total;
+    means[(2 * image + 1) * a.groups + blockIdx.x % a.groups] = q / total;
+  } else {
+    a.mean[blockIdx.x] = s;
+    a.rstd[blockIdx.x] = rstd_of(q, total, a.eps);
+  }
+}
+
+template <typename T, int kVec, bool kBack>
+__global__ void __launch_bounds__(kThreads) wide_result_kernel(const __grid_constant__ Params a, const float* means) {
+  using V = Vec<T, kVec>;
+  const int run = blockIdx.x % a.runs, n = run_length(a, run);
+  const int64_t image = blockIdx.x / a.runs, begin = run_begin(a, run);
+  for (int col = threadIdx.x; col < a.channels / kVec; col += kThreads) {
+    const T* x = static_cast<const T*>(a.x) + image * a.x_stride[0] + begin * a.x_stride[1] + (int64_t)col * kVec;
+    const T* dy = kBack ? static_cast<const T*>(a.dy) + image * a.dy_stride[0] + begin * a.dy_stride[1] + (int64_t)col * kVec : nullptr;
+    T* y = static_cast<T*>(a.y) + image * a.y_stride[0] + begin * a.y_stride[1] + (int64_t)col * kVec;
+    float mean[2 * V::kPairs] = {}, scale[2 * V::kPairs] = {}, shift[2 * V::kPairs] = {}, m[2 * V::kPairs] = {}, mx[2 * V::kPairs] = {};
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int ch = col * kVec + i, group = ch / a.per;
+      const float rstd = a.rstd[image * a.groups + group];
+      mean[i] = a.mean[image * a.groups + group];
+      scale[i] = a.gamma ? rstd * a.gamma[ch] : rstd;
+      shift[i] = a.gamma ? a.beta[ch] : 0.f;
+      if constexpr (kBack) {
+        m[i] = -rstd * means[2 * image * a.groups + group];
+        mx[i] = -rstd * rstd * means[(2 * image + 1) * a.groups + group];
+      }
     }
-  });
+    by_act(a.act, [&](auto act) {
+#pragma unroll 4
+      for (int p = 0; p < n; ++p) {
+        V v;
+        [[maybe_unused]] V u;
+        float2 f[V::kPairs];
+        [[maybe_unused]] float2 up[V::kPairs];
+        v.load(reinterpret_cast<const uint8_t*>(x + p * a.x_stride[1]));
+        v.get(f);
+        if constexpr (kBack) {
+          u.load(reinterpret_cast<const uint8_t*>(dy + p * a.dy_stride[1]));
+          u.get(up);
+        }
+        auto of = [&](float value, float upper, int i) {
+          const float d = value - mean[i], z = fmaf(d, scale[i], shift[i]);
+          if constexpr (kBack) return fmaf(act_slope<decltype(act)::value>(z, upper), scale[i], fmaf(d, mx[i], m[i]));
+          else return act_of<decltype(act)::value>(z);
+        };
+#pragma unroll
+        for (int i = 0; i < V::kPairs; ++i) f[i] = make_float2(of(f[i].x, kBack ? up[i].x : 0.f, 2 * i), of(f[i].y, kBack ? up[i].y : 0.f, 2 * i + 1));
+        v.set(f);
+        v.store(reinterpret_cast<uint8_t*>(y + p * a.y_stride[1]));
+      }
+    });
+  }
 }
 
 // dgamma and dbeta: `rows` rows of [dgamma's channels][dbeta's], added up by 32 rows of threads that take turns, then
@@ -1094,10 +1172,18 @@ int64_t table_bytes(const cbr_group_norm_desc_t& d) {
   return shared_bytes(kThreads * (d.dtype == CBR_F32 ? 4 : 8), d.channels, d.groups);
 }
 
+// Runs of an image whose channels are more than a block's columns, and the floats of their moments and means.
+int64_t wide_runs(const cbr_group_norm_desc_t& d) {
+  return std::max<int64_t>(1, std::min<int64_t>(d.pixels, (4 * kSms + d.images - 1) / std::max<int64_t>(d.images, 1)));
+}
+size_t wide_floats(const cbr_group_norm_desc_t& d) {
+  return d.channels > kThreads ? (size_t)d.images * 2 * ((size_t)wide_runs(d) * d.channels + d.groups) : 0;
+}
+
 Plan plan_of(const cbr_group_norm_desc_t& d, bool backward) {
   Plan p{};
   if (d.channels > kThreads * (d.dtype == CBR_F32 ? 4 : 8)) {
-    p.cluster = true;   // by groups
+    p.cluster = true;   // not used: see wide_runs()
     p.runs = p.slices = 1;
     return p;
   }
@@ -1120,9 +1206,11 @@ Plan plan_of(const cbr_group_norm_desc_t& d, bool backward) {
     }
     break;   // fewer slices are larger yet
   }
-  // What fits the shared memory of all SMs at once goes to clusters.
+  // Images that a cluster holds go to clusters (256 of 56x56x64 f16 forward: 58 us, as a stream 76); the backward of many that
+  // take wide ones goes as well as a stream (256 of 56x56x64 f16, nine blocks each: 108.7 and 107.7 us; 256 of 28x28x256: 117
+  // and 108).
   int64_t need = std::max<int64_t>(1, (image + room - 1) / room);
-  p.cluster = need <= kMaxCluster && images * need <= 2 * kSms && (d.pixels + need - 1) / need * pixel <= room;
+  p.cluster = need <= kMaxCluster && (!backward || need <= 8 || images * need <= 8 * kSms) && (d.pixels + need - 1) / need * pixel <= room;
   if (p.cluster) {
     // more blocks while SMs are without one, and a run keeps a few KB
     while (2 * need <= kMaxCluster && images * need <= kSms && image / (2 * need) >= 4096) need *= 2;
@@ -1130,9 +1218,10 @@ Plan plan_of(const cbr_group_norm_desc_t& d, bool backward) {
     return p;
   }
   // Runs of 192 KB, whose reading a run's fixed cost (the merges, a few us) is small beside; shorter ones where that
-  // leaves blocks without a few tasks each.
+  // leaves blocks without one (32 of 112x112x64 f16: forward in four runs a block 57 us, in one 36; backward in four
+  // and two 66 and 61).
   const int64_t blocks = kSms * (backward ? kResident<2> : kResident<1>);
-  const int64_t run = std::min(kRunBytes, std::max(kShortRun, image * images / (2 * kSms * 4)));
+  const int64_t run = std::min(kRunBytes, std::max(kShortRun, image * images / ((backward ? 4 : 2) * kSms)));
   p.runs = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(d.pixels, kMostRuns), (image + run - 1) / run));
   // a result is this many images behind: the tasks between are at least those in flight
   p.lag = std::min<int64_t>(images, (blocks + 2 * p.runs - 1) / (2 * p.runs) + 1);
@@ -1190,10 +1279,23 @@ int launch(const GroupNormArgs& g, bool backward, cudaStream_t st) {
   const int64_t longest = (d.pixels + plan.runs - 1) / plan.runs;
   int64_t rows = d.images;
   if (d.channels / kVec > kThreads) {
-    const auto kern = backward ? &wide_backward_kernel<T> : &wide_forward_kernel<T>;
     a.channels = d.channels;
     a.groups = d.groups;
-    kern<<<(unsigned)(d.images * d.groups), kThreads, 0, st>>>(a);
+    a.runs = (int)wide_runs(d);
+    a.base = d.pixels / a.runs;
+    a.extra = (int)(d.pixels % a.runs);
+    rows = d.images * a.runs;
+    float* means = a.part + 2 * rows * d.channels;
+    const unsigned blocks = (unsigned)rows, groups = (unsigned)(d.images * d.groups);
+    if (backward) {
+      wide_sums_kernel<T, kVec, true><<<blocks, kThreads, 0, st>>>(a);
+      wide_merge_kernel<true><<<groups, kThreads, 0, st>>>(a, means);
+      wide_result_kernel<T, kVec, true><<<blocks, kThreads, 0, st>>>(a, means);
+    } else {
+      wide_sums_kernel<T, kVec, false><<<blocks, kThreads, 0, st>>>(a);
+      wide_merge_kernel<false><<<groups, kThreads, 0, st>>>(a, means);
+      wide_result_kernel<T, kVec, false><<<blocks, kThreads, 0, st>>>(a, means);
+    }
   } else if (plan.cluster) {
     a.keep = (int)longest;
     const auto kern = backward ? &cluster_backward_kernel<T, kVec> : &cluster_forward_kernel<T, kVec>;
@@ -1279,15 +1381,13 @@ int dispatch(const GroupNormArgs& g, bool backward, cudaStream_t st) {
 
 size_t group_norm_forward_floats(const cbr_group_norm_desc_t& d) {
   const gn::Plan p = gn::plan_of(d, false);
-  return p.cluster ? 0 : (size_t)d.images * (2 * (size_t)p.runs * d.groups + 2);
+  return std::max(gn::wide_floats(d), p.cluster ? 0 : (size_t)d.images * (2 * (size_t)p.runs * d.groups + 2));
 }
 size_t group_norm_backward_floats(const cbr_group_norm_desc_t& d, bool parameters) {
   const gn::Plan p = gn::plan_of(d, true);
-  // by images: clusters, and what goes by groups for its many channels
-  const size_t by_image = parameters ? (size_t)d.images * 2 * d.channels : 0;
-  if (p.cluster) return by_image;
+  const size_t cluster = parameters ? (size_t)d.images * 2 * d.channels : 0;
   const size_t stream = (size_t)d.images * (2 * ((size_t)p.runs + 1) * d.groups + 2) + 2 * (size_t)gn::kStreamBlocks * d.channels;
-  return std::max(stream, d.channels > gn::kThreads ? by_image : 0);
+  return std::max(gn::wide_floats(d), p.cluster ? cluster : stream);
 }
 int launch_group_norm(const GroupNormArgs& a, cudaStream_t st) { return gn::dispatch(a, false, st); }
 int launch_group_norm_backward(const GroupNormArgs& a, cudaStream_t st) { return gn::dispatch(a, true, st); }

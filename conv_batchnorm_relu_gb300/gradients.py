@@ -37,7 +37,7 @@ _dtype_of = _T.dtype.__get__
 
 
 def _addresses(tensors, dev, what: str) -> array:
-    if not all(map(_T.is_contiguous, tensors)) or any(map(dev.index.__ne__, map(_T.get_device, tensors))):
+    if set(map(_T.get_device, tensors)) != {dev.index} or not all(map(_T.is_contiguous, tensors)):
         _bad(f"{what} have to be contiguous on {dev}")
     return array("Q", map(_T.data_ptr, tensors))
 
@@ -51,7 +51,7 @@ def _run(grads, outs, max_norm, unscale, ws, out):
     at = _addresses(grads, dev, "gradients")
     dtypes, sizes = list(map(_dtype_of, grads)), array("q", map(_T.numel, grads))
     try:
-        types = array("i", map(_DTYPE.__getitem__, dtypes))
+        types = array("i", [_DTYPE[dtypes[0]]]) * n if dtypes.count(dtypes[0]) == n else array("i", map(_DTYPE.__getitem__, dtypes))
     except KeyError as e:
         _bad(f"gradients: {e}", _UNSUPPORTED)
     out_at = at

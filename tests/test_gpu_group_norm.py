@@ -62,6 +62,12 @@ def test_images_that_no_block_holds(shape, groups, act, dtype):
     check(make(shape, dtype, seed=3), groups, act)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape,groups,act", [((2, 9, 11, 333), 1, "silu"), ((3, 5, 7, 2056), 4, "relu"), ((1, 60, 41, 1026), 3, "silu"), ((40, 2, 2, 515), 5, "none")])
+def test_more_channels_than_a_block_has_columns_for(shape, groups, act, dtype):
+    check(make(shape, dtype, seed=14), groups, act)
+
+
 @pytest.mark.parametrize("offset", [30.0, -1000.0])
 def test_means_far_from_zero(offset):
     check(make((2, 28, 28, 64), "f32", 5, offset), 8, "none")
