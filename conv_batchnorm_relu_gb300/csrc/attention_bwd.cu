@@ -443,6 +443,12 @@ struct KeySmem {
   static constexpr int kBars = 1 + 8 + 4 + 2, kTotal = kBar + kBars * 8 + 16 + 1024;
 };
 
+__device__ __forceinline__ float4 ld_shared_v4(uint32_t from) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(from));
+  return v;
+}
+
 // Rows are keys here, columns queries.  TMEM by quarters: dV, dK, S (P over it), dP (dS over it).
 template <int kDim, bool BF16>
 __device__ __forceinline__ void by_keys(const CUtensorMap& map_q, const CUtensorMap& map_k, const CUtensorMap& map_v, const CUtensorMap& map_do,
@@ -594,8 +600,7 @@ __device__ __forceinline__ void by_keys(const CUtensorMap& map_q, const CUtensor
         hidden = (int)max((int64_t)0, min((int64_t)64, from));
       }
       const bool edge = __any_sync(0xffffffffu, hidden > 0);
-      const float4* offset = reinterpret_cast<const float4*>(smem + L::kRow + (j & 1) * L::kRowStep) + half * 16;
-      const float4* delta = offset + kN / 4;
+      const uint32_t offset = sbase + L::kRow + (j & 1) * L::kRowStep + half * 256, delta = offset + 4 * kN;
       bad = !__all_sync(0xffffffffu, mbar_wait(bar_qf + 8 * (j & 1), (j >> 1) & 1) && mbar_wait(bar_s, j & 1));
       if (bad) break;
       tc_fence_after();
@@ -606,7 +611,7 @@ __device__ __forceinline__ void by_keys(const CUtensorMap& map_q, const CUtensor
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float4 o = offset[i];   // negative
+        const float4 o = ld_shared_v4(offset + 16 * i);   // negative
         const uint64_t x = fma2(pair(r[4 * i], r[4 * i + 1]), c2, pair(o.x, o.y));
         const uint64_t y = fma2(pair(r[4 * i + 2], r[4 * i + 3]), c2, pair(o.z, o.w));
         p[4 * i] = ex2(low(x));
@@ -635,7 +640,7 @@ __device__ __forceinline__ void by_keys(const CUtensorMap& map_q, const CUtensor
       tmem_ld_wait();
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float4 d = delta[i];   // negative
+        const float4 d = ld_shared_v4(delta + 16 * i);   // negative
         uint64_t x = add2(pair(r[4 * i], r[4 * i + 1]), pair(d.x, d.y)), y = add2(pair(r[4 * i + 2], r[4 * i + 3]), pair(d.z, d.w));
         if constexpr (!BF16) x = mul2(x, sc22), y = mul2(y, sc22);
         x = mul2(x, pair(p[4 * i], p[4 * i + 1]));
