@@ -1,4 +1,7 @@
 // C ABI of the trunk operators (declared in include/cbr.h): argument checks and dispatch.
+#include <algorithm>
+#include <vector>
+
 #include "api_checks.h"
 #include "cbr_internal.h"
 #include "token_ops.h"
@@ -56,6 +59,31 @@ bool map_strides(const cbr_group_norm_desc_t& d, const int64_t* s) {
     if (!extent(s[i]) || !in_reach(s[i], i ? d.pixels : d.images)) return false;
   const int64_t axes[3] = {s[0], s[1], 0};
   return distinct(axes, d.images, d.pixels, 1, d.channels);
+}
+
+// Whether an out shares memory with another out or with a gradient that is not its own: which of the two a block would
+// read or write last is chance.  (Gradients that are only read may share theirs.)
+bool outs_overlap(int64_t count, const void* const* grads, const int64_t* sizes, const int32_t* dtypes, void* const* outs) {
+  struct Range {
+    uintptr_t begin, end;
+    bool out;
+  };
+  std::vector<Range> r;
+  r.reserve(2 * count);
+  for (int64_t i = 0; i < count; ++i) {
+    if (!sizes[i]) continue;
+    const uintptr_t bytes = (uintptr_t)sizes[i] * elt(dtypes[i]), g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(outs[i]);
+    r.push_back({o, o + bytes, true});
+    if (g != o) r.push_back({g, g + bytes, false});
+  }
+  std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  uintptr_t any = 0, out = 0;   // the furthest ends so far
+  for (const Range& x : r) {
+    if (x.begin < (x.out ? any : out)) return true;
+    any = std::max(any, x.end);
+    if (x.out) out = std::max(out, x.end);
+  }
+  return false;
 }
 
 bool same_map(const cbr_group_norm_desc_t& d, const int64_t* a, const int64_t* b) {
@@ -268,6 +296,7 @@ cbr_status_t cbr_clip_gradients(int64_t count, const void* const* grads, const i
       if (off(grads[i], elt(dtypes[i])) || (outs && off(outs[i], elt(dtypes[i])))) return CBR_ERR_MISALIGNED;
     }
     if (off(norm, 4) || off(scale, 4) || off(ws, 16)) return CBR_ERR_MISALIGNED;
+    if (outs && outs_overlap(count, grads, sizes, dtypes, outs)) return CBR_ERR_INVALID_ARG;
     if (ws_bytes < clip_part_doubles(count) * sizeof(double)) return CBR_ERR_WORKSPACE;
     ClipArgs a{count, grads, sizes, dtypes, outs, max_norm, unscale, norm, scale, static_cast<double*>(ws), 0};
     uint32_t* err = nullptr;

@@ -99,7 +99,8 @@ def clip_gradients(grads, max_norm, *, unscale=1.0, ws=None, out=None, scalars=N
         norm = unscale * sqrt(sum of all squares),  scale = unscale * min(1, max_norm / norm)
 
     grads: contiguous tensors (f32, f16, bf16 in any mixture).  unscale takes a loss scale off.  out: tensors
-    of the same sizes and types to write instead of the gradients.  scalars: {"norm": ..., "scale": ...} to
+    of the same sizes and types to write instead of the gradients.  A tensor that is written may not share memory with
+    another (the same gradient twice, for one).  scalars: {"norm": ..., "scale": ...} to
     write.  ws: a workspace of :func:`clip_workspace_size` bytes to use instead of a new one.  An infinite
     gradient makes the scale 0, a NaN makes it NaN; a step that is to be skipped then can look at "norm"."""
     grads = list(grads)

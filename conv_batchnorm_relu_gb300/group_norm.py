@@ -65,11 +65,13 @@ def _floats(t: torch.Tensor | None, n: int, index: int, what: str):
     return t.data_ptr()
 
 
-def _shape(x: torch.Tensor, act: str):
+def _shape(x: torch.Tensor, groups: int, act: str):
     """(shape, pixels, channels, type, its code, device, activation's code) of a map."""
     shape, dt, index = x.shape, x.dtype, x.get_device()
     if len(shape) < 2 or index < 0:
         _bad("x has to be an [images][...][channels] CUDA tensor")
+    if groups < 1:
+        _bad(f"{groups} groups")
     if index != _get_device():
         _bad(f"tensors on {x.device}, which is not the current device", 5)
     code, what = _DTYPE.get(dt), _ACT.get(act)
@@ -133,7 +135,7 @@ def group_norm_forward(x, gamma, beta, groups, *, eps=1e-5, act="none", ws=None,
     and beta fp32 [channels], or both None; act "none", "relu" or "silu".  out may hold "y" (x itself, to save
     its memory), "mean" and "rstd".  ws: a workspace (:func:`group_norm_workspace_size`) to use instead of a new
     one."""
-    shape, pixels, channels, dt, code, index, act = _shape(x, act)
+    shape, pixels, channels, dt, code, index, act = _shape(x, groups, act)
     images, dev = shape[0], x.device
     sx = _map(x, shape, pixels, dt, index, "x")
     y = _given(out, "y", shape, dt, dev)
@@ -157,7 +159,7 @@ def group_norm_backward(dy, x, gamma, beta, mean, rstd, groups, *, act="none", w
 
     dy: the gradient at y; mean and rstd from :func:`group_norm_forward`; the rest as there.  out may hold "dx" (dy
     itself, to save its memory), "dgamma" and "dbeta".  ws: as there."""
-    shape, pixels, channels, dt, code, index, act = _shape(x, act)
+    shape, pixels, channels, dt, code, index, act = _shape(x, groups, act)
     images, dev = shape[0], x.device
     sx = _map(x, shape, pixels, dt, index, "x")
     sdy = _map(dy, shape, pixels, dt, index, "dy")
@@ -181,5 +183,5 @@ def group_norm_backward(dy, x, gamma, beta, mean, rstd, groups, *, act="none", w
 
 def group_norm_workspace_size(x, groups) -> tuple[int, int]:
     """Workspace bytes of (:func:`group_norm_forward`, :func:`group_norm_backward`) for a map of x's shape."""
-    shape, pixels, channels, _, code, _, _ = _shape(x, "none")
+    shape, pixels, channels, _, code, _, _ = _shape(x, groups, "none")
     return _bytes(shape[0], pixels, channels, groups, code)

@@ -591,7 +591,7 @@ cbr_status_t cbr_group_norm_backward(const cbr_group_norm_desc_t* desc, const vo
  * unscale (finite, > 0) takes a loss scale off.  grads, outs, sizes and dtypes are host arrays of `count` device
  * addresses, numbers of elements and types (f32, f16, bf16 in any mixture); the addresses are read before
  * the call returns.  Gradients are contiguous and aligned to their element; an out may be its gradient (it is
- * then not written where scale is 1) and may not overlap another gradient or out.  outs NULL: only norm
+ * then not written where scale is 1); one that overlaps another gradient or out is refused.  outs NULL: only norm
  * and scale (max_norm may be infinity).  norm and scale are fp32 scalars.  Squares are summed so that none
  * overflows or underflows: a norm past the range of fp32 reads as infinity, but scale goes by its value.  An
  * infinite gradient makes scale 0 (max_norm finite), a NaN makes norm and scale NaN; gradients are scaled

@@ -155,6 +155,17 @@ def test_clip_refusals(lib):
     assert lib.cbr_clip_workspace_size(-1, ctypes.byref(n)) == 1 and lib.cbr_clip_workspace_size(2, None) == 1
 
 
+def test_clip_refuses_outs_that_share_memory(lib):
+    a, b, c = P, P + 4096, P + 8192
+    ok, no = (5, 1) if not torch.cuda.is_available() else (None, 1)
+    for grads, outs, want in [((a, b), (a, b), ok), ((a, b), (c, c + 10), no), ((a, b), (c, c + 20), ok), ((a, a), (a, a), no), ((a, a), (b, c), ok),
+                              ((a, b), (b, a), no), ((a, b), (c, a + 16), no), ((a, b), (a + 4, b), no), ((a, b), (a, b + 4), no)]:
+        if want is not None:
+            assert clip(lib, grads=grads, outs=outs) == want, (grads, outs)      # 5 values of 2 bytes, 7 of 4
+    if ok is not None:
+        assert clip(lib, grads=(a, a), sizes=(0, 7), outs=(a, a)) == ok
+
+
 @NO_DEVICE
 def test_valid_calls_reach_the_device_check(lib):
     assert af(lib, att_desc()) == 5 and ab(lib, att_desc()) == 5
