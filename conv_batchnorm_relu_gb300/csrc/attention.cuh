@@ -89,14 +89,15 @@ __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
 }
 
-// Keys of sequence b.
-__device__ __forceinline__ int keys_of(const Params& a, int b) {
-  return a.key_lengths ? min(max(a.key_lengths[b], 0), a.k_tokens) : a.k_tokens;
-}
 // The place of sequence b's first query, kept within a range in which sums of tokens (up to 2^29) cannot
 // overflow: beyond the last key, or so far before the first that no query sees one, all are alike.
 __device__ __forceinline__ int start_of(const Params& a, int b) {
   return a.query_start ? min(max(a.query_start[b], -(1 << 30)), a.k_tokens) : 0;
+}
+// Keys of sequence b: those that there are, and, causal, that its last query sees.  What lies behind them is not looked at.
+__device__ __forceinline__ int keys_of(const Params& a, int b) {
+  const int there = a.key_lengths ? min(max(a.key_lengths[b], 0), a.k_tokens) : a.k_tokens;
+  return a.causal ? min(there, max(0, start_of(a, b) + a.q_tokens)) : there;
 }
 
 // scale log2(e); above 0, so that a hidden score's -infinity stays one (10^-35 of a score is 0 beside 1).

@@ -509,7 +509,8 @@ cbr_status_t cbr_rotary_backward(const cbr_rotary_desc_t* desc, const void* dq_o
  *                                    among its keys; may be negative)
  *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp s_ij,  p_ij = exp(s_ij - lse_i),  o_i = sum_j p_ij v_j
  * over the keys it sees.  A query that sees none has o = 0, lse = -infinity and dq = 0.  Keys and values
- * from key_lengths on are not used, whatever stands there (NaN included).  Sums are kept in fp32; p and
+ * from key_lengths on, or behind the last that a query of the sequence sees, are not used, whatever stands there
+ * (NaN included); a NaN among those that one query sees may reach the others of its sequence.  Sums are kept in fp32; p and
  * ds enter the second products rounded to the storage dtype, as q, k and v are.
  * Types: CBR_F16 and CBR_BF16 (the products run on the tensor cores' 16-bit instructions).  head_dim: a
  * multiple of 8 up to 128.  Addresses are 16-byte aligned and strides multiples of 8 elements (those of

@@ -42,6 +42,23 @@ def test_attention_past_32_bits(axis):
     cbr.stream_status()
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_a_cache_that_is_not_written_yet(dtype):
+    """Causal, no lengths: what lies behind the last query's own key may be NaN, in keys as in values."""
+    start = torch.tensor([0, 37, 150, -3, 292], dtype=torch.int32, device="cuda")
+    q, do = normal(5, 8, 4, 64, seed=1, dtype=dtype), normal(5, 8, 4, 64, seed=2, dtype=dtype)
+    k, v = normal(5, 300, 2, 64, seed=3, dtype=dtype), normal(5, 300, 2, 64, seed=4, dtype=dtype)
+    behind = torch.arange(300, device="cuda") >= start[:, None] + 8
+    want = att.attention_forward(q, k, v, causal=True, query_start=start)
+    back = att.attention_backward(do, q, k, v, want["o"], want["lse"], causal=True, query_start=start)
+    k, v = (t.masked_fill(behind[:, :, None, None], math.nan) for t in (k, v))
+    got = att.attention_forward(q, k, v, causal=True, query_start=start)
+    grads = att.attention_backward(do, q, k, v, got["o"], got["lse"], causal=True, query_start=start)
+    assert bool(got["o"].isfinite().all()) and torch.equal(got["o"], want["o"]) and torch.equal(got["lse"], want["lse"])
+    assert all(torch.equal(grads[n], back[n]) for n in back)
+    assert bool((grads["dk"][behind] == 0).all()) and bool((grads["dv"][behind] == 0).all())
+
+
 @pytest.mark.parametrize("axis,shape", [(0, (3, 40, 64)), (1, (1, 70, 64)), (1, (1, 6000, 64)), (0, (2, 9, 2200))])
 def test_group_norm_past_32_bits(axis, shape):
     x, dy = normal(*shape, seed=5), normal(*shape, seed=6)
