@@ -5,11 +5,14 @@
 // holds a tile of 128 keys and walks over the queries of all heads that read it: S' = K Q^T, dP' = V dO^T,
 // dV += P' dO, dK += dS' Q.  Scores and dP are taken twice (seven products instead of five), and in return every sum
 // stays in TMEM to its end, in a fixed order: no atomics, no sums in memory.
-//   P and dS go from registers over their scores in TMEM and enter the second products from there.  Both tiles'
-// elements are shared by two warpgroups: a thread has a row and 64 of its 128 columns.
+//   P and dS go from registers over their scores in TMEM and enter the second products from there; each rounded to the
+// storage type for that.  A thread has a row of a tile and 64 of its columns.
 //   f16: p is taken 2^12 times as large, and dS a power of two times as large that a bound on |do| |v| gives
 // for each key head, so that small ones keep their digits; the results are scaled back.
 //   Queries past the last one have the offset -infinity (p = 0), keys past theirs are cut off at the outputs.
+//   Bound by the products with heads of 128 (2 of 8192 tokens, 16 heads, bf16: 1.13 ms; the seven products alone take
+// 1.02 at the rate that a library's matrix product has here); with heads of 64 a step's chain of products and
+// exponentials, the tensor cores half busy (16 of 784, 12 heads, f16: 180 us).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -21,8 +24,8 @@ namespace {
 
 // By the head: kN, the tokens that a step of a walk takes (what stays has 128), and the warps.  Warps 0-3 (and 4-7) have the
 // 128 rows of a tile of scores, 64 columns of each to a thread; one loads, one issues the products.  Heads of 64 take
-// half of TMEM, and two blocks to an SM, one's start and end over the other's walk (16x784 tokens, 12 heads of 64: query
-// kernel 99 us, key kernel 141 with one block and kN = 128).
+// half of TMEM, and two blocks to an SM, one's start and end over the other's walk (16x784 tokens, 12 heads of 64: 164 us; one
+// block and kN = 128, in two launches, 240; 32 columns to a thread and twice the warps 172).
 template <int kDim>
 struct Form {
   static constexpr int kN = kDim, kRowWarps = kN / 16, kHalves = kN / 64, kThreads = 32 * (kRowWarps + 2), kBlocks = 128 / kDim;

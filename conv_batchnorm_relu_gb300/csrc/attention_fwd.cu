@@ -7,8 +7,12 @@
 // TMEM.  While one tile's scores are exponentiated the tensor cores work on the other's products.
 //   m moves only when a score passes it by 8 in the exponent (p stays below 2^8): O is rescaled then, which is
 // rare after the first tiles.  In f16 p is 2^6 times as large, which keeps small p's out of the subnormals.
-//   Warps: 0-3 and 4-7 the two tiles' rows, 8 loads (TMA), 9 products.  TMEM: S0, S1 (128 columns each; P in the
-// first 64 of each), O0, O1.
+//   Few queries on long keys: the walk is shared among blocks, whose results a second kernel joins by their sums.
+//   Warps: four for each tile's rows, one loads (TMA), one issues the products.  TMEM: the tiles' scores (128 columns
+// each; P in the first 64 of each), then their O.
+//   Bound by the products where rows are long (2 of 8192 tokens, 16 heads of 128, bf16: 343 us, 85% of the rate that a
+// library's matrix product has here), and by the exponentials' issue for heads of 64 and less; few queries by
+// the keys' and values' bytes (4 of 16384: 27 us, 3.7 TB/s).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -176,8 +180,7 @@ __global__ void __launch_bounds__(Form<kTiles>::kThreads, Form<kTiles>::kBlocks)
         const uint64_t qd = k_major(sbase + L::kQ + t * tile_bytes(kDim));
         const uint64_t kd = k_major(sbase + L::kKv + (i % L::kStages) * tile_bytes(kDim));
 #pragma unroll
-        for (int k = 0; k < kDim / 16; ++k)
-          mma_f16_ss_warp(tmem + t * 128, qd + k_major_step(k), kd + k_major_step(k), kIdS, k != 0);
+        for (int k = 0; k < kDim / 16; k += 4) mma_f16_ss_slab(tmem + t * 128, qd + k_major_step(k), kd + k_major_step(k), kIdS, k != 0);
         mma_commit_warp(bar_s + 8 * t);
       };
       full(0);
@@ -196,9 +199,7 @@ __global__ void __launch_bounds__(Form<kTiles>::kThreads, Form<kTiles>::kBlocks)
             if (!bad) bad = !__all_sync(0xffffffffu, mbar_wait(bar_p + 16 * t + 8 * half, ph));
             if (bad) break;
             tc_fence_after();
-#pragma unroll
-            for (int k = 4 * half; k < 4 * half + 4; ++k)
-              mma_f16_ts_warp(tmem + F::kO + t * kDim, tmem + t * 128 + k * 8, vd + mn_major_step(k), kIdO, (k != 0) | (j != begin));
+            mma_f16_ts_slab(tmem + F::kO + t * kDim, tmem + t * 128 + 32 * half, vd + mn_major_step(4 * half), kIdO, (half != 0) | (j != begin));
           }
           if (bad) break;
           if (t == kTiles - 1 || j >= end[kTiles - 1]) mma_commit_warp(bar_empty + 8 * (v_at % L::kStages));
