@@ -65,7 +65,7 @@ typedef enum {
   CBR_ERR_TIMEOUT = 7      /* (cbr_stream_status) a kernel gave up on a bounded wait */
 } cbr_status_t;
 
-/* CBR_F32 is taken by the token operators only. */
+/* CBR_F32 is taken by the token operators, group norm and clipping only. */
 typedef enum { CBR_F16 = 0, CBR_BF16 = 1, CBR_F32 = 2 } cbr_dtype_t;
 
 /* Source of the ReLU mask for cbr_backward. */
