@@ -11,6 +11,7 @@
 
 #include "cbr_internal.h"
 #include "common.cuh"
+#include "follow.cuh"
 #include "ptx_rows.cuh"
 #include "token_ops.cuh"
 #include "trunk_ops.h"

@@ -113,6 +113,7 @@ template <int kDim, bool BF16>
 __global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepareParams g) {
   const Params& a = g.f.p;
   __shared__ float largest[8];
+  let_next_kernel_start();
   constexpr int kSubs = 256 / kLanes<kDim>;
   const int lane = threadIdx.x % kLanes<kDim>, sub = threadIdx.x / kLanes<kDim>, e = lane * 8;
   const bool queries = blockIdx.x < g.query_blocks;
@@ -262,6 +263,8 @@ __device__ __forceinline__ void by_queries(const CUtensorMap& map_q, const CUten
     tmem_relinquish();
   }
   tc_fence_before();
+  wait_for_kernel_ahead();
+  let_next_kernel_start();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -491,6 +494,8 @@ __device__ __forceinline__ void by_keys(const CUtensorMap& map_q, const CUtensor
     tmem_relinquish();
   }
   tc_fence_before();
+  wait_for_kernel_ahead();
+  let_next_kernel_start();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -698,6 +703,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(128) sum_kernel(const __grid_constant__ Results f, int dim, int outs, int64_t heads, int64_t tokens) {
   const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  wait_for_kernel_ahead();
   if (at >= outs * f.part_rows) return;
   const int64_t which = at / f.part_rows, row = at % f.part_rows;
   using T = std::conditional_t<BF16, __nv_bfloat16, __half>;
@@ -810,11 +816,15 @@ int launch(const AttentionArgs& g, cudaStream_t st) {
   const auto kern = &backward_kernel<kDim, BF16>;
   if (!ensure_smem_attr(reinterpret_cast<const void*>(kern), 227 * 1024)) return CBR_ERR_CUDA;
   constexpr int kSmem = std::max(QuerySmem<kDim>::kTotal, KeySmem<kDim>::kTotal);
-  kern<<<(unsigned)(f.keys.blocks * f.keys.splits + f.queries.blocks * f.queries.splits), kThreads, kSmem, st>>>(q, k, v, d_o, f);
-  if (s.query_splits > 1)
-    sum_kernel<BF16><<<(unsigned)((f.queries.part_rows + 3) / 4), 128, 0, st>>>(f.queries, d.head_dim, 1, d.heads_q, d.q_tokens);
-  if (s.key_splits > 1)
-    sum_kernel<BF16><<<(unsigned)((2 * f.keys.part_rows + 3) / 4), 128, 0, st>>>(f.keys, d.head_dim, 2, d.heads_k, d.k_tokens);
+  bool fine = launch_behind(kern, dim3((unsigned)(f.keys.blocks * f.keys.splits + f.queries.blocks * f.queries.splits)), kThreads, kSmem, st,
+                            q, k, v, d_o, f);
+  auto sum = [&](const Results& r, int outs, int64_t heads, int64_t tokens) {
+    if (r.splits > 1 && fine)
+      fine = launch_behind(&sum_kernel<BF16>, dim3((unsigned)((outs * r.part_rows + 3) / 4)), 128, 0, st, r, d.head_dim, outs, heads, tokens);
+  };
+  sum(f.queries, 1, d.heads_q, d.q_tokens);
+  sum(f.keys, 2, d.heads_k, d.k_tokens);
+  if (!fine) return CBR_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? CBR_OK : CBR_ERR_CUDA;
 }
 

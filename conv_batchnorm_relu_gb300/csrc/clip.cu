@@ -9,6 +9,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "follow.cuh"
 #include "token_ops.cuh"
 #include "trunk_ops.h"
 
@@ -213,6 +214,7 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, 2) norm_kernel(const __grid_constant__ Table<N> t, double* part) {
   __shared__ double sums[kThreads / 32];
   const uint32_t tiles = t.tile[t.count];
+  let_next_kernel_start();
   double sum = 0.0;
   Raw next;
   Spot at{}, after{};
@@ -267,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     after = spot_of(t, tiles - 1 - blockIdx.x);
     next.load(t, after);
   }
+  wait_for_kernel_ahead();   // (gradients are only read up to here)
   if (threadIdx.x < 32) {
     const float f = scale_of(part, parts, max_norm, unscale, norm_out, scale_out, first && blockIdx.x == 0);
     if (threadIdx.x == 0) shared_scale = f;
@@ -324,7 +327,13 @@ int launch(const ClipArgs& a, cudaStream_t st) {
   for (int64_t l = a.outs ? n - 1 : 0; l >= 0; --l) {
     if (n > 1) table<N>(a, l * N, t);
     if (!a.outs) t.tile[t.count] = 0;
-    scale_kernel<N><<<a.outs ? kBlocks : 1, kThreads, 0, st>>>(t, a.part, parts, a.max_norm, a.unscale, a.norm, a.scale, l == 0);
+    if (l == n - 1 || !a.outs) {
+      if (!launch_behind(&scale_kernel<N>, dim3(a.outs ? kBlocks : 1), kThreads, 0, st, t, a.part, parts, a.max_norm, a.unscale, a.norm, a.scale,
+                         (int)(l == 0)))
+        return CBR_ERR_CUDA;
+    } else {
+      scale_kernel<N><<<kBlocks, kThreads, 0, st>>>(t, a.part, parts, a.max_norm, a.unscale, a.norm, a.scale, l == 0);
+    }
   }
   return cudaGetLastError() == cudaSuccess ? CBR_OK : CBR_ERR_CUDA;
 }

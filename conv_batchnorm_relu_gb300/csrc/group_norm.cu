@@ -23,6 +23,7 @@
 
 #include "cbr_internal.h"
 #include "common.cuh"
+#include "follow.cuh"
 #include "token_ops.cuh"
 #include "trunk_ops.h"
 
@@ -714,6 +715,7 @@ __device__ __forceinline__ void gradient(const Params& a, const Lay& l, const Sh
 
 template <typename T, int kVec>
 __global__ void __launch_bounds__(kThreads, 2) cluster_backward_kernel(const __grid_constant__ Params whole) {
+  let_next_kernel_start();
   const Params a = slice_of<T>(whole);
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -979,6 +981,7 @@ __global__ void __launch_bounds__(kThreads, kResident<1 + kBack>) stream_kernel(
 // every channel of every run, [image][run][2][channels]; the images' groups from them; the results, which read x again.
 template <typename T, int kVec, bool kBack>
 __global__ void __launch_bounds__(kThreads) wide_sums_kernel(const __grid_constant__ Params a) {
+  let_next_kernel_start();
   using V = Vec<T, kVec>;
   const int run = blockIdx.x % a.runs, n = run_length(a, run);
   const int64_t image = blockIdx.x / a.runs, begin = run_begin(a, run);
@@ -1050,6 +1053,8 @@ template <bool kBack>
 __global__ void __launch_bounds__(kMergeThreads) wide_merge_kernel(const __grid_constant__ Params a, float* means) {
   constexpr int kFew = 8;
   __shared__ float3 sets[kMergeThreads / 32];
+  wait_for_kernel_ahead();
+  let_next_kernel_start();
   const int64_t image = blockIdx.x / a.groups;
   const int c0 = blockIdx.x % a.groups * a.per;
   const float total = (float)a.pixels * (float)a.per;
@@ -1103,6 +1108,8 @@ __global__ void __launch_bounds__(kThreads) wide_result_kernel(const __grid_cons
   using V = Vec<T, kVec>;
   const int run = blockIdx.x % a.runs, n = run_length(a, run);
   const int64_t image = blockIdx.x / a.runs, begin = run_begin(a, run);
+  wait_for_kernel_ahead();
+  let_next_kernel_start();
   for (int col = threadIdx.x; col < a.channels / kVec; col += kThreads) {
     const T* x = static_cast<const T*>(a.x) + image * a.x_stride[0] + begin * a.x_stride[1] + (int64_t)col * kVec;
     const T* dy = kBack ? static_cast<const T*>(a.dy) + image * a.dy_stride[0] + begin * a.dy_stride[1] + (int64_t)col * kVec : nullptr;
@@ -1153,6 +1160,7 @@ __global__ void __launch_bounds__(1024) parameters_kernel(const float* part, int
   __shared__ float sum[32][33];
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   float s = 0.f;
+  wait_for_kernel_ahead();
   if (c < 2 * channels) {
 #pragma unroll 8
     for (int64_t r = row; r < rows; r += 32) s += part[r * 2 * channels + c];
@@ -1303,12 +1311,14 @@ int launch(const GroupNormArgs& g, bool backward, cudaStream_t st) {
     const unsigned blocks = (unsigned)rows, groups = (unsigned)(d.images * d.groups);
     if (backward) {
       wide_sums_kernel<T, kVec, true><<<blocks, kThreads, 0, st>>>(a);
-      wide_merge_kernel<true><<<groups, kMergeThreads, 0, st>>>(a, means);
-      wide_result_kernel<T, kVec, true><<<blocks, kThreads, 0, st>>>(a, means);
+      if (!launch_behind(&wide_merge_kernel<true>, dim3(groups), kMergeThreads, 0, st, a, means) ||
+          !launch_behind(&wide_result_kernel<T, kVec, true>, dim3(blocks), kThreads, 0, st, a, means))
+        return CBR_ERR_CUDA;
     } else {
       wide_sums_kernel<T, kVec, false><<<blocks, kThreads, 0, st>>>(a);
-      wide_merge_kernel<false><<<groups, kMergeThreads, 0, st>>>(a, means);
-      wide_result_kernel<T, kVec, false><<<blocks, kThreads, 0, st>>>(a, means);
+      if (!launch_behind(&wide_merge_kernel<false>, dim3(groups), kMergeThreads, 0, st, a, means) ||
+          !launch_behind(&wide_result_kernel<T, kVec, false>, dim3(blocks), kThreads, 0, st, a, means))
+        return CBR_ERR_CUDA;
     }
   } else if (plan.cluster) {
     a.keep = (int)longest;
@@ -1358,8 +1368,9 @@ int launch(const GroupNormArgs& g, bool backward, cudaStream_t st) {
       return CBR_ERR_CUDA;
     }
   }
-  if (backward && g.gamma)
-    parameters_kernel<<<(2 * d.channels + 31) / 32, 1024, 0, st>>>(a.part, rows, d.channels, g.dgamma, g.dbeta);
+  if (backward && g.gamma &&
+      !launch_behind(&parameters_kernel, dim3((unsigned)(2 * d.channels + 31) / 32), 1024, 0, st, a.part, rows, (int)d.channels, g.dgamma, g.dbeta))
+    return CBR_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? CBR_OK : CBR_ERR_CUDA;
 }
 
