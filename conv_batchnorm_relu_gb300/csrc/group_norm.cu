@@ -95,8 +95,12 @@ struct Vec {
     else if constexpr (kBytes >= 4) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(p), "n"(kBytes) : "memory");
     else asm volatile("{\n\t.reg .u16 h;\n\tld.global.u16 h, [%1];\n\tst.shared.u16 [%0], h;\n\t}" ::"r"(to), "l"(p) : "memory");
   }
+  // once: nobody reads it while this call runs, so L2 may give up its place first
+  template <bool once = false>
   __device__ __forceinline__ void store(uint8_t* p) const {
-    if constexpr (kBytes == 16) st_global_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
+    if constexpr (once && kBytes == 16) __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    else if constexpr (once && kBytes == 8) __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+    else if constexpr (kBytes == 16) st_global_v4(p, make_uint4(w[0], w[1], w[2], w[3]));
     else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
     else *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
@@ -549,7 +553,7 @@ __device__ __forceinline__ void normalise(const Params& a, const Lay& l, const S
         f[i] = make_float2(act_of<decltype(act)::value>(f[i].x), act_of<decltype(act)::value>(f[i].y));
       }
       v[0].set(f);
-      v[0].store(out);
+      v[0].template store<!kHeld>(out);
       out += out_step;
     };
     if constexpr (kHeld) reread<V, 1>(source, make);
@@ -705,7 +709,7 @@ __device__ __forceinline__ void gradient(const Params& a, const Lay& l, const Sh
         f[i] = fma(g, scale[i], fma(d, mx[i], m[i]));
       }
       v[0].set(f);
-      v[0].store(out);
+      v[0].template store<!kHeld>(out);
       out += out_step;
     };
     if constexpr (kHeld) reread<V, 2>(source, make);
