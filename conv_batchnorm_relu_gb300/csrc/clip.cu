@@ -1,9 +1,10 @@
 // The norm of a set of gradients and their clipping (declared in include/cbr.h).
 //
 // Bound by memory: every gradient is read for the norm, and read and written for the result, as far as L2 does not
-// hold it (400 fp32 tensors of 1.6 GB: 750 us, 6.4 TB/s, 94% of the copy rate).  Two kernels: every block's part of the sum of squares, then (after it, on the stream) the scale from all
-// parts and the scaled gradients, from the last tensors to the first, whose ends are still in L2.  The tensors'
-// addresses travel in the launches' own parameters, so a call keeps nothing on the device and can be captured.
+// hold it (400 fp32 tensors of 1.6 GB: 750 us, 6.4 TB/s, 94% of the copy rate).  Two kernels: every block's part of the
+// sum of squares, then (after it, on the stream) the scale from all parts and the scaled gradients, from the last
+// tensors to the first, whose ends are still in L2.  The tensors' addresses travel in the launches' own parameters, so a
+// call keeps nothing on the device and can be captured.
 //   A tile is 32 KB that start on a 16-byte boundary at or before the tensor's first element; a thread loads its next
 // tile's vectors before it works on the last ones.
 #include <algorithm>
