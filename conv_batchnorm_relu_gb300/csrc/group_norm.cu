@@ -471,9 +471,14 @@ __device__ __forceinline__ void group_moments(const Params& a, Team team, int n,
   }
 }
 
-// (count, mean, squared deviations) of two sets as one.
+// (count, mean, squared deviations) of two sets as one.  An empty set has no mean to differ from: the square of the other's
+// may be past the range.
 __device__ __forceinline__ void merge_moments(float& n, float& mean, float& q, float n2, float mean2, float q2) {
   if (n2 == 0.f) return;
+  if (n == 0.f) {
+    n = n2, mean = mean2, q = q2;
+    return;
+  }
   const float d = mean2 - mean, share = n2 / (n + n2);
   mean = fmaf(d, share, mean);
   q += fmaf(d * d, n * share, q2);
