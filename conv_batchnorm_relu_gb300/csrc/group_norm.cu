@@ -485,7 +485,8 @@ __device__ __forceinline__ void merge_moments(float& n, float& mean, float& q, f
   n += n2;
 }
 
-__device__ __forceinline__ float rstd_of(float squares, float n, float eps) { return 1.f / sqrtf(fmaxf(squares, 0.f) / n + eps); }
+// (squares may be below 0 by their roundings; NaN if they are)
+__device__ __forceinline__ float rstd_of(float squares, float n, float eps) { return 1.f / sqrtf(Max::of(squares, 0.f) / n + eps); }
 
 // Shared memory: two values of each channel for each row of threads; two of each group (a run's); two more (an image's);
 // five of each channel (what the results are computed with); the channels' groups; the kept pixels or rings.
