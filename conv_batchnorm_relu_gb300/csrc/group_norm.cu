@@ -485,8 +485,69 @@ __device__ __forceinline__ void merge_moments(float& n, float& mean, float& q, f
   n += n2;
 }
 
-// (squares may be below 0 by their roundings; NaN if they are)
-__device__ __forceinline__ float rstd_of(float squares, float n, float eps) { return 1.f / sqrtf(Max::of(squares, 0.f) / n + eps); }
+// (squares may be below 0 by their roundings; 0 where they are not finite)
+__device__ __forceinline__ float rstd_of(float squares, float n, float eps) {
+  return 1.f / sqrtf((fabsf(squares) < INFINITY ? fmaxf(squares, 0.f) : INFINITY) / n + eps);
+}
+
+// Squares past fp32's range (of values some 2^64 apart), infinities and NaN leave a group's sums infinite or NaN, and its
+// rstd 0.  Its moments are then taken again by the block that merges them, from x, in 64 bits, whose sums are what the
+// definition says wherever an infinity stands.  (That the code is there costs 1% of the stream, 128x112x112x128 bf16 176.5 and
+// 179 us, and 0.2 us of the smallest maps; as a function that is called it cost the stream 16%.)
+__device__ __forceinline__ bool lost(float rstd) { return !(rstd > 0.f); }
+
+template <int kWarps>
+__device__ __forceinline__ double block_sum(double v, double* sums) {
+#pragma unroll 1
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll 1
+  for (int i = 0; i < kWarps; ++i) v += sums[i];
+  return v;
+}
+
+// x: a group's first value; the block has kWarps warps, which `sums` has places for.  By the whole block.  Whether there is
+// an infinity or a NaN is seen first, by a plain sum; one NaN is enough (128x112x112x128 bf16, all NaN: 4.9 ms).
+template <int kWarps, typename T>
+__device__ __forceinline__ void far_moments(const T* x, int64_t stride, int64_t pixels, int per, float eps, double* sums, float* mean, float* rstd) {
+  constexpr uint32_t kTurns = 64;
+  const int width = min(per, kWarps * 32), rows = kWarps * 32 / width, row = threadIdx.x / width;
+  float plain = 0.f;
+#pragma unroll 1
+  for (uint32_t first = 0; first < (uint32_t)pixels; first += kTurns * rows) {
+    if (row < rows)
+#pragma unroll 1
+      for (int c = threadIdx.x - row * width; c < per; c += width)
+#pragma unroll 4
+        for (uint32_t p = first + row; p < min((uint32_t)pixels, first + kTurns * rows); p += rows) plain = fmaf(to_f(x[p * stride + c]), 0x1p-40f, plain);
+    if (__syncthreads_or(plain != plain)) break;
+  }
+  const double all = (double)pixels * per;
+  double center = block_sum<kWarps>((double)plain, sums);
+  if (!(fabs(center) < 0x1p127)) {
+    if (threadIdx.x == 0) *mean = (float)center, *rstd = __int_as_float(0x7fffffff);
+    return;
+  }
+  center = 0.0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    double s = 0.0;
+    if (row < rows)
+#pragma unroll 1
+      for (int c = threadIdx.x - row * width; c < per; c += width)
+#pragma unroll 4
+        for (uint32_t p = row; p < (uint32_t)pixels; p += rows) {
+          const double d = (double)to_f(x[p * stride + c]) - center;
+          s += pass ? d * d : d;
+        }
+    s = block_sum<kWarps>(s, sums) / all;
+    if (pass && threadIdx.x == 0) *mean = (float)center, *rstd = (float)(1.0 / sqrt(s + (double)eps));
+    center = s;
+  }
+}
 
 // Shared memory: two values of each channel for each row of threads; two of each group (a run's); two more (an image's);
 // five of each channel (what the results are computed with); the channels' groups; the kept pixels or rings.
@@ -588,6 +649,7 @@ __global__ void __launch_bounds__(kThreads, 2) cluster_forward_kernel(const __gr
   group_moments<kVec>(a, teams.groups, n, s.table, s.groups);
   cluster.sync();
   const float total = (float)a.pixels * (float)a.per;
+  bool again = false;
   for (int g = threadIdx.x; g < a.groups; g += kThreads) {
     float2 m[kMaxCluster];
 #pragma unroll
@@ -604,11 +666,21 @@ __global__ void __launch_bounds__(kThreads, 2) cluster_forward_kernel(const __gr
     for (int r = 0; r < kMaxCluster; ++r)
       if (r < a.runs && run_length(a, r)) q += fmaf((float)run_length(a, r) * (float)a.per * (m[r].x - mean), m[r].x - mean, m[r].y);
     const float rstd = rstd_of(q, total, a.eps);
+    again |= lost(rstd);
     s.stat[g] = mean;
     s.stat[a.groups + g] = rstd;
     if (run == 0) a.mean[image * a.all_groups + g] = mean, a.rstd[image * a.all_groups + g] = rstd;
   }
-  __syncthreads();
+  if (__builtin_expect(__syncthreads_or(again), 0)) {   // the same in all blocks, as their sums are
+#pragma unroll 1
+    for (int g = 0; g < a.groups; ++g) {
+      if (!lost(s.stat[a.groups + g])) continue;
+      far_moments<kThreads / 32>(x - run_begin(a, run) * a.x_stride[1] + g * a.per, a.x_stride[1], a.pixels, a.per, a.eps,
+                                 reinterpret_cast<double*>(s.table), s.stat + g, s.stat + a.groups + g);
+      if (run == 0 && threadIdx.x == 0) a.mean[image * a.all_groups + g] = s.stat[g], a.rstd[image * a.all_groups + g] = s.stat[a.groups + g];
+    }
+    cluster.sync();   // nobody writes before all have read: y may be x
+  }
   cluster.barrier_arrive();   // the other blocks' moments are not read any more
   s.set_channels(a, s.stat, s.stat + a.groups);
   __syncthreads();
@@ -840,12 +912,13 @@ struct Task {
   static __host__ __device__ uint32_t total(uint32_t images, uint32_t runs) { return images * (2 * runs + 1); }
 };
 
-// Waits until a count has been reached; a wait that runs out is reported.
+// Waits until a count has been reached; a wait that runs out is reported.  (A block that takes an image's moments again
+// needs 4 ns for each of its values.)
 __device__ __forceinline__ void wait_for(const Stream& f, const uint32_t* count, uint32_t n) {
   if (ld_acquire_gpu(count) >= n) return;
-  const uint64_t t0 = globaltimer_ns();
+  const uint64_t t0 = globaltimer_ns(), limit = kWaitLimitNs + 32 * (uint64_t)f.a.pixels * f.a.channels;
   while (ld_acquire_gpu(count) < n) {
-    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+    if (globaltimer_ns() - t0 > limit) {
       report_error(f.err, kErrWaitOperand);
       return;
     }
@@ -861,12 +934,13 @@ __device__ __forceinline__ void tell(uint32_t* count) {
 }
 
 // The image's moments (backward: means) from its runs'.  What other blocks have written comes through L2, kFew of a lane's
-// values at a time.
+// values at a time.  Whether a group of this thread has lost its squares.
 template <bool kBack>
-__device__ __forceinline__ void merge_runs(const Params& a, Team team, const float2* part, float* mean, float* second) {
+__device__ __forceinline__ bool merge_runs(const Params& a, Team team, const float2* part, float* mean, float* second) {
   constexpr int kFew = kBack ? 8 : 16;
   const int lanes = team.lanes(), sub = team.sub();
   const float total = (float)a.pixels * (float)a.per;
+  bool any = false;
   for (int first = 0; first < a.groups; first += team.teams()) {
     const int g = first + team.first();
     const float2* m = part + min(g, a.groups - 1);
@@ -899,9 +973,11 @@ __device__ __forceinline__ void merge_runs(const Params& a, Team team, const flo
         }
       }
       q = rstd_of(q, total, a.eps);
+      any |= lost(q);
     }
     if (g < a.groups && sub == 0) mean[g] = s, second[g] = q;
   }
+  return any;
 }
 
 template <typename T, int kVec, bool kBack>
@@ -952,10 +1028,19 @@ __global__ void __launch_bounds__(kThreads, kResident<1 + kBack>) stream_kernel(
       }
       __syncthreads();
       tell(f.counts + image);
-    } else if (task.kind == kMerge) {
+    } else if (__builtin_expect(task.kind == kMerge, 0)) {
       wait_for(f, f.counts + image, runs);
-      merge_runs<kBack>(a, teams.runs, part, kBack ? f.means + 2 * at : a.mean + at, kBack ? f.means + 2 * at + a.groups : a.rstd + at);
-      __syncthreads();
+      if constexpr (kBack) {
+        merge_runs<true>(a, teams.runs, part, f.means + 2 * at, f.means + 2 * at + a.groups);
+        __syncthreads();
+      } else if (__builtin_expect(__syncthreads_or(merge_runs<false>(a, teams.runs, part, a.mean + at, a.rstd + at)), 0)) {
+#pragma unroll 1
+        for (int g = 0; g < a.groups; ++g)
+          if (lost(rstd[g]))
+            far_moments<kThreads / 32>(x + g * a.per, a.x_stride[1], a.pixels, a.per, a.eps, reinterpret_cast<double*>(s.table), a.mean + at + g,
+                                       a.rstd + at + g);
+        __syncthreads();
+      }
       tell(f.counts + f.images + image);
     } else {
       auto ready = [&] {
@@ -1059,7 +1144,7 @@ __global__ void __launch_bounds__(kThreads) wide_sums_kernel(const __grid_consta
 // A block for each group of an image; kFew moments of a thread are on their way at a time (3 of 90x100x333 f32, one group:
 // forward with one at a time and 256 threads 179 us).
 constexpr int kMergeThreads = 1024;
-template <bool kBack>
+template <typename T, bool kBack>
 __global__ void __launch_bounds__(kMergeThreads) wide_merge_kernel(const __grid_constant__ Params a, float* means) {
   constexpr int kFew = 8;
   __shared__ float3 sets[kMergeThreads / 32];
@@ -1102,14 +1187,25 @@ __global__ void __launch_bounds__(kMergeThreads) wide_merge_kernel(const __grid_
   }
   if ((threadIdx.x & 31) == 0) sets[threadIdx.x >> 5] = make_float3(n, s, q);
   __syncthreads();
-  if (threadIdx.x) return;
-  for (int w = 1; w < kMergeThreads / 32; ++w) merge(sets[w].x, sets[w].y, sets[w].z);
   if constexpr (kBack) {
+    if (threadIdx.x) return;
+    for (int w = 1; w < kMergeThreads / 32; ++w) merge(sets[w].x, sets[w].y, sets[w].z);
     means[2 * image * a.groups + blockIdx.x % a.groups] = s / total;
     means[(2 * image + 1) * a.groups + blockIdx.x % a.groups] = q / total;
   } else {
-    a.mean[blockIdx.x] = s;
-    a.rstd[blockIdx.x] = rstd_of(q, total, a.eps);
+    __shared__ bool again;
+    __shared__ double sums[kMergeThreads / 32];
+    if (threadIdx.x == 0) {
+      for (int w = 1; w < kMergeThreads / 32; ++w) merge(sets[w].x, sets[w].y, sets[w].z);
+      const float rstd = rstd_of(q, total, a.eps);
+      a.mean[blockIdx.x] = s;
+      a.rstd[blockIdx.x] = rstd;
+      again = lost(rstd);
+    }
+    __syncthreads();
+    if (again)
+      far_moments<kMergeThreads / 32>(static_cast<const T*>(a.x) + image * a.x_stride[0] + c0, a.x_stride[1], a.pixels, a.per, a.eps, sums,
+                                      a.mean + blockIdx.x, a.rstd + blockIdx.x);
   }
 }
 
@@ -1321,12 +1417,12 @@ int launch(const GroupNormArgs& g, bool backward, cudaStream_t st) {
     const unsigned blocks = (unsigned)rows, groups = (unsigned)(d.images * d.groups);
     if (backward) {
       wide_sums_kernel<T, kVec, true><<<blocks, kThreads, 0, st>>>(a);
-      if (!launch_behind(&wide_merge_kernel<true>, dim3(groups), kMergeThreads, 0, st, a, means) ||
+      if (!launch_behind(&wide_merge_kernel<T, true>, dim3(groups), kMergeThreads, 0, st, a, means) ||
           !launch_behind(&wide_result_kernel<T, kVec, true>, dim3(blocks), kThreads, 0, st, a, means))
         return CBR_ERR_CUDA;
     } else {
       wide_sums_kernel<T, kVec, false><<<blocks, kThreads, 0, st>>>(a);
-      if (!launch_behind(&wide_merge_kernel<false>, dim3(groups), kMergeThreads, 0, st, a, means) ||
+      if (!launch_behind(&wide_merge_kernel<T, false>, dim3(groups), kMergeThreads, 0, st, a, means) ||
           !launch_behind(&wide_result_kernel<T, kVec, false>, dim3(blocks), kThreads, 0, st, a, means))
         return CBR_ERR_CUDA;
     }

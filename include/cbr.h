@@ -554,7 +554,9 @@ cbr_status_t cbr_attention_backward(const cbr_attention_desc_t* desc, const void
  * one image, r = 1 / sqrt(v + eps):
  *   y = act(gamma (x - m) r + beta),   act(z) = z, max(0, z), or z / (1 + exp(-z))
  * gamma, beta and their gradients are fp32 [channels]; both NULL: 1 and 0.  Statistics are fp32, merged
- * from partial means and squared deviations, so a mean far from 0 costs no digits.
+ * from partial means and squared deviations, so that a mean far from 0 costs no more digits than its own rounding
+ * to fp32; where a group's squares leave fp32's range they are taken in 64 bits.  An infinity or a NaN makes
+ * its group's rstd and results NaN.
  */
 typedef enum { CBR_ACT_NONE = 0, CBR_ACT_RELU = 1, CBR_ACT_SILU = 2 } cbr_act_t;
 typedef struct {

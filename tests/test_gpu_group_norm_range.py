@@ -6,12 +6,25 @@ import pytest
 import torch
 
 import trunk_reference as ref
+from conv_batchnorm_relu_gb300 import cbr
 from conv_batchnorm_relu_gb300 import group_norm as gn
-from test_gpu_group_norm import EPS, make
+from test_gpu_group_norm import DT, EPS, make
 
 pytestmark = pytest.mark.gpu
 
 LAYOUTS = {"slices": ((2, 7, 7, 512), 32), "cluster": ((3, 28, 28, 64), 8), "stream": ((2, 160, 150, 96), 8), "wide": ((2, 9, 11, 333), 3)}
+
+
+def check(s, groups, act="silu"):
+    """Against 64 bits."""
+    assert bool(s["x"].isfinite().all())
+    got = gn.group_norm_forward(s["x"], s["gamma"], s["beta"], groups, eps=EPS, act=act)
+    want = ref.group_norm(s["x"], s["gamma"], s["beta"], groups, EPS, act)
+    ref.close(got["mean"], want["mean"], want["mean_bound"], "mean")
+    ref.close(got["rstd"], want["rstd"], want["rstd_bound"], "rstd")
+    ref.close(got["y"], want["y"], want["y_bound"], "y", s["x"].dtype)
+    assert cbr.stream_status_code() == 0
+    return got
 
 
 def group(c, groups, g):
@@ -20,23 +33,63 @@ def group(c, groups, g):
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
-@pytest.mark.parametrize("mean,spread", [(1e20, 1e16), (-3e20, 1e16)])
+@pytest.mark.parametrize("mean,spread", [(1e20, 1e16), (-3e20, 1e16), (-3e30, 1e26), (1e37, 1e34)])
 def test_means_whose_squares_leave_the_range(layout, mean, spread):
+    """(The spreads' own squares: the last two's.)"""
     shape, groups = LAYOUTS[layout]
     s = make(shape, "f32", seed=21)
     s["x"] = mean + spread * s["x"]
-    x, want = s["x"], ref.group_norm(s["x"], s["gamma"], s["beta"], groups, EPS, "none")
-    got = gn.group_norm_forward(x, s["gamma"], s["beta"], groups, eps=EPS)
-    ref.close(got["mean"], want["mean"], want["mean_bound"], "mean")
-    ref.close(got["rstd"], want["rstd"], want["rstd_bound"], "rstd")
-    ref.close(got["y"], want["y"], want["y_bound"], "y")
+    check(s, groups, "none")
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("spread", [1e15, 3e19, 1e25, 3e37])
+def test_spreads_whose_squares_leave_the_range(layout, dtype, spread):
+    shape, groups = LAYOUTS[layout]
+    s = make(shape, dtype, seed=22)
+    s["x"] = (s["x"].float() * spread).to(DT[dtype])
+    check(s, groups, "silu" if dtype == "f32" else "relu")
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_a_constant_in_each_run_of_pixels(layout):
+    """No spread in a thread's, row's or run's values, only among them."""
+    shape, groups = LAYOUTS[layout]
+    s = make(shape, "f32", seed=24)
+    pixels = math.prod(shape[1:-1])
+    level = 1e30 * torch.randn(8, generator=torch.Generator().manual_seed(1))
+    s["x"] = level[torch.arange(pixels) * 8 // pixels].view(1, *shape[1:-1], 1).expand(shape).contiguous().cuda()
+    check(s, groups, "none")
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("spread", [1e22, 1e36])
+def test_the_other_groups_keep_their_bits(layout, spread):
+    shape, groups = LAYOUTS[layout]
+    s = make(shape, "f32", seed=25)
+    clean = gn.group_norm_forward(s["x"], s["gamma"], s["beta"], groups, eps=EPS)
+    far = group(shape[-1], groups, 1)
+    s["x"][1][..., far] *= spread
+    got = check(s, groups)
+    again = gn.group_norm_forward(s["x"], s["gamma"], s["beta"], groups, eps=EPS)
+    keep = torch.ones(shape[0], groups, dtype=torch.bool, device="cuda")
+    keep[1, 1] = False
+    for n in ("mean", "rstd"):
+        assert torch.equal(got[n][keep], clean[n][keep])
+    assert torch.equal(again["y"][0], clean["y"][0])
+    ordinary = torch.ones(shape[-1], dtype=torch.bool, device="cuda")
+    ordinary[far] = False
+    # y of the image's other groups: the same values up to the order of two roundings
+    a, b = again["y"][1][..., ordinary], clean["y"][1][..., ordinary]
+    assert bool(((a - b).abs() <= 4 * ref.W * (1 + b.abs())).all())
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "silu"])
 @pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
 def test_nan_and_infinity_at_any_place(layout, act, value):
-    """The group's rstd and all its results are NaN, wherever the value stands."""
+    """The group's rstd and all its results are NaN, and its mean is what the sum is, wherever the value stands."""
     shape, groups = LAYOUTS[layout]
     s = make(shape, "f32", seed=26)
     clean = gn.group_norm_forward(s["x"], s["gamma"], s["beta"], groups, eps=EPS, act=act)
@@ -49,11 +102,26 @@ def test_nan_and_infinity_at_any_place(layout, act, value):
         x.view(shape[0], pixels, c)[1, i, here.start + i % (c // groups)] = value
         o = gn.group_norm_forward(x, s["gamma"], s["beta"], groups, eps=EPS, act=act)
         assert torch.isnan(o["rstd"][1, 1]), i
+        assert torch.equal(o["mean"][1, 1].cpu(), torch.tensor(value)) or math.isnan(value) and torch.isnan(o["mean"][1, 1]), i
         assert bool(torch.isnan(o["y"][~keep]).all()), i
         assert torch.equal(o["y"][keep], clean["y"][keep]), i
         b = gn.group_norm_backward(s["dy"], x, s["gamma"], s["beta"], o["mean"], o["rstd"], groups, act=act)
         assert bool(torch.isnan(b["dx"][~keep]).all()) and bool(b["dx"][keep].isfinite().all()), i
-    x = s["x"].clone()      # both infinities
+    x = s["x"].clone()      # both infinities: the mean is none
     x.view(shape[0], pixels, c)[1, [0, pixels - 1], here.start] = torch.tensor([math.inf, -math.inf], device="cuda")
     o = gn.group_norm_forward(x, s["gamma"], s["beta"], groups, eps=EPS, act=act)
-    assert torch.isnan(o["rstd"][1, 1]) and bool(torch.isnan(o["y"][~keep]).all())
+    assert torch.isnan(o["mean"][1, 1]) and torch.isnan(o["rstd"][1, 1]) and bool(torch.isnan(o["y"][~keep]).all())
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_a_map_of_nan_in_place(layout):
+    """Every sum is taken again, in a map that its own results replace."""
+    shape, groups = LAYOUTS[layout]
+    x = torch.full(shape, math.nan, device="cuda")
+    o = gn.group_norm_forward(x, None, None, groups, act="relu", out={"y": x})
+    assert bool(torch.isnan(x).all()) and bool(torch.isnan(o["rstd"]).all()) and bool(torch.isnan(o["mean"]).all())
+    x = torch.randn(shape, generator=torch.Generator().manual_seed(2)).cuda() * 1e30
+    want = gn.group_norm_forward(x, None, None, groups, act="relu")
+    got = gn.group_norm_forward(x, None, None, groups, act="relu", out={"y": x})
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    cbr.stream_status()
