@@ -6,6 +6,7 @@
 from __future__ import annotations
 
 import ctypes
+import math
 import struct
 
 import torch
@@ -133,8 +134,8 @@ def group_norm_forward(x, gamma, beta, groups, *, eps=1e-5, act="none", ws=None,
 
     x [images][...][channels] (an NHWC feature map; f32, f16 or bf16), whose pixels lie a fixed step apart; gamma
     and beta fp32 [channels], or both None; act "none", "relu" or "silu".  out may hold "y" (x itself, to save
-    its memory), "mean" and "rstd".  ws: a workspace (:func:`group_norm_workspace_size`) to use instead of a new
-    one."""
+    its memory), "mean" and "rstd" (NaN for a map without pixels).  ws: a workspace
+    (:func:`group_norm_workspace_size`) to use instead of a new one."""
     shape, pixels, channels, dt, code, index, act = _shape(x, groups, act)
     images, dev = shape[0], x.device
     sx = _map(x, shape, pixels, dt, index, "x")
@@ -151,6 +152,9 @@ def group_norm_forward(x, gamma, beta, groups, *, eps=1e-5, act="none", ws=None,
         _raw_stream(index) if _raw_stream else _stream_of(dev))
     if status != CBR_OK:
         raise CBRError(status, "cbr_group_norm_forward")
+    if not pixels:      # the mean of no values
+        mean.fill_(math.nan)
+        rstd.fill_(math.nan)
     return {"y": y, "mean": mean, "rstd": rstd}
 
 

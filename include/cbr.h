@@ -571,7 +571,8 @@ typedef struct {
 /* Workspace bytes of the two calls for this desc (either pointer may be NULL). */
 cbr_status_t cbr_group_norm_workspace_size(const cbr_group_norm_desc_t* desc, size_t* fwd_bytes, size_t* bwd_bytes);
 
-/* Forward -> y, mean and rstd [images][groups] fp32.  y may be x itself (same strides). */
+/* Forward -> y, mean and rstd [images][groups] fp32.  y may be x itself (same strides).  A map without pixels has no
+ * statistics: nothing is written. */
 cbr_status_t cbr_group_norm_forward(const cbr_group_norm_desc_t* desc, const void* x, const float* gamma,
                                     const float* beta, void* y, float* mean, float* rstd, void* ws, size_t ws_bytes,
                                     cbr_stream_t stream);

@@ -125,3 +125,11 @@ def test_a_map_of_nan_in_place(layout):
     got = gn.group_norm_forward(x, None, None, groups, act="relu", out={"y": x})
     assert all(torch.equal(got[n], want[n]) for n in want)
     cbr.stream_status()
+
+
+@pytest.mark.parametrize("shape", [(2, 0, 4, 8), (3, 5, 0, 8)])
+def test_a_map_without_pixels_has_no_statistics(shape):
+    x = torch.empty(shape, device="cuda")
+    out = {n: torch.full((shape[0], 2), 7.0, device="cuda") for n in ("mean", "rstd")}
+    o = gn.group_norm_forward(x, None, None, 2, out=out)
+    assert bool(torch.isnan(o["mean"]).all()) and bool(torch.isnan(o["rstd"]).all())
