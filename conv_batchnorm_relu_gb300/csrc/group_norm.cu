@@ -193,6 +193,12 @@ __device__ __forceinline__ float act_slope(float z, float up) {
   }
   return up;
 }
+__device__ __forceinline__ float act_of(float z, int act) {
+  return act == CBR_ACT_RELU ? act_of<CBR_ACT_RELU>(z) : act == CBR_ACT_SILU ? act_of<CBR_ACT_SILU>(z) : z;
+}
+__device__ __forceinline__ float act_slope(float z, float up, int act) {
+  return act == CBR_ACT_RELU ? act_slope<CBR_ACT_RELU>(z, up) : act == CBR_ACT_SILU ? act_slope<CBR_ACT_SILU>(z, up) : up;
+}
 // Runs the body made for the activation.
 template <typename Body>
 __device__ __forceinline__ void by_act(int act, Body body) {
@@ -200,6 +206,33 @@ __device__ __forceinline__ void by_act(int act, Body body) {
   else if (act == CBR_ACT_SILU) body(std::integral_constant<int, CBR_ACT_SILU>{});
   else body(std::integral_constant<int, CBR_ACT_NONE>{});
 }
+
+// Values so far apart that rstd^2 leaves fp32's range, or their differences do: x is taken times a power of two near rstd,
+// and rstd divided by it, one value at a time, by blocks that have such a channel.  (That the code is there costs 256x56x56x64
+// f16 backward 1.5%, 105 and 106.7 us, clusters' backward 1 to 2% and 1x224x224x64 f32's 3.5%.)
+__device__ __forceinline__ bool is_far(float rstd) { return rstd < 0x1p-50f; }
+__device__ __forceinline__ float far_unit(float rstd) { return __uint_as_float(max(__float_as_uint(rstd) & 0x7f800000u, 0x00800000u)); }
+// 1 / unit
+__device__ __forceinline__ float far_rest(float unit) { return __uint_as_float(0x7f000000u - __float_as_uint(unit)); }
+struct Far {
+  float unit, mean, scale, shift, rest;   // rest: rstd less its unit
+
+  __device__ __forceinline__ Far(const Params& a, int c, float center, float rstd) {
+    unit = far_unit(rstd);
+    mean = -center * unit;
+    rest = rstd * far_rest(unit);
+    scale = a.gamma ? rest * a.gamma[c] : rest;
+    shift = a.gamma ? a.beta[c] : 0.f;
+  }
+  __device__ __forceinline__ float distance(float x) const { return fmaf(x, unit, mean); }
+  __device__ __forceinline__ float result(float x, int act) const { return act_of(fmaf(distance(x), scale, shift), act); }
+  __device__ __forceinline__ float slope(float x, float up, int act) const { return act_slope(fmaf(distance(x), scale, shift), up, act); }
+  // (the two means are of gamma g and gamma g xh)
+  __device__ __forceinline__ float gradient(float x, float up, int act, float rstd, float mean_g, float mean_gx) const {
+    const float times = scale * unit, mx = -rstd * rest * mean_gx;
+    return fmaf(slope(x, up, act), times, fmaf(distance(x), mx, -rstd * mean_g));
+  }
+};
 
 // A thread's channels of an array in shared memory.
 template <int kVec>
@@ -525,7 +558,8 @@ __device__ __forceinline__ void far_moments(const T* x, int64_t stride, int64_t 
         for (uint32_t p = first + row; p < min((uint32_t)pixels, first + kTurns * rows); p += rows) plain = fmaf(to_f(x[p * stride + c]), 0x1p-40f, plain);
     if (__syncthreads_or(plain != plain)) break;
   }
-  const double all = (double)pixels * per;
+  // 1 / (values of the group), from 32 bits by a Newton step
+  const double all = (double)pixels * per, near = (double)(1.f / (float)all), share = near * (2.0 - all * near);
   double center = block_sum<kWarps>((double)plain, sums);
   if (!(fabs(center) < 0x1p127)) {
     if (threadIdx.x == 0) *mean = (float)center, *rstd = __int_as_float(0x7fffffff);
@@ -543,8 +577,9 @@ __device__ __forceinline__ void far_moments(const T* x, int64_t stride, int64_t 
           const double d = (double)to_f(x[p * stride + c]) - center;
           s += pass ? d * d : d;
         }
-    s = block_sum<kWarps>(s, sums) / all;
-    if (pass && threadIdx.x == 0) *mean = (float)center, *rstd = (float)(1.0 / sqrt(s + (double)eps));
+    s = block_sum<kWarps>(s, sums) * share;
+    // (eps beside squares that fp32 does not hold, or sums of them: the root in 32 bits, of what is above 2^-80)
+    if (pass && threadIdx.x == 0) *mean = (float)center, *rstd = 0x1p-80f / sqrtf((float)((s + (double)eps) * 0x1p-160));
     center = s;
   }
 }
@@ -577,14 +612,17 @@ struct Shared {
   __device__ __forceinline__ void set_groups(const Params& a) const {
     for (int c = threadIdx.x; c < a.channels; c += kThreads) group[c] = (uint16_t)(c / a.per);
   }
-  // z = (x - mean) scale + shift
-  __device__ __forceinline__ void set_channels(const Params& a, const float* mean, const float* rstd) const {
+  // z = (x - mean) scale + shift.  Whether a channel's values are far apart.
+  __device__ __forceinline__ bool set_channels(const Params& a, const float* mean, const float* rstd) const {
+    bool far = false;
     for (int c = threadIdx.x; c < a.channels; c += kThreads) {
       const int g = group[c];
       coef[c] = mean[g];
       coef[step + c] = a.gamma ? rstd[g] * a.gamma[c] : rstd[g];
       coef[2 * step + c] = a.gamma ? a.beta[c] : 0.f;
+      far |= is_far(rstd[g]);
     }
+    return far;
   }
   // dx = scale g - rstd (mean_g + (x - mean) rstd mean_gx)
   __device__ __forceinline__ void set_gradient(const Params& a, const float* rstd) const {
@@ -597,13 +635,28 @@ struct Shared {
   }
 };
 
+// Where values are far apart: each(channel, its coefficients) for a thread's channels, whose values are taken from memory.
+template <typename T, int kVec, typename Each>
+__device__ __forceinline__ void each_far(const Params& a, const Lay& l, const Shared<T, kVec>& s, const float* rstd, Each each) {
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  if (l.row >= l.rows) return;
+#pragma unroll 1
+  for (int c = l.col * kVec; c < (l.col + 1) * kVec; ++c) each(c, Far(a, c, s.coef[c], rstd[s.group[c]]));
+}
+
 // A run normalised: what shared memory holds (kHeld), or read again.  ready() brings the coefficients, the whole block
-// in step, after the first loads.
+// in step, after the first loads, and says whether a channel's values are far apart.
 template <typename T, int kVec, bool kHeld, typename Ready>
 __device__ __forceinline__ void normalise(const Params& a, const Lay& l, const Shared<T, kVec>& s, const T* x, T* y, int n, Ready ready) {
   using V = Vec<T, kVec>;
   std::conditional_t<kHeld, Way<1>, Reader<V, 1>> source(way_of<T, kVec, 1>(a, l, x, nullptr, s.kept, n));
-  ready();
+  if (__builtin_expect(ready(), 0)) {
+    each_far(a, l, s, s.stat + a.groups, [&](int c, const Far& w) {
+#pragma unroll 1
+      for (int p = l.row; p < n; p += l.rows) y[p * a.y_stride[1] + c] = from_f<T>(w.result(to_f(x[p * a.x_stride[1] + c]), a.act));
+    });
+    return;
+  }
   float2 mean[V::kPairs], scale[V::kPairs], shift[V::kPairs];
   take_channels<kVec>(mean, s.coef, l.col);
   take_channels<kVec>(scale, s.coef + s.step, l.col);
@@ -682,21 +735,34 @@ __global__ void __launch_bounds__(kThreads, 2) cluster_forward_kernel(const __gr
     cluster.sync();   // nobody writes before all have read: y may be x
   }
   cluster.barrier_arrive();   // the other blocks' moments are not read any more
-  s.set_channels(a, s.stat, s.stat + a.groups);
-  __syncthreads();
-  normalise<T, kVec, true>(a, l, s, x, static_cast<T*>(a.y) + image * a.y_stride[0] + run_begin(a, run) * a.y_stride[1], n, [] {});
+  const bool far = __syncthreads_or(s.set_channels(a, s.stat, s.stat + a.groups));
+  normalise<T, kVec, true>(a, l, s, x, static_cast<T*>(a.y) + image * a.y_stride[0] + run_begin(a, run) * a.y_stride[1], n, [&] { return far; });
   cluster.barrier_wait();
 }
 
 // ---------------------------------------------------------------- backward
 
-// A run's sums of g and g xh: `table` gets them (the second still to be multiplied by rstd) of every channel in every row
-// of threads.  ready() as above.
+// A run's sums of g and g xh: `table` gets them (the second still to be multiplied by rstd, or by the rest of it) of every
+// channel in every row of threads.  ready() as above, whose answer it gives.
 template <typename T, int kVec, typename Ready>
-__device__ __forceinline__ void sums(const Params& a, const Lay& l, const Shared<T, kVec>& s, const T* x, const T* dy, int n, Ready ready) {
+__device__ __forceinline__ bool sums(const Params& a, const Lay& l, const Shared<T, kVec>& s, const T* x, const T* dy, int n, const float* rstd,
+                                     Ready ready) {
   using V = Vec<T, kVec>;
   Reader<V, 2> reader(way_of<T, kVec, 2>(a, l, x, dy, s.kept, n));
-  ready();
+  if (__builtin_expect(ready(), 0)) {
+    each_far(a, l, s, rstd, [&](int c, const Far& w) {
+      float sum = 0.f, sum_x = 0.f;
+#pragma unroll 1
+      for (int p = l.row; p < n; p += l.rows) {
+        const float v = to_f(x[p * a.x_stride[1] + c]), g = w.slope(v, to_f(dy[p * a.dy_stride[1] + c]), a.act);
+        sum += g;
+        sum_x = fmaf(g, w.distance(v), sum_x);
+      }
+      s.table[l.row * a.channels + c] = sum;
+      s.table[kTable<kVec> + l.row * a.channels + c] = sum_x;
+    });
+    return true;
+  }
   float2 mean[V::kPairs], scale[V::kPairs], shift[V::kPairs], sum[V::kPairs], sum_x[V::kPairs];
   take_channels<kVec>(mean, s.coef, l.col);
   take_channels<kVec>(scale, s.coef + s.step, l.col);
@@ -717,18 +783,20 @@ __device__ __forceinline__ void sums(const Params& a, const Lay& l, const Shared
       }
     });
   });
-  if (l.row >= l.rows) return;
+  if (l.row >= l.rows) return false;
   float* t = s.table + l.row * a.channels + l.col * kVec;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     t[i] = i & 1 ? sum[i / 2].y : sum[i / 2].x;
     t[kTable<kVec> + i] = i & 1 ? sum_x[i / 2].y : sum_x[i / 2].x;
   }
+  return false;
 }
 
 // The channels' sums of a run, from the rows of threads', into the first row's place.
 template <int kVec>
-__device__ __forceinline__ void channel_sums(const Params& a, const Lay& l, Team team, float* table, const uint16_t* group, const float* rstd) {
+__device__ __forceinline__ void channel_sums(const Params& a, const Lay& l, Team team, float* table, const uint16_t* group, const float* rstd,
+                                             bool far) {
   const int lanes = team.lanes(), sub = team.sub();
   for (int first = 0; first < a.channels; first += team.teams()) {
     const int c = first + team.first();
@@ -738,7 +806,11 @@ __device__ __forceinline__ void channel_sums(const Params& a, const Lay& l, Team
     s = team.sum(s);
     sx = team.sum(sx);
     __syncwarp();
-    if (c < a.channels && sub == 0) table[c] = s, table[kTable<kVec> + c] = sx * rstd[group[c]];
+    if (c < a.channels && sub == 0) {
+      float r = rstd[group[c]];
+      if (far) r *= far_rest(far_unit(r));
+      table[c] = s, table[kTable<kVec> + c] = sx * r;
+    }
   }
 }
 
@@ -763,10 +835,19 @@ __device__ __forceinline__ void group_sums(const Params& a, Team team, const flo
 // A run's dx, from the means of gamma g and gamma g xh over its image's groups; kHeld and ready() as above.
 template <typename T, int kVec, bool kHeld, typename Ready>
 __device__ __forceinline__ void gradient(const Params& a, const Lay& l, const Shared<T, kVec>& s, const T* x, const T* dy, T* dx, int n,
-                                         Ready ready) {
+                                         const float* rstd, Ready ready) {
   using V = Vec<T, kVec>;
   std::conditional_t<kHeld, Way<2>, Reader<V, 2>> source(way_of<T, kVec, 2>(a, l, x, dy, s.kept, n));
-  ready();
+  if (__builtin_expect(ready(), 0)) {
+    each_far(a, l, s, rstd, [&](int c, const Far& w) {
+      const int g = s.group[c];
+#pragma unroll 1
+      for (int p = l.row; p < n; p += l.rows)
+        dx[p * a.y_stride[1] + c] = from_f<T>(w.gradient(to_f(x[p * a.x_stride[1] + c]), to_f(dy[p * a.dy_stride[1] + c]), a.act, rstd[g], s.stat[g],
+                                                         s.stat[a.groups + g]));
+    });
+    return;
+  }
   float2 mean[V::kPairs], scale[V::kPairs], shift[V::kPairs], m[V::kPairs], mx[V::kPairs];
   take_channels<kVec>(mean, s.coef, l.col);
   take_channels<kVec>(scale, s.coef + s.step, l.col);
@@ -812,13 +893,12 @@ __global__ void __launch_bounds__(kThreads, 2) cluster_backward_kernel(const __g
   const Teams teams = Teams::of(a, l);
   const float *mean = a.mean + image * a.all_groups, *rstd = a.rstd + image * a.all_groups;
   s.set_groups(a);
-  sums<T, kVec>(a, l, s, x, dy, n, [&] {
+  const bool far = sums<T, kVec>(a, l, s, x, dy, n, rstd, [&] {
     __syncthreads();
-    s.set_channels(a, mean, rstd);
-    __syncthreads();
+    return __syncthreads_or(s.set_channels(a, mean, rstd)) != 0;
   });
   __syncthreads();
-  channel_sums<kVec>(a, l, teams.channels, s.table, s.group, rstd);
+  channel_sums<kVec>(a, l, teams.channels, s.table, s.group, rstd, far);
   __syncthreads();
   group_sums<kVec>(a, teams.groups, s.table, s.groups);
   cluster.sync();
@@ -854,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 2) cluster_backward_kernel(const __g
   cluster.barrier_arrive();   // the other blocks' sums are not read any more
   s.set_gradient(a, rstd);
   __syncthreads();
-  gradient<T, kVec, true>(a, l, s, x, dy, static_cast<T*>(a.y) + image * a.y_stride[0] + begin * a.y_stride[1], n, [] {});
+  gradient<T, kVec, true>(a, l, s, x, dy, static_cast<T*>(a.y) + image * a.y_stride[0] + begin * a.y_stride[1], n, rstd, [&] { return far; });
   cluster.barrier_wait();
 }
 
@@ -1004,17 +1084,17 @@ __global__ void __launch_bounds__(kThreads, kResident<1 + kBack>) stream_kernel(
     float2* part = reinterpret_cast<float2*>(a.group_part) + at * runs;
     const float *mean = a.mean + at, *rstd = a.rstd + at;
     if (task.kind == kMoments) {
+      [[maybe_unused]] bool far = false;
       if constexpr (kBack) {
-        sums<T, kVec>(a, l, s, x, dy, n, [&] {
+        far = sums<T, kVec>(a, l, s, x, dy, n, rstd, [&] {
           __syncthreads();   // the task before may have its coefficients yet to read
-          s.set_channels(a, mean, rstd);
-          __syncthreads();
+          return __syncthreads_or(s.set_channels(a, mean, rstd)) != 0;
         });
       } else {
         moments<T, kVec>(a, l, x, n, s.table, s.kept);
       }
       __syncthreads();
-      if constexpr (kBack) channel_sums<kVec>(a, l, teams.channels, s.table, s.group, rstd);
+      if constexpr (kBack) channel_sums<kVec>(a, l, teams.channels, s.table, s.group, rstd, far);
       else channel_moments<kVec>(a, l, teams.channels, n, s.table);
       __syncthreads();
       if constexpr (kBack) {
@@ -1050,16 +1130,17 @@ __global__ void __launch_bounds__(kThreads, kResident<1 + kBack>) stream_kernel(
         const float *first = kBack ? f.means + 2 * at : mean, *second = kBack ? f.means + 2 * at + a.groups : rstd;
         for (int g = threadIdx.x; g < a.groups; g += kThreads) s.stat[g] = __ldcg(first + g), s.stat[a.groups + g] = __ldcg(second + g);
         __syncthreads();
+        bool far;
         if constexpr (kBack) {
-          s.set_channels(a, mean, rstd);
+          far = s.set_channels(a, mean, rstd);
           s.set_gradient(a, rstd);
         } else {
-          s.set_channels(a, s.stat, s.stat + a.groups);
+          far = s.set_channels(a, s.stat, s.stat + a.groups);
         }
-        __syncthreads();
+        return __syncthreads_or(far) != 0;
       };
       T* y = static_cast<T*>(a.y) + image * a.y_stride[0] + begin * a.y_stride[1];
-      if constexpr (kBack) gradient<T, kVec, false>(a, l, s, x, dy, y, n, ready);
+      if constexpr (kBack) gradient<T, kVec, false>(a, l, s, x, dy, y, n, rstd, ready);
       else normalise<T, kVec, false>(a, l, s, x, y, n, ready);
     }
   }
@@ -1086,6 +1167,7 @@ __global__ void __launch_bounds__(kThreads) wide_sums_kernel(const __grid_consta
     const T* dy = kBack ? static_cast<const T*>(a.dy) + image * a.dy_stride[0] + begin * a.dy_stride[1] + (int64_t)col * kVec : nullptr;
     float2 mean[V::kPairs], scale[V::kPairs], shift[V::kPairs], s[V::kPairs], q[V::kPairs];
     [[maybe_unused]] float rstd[kVec];
+    bool far = false;
     V v;
     [[maybe_unused]] V u;
     v.load(reinterpret_cast<const uint8_t*>(x));
@@ -1099,12 +1181,30 @@ __global__ void __launch_bounds__(kThreads) wide_sums_kernel(const __grid_consta
         const int64_t ch = col * kVec + i, g = image * a.groups + ch / a.per;
         m[i] = a.mean[g];
         rstd[i] = a.rstd[g];
+        far |= is_far(rstd[i]);
         c[i] = a.gamma ? rstd[i] * a.gamma[ch] : rstd[i];
         h[i] = a.gamma ? a.beta[ch] : 0.f;
       }
 #pragma unroll
       for (int i = 0; i < V::kPairs; ++i)
         mean[i] = make_float2(m[2 * i], m[2 * i + 1]), scale[i] = make_float2(c[2 * i], c[2 * i + 1]), shift[i] = make_float2(h[2 * i], h[2 * i + 1]);
+    }
+    if (kBack && __builtin_expect(far, 0)) {
+#pragma unroll 1
+      for (int i = 0; i < kVec; ++i) {
+        const int ch = col * kVec + i;
+        const Far w(a, ch, a.mean[image * a.groups + ch / a.per], a.rstd[image * a.groups + ch / a.per]);
+        float sum = 0.f, sum_x = 0.f;
+#pragma unroll 1
+        for (int p = 0; p < n; ++p) {
+          const float value = to_f(x[p * a.x_stride[1] + i]), g = w.slope(value, to_f(dy[p * a.dy_stride[1] + i]), a.act);
+          sum += g;
+          sum_x = fmaf(g, w.distance(value), sum_x);
+        }
+        part[ch] = sum_x * w.rest;
+        part[a.channels + ch] = sum;
+      }
+      continue;
     }
     by_act(a.act, [&](auto act) {
 #pragma unroll 4
@@ -1221,10 +1321,12 @@ __global__ void __launch_bounds__(kThreads) wide_result_kernel(const __grid_cons
     const T* dy = kBack ? static_cast<const T*>(a.dy) + image * a.dy_stride[0] + begin * a.dy_stride[1] + (int64_t)col * kVec : nullptr;
     T* y = static_cast<T*>(a.y) + image * a.y_stride[0] + begin * a.y_stride[1] + (int64_t)col * kVec;
     float mean[2 * V::kPairs] = {}, scale[2 * V::kPairs] = {}, shift[2 * V::kPairs] = {}, m[2 * V::kPairs] = {}, mx[2 * V::kPairs] = {};
+    bool far = false;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const int ch = col * kVec + i, group = ch / a.per;
       const float rstd = a.rstd[image * a.groups + group];
+      far |= is_far(rstd);
       mean[i] = a.mean[image * a.groups + group];
       scale[i] = a.gamma ? rstd * a.gamma[ch] : rstd;
       shift[i] = a.gamma ? a.beta[ch] : 0.f;
@@ -1232,6 +1334,26 @@ __global__ void __launch_bounds__(kThreads) wide_result_kernel(const __grid_cons
         m[i] = -rstd * means[2 * image * a.groups + group];
         mx[i] = -rstd * rstd * means[(2 * image + 1) * a.groups + group];
       }
+    }
+    if (__builtin_expect(far, 0)) {
+#pragma unroll 1
+      for (int i = 0; i < kVec; ++i) {
+        const int ch = col * kVec + i, group = ch / a.per;
+        const float rstd = a.rstd[image * a.groups + group];
+        const Far w(a, ch, a.mean[image * a.groups + group], rstd);
+#pragma unroll 1
+        for (int p = 0; p < n; ++p) {
+          const float value = to_f(x[p * a.x_stride[1] + i]);
+          float v;
+          if constexpr (kBack)
+            v = w.gradient(value, to_f(dy[p * a.dy_stride[1] + i]), a.act, rstd, means[2 * image * a.groups + group],
+                           means[(2 * image + 1) * a.groups + group]);
+          else
+            v = w.result(value, a.act);
+          y[p * a.y_stride[1] + i] = from_f<T>(v);
+        }
+      }
+      continue;
     }
     by_act(a.act, [&](auto act) {
 #pragma unroll 4

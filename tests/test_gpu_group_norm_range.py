@@ -15,14 +15,24 @@ pytestmark = pytest.mark.gpu
 LAYOUTS = {"slices": ((2, 7, 7, 512), 32), "cluster": ((3, 28, 28, 64), 8), "stream": ((2, 160, 150, 96), 8), "wide": ((2, 9, 11, 333), 3)}
 
 
+# coefficients of a gradient of subnormal size are each off by half a step of 2^-149, and |g| and |xh| are below 8
+SUBNORMAL = 32 * 2.0 ** -150
+
+
 def check(s, groups, act="silu"):
-    """Against 64 bits."""
-    assert bool(s["x"].isfinite().all())
-    got = gn.group_norm_forward(s["x"], s["gamma"], s["beta"], groups, eps=EPS, act=act)
-    want = ref.group_norm(s["x"], s["gamma"], s["beta"], groups, EPS, act)
+    """Forward and backward against 64 bits."""
+    x, dt = s["x"], s["x"].dtype
+    assert bool(x.isfinite().all())
+    got = gn.group_norm_forward(x, s["gamma"], s["beta"], groups, eps=EPS, act=act)
+    want = ref.group_norm(x, s["gamma"], s["beta"], groups, EPS, act)
     ref.close(got["mean"], want["mean"], want["mean_bound"], "mean")
     ref.close(got["rstd"], want["rstd"], want["rstd_bound"], "rstd")
-    ref.close(got["y"], want["y"], want["y_bound"], "y", s["x"].dtype)
+    ref.close(got["y"], want["y"], want["y_bound"], "y", dt)
+    back = gn.group_norm_backward(s["dy"], x, s["gamma"], s["beta"], got["mean"], got["rstd"], groups, act=act)
+    wb = ref.group_norm_backward(s["dy"], x, s["gamma"], s["beta"], got["mean"], got["rstd"], groups, act)
+    ref.close(back["dx"], wb["dx"], wb["dx_bound"] + SUBNORMAL, "dx", dt)
+    for n in ("dgamma", "dbeta"):
+        ref.close(back[n], wb[n], wb[n + "_bound"], n)
     assert cbr.stream_status_code() == 0
     return got
 
@@ -50,6 +60,15 @@ def test_spreads_whose_squares_leave_the_range(layout, dtype, spread):
     s = make(shape, dtype, seed=22)
     s["x"] = (s["x"].float() * spread).to(DT[dtype])
     check(s, groups, "silu" if dtype == "f32" else "relu")
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_values_at_both_ends_of_the_range(layout):
+    """Half of a group is the largest number, half its negative: differences are past the range."""
+    shape, groups = LAYOUTS[layout]
+    s = make(shape, "f32", seed=23)
+    s["x"] = torch.where(s["x"] > 0, 1.0, -1.0) * torch.finfo(torch.float32).max
+    check(s, groups, "none")
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
