@@ -101,8 +101,8 @@ __device__ __forceinline__ int keys_of(const Params& a, int b) {
   return a.causal ? min(there, max(0, start_of(a, b) + a.q_tokens)) : there;
 }
 
-// scale log2(e); above 0, so that a hidden score's -infinity stays one (10^-35 of a score is 0 beside 1).
-__device__ __forceinline__ float exponent_scale(const Params& a) { return fmaxf(a.scale * kLog2e, 1e-35f); }
+// scale log2(e); above 0, so that a hidden score's -infinity stays one (2^-149 of any score is 0 beside 1).
+__device__ __forceinline__ float exponent_scale(const Params& a) { return fmaxf(a.scale * kLog2e, 0x1p-149f); }
 
 // A tile of keys or values (kRows rows from `row` on of one head), by one thread, in boxes of kBox rows and 64 elements.
 template <int kDim, int kRows = kTile, int kBox = kRows>
