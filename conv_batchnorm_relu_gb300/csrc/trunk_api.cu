@@ -20,6 +20,7 @@ int check(const cbr_attention_desc_t* d) {
   if (!extent(d->batch) || d->q_tokens < 0 || d->k_tokens < 0 || d->heads_q < 1 || d->heads_k < 1 ||
       d->heads_q % d->heads_k || d->head_dim < 1 || !finite(d->scale) || d->scale < 0.f)
     return CBR_ERR_INVALID_ARG;
+  if (d->scale > 0x1p127f) return CBR_ERR_UNSUPPORTED;   // times log2(e) it is to stay finite
   if ((d->dtype != CBR_F16 && d->dtype != CBR_BF16) || d->head_dim > kMaxAttentionDim || d->head_dim % 8 ||
       d->q_tokens > kMaxTokens || d->k_tokens > kMaxTokens || d->heads_q > kMaxHeads)
     return CBR_ERR_UNSUPPORTED;

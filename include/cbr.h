@@ -522,7 +522,7 @@ typedef struct {
   int64_t do_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];  /* backward */
   int32_t heads_q, heads_k, head_dim;
   int32_t causal, dtype;
-  float scale;                                                     /* finite, >= 0 */
+  float scale;                                                     /* 0 .. 2^127 */
 } cbr_attention_desc_t;
 
 /* Workspace bytes of the two calls for this desc (either pointer may be NULL). */
