@@ -242,8 +242,9 @@ __global__ void __launch_bounds__(kThreads, 2) norm_kernel(const __grid_constant
   }
 }
 
-// Every block adds the parts up in the same order, in one warp; the first block of the call writes norm and scale.  The
-// scale goes by the norm before it is rounded: one that is subnormal in fp32 has few digits, one past its range none.
+// Every block of the first launch adds the parts up in the same order, in one warp, and its first block writes norm and scale,
+// which the launches behind it read (65536 tensors, 128 launches of each kernel: 1.6 ms; 8.0 where all added the parts up).
+// The scale goes by the norm before it is rounded: one that is subnormal in fp32 has few digits, one past its range none.
 __device__ __forceinline__ float scale_of(const double* part, int parts, float max_norm, float unscale, float* norm_out, float* scale_out,
                                           bool write) {
   double s = 0.0;
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   wait_for_kernel_ahead();   // (gradients are only read up to here)
   if (threadIdx.x < 32) {
-    const float f = scale_of(part, parts, max_norm, unscale, norm_out, scale_out, first && blockIdx.x == 0);
+    const float f = first ? scale_of(part, parts, max_norm, unscale, norm_out, scale_out, blockIdx.x == 0) : *scale_out;
     if (threadIdx.x == 0) shared_scale = f;
   }
   __syncthreads();
@@ -329,11 +330,10 @@ int launch(const ClipArgs& a, cudaStream_t st) {
     if (n > 1) table<N>(a, l * N, t);
     if (!a.outs) t.tile[t.count] = 0;
     if (l == n - 1 || !a.outs) {
-      if (!launch_behind(&scale_kernel<N>, dim3(a.outs ? kBlocks : 1), kThreads, 0, st, t, a.part, parts, a.max_norm, a.unscale, a.norm, a.scale,
-                         (int)(l == 0)))
+      if (!launch_behind(&scale_kernel<N>, dim3(a.outs ? kBlocks : 1), kThreads, 0, st, t, a.part, parts, a.max_norm, a.unscale, a.norm, a.scale, 1))
         return CBR_ERR_CUDA;
     } else {
-      scale_kernel<N><<<kBlocks, kThreads, 0, st>>>(t, a.part, parts, a.max_norm, a.unscale, a.norm, a.scale, l == 0);
+      scale_kernel<N><<<kBlocks, kThreads, 0, st>>>(t, a.part, parts, a.max_norm, a.unscale, a.norm, a.scale, 0);
     }
   }
   return cudaGetLastError() == cudaSuccess ? CBR_OK : CBR_ERR_CUDA;
