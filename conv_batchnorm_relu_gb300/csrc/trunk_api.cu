@@ -24,7 +24,8 @@ int check(const cbr_attention_desc_t* d) {
   if ((d->dtype != CBR_F16 && d->dtype != CBR_BF16) || d->head_dim > kMaxAttentionDim || d->head_dim % 8 ||
       d->q_tokens > kMaxTokens || d->k_tokens > kMaxTokens || d->heads_q > kMaxHeads)
     return CBR_ERR_UNSUPPORTED;
-  // the launches' blocks, one for each 64 queries (keys) of a head at the most, stay far below 2^31
+  // the launches' blocks, one for each 128 queries and one for each 128 keys of a head (64 of either where D and the
+  // bounds are taken) and one tile more at the most, stay far below 2^31
   const int64_t tiles = std::max(d->q_tokens, d->k_tokens) / 128 + 1;
   if (d->batch > (int64_t(1) << 28) / d->heads_q / tiles) return CBR_ERR_UNSUPPORTED;
   return CBR_OK;
@@ -126,7 +127,8 @@ cbr_status_t cbr_attention_forward(const cbr_attention_desc_t* desc, const void*
     if (need && !ws) return CBR_ERR_INVALID_ARG;
     if (need && ws_bytes < need) return CBR_ERR_WORKSPACE;
     AttentionArgs a{};
-    if (const int s = device_for_call(&a.num_sms, &a.err)) return s;
+    int sms = 0;
+    if (const int s = device_for_call(&sms, &a.err)) return s;
     a.d = d;
     a.q = q;
     a.k = k;
@@ -172,7 +174,8 @@ cbr_status_t cbr_attention_backward(const cbr_attention_desc_t* desc, const void
     if (need && !ws) return CBR_ERR_INVALID_ARG;
     if (need && ws_bytes < need) return CBR_ERR_WORKSPACE;
     AttentionArgs a{};
-    if (const int s = device_for_call(&a.num_sms, &a.err)) return s;
+    int sms = 0;
+    if (const int s = device_for_call(&sms, &a.err)) return s;
     a.d = d;
     a.q = q;
     a.k = k;
@@ -299,9 +302,10 @@ cbr_status_t cbr_clip_gradients(int64_t count, const void* const* grads, const i
     if (off(norm, 4) || off(scale, 4) || off(ws, 16)) return CBR_ERR_MISALIGNED;
     if (outs && outs_overlap(count, grads, sizes, dtypes, outs)) return CBR_ERR_INVALID_ARG;
     if (ws_bytes < clip_part_doubles(count) * sizeof(double)) return CBR_ERR_WORKSPACE;
-    ClipArgs a{count, grads, sizes, dtypes, outs, max_norm, unscale, norm, scale, static_cast<double*>(ws), 0};
+    const ClipArgs a{count, grads, sizes, dtypes, outs, max_norm, unscale, norm, scale, static_cast<double*>(ws)};
+    int sms = 0;
     uint32_t* err = nullptr;
-    if (const int s = device_for_call(&a.num_sms, &err)) return s;
+    if (const int s = device_for_call(&sms, &err)) return s;
     return launch_clip(a, reinterpret_cast<cudaStream_t>(stream));
   });
 }

@@ -24,7 +24,6 @@ struct AttentionArgs {
   void* dv;
   void* ws;
   uint32_t* err;
-  int num_sms;
 };
 size_t attention_forward_ws(const cbr_attention_desc_t& d);
 size_t attention_backward_ws(const cbr_attention_desc_t& d);
@@ -62,7 +61,6 @@ struct ClipArgs {
   float* norm;
   float* scale;
   double* part;
-  int num_sms;
 };
 size_t clip_part_doubles(int64_t count);
 int launch_clip(const ClipArgs& a, cudaStream_t st);
