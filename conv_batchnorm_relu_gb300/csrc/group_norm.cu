@@ -24,6 +24,7 @@
 #include "cbr_internal.h"
 #include "common.cuh"
 #include "follow.cuh"
+#include "group_norm_tasks.h"
 #include "token_ops.cuh"
 #include "trunk_ops.h"
 
@@ -945,51 +946,15 @@ __host__ __device__ constexpr int ring_bytes() {
   return kOps * kAhead<kOps, Vec<T, kVec>::kBytes> * kBatch<kOps> * kThreads * Vec<T, kVec>::kBytes;
 }
 
-// Tasks in one order, dealt out to the blocks in turn.  Step s of them has the moments (sums) of image s, run by run; the
-// merge of image s - half's moments; and the results of image s - lag, run by run.  A block takes its tasks in that
-// order, so whatever one waits for is done or being done by a block that waits for less; `lag` is such that it is
-// nearly always done, and that what is read again is in L2.
+// Tasks in one order (group_norm_tasks.h), dealt out to the blocks in turn.  A block takes its tasks in that order, so
+// whatever one waits for is done or being done by a block that waits for less; `lag` is such that it is nearly always
+// done, and that what is read again is in L2.
 struct Stream {
   Params a;
+  Order order;
   uint32_t* counts;   // of each image's runs whose moments are there, then one for each image: 1 when they are merged
   float* means;       // backward: the images' two means of each group
-  uint32_t images, half, lag;
   uint32_t* err;
-};
-enum Kind { kMoments, kMerge, kResult };
-struct Task {
-  Kind kind;
-  uint32_t image, run;
-  static __device__ __forceinline__ Task of(const Stream& f, uint32_t i) {
-    const uint32_t runs = f.a.runs;
-    // steps of the same size: before the first merge, before the first result, with all three, without moments, with
-    // results alone
-    uint32_t step = 0, size = runs, n = f.half * runs;
-    bool first = true, merge = false;
-    if (i >= n) {
-      i -= n, step = f.half, size = runs + 1, n = (f.lag - f.half) * size, merge = true;
-      if (i >= n) {
-        i -= n, step = f.lag, size = 2 * runs + 1, n = (f.images - f.lag) * size;
-        if (i >= n) {
-          i -= n, step = f.images, size = runs + 1, n = f.half * size, first = false;
-          if (i >= n) i -= n, step = f.images + f.half, size = runs, merge = false;
-        }
-      }
-    }
-    const uint32_t past = i / size;
-    i -= past * size;
-    step += past;
-    if (first) {
-      if (i < runs) return Task{kMoments, step, i};
-      i -= runs;
-    }
-    if (merge) {
-      if (i == 0) return Task{kMerge, step - f.half, 0};
-      --i;
-    }
-    return Task{kResult, step - f.lag, i};
-  }
-  static __host__ __device__ uint32_t total(uint32_t images, uint32_t runs) { return images * (2 * runs + 1); }
 };
 
 // Waits until a count has been reached; a wait that runs out is reported.  (A block that takes an image's moments again
@@ -1073,9 +1038,9 @@ __global__ void __launch_bounds__(kThreads, kResident<1 + kBack>) stream_kernel(
   if constexpr (kBack)
     for (int c = threadIdx.x; c < 2 * a.channels; c += kThreads) own[c] = 0.f;
   __syncthreads();
-  const uint32_t runs = a.runs, all = Task::total(f.images, runs);
+  const uint32_t runs = a.runs, all = Task::total(f.order.images, runs);
   for (uint32_t i = blockIdx.x; i < all; i += gridDim.x) {
-    const Task task = Task::of(f, i);
+    const Task task = Task::of(f.order, i);
     const uint32_t image = task.image;
     const int run = (int)task.run, n = run_length(a, run);
     const int64_t begin = run_begin(a, run), at = (int64_t)image * a.groups;
@@ -1121,10 +1086,10 @@ __global__ void __launch_bounds__(kThreads, kResident<1 + kBack>) stream_kernel(
                                        a.rstd + at + g);
         __syncthreads();
       }
-      tell(f.counts + f.images + image);
+      tell(f.counts + f.order.images + image);
     } else {
       auto ready = [&] {
-        wait_for(f, f.counts + f.images + image, 1);
+        wait_for(f, f.counts + f.order.images + image, 1);
         __syncthreads();   // the task before may have its coefficients yet to read
         // what another block has written comes through L2
         const float *first = kBack ? f.means + 2 * at : mean, *second = kBack ? f.means + 2 * at + a.groups : rstd;
@@ -1577,9 +1542,7 @@ int launch(const GroupNormArgs& g, bool backward, cudaStream_t st) {
     a.part = f.means + (backward ? 2 * d.images * a.groups : 0);
     f.counts = reinterpret_cast<uint32_t*>(a.part + (backward ? 2 * kStreamBlocks * a.channels : 0));
     f.a = a;
-    f.images = (uint32_t)d.images;
-    f.lag = (uint32_t)plan.lag;
-    f.half = (uint32_t)(plan.lag + 1) / 2;
+    f.order = Order{(uint32_t)d.images, (uint32_t)plan.runs, (uint32_t)(plan.lag + 1) / 2, (uint32_t)plan.lag};
     f.err = g.err;
     if (cudaMemsetAsync(f.counts, 0, (size_t)d.images * 8, st) != cudaSuccess) return CBR_ERR_CUDA;
     const auto kern = backward ? &stream_kernel<T, kVec, true> : &stream_kernel<T, kVec, false>;
