@@ -152,3 +152,20 @@ def test_a_map_without_pixels_has_no_statistics(shape):
     out = {n: torch.full((shape[0], 2), 7.0, device="cuda") for n in ("mean", "rstd")}
     o = gn.group_norm_forward(x, None, None, 2, out=out)
     assert bool(torch.isnan(o["mean"]).all()) and bool(torch.isnan(o["rstd"]).all())
+
+
+def test_silu_over_its_range():
+    """z is beta exactly where an image is constant.  exp is good to (2 + 1.173 |z|) steps of 2^-23 of it, the quotient to two,
+    the sum in between to half of one; below -87 the quotient's divisor is past 2^126 and the result 0."""
+    z = torch.linspace(-110, 90, 1600, dtype=torch.float64).float()
+    x = torch.full((1, 3, 5, 1600), 2.5, device="cuda")
+    y = gn.group_norm_forward(x, torch.ones(1600, device="cuda"), z.cuda(), 4, act="silu")["y"][0, 1, 2]
+    z = z.double()
+    want = z * torch.sigmoid(z)
+    ref.close(y, want, (5 + 1.2 * z.abs()) * 2.0 ** -23 * want.abs() + 2.0 ** -118, "y")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape,groups", [((2, 24, 20, 1536), 24), ((3, 7, 9, 2048), 32), ((2, 60, 61, 1048), 8), ((1, 100, 90, 1024), 1)])
+def test_wide_pixels_that_a_block_has_columns_for(shape, groups, dtype):
+    check(make(shape, dtype, seed=27), groups, "relu")
