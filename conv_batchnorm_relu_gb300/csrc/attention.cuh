@@ -1,7 +1,7 @@
 // What the attention kernels share: tiles, masks, the load of keys and values, TMEM rows.
 //
-// Every kernel works on tiles of 128 tokens of one head.  A tile in shared memory is kDim / 64 slabs of
-// [128 rows][128 bytes] in the 128-byte swizzle, as the tensor maps write them; it serves as a K-major
+// Every kernel works on tiles of 128 tokens of one head (the backward's walks over heads of 64 take steps of 64).  A tile in
+// shared memory is kDim / 64 slabs of [its rows][128 bytes] in the 128-byte swizzle, as the tensor maps write them; it serves as a K-major
 // operand (rows along M or N, the head's elements along K) and as an MN-major one (rows along K).  Heads of
 // up to 64 (128) elements fill kDim = 64 (128); the maps fill the rest with zeros.
 #pragma once

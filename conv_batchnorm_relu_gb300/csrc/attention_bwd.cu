@@ -12,7 +12,7 @@
 //   Queries past the last one have the offset -infinity (p = 0), keys past theirs are cut off at the outputs.
 //   Bound by the products with heads of 128 (2 of 8192 tokens, 16 heads, bf16: 1.13 ms; the seven products alone take
 // 1.02 at the rate that a library's matrix product has here); with heads of 64 a step's chain of products and
-// exponentials, the tensor cores half busy (16 of 784, 12 heads, f16: 180 us).
+// exponentials, the tensor cores busy 35% of the time (16 of 784, 12 heads, f16: 177 us).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -24,8 +24,8 @@ namespace {
 
 // By the head: kN, the tokens that a step of a walk takes (what stays has 128), and the warps.  Warps 0-3 (and 4-7) have the
 // 128 rows of a tile of scores, 64 columns of each to a thread; one loads, one issues the products.  Heads of 64 take
-// half of TMEM, and two blocks to an SM, one's start and end over the other's walk (16x784 tokens, 12 heads of 64: 164 us; one
-// block and kN = 128, in two launches, 240; 32 columns to a thread and twice the warps 172).
+// half of TMEM, and two blocks to an SM, one's start and end over the other's walk (16x784 tokens, 12 heads of 64: one block
+// and kN = 128, in two launches, took 1.46 times as long; 32 columns to a thread and twice the warps 1.05 times).
 template <int kDim>
 struct Form {
   static constexpr int kN = kDim, kRowWarps = kN / 16, kHalves = kN / 64, kThreads = 32 * (kRowWarps + 2), kBlocks = 128 / kDim;

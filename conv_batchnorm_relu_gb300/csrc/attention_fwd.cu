@@ -10,9 +10,11 @@
 //   Few queries on long keys: the walk is shared among blocks, whose results a second kernel joins by their sums.
 //   Warps: four for each tile's rows, one loads (TMA), one issues the products.  TMEM: the tiles' scores (128 columns
 // each; P in the first 64 of each), then their O.
-//   Bound by the products where rows are long (2 of 8192 tokens, 16 heads of 128, bf16: 343 us, 85% of the rate that a
-// library's matrix product has here), and by the exponentials' issue for heads of 64 and less; few queries by
-// the keys' and values' bytes (4 of 16384: 27 us, 3.7 TB/s).
+//   Bound by the products where rows are long (2 of 8192 tokens, 16 heads of 128, bf16: 340 us, 85% of the rate that a
+// library's matrix product has here).  Heads of 64 and less: by the row warps' chain of a tile (scores to registers,
+// maximum, exponentials, p back), two warps to a scheduler: tensor cores, the exponentials' pipe and the issue slots
+// are busy 35, 35 and 41% of the time (1 of 16384, 2 heads, bf16: 174 us), and with rows of 196 tokens 13, 15 and 31%.  Few
+// queries: the keys' and values' bytes, a tile ahead at most, and the join (4 of 16384: 27 us, 3.7 TB/s).
 #include <algorithm>
 
 #include "attention.cuh"

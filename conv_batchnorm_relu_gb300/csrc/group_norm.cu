@@ -7,7 +7,7 @@
 // of whole groups instead, which need no exchange.
 //   Larger maps are a stream of tasks on a resident grid: the moments of an image's runs, and, some images later, their
 // results, which read x again from L2.  So HBM is read and written all the time, which clusters that load, wait and
-// store do not do (128x112x112x128 bf16 in clusters of 16: 298 us, as a stream 175: 4.7 TB/s of what has to move, and as
+// store do not do (128x112x112x128 bf16 in clusters of 16: 298 us, as a stream 179: 4.6 TB/s of what has to move, and as
 // much again from L2).
 //   The backward does the same with x and dy, and the sums of g and g xh.
 //   Moments: a thread sums its values' differences from its first one, and their squares, which costs no digits
@@ -179,6 +179,8 @@ __device__ __forceinline__ int run_length(const Params& a, int r) { return (int)
 // Of `n` pixels, those of this thread's row.
 __device__ __forceinline__ int turns(int n, const Lay& l) { return l.row < l.rows && l.row < n ? (n - l.row + l.rows - 1) / l.rows : 0; }
 
+// SiLU's exponential and quotient are the hardware's, for f32 maps too: by their bounds good to (5 + 1.2 |z|) 2^-23 of the
+// result (a z that is off by half a step alone makes |z| 2^-24 of it), and 0 below -87.  (With expf and a rounded quotient 64x112x112x64 f32 took 121 us for 95, backward 206 for 157.)
 template <int kAct>
 __device__ __forceinline__ float act_of(float z) {
   if constexpr (kAct == CBR_ACT_RELU) return Max::of(z, 0.f);
@@ -261,8 +263,9 @@ struct Way {
   int all, slots;
 };
 // By the maps read: pixels that a thread takes at a time, batches of them that it has asked for, blocks to an SM.  The
-// forward moves more and computes less: deeper rings (two blocks with 5 batches and three with 3: 176 and 182 us at
-// 128x112x112x128 bf16); the backward wants warps (101 and 95 us at 256x56x56x64 f16).
+// forward moves more and computes less: deeper rings (two blocks with 5 batches and three with 3: 180 and 234 us at
+// 128x112x112x128 bf16, 67 and 70 at 64x64x64x128 f32); the backward is near enough with two blocks and three (107.7 and
+// 106.9 us at 256x56x56x64 f16, 99 and 108 at 64x64x64x128 f32).
 template <int kOps>
 constexpr int kBatch = 4 / kOps;
 template <int kOps, int kBytes>
@@ -1579,8 +1582,8 @@ int dispatch(const GroupNormArgs& g, bool backward, cudaStream_t st) {
     }
     return true;
   };
-  // The backward of 8 channels a thread does not fit the registers of three blocks to an SM (100 us and more, 8-byte vectors
-  // 94 at 256x56x56x64 f16); it is left to pixels with more vectors than a block has threads.
+  // The backward of 8 channels a thread does not fit the registers of three blocks to an SM (138 us, and 107 with 8-byte
+  // vectors, at 256x56x56x64 f16); it is left to pixels with more vectors than a block has threads.
   if constexpr (sizeof(T) == 2)
     if ((!backward || d.channels > 4 * kThreads) && fits(8)) return launch<T, 8>(g, backward, st);
   if (fits(4)) return launch<T, 4>(g, backward, st);

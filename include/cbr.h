@@ -510,7 +510,8 @@ cbr_status_t cbr_rotary_backward(const cbr_rotary_desc_t* desc, const void* dq_o
  *   s_ij = scale q_i . k_j,  lse_i = log sum_j exp s_ij,  p_ij = exp(s_ij - lse_i),  o_i = sum_j p_ij v_j
  * over the keys it sees.  A query that sees none has o = 0, lse = -infinity and dq = 0.  Keys and values
  * from key_lengths on, or behind the last that a query of the sequence sees, are not used, whatever stands there
- * (NaN included); a NaN among those that one query sees may reach the others of its sequence.  Sums are kept in fp32; p and
+ * (NaN included); a NaN among those that one query sees may reach the others of its sequence, and one in a
+ * query's row of q or do the gradients of keys that the query does not see.  Sums are kept in fp32; p and
  * ds enter the second products rounded to the storage dtype, as q, k and v are.
  * Types: CBR_F16 and CBR_BF16 (the products run on the tensor cores' 16-bit instructions).  head_dim: a
  * multiple of 8 up to 128.  Addresses are 16-byte aligned and strides multiples of 8 elements (those of
@@ -556,7 +557,8 @@ cbr_status_t cbr_attention_backward(const cbr_attention_desc_t* desc, const void
  * gamma, beta and their gradients are fp32 [channels]; both NULL: 1 and 0.  Statistics are fp32, merged
  * from partial means and squared deviations, so that a mean far from 0 costs no more digits than its own rounding
  * to fp32; where a group's squares leave fp32's range they are taken in 64 bits.  An infinity or a NaN makes
- * its group's rstd and results NaN.
+ * its group's rstd and results NaN.  SiLU is good to (5 + 1.2 |z|) 2^-23 of its value (0 below -87) before it is
+ * rounded to the storage type.
  */
 typedef enum { CBR_ACT_NONE = 0, CBR_ACT_RELU = 1, CBR_ACT_SILU = 2 } cbr_act_t;
 typedef struct {
