@@ -169,3 +169,24 @@ def test_silu_over_its_range():
 @pytest.mark.parametrize("shape,groups", [((2, 24, 20, 1536), 24), ((3, 7, 9, 2048), 32), ((2, 60, 61, 1048), 8), ((1, 100, 90, 1024), 1)])
 def test_wide_pixels_that_a_block_has_columns_for(shape, groups, dtype):
     check(make(shape, dtype, seed=27), groups, "relu")
+
+
+@pytest.mark.parametrize("shape,groups", [((2, 20, 21, 512), 1), ((2, 70, 71, 1024), 2), ((2, 9, 5, 2056), 1)])
+def test_groups_wider_than_a_block(shape, groups):
+    """Values far apart, and one NaN, in groups of more channels than a block has threads; strided, and in place."""
+    s = make(shape, "bf16", seed=28)
+    s["x"] = (s["x"].float() * 1e27).to(torch.bfloat16)
+    want = check(s, groups, "relu")
+    c = shape[-1]
+    room = torch.full((*shape[:-1], c + 24), 7.0, dtype=torch.bfloat16, device="cuda")
+    x = room[..., 8:8 + c]
+    x.copy_(s["x"])
+    got = gn.group_norm_forward(x, s["gamma"], s["beta"], groups, eps=EPS, act="relu", out={"y": x})
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    assert bool((room[..., :8] == 7).all()) and bool((room[..., 8 + c:] == 7).all())
+    s["x"][1, 3, 4, c - 1] = math.nan
+    got = gn.group_norm_forward(s["x"], s["gamma"], s["beta"], groups, eps=EPS, act="relu")
+    bad = torch.zeros(shape[0], groups, dtype=torch.bool, device="cuda")
+    bad[1, groups - 1] = True
+    assert torch.equal(torch.isnan(got["mean"]), bad) and torch.equal(torch.isnan(got["rstd"]), bad)
+    assert torch.equal(torch.isnan(got["y"]).flatten(1, -2).any(1), bad.repeat_interleave(c // groups, 1))
